@@ -217,8 +217,6 @@ def prepare(case, seed):
             size = qsa.paged_attn_workspace_size(s["q"].shape[0], case["seqs"], s["max_q"], case["q_heads"], case["heads"], case["dim"])
         elif op == "prompt":
             size = qsa.prompt_attn_workspace_size(s["q"].shape[0], s["cu"].numel() - 1, case["q_heads"], case["heads"], case["dim"])
-        elif op == "verify":
-            size = qsa.draft_verify_workspace_size(case["seqs"], case["vocab"])
         s["workspace"] = torch.zeros(max(size, 16), dtype=torch.uint8, device=DEV)
     return s
 
@@ -254,7 +252,7 @@ def _own_prompt(s):
 
 
 def _own_verify(s):
-    s["qsa"].draft_verify(s["target"], s["draft"], s["tokens"], s["u"], s["out"], s["accepted"], n_draft=s["n_draft"], workspace=s["workspace"])
+    s["qsa"].draft_verify(s["target"], s["draft"], s["tokens"], s["u"], s["out"], s["accepted"], n_draft=s["n_draft"])
     return s["out"], s["accepted"]
 
 
