@@ -6,15 +6,18 @@ that owns the per-layer device buffers.  There is no CPU or PyTorch fallback.
 """
 from ._binding import (  # noqa: F401
     QSA_BF16,
+    QSA_E4M3,
     QSA_F32,
     QSA_PREC_BF16_TC,
     QSA_PREC_F32,
     QSA_WAIT_DEFAULT_NS,
+    PagedCache,
     QSAError,
     decode_step,
     decode_step_host_layout,
     decode_step_host_workspace_size,
     decode_step_workspace_size,
+    draft_verify,
     expand_block_scores,
     gather_kv,
     header_functions,
@@ -25,7 +28,13 @@ from ._binding import (  # noqa: F401
     mask_sparse_attn,
     mask_sparse_eligible,
     mask_to_list,
+    paged_attn,
+    paged_attn_workspace_size,
+    paged_read,
+    paged_write,
     pool_update,
+    prompt_attn,
+    prompt_attn_workspace_size,
     set_wait_options,
     sparse_attn,
     sparse_attn_union,

@@ -17,7 +17,7 @@ LIB_PATH = os.path.join(HERE, "_build", "libqsa.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "qsa.h")
 
 QSA_OK, QSA_ERR_INVALID_ARG, QSA_ERR_UNSUPPORTED, QSA_ERR_CUDA, QSA_ERR_TIMEOUT = range(5)
-QSA_F32, QSA_BF16 = 0, 1
+QSA_F32, QSA_BF16, QSA_E4M3 = 0, 1, 2
 QSA_PREC_F32, QSA_PREC_BF16_TC = 0, 1
 QSA_WAIT_DEFAULT_NS = 2_000_000_000
 
@@ -74,6 +74,15 @@ _SIGNATURES = {
     "qsa_mask_sparse_eligible": (_int, [_int, _f, _f, _i64, _i64]),
     "qsa_mask_sparse_attn": (_int, [_p, _i64, _int, _int, _int, _int, _f, _p, _int, _i64, _i64,
                                     _p, _i64, _i64, _p, _p, _p, _p]),
+    "qsa_paged_write": (_int, [_p, _p, _i64, _i64, _p, _p, _p, _p, _int, _i64, _i64, _i64, _p]),
+    "qsa_paged_read": (_int, [_p, _p, _i64, _i64, _p, _p, _p, _p, _i64, _i64, _p, _p, _int, _p]),
+    "qsa_paged_attn": (_int, [_p, _p, _i64, _i64, _p, _p, _p, _int, _i64, _i64, _i64, _int, _f,
+                              _int, _p, _p, _p, _sz, _p]),
+    "qsa_paged_attn_workspace_size": (_sz, [_i64, _i64, _i64, _int, _int, _int]),
+    "qsa_prompt_attn": (_int, [_p, _p, _p, _int, _i64, _i64, _i64, _i64, _p, _i64, _int, _int,
+                               _int, _f, _int, _p, _p, _p, _sz, _p]),
+    "qsa_prompt_attn_workspace_size": (_sz, [_i64, _i64, _int, _int, _int]),
+    "qsa_draft_verify": (_int, [_p, _i64, _p, _i64, _p, _p, _p, _i64, _i64, _i64, _p, _p, _p]),
 }
 
 _lib = None
@@ -384,3 +393,231 @@ def mask_sparse_eligible(has_mask, max_bias, softcap, n_kv, max_list) -> bool:
     if st not in (QSA_OK, QSA_ERR_UNSUPPORTED):
         raise QSAError("qsa_mask_sparse_eligible", st)
     return st == QSA_OK
+
+
+# ------------------------------------------------- paged cache, dense attention, verification
+
+class _PagedCacheStruct(ctypes.Structure):
+    _fields_ = [("K", _p), ("V", _p), ("K_exp", _p), ("V_exp", _p), ("dtype", _int),
+                ("H_kv", _int), ("d", _int), ("ld_k", _i64), ("ld_v", _i64), ("n_pages", _i64),
+                ("page_size", _int)]
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _dp(t):
+    """Data pointer as an integer, or None."""
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream):
+    import torch
+
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _need_i32(name, t, *shape):
+    """An int32 CUDA tensor with contiguous rows and at least the given shape (None: any)."""
+    import torch
+
+    ok = (t.dtype == torch.int32 and t.is_cuda and t.dim() == len(shape)
+          and all(w is None or n >= w for n, w in zip(t.shape, shape))
+          and (t.numel() <= 1 or t.stride(-1) == 1))
+    _need(ok, f"{name}: an int32 CUDA tensor of shape {shape} or more is wanted, "
+              f"got {t.dtype} {tuple(t.shape)}")
+
+
+def _need_table(table, n_seq):
+    _need_i32("table", table, n_seq, None)
+    _need(table.is_contiguous(), "table: packed [n_seq][pages]")
+
+
+def _head_rows(name, t, H, d):
+    """[n][H][d] (or [n][H*d]) rows whose heads are contiguous; the stride between rows."""
+    n = t.shape[0] if t.dim() > 1 else 0
+    width = t.shape[1] * t.shape[2] if t.dim() == 3 else (t.shape[1] if t.dim() == 2 else -1)
+    ok = t.is_cuda and width == H * d and (t.stride(-1) == 1 or n == 0)
+    if ok and t.dim() == 3:
+        ok = t.shape[2] == d and (H == 1 or t.stride(1) == d or n == 0)
+    _need(ok, f"{name}: a CUDA tensor of shape [n][{H}][{d}] with contiguous rows is wanted, "
+              f"got {tuple(t.shape)} with strides {tuple(t.stride())}")
+    return t.stride(0) if n > 1 else H * d
+
+
+class PagedCache:
+    """A qsa_paged_cache: a pool of pages in K and V, [n_pages * page_size][H_kv][d] (or with a
+    leading [n_pages][page_size]) of float32, bfloat16 or float8_e4m3fn; the last with its
+    exponent bytes K_exp, V_exp [n_pages * page_size][H_kv] uint8.  Holds the tensors."""
+
+    def __init__(self, K, V, page_size, K_exp=None, V_exp=None):
+        import torch
+
+        if K.dim() == 4:
+            K, V = K.flatten(0, 1), V.flatten(0, 1)
+            if K_exp is not None:
+                K_exp, V_exp = K_exp.flatten(0, 1), V_exp.flatten(0, 1)
+        _need(K.dim() == 3 and K.shape == V.shape and K.dtype == V.dtype and K.device == V.device,
+              "K and V: two tensors of one type and shape [rows][H_kv][d]")
+        types = {torch.float32: QSA_F32, torch.bfloat16: QSA_BF16, torch.float8_e4m3fn: QSA_E4M3}
+        if K.dtype not in types:
+            raise TypeError(f"a paged cache is float32, bfloat16 or float8_e4m3fn, got {K.dtype}")
+        rows, self.H_kv, self.d = K.shape
+        _need(page_size > 0 and rows % page_size == 0, "K and V: a whole number of pages")
+        ld_k = _head_rows("K", K, self.H_kv, self.d)
+        ld_v = _head_rows("V", V, self.H_kv, self.d)
+        if K.dtype == torch.float8_e4m3fn:
+            for e in (K_exp, V_exp):
+                _need(e is not None and e.dtype == torch.uint8 and e.is_contiguous()
+                      and e.device == K.device and tuple(e.shape) == (rows, self.H_kv),
+                      "K_exp and V_exp: contiguous uint8 [rows][H_kv] beside an 8-bit cache")
+        self.K, self.V, self.K_exp, self.V_exp = K, V, K_exp, V_exp
+        self.page_size, self.n_pages = page_size, rows // page_size
+        self._struct = _PagedCacheStruct(_dp(K), _dp(V), _dp(K_exp), _dp(V_exp), types[K.dtype],
+                                         self.H_kv, self.d, ld_k, ld_v, self.n_pages, page_size)
+        self._ref = ctypes.addressof(self._struct)
+
+
+def paged_write(cache, table, cu_q, kv_len, k, v, stream=None):
+    """qsa_paged_write: rows k, v [n_tok][H_kv][d] (float32 or bfloat16) of the new tokens into
+    the pages of their sequences (table [n_seq][>= pages], cu_q [n_seq + 1], kv_len [n_seq])."""
+    n_seq = kv_len.shape[0]
+    _need_table(table, n_seq)
+    _need_i32("cu_q", cu_q, n_seq + 1)
+    _need_i32("kv_len", kv_len, None)
+    ld_k = _head_rows("k", k, cache.H_kv, cache.d)
+    ld_v = _head_rows("v", v, cache.H_kv, cache.d)
+    _need(k.shape[0] == v.shape[0] and k.dtype == v.dtype, "k and v: one type and length")
+    if k.shape[0] == 0:
+        return  # an empty tensor has no address
+    _check("qsa_paged_write", load().qsa_paged_write(
+        cache._ref, _dp(table), table.shape[1], n_seq, _dp(cu_q), _dp(kv_len), _dp(k), _dp(v),
+        _dtype(k), k.shape[0], ld_k, ld_v, _raw_stream(stream)))
+
+
+def paged_read(cache, table, kv_len, n_cells, max_cells, K_out, V_out, pos=None, seq=None,
+               stream=None):
+    """qsa_paged_read: the listed cells (pos [n_list][max_cells], or the first n_cells[i] of each
+    sequence) as values, K_out / V_out [n_list][max_cells][H_kv][d] float32 or bfloat16."""
+    n_seq, n_list = kv_len.shape[0], n_cells.shape[0]
+    _need_table(table, n_seq)
+    _need_i32("kv_len", kv_len, None)
+    _need_i32("n_cells", n_cells, None)
+    if pos is not None:
+        _need_i32("pos", pos, n_list, max_cells)
+        _need(pos.shape[1] == max_cells and pos.is_contiguous(), "pos: packed [n_list][max_cells]")
+    if seq is not None:
+        _need_i32("seq", seq, n_list)
+    else:
+        _need(n_list <= n_seq, "n_cells: one list per sequence unless seq is given")
+    size = n_list * max_cells * cache.H_kv * cache.d
+    for t in (K_out, V_out):
+        _need(t.is_cuda and t.is_contiguous() and t.numel() >= size,
+              "K_out and V_out: packed [n_list][max_cells][H_kv][d]")
+    _need(K_out.dtype == V_out.dtype, "K_out and V_out: one type")
+    if size == 0:
+        return
+    _check("qsa_paged_read", load().qsa_paged_read(
+        cache._ref, _dp(table), table.shape[1], n_seq, _dp(kv_len), _dp(seq), _dp(pos),
+        _dp(n_cells), n_list, max_cells, _dp(K_out), _dp(V_out), _dtype(K_out),
+        _raw_stream(stream)))
+
+
+def _attn_buffers(q, out, lse, H_q, d):
+    n_tok = q.shape[0]
+    ld_q = _head_rows("q", q, H_q, d)
+    _need(out.is_cuda and out.dtype == q.dtype and out.is_contiguous() and out.numel() == n_tok * H_q * d,
+          "out: packed, of q's type and shape")
+    if lse is not None:
+        import torch
+
+        _need(lse.is_cuda and lse.dtype == torch.float32 and lse.is_contiguous()
+              and lse.numel() == n_tok * H_q, "lse: packed float32 [n_tok][H_q]")
+    return n_tok, ld_q
+
+
+def paged_attn_workspace_size(n_tok, n_seq, max_q, H_q, H_kv, d) -> int:
+    return int(load().qsa_paged_attn_workspace_size(n_tok, n_seq, max_q, H_q, H_kv, d))
+
+
+def paged_attn(cache, table, cu_q, kv_len, q, out, scale, max_q, causal=True, lse=None,
+               workspace=None, stream=None):
+    """qsa_paged_attn: q [n_tok][H_q][d] (float32 or bfloat16) of the new tokens over the cells
+    of their sequences; out like q, lse [n_tok][H_q] float32.  workspace:
+    paged_attn_workspace_size() bytes of device memory."""
+    n_seq = kv_len.shape[0]
+    H_q = q.shape[1] if q.dim() == 3 else q.shape[-1] // cache.d
+    _need_table(table, n_seq)
+    _need_i32("cu_q", cu_q, n_seq + 1)
+    _need_i32("kv_len", kv_len, None)
+    n_tok, ld_q = _attn_buffers(q, out, lse, H_q, cache.d)
+    if n_tok == 0:
+        return
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check("qsa_paged_attn", load().qsa_paged_attn(
+        cache._ref, _dp(table), table.shape[1], n_seq, _dp(cu_q), _dp(kv_len), _dp(q),
+        _dtype(q), n_tok, max_q, ld_q, H_q, scale, int(bool(causal)), _dp(out), _dp(lse),
+        _dp(workspace), ws_bytes, _raw_stream(stream)))
+
+
+def prompt_attn_workspace_size(n_tok, n_seq, H_q, H_kv, d) -> int:
+    return int(load().qsa_prompt_attn_workspace_size(n_tok, n_seq, H_q, H_kv, d))
+
+
+def prompt_attn(q, k, v, cu_seq, out, scale, causal=True, lse=None, workspace=None, stream=None):
+    """qsa_prompt_attn: packed prompts q [n_tok][H_q][d], k, v [n_tok][H_kv][d] (float32 or
+    bfloat16), sequence s at tokens cu_seq[s] .. cu_seq[s+1] - 1; out like q, lse [n_tok][H_q]
+    float32.  workspace: prompt_attn_workspace_size() bytes of device memory."""
+    _need(q.dim() == 3 and k.dim() == 3 and v.dim() == 3, "q, k, v: [n_tok][heads][d]")
+    H_q, H_kv, d = q.shape[1], k.shape[1], q.shape[2]
+    _need_i32("cu_seq", cu_seq, 1)
+    n_tok, ld_q = _attn_buffers(q, out, lse, H_q, d)
+    ld_k, ld_v = _head_rows("k", k, H_kv, d), _head_rows("v", v, H_kv, d)
+    _need(k.shape[0] == n_tok and v.shape[0] == n_tok and k.dtype == q.dtype == v.dtype,
+          "q, k, v: one type and length")
+    if n_tok == 0:
+        return
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check("qsa_prompt_attn", load().qsa_prompt_attn(
+        _dp(q), _dp(k), _dp(v), _dtype(q), n_tok, ld_q, ld_k, ld_v, _dp(cu_seq),
+        cu_seq.shape[0] - 1, H_q, H_kv, d, scale, int(bool(causal)), _dp(out), _dp(lse),
+        _dp(workspace), ws_bytes, _raw_stream(stream)))
+
+
+def draft_verify(target, draft, tokens, u, tokens_out, n_accepted, n_draft=None, stream=None):
+    """qsa_draft_verify: target [n_seq][max_draft + 1][vocab] and draft [n_seq][max_draft][vocab]
+    (or None) fp32 probabilities, tokens [n_seq][max_draft] and n_draft [n_seq] int32, u
+    [n_seq][max_draft + 1] fp32; tokens_out [n_seq][max_draft + 1] and n_accepted [n_seq] int32."""
+    import torch
+
+    _need(target.dim() == 3, "target: [n_seq][max_draft + 1][vocab]")
+    n_seq, n_rows, vocab = target.shape
+    max_draft = n_rows - 1
+    _need(max_draft >= 0, "target: [n_seq][max_draft + 1][vocab]")
+
+    def rows(name, t, n):
+        _need(t.is_cuda and t.dtype == torch.float32 and tuple(t.shape) == (n_seq, n, vocab)
+              and (t.stride(2) == 1 or vocab == 1 or t.numel() == 0),
+              f"{name}: float32 [{n_seq}][{n}][{vocab}] with contiguous rows")
+        if n == 0 or n_seq == 0:
+            return vocab
+        ld = t.stride(1) if n > 1 else (t.stride(0) if n_seq > 1 else vocab)
+        _need(n_seq == 1 or t.stride(0) == n * ld, f"{name}: rows at one stride")
+        return ld
+
+    ld_t = rows("target", target, n_rows)
+    ld_d = rows("draft", draft, max_draft) if draft is not None else 0
+    for name, t, shape in (("tokens", tokens, (n_seq, max_draft)),
+                           ("tokens_out", tokens_out, (n_seq, n_rows)),
+                           ("n_accepted", n_accepted, (n_seq,))):
+        _need(t.is_cuda and t.dtype == torch.int32 and tuple(t.shape) == shape
+              and t.is_contiguous(), f"{name}: packed int32 {shape}")
+    if n_draft is not None:
+        _need_i32("n_draft", n_draft, n_seq)
+    _need(u.is_cuda and u.dtype == torch.float32 and tuple(u.shape) == (n_seq, n_rows)
+          and u.is_contiguous(), f"u: packed float32 ({n_seq}, {n_rows})")
+    _check("qsa_draft_verify", load().qsa_draft_verify(
+        _dp(target), ld_t, _dp(draft), ld_d, _dp(tokens), _dp(n_draft), _dp(u), n_seq, max_draft,
+        vocab, _dp(tokens_out), _dp(n_accepted), _raw_stream(stream)))

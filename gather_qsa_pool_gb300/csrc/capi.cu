@@ -69,7 +69,7 @@ const char *qsa_status_str(qsa_status s)
     return "QSA_ERR_UNKNOWN";
 }
 
-int qsa_version(void) { return (2 << 16) | 4; }
+int qsa_version(void) { return (2 << 16) | 5; }
 
 void qsa_set_wait_options(int32_t *status_out, uint64_t pipeline_limit_ns)
 {

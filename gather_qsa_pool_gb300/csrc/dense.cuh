@@ -1,0 +1,248 @@
+// dense.cuh -- shared pieces of the paged key/value cache and of the dense attention over it
+// (paged_rw.cu, dense_attn.cu, dense_decode.cu, dense_attn_tc.cu): the device view of a cache,
+// the row of a cell, the packed sequences and the flattened list of work.
+#pragma once
+
+#include <math.h>
+
+#include "qsa_internal.cuh"
+
+namespace qsa {
+
+// Exponents of a QSA_E4M3 row: value = code * 2^(byte - 127), byte in [27, 227].
+constexpr int kExpBias = 127;
+constexpr int kExpMin = -100, kExpMax = 100;
+
+// 2^e for e in [-126, 127], from its bits.
+__host__ __device__ __forceinline__ float two_to(int e)
+{
+    union {
+        uint32_t u;
+        float f;
+    } x;
+    x.u = (uint32_t)(e + 127) << 23;
+    return x.f;
+}
+
+// Keys and values as the attention kernels see them.  table != NULL: a paged pool, the cell at
+// position p of sequence s lives in row table[s][p >> page_shift] << page_shift | (p & mask).
+// table == NULL: packed sequences, the cell is row cu[s] + p.
+struct KvView {
+    const void *K, *V;
+    const uint8_t *K_exp, *V_exp;  // [rows][H_kv], QSA_E4M3 only
+    int64_t ld_k, ld_v;            // elements between rows
+    const int32_t *table;
+    int64_t ld_table;
+    int32_t n_pages;
+    int32_t page_shift;
+    int32_t H_kv;
+};
+
+// Packed query tokens: sequence s has tokens cu[s] .. cu[s+1] - 1, the last of its kv_len[s]
+// cells (kv_len == NULL: as many cells as tokens).
+struct SeqView {
+    const int32_t *cu;
+    const int32_t *kv_len;
+    int32_t n_seq;
+    int64_t n_tok;  // tokens in the buffers: whatever cu says, none beyond is touched
+};
+
+// Tokens of a sequence, clipped to the buffers.
+__device__ __forceinline__ void seq_tokens(const SeqView &sv, int s, int64_t &t0, int &len)
+{
+    int64_t a = sv.cu[s], b = sv.cu[s + 1];
+    a = a < 0 ? 0 : (a > sv.n_tok ? sv.n_tok : a);
+    b = b < a ? a : (b > sv.n_tok ? sv.n_tok : b);
+    t0 = a;
+    len = (int)(b - a);
+}
+
+__device__ __forceinline__ int seq_cells(const SeqView &sv, int s, int len)
+{
+    return sv.kv_len ? max(sv.kv_len[s], 0) : len;
+}
+
+// A paged sequence longer than its row of the table cannot be right: its outputs become NaN.
+__device__ __forceinline__ bool cells_fit(const KvView &kv, int cells)
+{
+    return kv.table == nullptr || (int64_t)cells <= (kv.ld_table << kv.page_shift);
+}
+
+// Pool row of the cell at position p of sequence s; -1 when its page is not in the pool.
+// first: cu[s] of packed sequences.
+__device__ __forceinline__ int64_t cell_row(const KvView &kv, int s, int64_t first, int p)
+{
+    if (kv.table == nullptr) return first + p;
+    const int64_t j = p >> kv.page_shift;
+    if (j >= kv.ld_table) return -1;
+    const int32_t page = kv.table[(int64_t)s * kv.ld_table + j];
+    if ((uint32_t)page >= (uint32_t)kv.n_pages) return -1;
+    return ((int64_t)page << kv.page_shift) | (p & ((1 << kv.page_shift) - 1));
+}
+
+// ------------------------------------------------------------------ the flattened work list
+// The rows of a sequence and KV head (its tokens times the G query heads of the KV head, token
+// major) are cut into row tiles of `rt` tokens; a (sequence, KV head, row tile) is an item, and
+// an item's work is its visible cells in tiles of `kt` cells (at least one, so that the rows of
+// an item that sees nothing are written too).  Items are numbered sequence-major, then KV head,
+// then row tile, and their tiles form one list, which is cut into equal shares: a CTA's share
+// covers parts of at most a few items, and only its first and last part can be incomplete.
+struct WorkShape {
+    int32_t rt;      // query tokens per row tile
+    int32_t kt;      // cells per tile; 0: every item is one tile (work that is not cut)
+    int32_t H_kv;
+    int32_t causal;
+};
+
+// Cells that the tokens of row tile t see together.
+__device__ __forceinline__ int item_cells(const WorkShape &w, int len, int cells, int t)
+{
+    if (!w.causal) return cells;
+    const int64_t last = (int64_t)(t + 1) * w.rt;
+    const int64_t seen = (int64_t)cells - len + (last < len ? last : len);
+    return seen < 0 ? 0 : (int)seen;
+}
+
+__device__ __forceinline__ int item_tiles(const WorkShape &w, int len, int cells, int t)
+{
+    if (w.kt == 0) return 1;
+    const int n = item_cells(w, len, cells, t);
+    return n > 0 ? (n + w.kt - 1) / w.kt : 1;
+}
+
+// Tiles of one KV head of a sequence.
+__device__ __forceinline__ int64_t seq_tiles(const WorkShape &w, int len, int cells)
+{
+    const int nt = (len + w.rt - 1) / w.rt;
+    if (!w.causal || w.kt == 0) return (int64_t)nt * item_tiles(w, len, cells, 0);
+    int64_t sum = 0;
+    for (int t = 0; t < nt; ++t) sum += item_tiles(w, len, cells, t);
+    return sum;
+}
+
+struct WorkItem {
+    int32_t s, g, t;        // sequence, KV head, row tile
+    int64_t start;          // its first tile in the list
+    int32_t tiles;
+};
+
+// Total tiles of the list; all 32 lanes call it and get the same value.
+__device__ __forceinline__ int64_t work_total(const SeqView &sv, const WorkShape &w)
+{
+    const int lane = threadIdx.x & 31;
+    int64_t sum = 0;
+    for (int s = lane; s < sv.n_seq; s += 32) {
+        int64_t t0;
+        int len;
+        seq_tokens(sv, s, t0, len);
+        sum += seq_tiles(w, len, seq_cells(sv, s, len));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum * w.H_kv;
+}
+
+// The item that holds tile x of the list (0 <= x < work_total); all 32 lanes call it.
+__device__ __forceinline__ WorkItem work_find(const SeqView &sv, const WorkShape &w, int64_t x)
+{
+    const int lane = threadIdx.x & 31;
+    int64_t base = 0;
+    WorkItem it = {0, 0, 0, 0, 1};
+    for (int s0 = 0; s0 < sv.n_seq; s0 += 32) {
+        const int s = s0 + lane;
+        int64_t mine = 0;
+        int len = 0, cells = 0;
+        if (s < sv.n_seq) {
+            int64_t t0;
+            seq_tokens(sv, s, t0, len);
+            cells = seq_cells(sv, s, len);
+            mine = seq_tiles(w, len, cells) * w.H_kv;
+        }
+        int64_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        const bool in = x < base + incl;
+        const uint32_t hit = __ballot_sync(0xffffffffu, in);
+        if (hit) {
+            const int j = __ffs(hit) - 1;  // the first lane whose prefix passes x
+            const int64_t sbase = base + __shfl_sync(0xffffffffu, incl - mine, j);
+            const int64_t stot = __shfl_sync(0xffffffffu, mine, j);
+            len = __shfl_sync(0xffffffffu, len, j);
+            cells = __shfl_sync(0xffffffffu, cells, j);
+            const int64_t per_head = stot / w.H_kv;
+            it.s = s0 + j;
+            it.g = (int32_t)((x - sbase) / per_head);
+            int64_t at = sbase + it.g * per_head;
+            const int nt = (len + w.rt - 1) / w.rt;
+            int t = 0;
+            if (w.kt == 0) {
+                t = (int)(x - at);
+                at = x;
+            }
+            for (; w.kt != 0 && t < nt - 1; ++t) {
+                const int n = item_tiles(w, len, cells, t);
+                if (x < at + n) break;
+                at += n;
+            }
+            it.t = t;
+            it.start = at;
+            it.tiles = item_tiles(w, len, cells, t);
+            return it;
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return it;
+}
+
+// The item after `it` in the list (its sequence's length and cells are looked up again).
+// Returns false past the end.  All 32 lanes call it with the same item.
+__device__ __forceinline__ bool work_next(const SeqView &sv, const WorkShape &w, WorkItem &it)
+{
+    int64_t t0;
+    int len;
+    seq_tokens(sv, it.s, t0, len);
+    int cells = seq_cells(sv, it.s, len);
+    const int nt = (len + w.rt - 1) / w.rt;
+    it.start += it.tiles;
+    if (++it.t >= nt) {
+        it.t = 0;
+        if (++it.g >= w.H_kv) {
+            it.g = 0;
+            do {
+                if (++it.s >= sv.n_seq) return false;
+                seq_tokens(sv, it.s, t0, len);
+            } while (len == 0);
+            cells = seq_cells(sv, it.s, len);
+        }
+    }
+    it.tiles = item_tiles(w, len, cells, it.t);
+    return true;
+}
+
+// Partial result of part of an item: one record per (CTA, first / last part), holding for each
+// row the running maximum (log2 units), the sum and the unnormalised output.
+__host__ __device__ inline int64_t partial_floats(int rows, int d) { return (int64_t)rows * (d + 2); }
+
+// ------------------------------------------------------------------ launchers
+
+struct DenseArgs {
+    KvView kv;
+    SeqView sv;
+    qsa_dtype kv_dtype, q_dtype;  // out has q's type
+    const void *q;
+    int64_t ld_q;  // elements between tokens
+    void *out;     // [n_tok][H_q][d] packed
+    float *lse;    // [n_tok][H_q] or NULL
+    int H_q, d;
+    float scale;
+    int causal;
+    int64_t pool_rows;  // rows of K and V
+};
+
+// Any shape: d a multiple of 8 up to 256, fp32 arithmetic on the CUDA cores.
+cudaError_t launch_dense_attn(const DenseArgs &a, cudaStream_t st);
+
+}  // namespace qsa

@@ -52,7 +52,9 @@ typedef enum {
                                 see qsa_set_wait_options) */
 } qsa_status;
 
-typedef enum { QSA_F32 = 0, QSA_BF16 = 1 } qsa_dtype;
+/* QSA_E4M3 (8-bit floating point with one exponent byte per row) is a type of paged caches
+ * only, see qsa_paged_cache. */
+typedef enum { QSA_F32 = 0, QSA_BF16 = 1, QSA_E4M3 = 2 } qsa_dtype;
 
 typedef enum {
     QSA_PREC_F32 = 0,    /* fp32 operands, fp32 accumulation (CUDA cores) */
@@ -66,7 +68,8 @@ const char *qsa_status_str(qsa_status s);
 /* Library ABI version: (major << 16) | minor.  Major 2: pooled-cache dtype arguments,
  * several queries per decode step, the host-fed decode step; minor 1: decode plans;
  * minor 2: qsa_mask_sparse_attn; minor 3: qsa_sparse_attn_union; minor 4:
- * qsa_set_wait_options. */
+ * qsa_set_wait_options; minor 5: the paged cache (qsa_paged_write, _read, _attn),
+ * qsa_prompt_attn and qsa_draft_verify. */
 int qsa_version(void);
 
 /*
@@ -651,6 +654,168 @@ qsa_status qsa_mask_sparse_attn(const float *q, int64_t n_q, int H_q, int H_kv, 
  */
 qsa_status qsa_mask_sparse_eligible(int has_mask, float max_bias, float softcap, int64_t n_kv,
                                     int64_t max_list);
+
+/* ------------------------------------------------------------------------------------------
+ * The paged key/value cache and the dense attention over it.
+ *
+ * The source pages keep one contiguous cache per sequence and leave dense attention to their
+ * host program; a server keeps many sequences of changing length in pages, often in 8 bits, and
+ * runs dense attention in its other layers and while a context is no longer than the selection.
+ * These calls are this library's.
+ *
+ * qsa_paged_cache -- a pool of pages, described on the host.  Row r = page * page_size + offset
+ * holds one token: KV head g of row r at K[r*ld_k + g*d .. + d), likewise V.
+ *
+ *   dtype      QSA_F32, QSA_BF16, or QSA_E4M3: e4m3 codes (one byte each; 4 significant bits)
+ *              with one exponent byte b per row and KV head in K_exp / V_exp [rows][H_kv]; the
+ *              value is code * 2^(b - 127), b in [27, 227]
+ *   page_size  tokens per page, a power of two from 8 to 4096
+ *   n_pages    pages in the pool, n_pages * page_size < 2^31
+ * Requirements (INVALID_ARG otherwise): K, V non-null and 16-byte aligned, ld_k, ld_v >= H_kv*d
+ * with rows a multiple of 16 bytes (8 for QSA_E4M3), d a multiple of 8; UNSUPPORTED for d > 256.
+ *
+ * Sequences.  table [n_seq][ld_table] int32 gives each sequence's pages in order (entries past
+ * its length are not read); kv_len [n_seq] int32 its cells, the new tokens among them; cu_q
+ * [n_seq + 1] int32 the running count of new tokens: sequence s has tokens cu_q[s] ..
+ * cu_q[s+1] - 1 of the packed buffers, and they are its last cells: token i of n sits at
+ * position kv_len - n + i.  All three are device memory and are read by the kernels, so a
+ * captured graph replays with whatever they hold then.  Tokens from cu_q[n_seq] on (padding)
+ * are ignored and their outputs left as they were; no token outside [0, n_tok) is touched.
+ */
+typedef struct {
+    void *K, *V;
+    uint8_t *K_exp, *V_exp; /* QSA_E4M3 only, else NULL */
+    qsa_dtype dtype;
+    int H_kv, d;
+    int64_t ld_k, ld_v; /* elements between rows */
+    int64_t n_pages;
+    int page_size;
+} qsa_paged_cache;
+
+/*
+ * qsa_paged_write -- store the new tokens' K and V rows in their cells.
+ *
+ *   k, v   [n_tok][ld] rows of H_kv*d values of type src_dtype (QSA_F32 or QSA_BF16)
+ * Cells of a QSA_BF16 pool get the value rounded to nearest even.  A QSA_E4M3 row (one token,
+ * one KV head) gets the least exponent e with max|x| <= 448 * 2^e over its finite values,
+ * clamped to [-100, 100], and the codes nearest to x * 2^-e (ties to even; clamped to 448 when
+ * e = 100; infinities and NaN become NaN).  A power of two scales exactly, so each value is
+ * rounded once, to 4 significant bits (3 below 2^-6 * 2^e and fewer from there).
+ * A token whose position is negative or whose page is not in the pool is skipped.  Two tokens
+ * of one call never share a cell unless the table names a page twice; then the cell holds
+ * either one's row, or a mixture.
+ * Errors: INVALID_ARG for null pointers, sizes < 0, n_seq < 1 with n_tok > 0, ld < H_kv*d, a
+ * type other than QSA_F32 / QSA_BF16, k or v not 16-byte aligned or rows that are not a multiple
+ * of 16 bytes; UNSUPPORTED for n_seq or n_tok above 2^31 - 1.
+ */
+qsa_status qsa_paged_write(const qsa_paged_cache *cache, const int32_t *table, int64_t ld_table,
+                           int64_t n_seq, const int32_t *cu_q, const int32_t *kv_len,
+                           const void *k, const void *v, qsa_dtype src_dtype, int64_t n_tok,
+                           int64_t ld_k, int64_t ld_v, qsa_stream_t stream);
+
+/*
+ * qsa_paged_read -- copy listed cells out of the pool, as values.
+ *
+ * List i (n_list of them) belongs to sequence seq[i], or to sequence i when seq is NULL.  Its
+ * cells are pos[i*max_cells + j], j < n_cells[i] (as qsa_gather_kv writes them), or the cells
+ * 0 .. n_cells[i] - 1 when pos is NULL:
+ *   K_out[(i*max_cells + j)][0 .. H_kv*d) = the cell's keys, V_out likewise (packed rows of type
+ *   out_dtype, QSA_F32 or QSA_BF16; codes times exponents are exact in both)
+ * which is the compact form that qsa_sparse_attn takes with pos = NULL.  Entries past n_cells[i]
+ * are left as they were (of a longer list the first max_cells are written); a cell outside
+ * [0, kv_len) or on a page outside the pool, or of a sequence outside [0, n_seq), gives zeros.
+ * Errors: INVALID_ARG for null required pointers, sizes < 0, a wrong type, K_out or V_out not
+ * 16-byte aligned; UNSUPPORTED for n_list * max_cells above 2^31 - 1.
+ */
+qsa_status qsa_paged_read(const qsa_paged_cache *cache, const int32_t *table, int64_t ld_table,
+                          int64_t n_seq, const int32_t *kv_len, const int32_t *seq,
+                          const int32_t *pos, const int32_t *n_cells, int64_t n_list,
+                          int64_t max_cells, void *K_out, void *V_out, qsa_dtype out_dtype,
+                          qsa_stream_t stream);
+
+/*
+ * qsa_paged_attn -- attention of new tokens (one per sequence, a few drafts, or a chunk) over
+ * every cell of their sequence.  The new tokens' own cells are in the pool already
+ * (qsa_paged_write).
+ *
+ * For token i of sequence s at position p and head h (KV head g = floor(h*H_kv/H_q)), over the
+ * cells j <= p (every cell of the sequence when causal is 0):
+ *   out[i][h][:] = sum_j softmax_j(scale * q[i][h] . K[j][g]) V[j][g][:]
+ *   lse_out[i][h] = log(sum_j exp(scale * q[i][h] . K[j][g]))   (natural log; optional)
+ * A token that sees no cell (p < 0) gives out = 0, lse = -inf.  Cells a token does not see do
+ * not enter its result, whatever they hold.  A sequence longer than its table row, or with a
+ * page outside the pool among its visible cells, gives out = NaN and lse = NaN.
+ *
+ *   q        [n_tok][H_q][d] of type q_dtype (QSA_F32 or QSA_BF16), ld_q elements between tokens
+ *   out      [n_tok][H_q][d] packed, of type q_dtype;  lse_out [n_tok][H_q] fp32 or NULL
+ *   max_q    the largest number of new tokens of one sequence, as far as the host knows: it
+ *            chooses the kernel, and no result depends on it
+ *   workspace  qsa_paged_attn_workspace_size() bytes, 256-byte aligned, for the parts of rows
+ *            whose cells are shared out; its contents do not matter, and calls that may run at
+ *            the same time need one each
+ * All sums, the softmax and the output accumulate in fp32.  With a QSA_BF16 query the tensor
+ * cores take the softmax weights in 16 bits (bf16 on a bf16 cache, fp16 on an e4m3 one); with a
+ * QSA_F32 query the arithmetic is fp32 throughout.
+ * Errors: INVALID_ARG for null pointers, sizes < 0, H_q not a multiple of H_kv, ld_q < H_q*d, a
+ * misaligned pointer (q and out 16 bytes, rows of q a multiple of 16 bytes), a workspace smaller
+ * than required; UNSUPPORTED for n_seq, n_tok or their work beyond 2^31 - 1 rows.
+ */
+qsa_status qsa_paged_attn(const qsa_paged_cache *cache, const int32_t *table, int64_t ld_table,
+                          int64_t n_seq, const int32_t *cu_q, const int32_t *kv_len, const void *q,
+                          qsa_dtype q_dtype, int64_t n_tok, int64_t max_q, int64_t ld_q, int H_q,
+                          float scale, int causal, void *out, float *lse_out, void *workspace,
+                          size_t workspace_bytes, qsa_stream_t stream);
+
+size_t qsa_paged_attn_workspace_size(int64_t n_tok, int64_t n_seq, int64_t max_q, int H_q, int H_kv,
+                                     int d);
+
+/*
+ * qsa_prompt_attn -- attention of whole prompts, packed one after another: every token over the
+ * tokens of its own sequence up to itself (all of them when causal is 0).
+ *
+ *   q        [n_tok][H_q][d], k, v [n_tok][H_kv][d], all of type `dtype` (QSA_F32 or QSA_BF16),
+ *            with ld_q, ld_k, ld_v elements between tokens
+ *   cu_seq   [n_seq + 1] int32 device: sequence s has tokens cu_seq[s] .. cu_seq[s+1] - 1
+ *   out      [n_tok][H_q][d] packed, of type `dtype`;  lse_out [n_tok][H_q] fp32 or NULL
+ *   workspace  as for qsa_paged_attn, of qsa_prompt_attn_workspace_size() bytes
+ * Result, errors and rows outside the sequences as for qsa_paged_attn (k and v 16-byte aligned
+ * with rows a multiple of 16 bytes).
+ */
+qsa_status qsa_prompt_attn(const void *q, const void *k, const void *v, qsa_dtype dtype,
+                           int64_t n_tok, int64_t ld_q, int64_t ld_k, int64_t ld_v,
+                           const int32_t *cu_seq, int64_t n_seq, int H_q, int H_kv, int d,
+                           float scale, int causal, void *out, float *lse_out, void *workspace,
+                           size_t workspace_bytes, qsa_stream_t stream);
+
+size_t qsa_prompt_attn_workspace_size(int64_t n_tok, int64_t n_seq, int H_q, int H_kv, int d);
+
+/*
+ * qsa_draft_verify -- which drafted tokens stand, and the token after them.
+ *
+ * Sequence s drafted n = n_draft[s] tokens (max_draft when n_draft is NULL) from the rows q_j of
+ * its draft model; p_0 .. p_n are the target's rows at the same places.  Draft j is taken while
+ *   u[s][j] * q_j(t_j) < p_j(t_j)
+ * (a token outside the vocabulary is refused); a is the number taken.  The next token is the
+ * first index whose running sum of w exceeds u[s][max_draft] * sum(w), with w = max(p_a - q_a, 0)
+ * after a refusal (w = p_a if that is zero everywhere) and w = p_n when all were taken.  Negative
+ * and NaN probabilities count as 0; without any weight the token is -1.  Products and sums are
+ * carried in 48 bits or more.
+ *
+ *   target   [n_seq][max_draft + 1] rows of ld_target >= vocab fp32 probabilities
+ *   draft    [n_seq][max_draft] rows of ld_draft >= vocab, or NULL for drafts chosen without
+ *            chance (q_j = 1 at t_j: taken with probability p_j(t_j), else w = p_a without t_a)
+ *   tokens   [n_seq][max_draft] int32;  n_draft [n_seq] int32 or NULL (clipped to max_draft)
+ *   u        [n_seq][max_draft + 1] fp32 numbers in [0, 1)
+ *   tokens_out  [n_seq][max_draft + 1] int32: the taken tokens, the next token, then -1
+ *   n_accepted  [n_seq] int32: a
+ * Errors: INVALID_ARG for null required pointers, sizes < 0, vocab < 1 or a stride below it, a
+ * pointer not aligned to 4 bytes; UNSUPPORTED for vocab, max_draft or n_seq * max_draft above
+ * 2^31 - 1 (n_seq * 8 too).
+ */
+qsa_status qsa_draft_verify(const float *target, int64_t ld_target, const float *draft,
+                            int64_t ld_draft, const int32_t *tokens, const int32_t *n_draft,
+                            const float *u, int64_t n_seq, int64_t max_draft, int64_t vocab,
+                            int32_t *tokens_out, int32_t *n_accepted, qsa_stream_t stream);
 
 #ifdef __cplusplus
 }
