@@ -76,10 +76,19 @@ qsa_status run_attn(const DenseArgs &a, int64_t max_q, void *workspace, size_t w
 {
     const int64_t items = (a.sv.n_tok + a.sv.n_seq) * (int64_t)a.kv.H_kv;
     if (items > kMaxInt || (int64_t)a.H_q * a.d > (1 << 24)) return QSA_ERR_UNSUPPORTED;
-    (void)max_q;
-    (void)workspace;
-    (void)workspace_bytes;
+    if (dense_decode_ok(a, max_q)) {
+        if (!workspace || !aligned(workspace, 256) || workspace_bytes < dense_decode_workspace())
+            return QSA_ERR_INVALID_ARG;
+        return from_cuda(launch_dense_decode(a, max_q, workspace, st));
+    }
     return from_cuda(launch_dense_attn(a, st));
+}
+
+// Enough for whichever kernel a call of this shape takes.
+size_t attn_workspace(int64_t n_tok, int64_t n_seq, int H_q, int H_kv, int d)
+{
+    if (n_tok <= 0 || n_seq <= 0 || H_q < 1 || H_kv < 1 || d < 1) return 0;
+    return dense_decode_workspace();
 }
 
 }  // namespace
@@ -130,8 +139,8 @@ qsa_status qsa_paged_read(const qsa_paged_cache *cache, const int32_t *table, in
 size_t qsa_paged_attn_workspace_size(int64_t n_tok, int64_t n_seq, int64_t max_q, int H_q, int H_kv,
                                      int d)
 {
-    (void)n_tok, (void)n_seq, (void)max_q, (void)H_q, (void)H_kv, (void)d;
-    return 0;
+    (void)max_q;
+    return attn_workspace(n_tok, n_seq, H_q, H_kv, d);
 }
 
 qsa_status qsa_paged_attn(const qsa_paged_cache *cache, const int32_t *table, int64_t ld_table,
@@ -169,8 +178,7 @@ qsa_status qsa_paged_attn(const qsa_paged_cache *cache, const int32_t *table, in
 
 size_t qsa_prompt_attn_workspace_size(int64_t n_tok, int64_t n_seq, int H_q, int H_kv, int d)
 {
-    (void)n_tok, (void)n_seq, (void)H_q, (void)H_kv, (void)d;
-    return 0;
+    return attn_workspace(n_tok, n_seq, H_q, H_kv, d);
 }
 
 qsa_status qsa_prompt_attn(const void *q, const void *k, const void *v, qsa_dtype dtype,

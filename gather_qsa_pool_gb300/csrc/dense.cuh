@@ -24,6 +24,24 @@ __host__ __device__ __forceinline__ float two_to(int e)
     return x.f;
 }
 
+// Eight consecutive values, 16-byte aligned.
+__device__ __forceinline__ void load8(const float *p, float *x)
+{
+    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float *x)
+{
+    const uint4 a = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
 // Keys and values as the attention kernels see them.  table != NULL: a paged pool, the cell at
 // position p of sequence s lives in row table[s][p >> page_shift] << page_shift | (p & mask).
 // table == NULL: packed sequences, the cell is row cu[s] + p.
@@ -244,5 +262,10 @@ struct DenseArgs {
 
 // Any shape: d a multiple of 8 up to 256, fp32 arithmetic on the CUDA cores.
 cudaError_t launch_dense_attn(const DenseArgs &a, cudaStream_t st);
+
+// A few new tokens per sequence (max_q as the host knows it) over bf16 or e4m3 cells, d 128.
+bool dense_decode_ok(const DenseArgs &a, int64_t max_q);
+size_t dense_decode_workspace();
+cudaError_t launch_dense_decode(const DenseArgs &a, int64_t max_q, void *workspace, cudaStream_t st);
 
 }  // namespace qsa

@@ -1,0 +1,834 @@
+// dense_decode.cu -- attention of a few new tokens per sequence over a long paged (or packed)
+// cache: bound by the one pass over the cells' keys and values.
+//
+// Mathematics: with s_j the logit of cell j in log2 units, a part of a row's cells gives
+// (m, l, o) = (reference, sum 2^(s_j - m), sum 2^(s_j - m) v_j), and parts join by scaling to a
+// common m.  m need not be the maximum: it moves only when a logit passes it by more than 8, so
+// sums and weights stay within 2^8 of the largest and the common tile needs no reduction across
+// lanes, one vote only.  On e4m3 cells v_j = c_j 2^e_j; the weight that multiplies the code is
+// 2^(s_j + e_j - mx) with a reference of its own, so that the fp16 weights keep their bits on
+// the cells that matter for o whatever the rows' exponents are.
+//
+// Shape: a CTA of four warps takes a share of the flattened list of (sequence, KV head, row
+// tile) items (dense.cuh), equal for every CTA, whatever the lengths: ragged batches stay
+// balanced and a captured graph follows lengths that change in place.  The rows of an item (new
+// tokens x the heads of its KV head) are one or two 16-row fragments of mma.m16n8k16; these
+// tensor instructions suffice since 16 rows per 256 or 512 bytes of K and V leave them under a
+// third busy.  Each warp runs its own ring of stages (cp.async, 8 KB each) over its own 16
+// (bf16) or 32 (e4m3) cells of every tile and meets the others only at the end of a part.
+// Fragments: a thread loads 16 contiguous bytes of a key row and uses them as the k indices it
+// is due (the query's fragments are permuted alike), so e4m3 codes go from shared memory to
+// registers to fp16 (exact) without a shuffle; values of two keys are interleaved by byte
+// permutes.  An item's parts in several CTAs are joined by a second kernel, one CTA per row.
+//
+// fp32 queries are carried as three bf16 terms (24 significant bits) on a bf16 cache and as two
+// fp16 terms (22 bits, scaled by the row's largest magnitude) on an e4m3 cache, and so are the
+// weights: the products of memory-bound rows cost nothing.  bf16 queries are exact in one term;
+// their weights are rounded to 16 bits as the bf16 output does not keep more.
+#include <cuda_fp8.h>
+
+#include "dense.cuh"
+#include "mma_frag.cuh"
+
+namespace qsa {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kStages = 3;
+constexpr int kD = 128;
+constexpr uint32_t kTile = 4096;                 // bytes of K (and of V) of a warp's stage
+constexpr float kMove = 8.0f;                    // move the reference past 2^8 growth
+constexpr float kHuge = 3.0e38f;
+
+template <bool E8>
+struct Shape {
+    static constexpr int kRowBytes = E8 ? kD : 2 * kD;
+    static constexpr int kKeys = (int)kTile / kRowBytes;  // a warp's cells of a tile: 16 or 32
+    static constexpr int kGroups = kKeys / 16;
+};
+
+template <bool E8, int MT, int NT>
+__host__ __device__ constexpr size_t q_bytes()
+{
+    return (size_t)MT * NT * 8 * 32 * 16;  // fragments: 8 k steps x 32 lanes x 16 bytes
+}
+template <bool E8, int MT, int NT>
+__host__ __device__ constexpr size_t decode_smem()
+{
+    return (size_t)kWarps * kStages * 2 * kTile + q_bytes<E8, MT, NT>() +
+           (E8 ? (size_t)kWarps * kStages * 32 * 8 : 0);
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool on)
+{
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(on ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma(float *c, const uint32_t *a, uint32_t b0, uint32_t b1)
+{
+    if constexpr (F16) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    } else {
+        mma_16816(c, a, b0, b1);
+    }
+}
+
+// Two values as a 16-bit pair (fp16 or bf16), and what the rounding left of each.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float &x, float &y)
+{
+    uint32_t u;
+    if constexpr (F16) {
+        const __half2 h = __floats2half2_rn(x, y);
+        const float2 f = __half22float2(h);
+        x -= f.x;
+        y -= f.y;
+        u = *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        u = pack_bf16(x, y);
+        x -= __uint_as_float(u << 16);
+        y -= __uint_as_float(u & 0xffff0000u);
+    }
+    return u;
+}
+
+// Two e4m3 codes (low byte first) as two fp16 values, exact.
+__device__ __forceinline__ uint32_t half_pair(uint32_t codes)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
+        : "=r"(r)
+        : "r"(codes));
+    return r;
+}
+__device__ __forceinline__ uint32_t half_pair_hi(uint32_t codes)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}"
+        : "=r"(r)
+        : "r"(codes));
+    return r;
+}
+
+// Offset of 16-byte chunk c of row r in a tile of K: rows of two parities in different halves
+// of the banks, for reads of two rows x four chunks.
+template <bool E8>
+__device__ __forceinline__ uint32_t k_off(int r, int c)
+{
+    return (uint32_t)r * Shape<E8>::kRowBytes + (uint32_t)((c ^ ((r & 1) << 2)) << 4);
+}
+// The same of V: bf16 rows are read by ldmatrix (eight rows of one chunk), e4m3 rows in 8-byte
+// words (rows 2c of four lanes, two chunks).
+template <bool E8>
+__device__ __forceinline__ uint32_t v_off(int r, int c)
+{
+    const int x = E8 ? (((r >> 1) & 3) << 1) : (r & 7);
+    return (uint32_t)r * Shape<E8>::kRowBytes + (uint32_t)((c ^ x) << 4);
+}
+
+struct Split {         // what the joining kernel needs of an item cut into parts
+    int32_t s, g, t;   // s < 0: none
+    int32_t parts;
+};
+
+// Value of a cell that may be infinite or NaN, as its row's sum sees it.
+template <bool E8>
+__device__ __forceinline__ float odd_value(const KvView &kv, int64_t row, int g, int e)
+{
+    if constexpr (E8) {
+        const uint8_t c = static_cast<const uint8_t *>(kv.V)[row * kv.ld_v + (int64_t)g * kD + e];
+        return (c & 0x7f) == 0x7f ? NAN : 0.0f;
+    } else {
+        const float v =
+            __bfloat162float(static_cast<const __nv_bfloat16 *>(kv.V)[row * kv.ld_v + (int64_t)g * kD + e]);
+        return isfinite(v) ? 0.0f : v;
+    }
+}
+
+// ------------------------------------------------------------------ the kernel
+// E8: e4m3 cells (else bf16).  MT: 16-row fragments of an item's rows.  TQ: type of q and out;
+// NT: 16-bit terms of a query or weight.
+template <bool E8, int MT, typename TQ, int NT>
+__global__ void __launch_bounds__(kThreads, 2)
+dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const TQ *__restrict__ q,
+                    int64_t ld_q, int H_q, float scale_log2, TQ *__restrict__ out,
+                    float *__restrict__ lse, float *__restrict__ partial, Split *__restrict__ splits)
+{
+    using S = Shape<E8>;
+    constexpr int kRows = 16 * MT;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ int bad_s, odd_s;
+    __shared__ float red_m[kWarps][kRows], red_l[kWarps][kRows], q_scale_s[kRows];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g8 = lane >> 2, c4 = lane & 3;
+    unsigned char *ring = smem + (size_t)warp * kStages * 2 * kTile;
+    uint4 *qf = reinterpret_cast<uint4 *>(smem + (size_t)kWarps * kStages * 2 * kTile);
+    // factor of the logit and exponent of the value, per cell of a stage (E8)
+    float2 *exps = reinterpret_cast<float2 *>(reinterpret_cast<unsigned char *>(qf) + q_bytes<E8, MT, NT>()) +
+                   warp * kStages * 32;
+
+    pdl_wait();
+    const TQ *qp = q;
+    KvView kw = kv;
+    SeqView sw = sv;
+    QSA_AFTER_WAIT(qp);
+    QSA_AFTER_WAIT(sw.cu);
+    QSA_AFTER_WAIT(sw.kv_len);
+    QSA_AFTER_WAIT(kw.table);
+    QSA_AFTER_WAIT(kw.K);
+    QSA_AFTER_WAIT(kw.V);
+    QSA_AFTER_WAIT(kw.K_exp);
+    QSA_AFTER_WAIT(kw.V_exp);
+    pdl_trigger();
+
+    const int64_t total = work_total(sw, ws);
+    const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+    const int64_t x0 = (int64_t)blockIdx.x * per;
+    const int64_t x1 = x0 + per < total ? x0 + per : total;
+    if (tid == 0) splits[blockIdx.x].s = -1;
+    if (x0 >= x1) return;
+    const int G = H_q / kw.H_kv;
+    WorkItem it = work_find(sw, ws, x0);
+    int64_t x = x0;
+    for (;;) {
+        const int64_t item_end = it.start + it.tiles;
+        const int tile0 = (int)(x - it.start);
+        const int tile1 = (int)((item_end < x1 ? item_end : x1) - it.start);
+        const bool starts = tile0 == 0, ends = tile1 == it.tiles;
+        int64_t t0;
+        int len;
+        seq_tokens(sw, it.s, t0, len);
+        const int cells = seq_cells(sw, it.s, len);
+        const bool fits = cells_fit(kw, cells);
+        const int n_see = fits ? item_cells(ws, len, cells, it.t) : 0;
+        const int tok0 = it.t * ws.rt;
+        const int rows = min(ws.rt, len - tok0) * G;
+        // the first token's position: cells behind it are not seen by every row
+        const int pos0 = ws.causal ? cells - len + tok0 : cells - 1;
+
+        __syncthreads();  // the previous part's shared memory is free
+        if (tid == 0) bad_s = odd_s = 0;
+        // ---- the query's fragments: lane's rows g8 and g8 + 8 of each fragment, k permuted as
+        // the key rows are read (thread c4 holds 16 contiguous bytes of each block)
+        float q_back[MT][2];  // what the rows' logits are multiplied by
+        {
+            constexpr int E = E8 ? 16 : 8;       // dims of a thread in a block
+            constexpr int kBlocks = kD / (4 * E);
+            for (int mt = warp; mt < MT; mt += kWarps) {
+                float xa[2][kBlocks * E];
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int r = mt * 16 + g8 + 8 * hf;
+                    const TQ *src =
+                        qp + (t0 + tok0 + r / G) * ld_q + (int64_t)(it.g * G + r % G) * kD + c4 * E;
+#pragma unroll
+                    for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+                        for (int e = 0; e < E; e += 8) {
+                            if (r < rows) {
+                                load8(src + b * 4 * E + e, &xa[hf][b * E + e]);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) xa[hf][b * E + e + k] = 0.0f;
+                            }
+                        }
+                    if constexpr (E8) {
+                        // fp16 holds the row once its largest magnitude is below 2^8
+                        float top = 0.0f;
+#pragma unroll
+                        for (int e = 0; e < kBlocks * E; ++e) top = fmaxf(top, fabsf(xa[hf][e]));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                        const int ex = top > 0.0f && top < kHuge ? (int)(__float_as_uint(top) >> 23) - 127 : 0;
+                        const int sh = min(max(7 - ex, -100), 100);
+                        const float mul = two_to(sh);
+#pragma unroll
+                        for (int e = 0; e < kBlocks * E; ++e) xa[hf][e] *= mul;
+                        q_scale_s[r] = two_to(-sh);
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        uint4 f;
+                        f.x = pack16<E8>(xa[0][4 * k], xa[0][4 * k + 1]);
+                        f.y = pack16<E8>(xa[1][4 * k], xa[1][4 * k + 1]);
+                        f.z = pack16<E8>(xa[0][4 * k + 2], xa[0][4 * k + 3]);
+                        f.w = pack16<E8>(xa[1][4 * k + 2], xa[1][4 * k + 3]);
+                        qf[((mt * NT + n) * 8 + k) * 32 + lane] = f;
+                    }
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+                q_back[mt][hf] = E8 ? q_scale_s[mt * 16 + g8 + 8 * hf] : 1.0f;
+        int last[MT][2];  // the last cell each row sees
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int r = mt * 16 + g8 + 8 * hf;
+                last[mt][hf] = r < rows ? (ws.causal ? pos0 + r / G : cells - 1) : -1;
+            }
+
+        float o[MT][16][4];
+        float ms[MT][2], mx[MT][2], l[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int n = 0; n < 16; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.0f;
+            ms[mt][0] = ms[mt][1] = mx[mt][0] = mx[mt][1] = -INFINITY;
+            l[mt][0] = l[mt][1] = 0.0f;
+        }
+
+        // ---- the ring: row_next is the pool row of this lane's cell of the tile to be issued
+        const int my_key = lane < S::kKeys ? lane : 0;
+        bool bad = false, odd = false;
+        auto row_of = [&](int tile) -> int64_t {
+            const int p = tile * ws.kt + warp * S::kKeys + my_key;
+            if (tile >= tile1 || p >= n_see) return -2;  // not there: zeros
+            const int64_t row = cell_row(kw, it.s, t0, p);
+            bad |= row < 0;
+            return row;
+        };
+        float2 pend = make_float2(0.0f, 0.0f);
+        auto load_exps = [&](int64_t row) {
+            float2 f = make_float2(0.0f, 0.0f);
+            if (row >= 0) {
+                const int ek = (int)kw.K_exp[row * kw.H_kv + it.g] - kExpBias;
+                const int ev = (int)kw.V_exp[row * kw.H_kv + it.g] - kExpBias;
+                f.x = two_to(min(max(ek, kExpMin), kExpMax)) * scale_log2;
+                f.y = (float)min(max(ev, kExpMin), kExpMax);
+            }
+            return f;
+        };
+        const unsigned char *Kb = static_cast<const unsigned char *>(kw.K) + (int64_t)it.g * S::kRowBytes;
+        const unsigned char *Vb = static_cast<const unsigned char *>(kw.V) + (int64_t)it.g * S::kRowBytes;
+        const int64_t ldk_b = kw.ld_k * (E8 ? 1 : 2), ldv_b = kw.ld_v * (E8 ? 1 : 2);
+        auto issue = [&](int stage, int64_t row) {
+            constexpr int kChunks = S::kRowBytes / 16, kAt = 32 / kChunks;
+            const uint32_t st = smem_u32(ring + stage * 2 * kTile);
+            const int c = lane & (kChunks - 1), r0 = lane / kChunks;
+#pragma unroll
+            for (int i = 0; i < S::kKeys / kAt; ++i) {
+                const int r = r0 + kAt * i;
+                const int64_t rr = __shfl_sync(0xffffffffu, row, r);
+                const bool on = rr >= 0;
+                const int64_t at = on ? rr : 0;
+                cp16(st + k_off<E8>(r, c), Kb + at * ldk_b + c * 16, on);
+                cp16(st + kTile + v_off<E8>(r, c), Vb + at * ldv_b + c * 16, on);
+            }
+        };
+        int64_t row_next = row_of(tile0);
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) {
+            const int64_t row = row_next;
+            row_next = row_of(tile0 + i + 1);
+            if (tile0 + i < tile1) {
+                issue(i, row);
+                if constexpr (E8) exps[i * 32 + lane] = load_exps(row);
+            }
+            cp_commit();
+        }
+        int slot = 0;
+        for (int tile = tile0; tile < tile1; ++tile) {
+            cp_wait<kStages - 2>();
+            __syncwarp();
+            const unsigned char *sk = ring + slot * 2 * kTile, *sv_ = sk + kTile;
+            const float2 *ex = exps + slot * 32;
+            const int j0 = tile * ws.kt + warp * S::kKeys;
+            // ---- issue the tile kStages - 1 ahead into the stage read in the last turn
+            {
+                const int nslot = slot == 0 ? kStages - 1 : slot - 1;
+                const int64_t row = row_next;
+                row_next = row_of(tile + kStages);
+                if (tile + kStages - 1 < tile1) {
+                    issue(nslot, row);
+                    if constexpr (E8) pend = load_exps(row);
+                }
+                cp_commit();
+            }
+            if (j0 < n_see) {
+                const bool edge = j0 + S::kKeys - 1 > pos0;  // some row may not see some cell
+                // values that not every row sees: what is infinite or NaN among them becomes
+                // zero here and is added to the rows that see it at the end
+                if (edge) {
+                    bool here = false;
+                    for (int r = max(0, pos0 + 1 - j0); r < S::kKeys && j0 + r < n_see; ++r) {
+                        unsigned char *row = const_cast<unsigned char *>(sv_);
+                        if constexpr (E8) {
+                            uint32_t *w = reinterpret_cast<uint32_t *>(
+                                row + v_off<E8>(r, lane >> 2) + (lane & 3) * 4);
+                            const uint32_t v = *w;
+                            const uint32_t m = __vcmpeq4(v & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                            here |= m != 0;
+                            if (m) *w = v & ~m;
+                        } else {
+                            uint2 *w = reinterpret_cast<uint2 *>(row + v_off<E8>(r, lane >> 1) + (lane & 1) * 8);
+                            uint2 v = *w;
+                            const uint32_t m0 = __vcmpeq2(v.x & 0x7f807f80u, 0x7f807f80u);
+                            const uint32_t m1 = __vcmpeq2(v.y & 0x7f807f80u, 0x7f807f80u);
+                            here |= (m0 | m1) != 0;
+                            if (m0 | m1) *w = make_uint2(v.x & ~m0, v.y & ~m1);
+                        }
+                    }
+                    odd |= here;
+                    __syncwarp();
+                }
+                // ---- logits: fragments of 16 rows x 8 cells
+                float s[MT][S::kGroups * 2][4];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int n = 0; n < S::kGroups * 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.0f;
+                constexpr int kBlocks = E8 ? 2 : 4, kStepsPer = 8 / kBlocks;
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b) {
+                    uint4 kr[S::kGroups * 2];
+#pragma unroll
+                    for (int n = 0; n < S::kGroups * 2; ++n)
+                        kr[n] = *reinterpret_cast<const uint4 *>(sk + k_off<E8>(8 * n + g8, 4 * b + c4));
+#pragma unroll
+                    for (int j = 0; j < kStepsPer; ++j) {
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) {
+                                const uint4 f = qf[((mt * NT + t) * 8 + b * kStepsPer + j) * 32 + lane];
+                                const uint32_t a[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                                for (int n = 0; n < S::kGroups * 2; ++n) {
+                                    const uint32_t w[4] = {kr[n].x, kr[n].y, kr[n].z, kr[n].w};
+                                    if constexpr (E8)
+                                        mma<true>(s[mt][n], a, half_pair(w[j]), half_pair_hi(w[j]));
+                                    else
+                                        mma<false>(s[mt][n], a, w[2 * j], w[2 * j + 1]);
+                                }
+                            }
+                    }
+                }
+                // ---- scaled to log2 units, masked; the references move when they have to
+                float ev[S::kGroups * 2][2];
+                bool move = false;
+#pragma unroll
+                for (int n = 0; n < S::kGroups * 2; ++n) {
+                    float f0 = scale_log2, f1 = scale_log2;
+                    ev[n][0] = ev[n][1] = 0.0f;
+                    if constexpr (E8) {
+                        const float4 f = *reinterpret_cast<const float4 *>(&ex[8 * n + 2 * c4]);
+                        f0 = f.x;
+                        ev[n][0] = f.y;
+                        f1 = f.z;
+                        ev[n][1] = f.w;
+                    }
+                    const int j = j0 + 8 * n + 2 * c4;
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            const float a = s[mt][n][2 * hf] * (f0 * q_back[mt][hf]);
+                            const float b = s[mt][n][2 * hf + 1] * (f1 * q_back[mt][hf]);
+                            s[mt][n][2 * hf] = edge && j > last[mt][hf] ? -INFINITY : a;
+                            s[mt][n][2 * hf + 1] = edge && j + 1 > last[mt][hf] ? -INFINITY : b;
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float v = s[mt][n][2 * hf + e];
+                                move |= v > ms[mt][hf] + kMove;
+                                if constexpr (E8) move |= v + ev[n][e] > mx[mt][hf] + kMove;
+                            }
+                        }
+                    }
+                }
+                if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            float a = ms[mt][hf], b = mx[mt][hf];
+#pragma unroll
+                            for (int n = 0; n < S::kGroups * 2; ++n)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    a = fmaxf(a, s[mt][n][2 * hf + e]);
+                                    if constexpr (E8) b = fmaxf(b, s[mt][n][2 * hf + e] + ev[n][e]);
+                                }
+                            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+                            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+                            const float al = a == -INFINITY ? 1.0f : ex2(ms[mt][hf] - a);
+                            ms[mt][hf] = a;
+                            l[mt][hf] *= al;
+                            float ao = al;
+                            if constexpr (E8) {
+                                b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 1));
+                                b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 2));
+                                ao = b == -INFINITY ? 1.0f : ex2(mx[mt][hf] - b);
+                                mx[mt][hf] = b;
+                            }
+#pragma unroll
+                            for (int n = 0; n < 16; ++n) {
+                                o[mt][n][2 * hf] *= ao;
+                                o[mt][n][2 * hf + 1] *= ao;
+                            }
+                        }
+                }
+                // ---- weights and their product with the values, 16 cells at a time
+#pragma unroll
+                for (int kg = 0; kg < S::kGroups; ++kg) {
+                    uint32_t a[MT][NT][4];
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        float w[2][2][2];  // [n tile][row half][cell]
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            const float us = ms[mt][hf] == -INFINITY ? 0.0f : ms[mt][hf];
+                            const float ux = mx[mt][hf] == -INFINITY ? 0.0f : mx[mt][hf];
+#pragma unroll
+                            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const float v = s[mt][2 * kg + n][2 * hf + e];
+                                    const float p = ex2(v - us);
+                                    l[mt][hf] += p;
+                                    w[n][hf][e] = E8 ? ex2(v + ev[2 * kg + n][e] - ux) : p;
+                                }
+                        }
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            a[mt][t][0] = pack16<E8>(w[0][0][0], w[0][0][1]);
+                            a[mt][t][1] = pack16<E8>(w[0][1][0], w[0][1][1]);
+                            a[mt][t][2] = pack16<E8>(w[1][0][0], w[1][0][1]);
+                            a[mt][t][3] = pack16<E8>(w[1][1][0], w[1][1][1]);
+                        }
+                    }
+                    if constexpr (E8) {
+                        // cells 2c4, 2c4 + 1 (and + 8): 8-byte words of their rows, interleaved
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            uint2 v[4];
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk) {
+                                const int r = 16 * kg + 2 * c4 + (kk & 1) + 8 * (kk >> 1);
+                                v[kk] = *reinterpret_cast<const uint2 *>(
+                                    sv_ + v_off<E8>(r, 4 * i + (g8 >> 1)) + (g8 & 1) * 8);
+                            }
+#pragma unroll
+                            for (int hw = 0; hw < 2; ++hw) {
+                                const uint32_t v0 = hw ? v[0].y : v[0].x, v1 = hw ? v[1].y : v[1].x;
+                                const uint32_t v2 = hw ? v[2].y : v[2].x, v3 = hw ? v[3].y : v[3].x;
+#pragma unroll
+                                for (int p = 0; p < 2; ++p) {
+                                    const uint32_t sel = p ? 0x7362u : 0x5140u;
+                                    const uint32_t lo = __byte_perm(v0, v1, sel);
+                                    const uint32_t hi = __byte_perm(v2, v3, sel);
+                                    const uint32_t b0 = half_pair(lo), b1 = half_pair(hi);
+                                    const uint32_t d0 = half_pair_hi(lo), d1 = half_pair_hi(hi);
+                                    const int n = 8 * i + 4 * hw + 2 * p;
+#pragma unroll
+                                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                                        for (int t = 0; t < NT; ++t) {
+                                            mma<true>(o[mt][n], a[mt][t], b0, b1);
+                                            mma<true>(o[mt][n + 1], a[mt][t], d0, d1);
+                                        }
+                                }
+                            }
+                        }
+                    } else {
+                        const int r = 16 * kg + (lane & 7) + 8 * ((lane >> 3) & 1);
+#pragma unroll
+                        for (int np = 0; np < 8; ++np) {
+                            uint32_t b[4];
+                            ldsm_x4_t(b, sv_ + v_off<E8>(r, 2 * np + (lane >> 4)));
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                                for (int t = 0; t < NT; ++t) {
+                                    mma<false>(o[mt][2 * np], a[mt][t], b[0], b[1]);
+                                    mma<false>(o[mt][2 * np + 1], a[mt][t], b[2], b[3]);
+                                }
+                        }
+                    }
+                }
+            }
+            if constexpr (E8) {
+                const int nslot = slot == 0 ? kStages - 1 : slot - 1;
+                if (tile + kStages - 1 < tile1) exps[nslot * 32 + lane] = pend;
+            }
+            __syncwarp();
+            slot = slot == kStages - 1 ? 0 : slot + 1;
+        }
+        cp_wait<0>();
+        if (__any_sync(0xffffffffu, bad) && lane == 0) bad_s = 1;
+        if (__any_sync(0xffffffffu, odd) && lane == 0) odd_s = 1;
+
+        // ---- join the four warps: o in units of the logits' reference
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                float s = l[mt][hf];
+                s += __shfl_xor_sync(0xffffffffu, s, 1);
+                s += __shfl_xor_sync(0xffffffffu, s, 2);
+                l[mt][hf] = s;
+                if (c4 == 0) {
+                    red_m[warp][mt * 16 + g8 + 8 * hf] = ms[mt][hf];
+                    red_l[warp][mt * 16 + g8 + 8 * hf] = s;
+                }
+            }
+        __syncthreads();  // every warp is done with its ring
+        constexpr int kPitch = kD + 4;
+        float *ob = reinterpret_cast<float *>(smem);  // [warp][row][kPitch]
+        static_assert((size_t)kWarps * kRows * kPitch * 4 <= (size_t)kWarps * kStages * 2 * kTile,
+                      "the warps' sums fit over the ring");
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int r = mt * 16 + g8 + 8 * hf;
+                const float m = fmaxf(fmaxf(red_m[0][r], red_m[1][r]), fmaxf(red_m[2][r], red_m[3][r]));
+                const float u = m == -INFINITY ? 0.0f : m;
+                const float f = E8 ? (mx[mt][hf] == -INFINITY ? 0.0f : exp2f(mx[mt][hf] - u))
+                                   : (ms[mt][hf] == -INFINITY ? 0.0f : exp2f(ms[mt][hf] - u));
+                float *dst = ob + (size_t)(warp * kRows + r) * kPitch;
+#pragma unroll
+                for (int n = 0; n < 16; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        // bf16: dims 8n + 2c4 + e; e4m3: dim 64 (n / 8) + 8 (2 c4 + e) + n % 8
+                        const int dim = E8 ? 64 * (n >> 3) + 8 * (2 * c4 + e) + (n & 7) : 8 * n + 2 * c4 + e;
+                        dst[dim] = o[mt][n][2 * hf + e] * f;
+                    }
+            }
+        __syncthreads();
+        const bool whole = starts && ends;
+        const bool nan_out = bad_s != 0 || !fits;
+        float *rec = partial + (2 * (int64_t)blockIdx.x + (starts ? 1 : 0)) * partial_floats(kRows, kD);
+        for (int e = tid; e < rows * (kD / 4); e += kThreads) {
+            const int r = e / (kD / 4), c = (e % (kD / 4)) * 4;
+            float m = -INFINITY, sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, red_m[w][r]);
+            const float u = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+                sum += red_m[w][r] == -INFINITY ? red_l[w][r] : red_l[w][r] * exp2f(red_m[w][r] - u);
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float4 p = *reinterpret_cast<const float4 *>(&ob[(size_t)(w * kRows + r) * kPitch + c]);
+                v[0] += p.x; v[1] += p.y; v[2] += p.z; v[3] += p.w;
+            }
+            const int tok = tok0 + r / G;
+            const int h = it.g * G + r % G;
+            if (odd_s) {
+                const int to = min(n_see - 1, ws.causal ? pos0 + r / G : cells - 1);
+                for (int j = max(pos0 + 1, tile0 * ws.kt); j <= to && j < tile1 * ws.kt; ++j) {
+                    const int64_t row = cell_row(kw, it.s, t0, j);
+                    if (row >= 0)
+                        for (int k = 0; k < 4; ++k) v[k] += odd_value<E8>(kw, row, it.g, c + k);
+                }
+            }
+            if (nan_out) sum = NAN;
+            if (whole) {
+                const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
+                TQ *dst = out + ((t0 + tok) * H_q + h) * (int64_t)kD + c;
+                if constexpr (sizeof(TQ) == 2) {
+                    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(v[0] * inv, v[1] * inv),
+                                                                 pack_bf16(v[2] * inv, v[3] * inv));
+                } else {
+                    *reinterpret_cast<float4 *>(dst) =
+                        make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+                }
+                if (c == 0 && lse)
+                    lse[(t0 + tok) * H_q + h] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
+            } else {
+                *reinterpret_cast<float4 *>(rec + 2 * kRows + (int64_t)r * kD + c) =
+                    make_float4(v[0], v[1], v[2], v[3]);
+                if (c == 0) {
+                    rec[r] = m;
+                    rec[kRows + r] = sum;
+                }
+            }
+        }
+        if (starts && !ends && tid == 0) {
+            const int64_t c1 = (item_end - 1) / per;  // the CTA of the item's last tile
+            Split sp = {it.s, it.g, it.t, (int32_t)(c1 - blockIdx.x) + 1};
+            splits[blockIdx.x] = sp;
+        }
+        x = it.start + tile1;
+        if (x >= x1) break;
+        if (!work_next(sw, ws, it)) break;
+    }
+}
+
+// ------------------------------------------------------------------ joining the parts
+// One CTA per row of an item that was cut: its parts are the second record of the CTA where the
+// item begins and the first records of the CTAs after it.  Eight warps take every eighth part.
+template <typename TQ>
+__global__ void __launch_bounds__(256)
+dense_join_kernel(const Split *__restrict__ splits, const float *__restrict__ partial, int rows_max,
+                  const SeqView sv, int rt, int G, int H_q, int d, TQ *__restrict__ out,
+                  float *__restrict__ lse)
+{
+    __shared__ float red_m[8], red_l[8];
+    __shared__ float4 red_o[8][32];
+    pdl_wait();
+    QSA_AFTER_WAIT(splits);
+    QSA_AFTER_WAIT(partial);
+    SeqView sw = sv;
+    QSA_AFTER_WAIT(sw.cu);
+    pdl_trigger();
+    const int c = blockIdx.x, r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Split sp = splits[c];
+    if (sp.s < 0) return;
+    int64_t t0;
+    int len;
+    seq_tokens(sw, sp.s, t0, len);
+    const int tok = sp.t * rt + r / G;
+    if (tok >= len || r >= rt * G) return;
+    const int64_t rec = partial_floats(rows_max, d);
+    float m = -INFINITY, l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int k = warp; k < sp.parts; k += 8) {
+        const float *p = partial + (2 * (int64_t)(c + k) + (k == 0 ? 1 : 0)) * rec;
+        const float pm = p[r], pl = p[rows_max + r];
+        const float4 po = *reinterpret_cast<const float4 *>(p + 2 * rows_max + (int64_t)r * d + 4 * lane);
+        const float mn = fmaxf(m, pm), u = mn == -INFINITY ? 0.0f : mn;
+        const float a = m == -INFINITY ? 1.0f : exp2f(m - u);   // an unset side is zero or NaN
+        const float b = pm == -INFINITY ? 1.0f : exp2f(pm - u);
+        l = l * a + pl * b;
+        o.x = o.x * a + po.x * b;
+        o.y = o.y * a + po.y * b;
+        o.z = o.z * a + po.z * b;
+        o.w = o.w * a + po.w * b;
+        m = mn;
+    }
+    if (lane == 0) {
+        red_m[warp] = m;
+        red_l[warp] = l;
+    }
+    red_o[warp][lane] = o;
+    __syncthreads();
+    if (warp != 0) return;
+    float M = -INFINITY, L = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) M = fmaxf(M, red_m[w]);
+    const float u = M == -INFINITY ? 0.0f : M;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        const float a = red_m[w] == -INFINITY ? 1.0f : exp2f(red_m[w] - u);
+        const float4 p = red_o[w][lane];
+        L += red_l[w] * a;
+        v.x += p.x * a;
+        v.y += p.y * a;
+        v.z += p.z * a;
+        v.w += p.w * a;
+    }
+    const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);
+    const int h = sp.g * G + r % G;
+    TQ *dst = out + ((t0 + tok) * H_q + h) * (int64_t)d + 4 * lane;
+    if constexpr (sizeof(TQ) == 2) {
+        *reinterpret_cast<uint2 *>(dst) =
+            make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+    } else {
+        *reinterpret_cast<float4 *>(dst) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+    }
+    if (lane == 0 && lse) lse[(t0 + tok) * H_q + h] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
+constexpr int kMaxCtas = 2 * kTargetSMs;
+
+int decode_ctas()
+{
+    const int n = 2 * device_sm_count();
+    return n < kMaxCtas ? n : kMaxCtas;
+}
+
+template <bool E8, int MT, typename TQ, int NT>
+cudaError_t run(const DenseArgs &a, void *workspace, cudaStream_t st)
+{
+    const int G = a.H_q / a.kv.H_kv;
+    WorkShape ws;
+    ws.rt = 16 * MT / G;
+    ws.kt = kWarps * Shape<E8>::kKeys;
+    ws.H_kv = a.kv.H_kv;
+    ws.causal = a.causal;
+    constexpr size_t smem = decode_smem<E8, MT, NT>();
+    cudaError_t e = ensure_kernel_attrs<dense_decode_kernel<E8, MT, TQ, NT>>(smem);
+    if (e != cudaSuccess) return e;
+    const int ctas = decode_ctas();
+    Split *splits = static_cast<Split *>(workspace);
+    float *partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + kMaxCtas * sizeof(Split));
+    e = launch(dense_decode_kernel<E8, MT, TQ, NT>, dim3((unsigned)ctas), dim3(kThreads), smem, st, 1, a.kv,
+               a.sv, ws, static_cast<const TQ *>(a.q), a.ld_q, a.H_q, a.scale * kLog2e,
+               static_cast<TQ *>(a.out), a.lse, partial, splits);
+    if (e != cudaSuccess) return e;
+    return launch(dense_join_kernel<TQ>, dim3((unsigned)ctas, (unsigned)(ws.rt * G)), dim3(256), 0, st, 1,
+                  (const Split *)splits, (const float *)partial, 16 * MT, a.sv, ws.rt, G, a.H_q, kD,
+                  static_cast<TQ *>(a.out), a.lse);
+}
+
+}  // namespace
+
+bool dense_decode_ok(const DenseArgs &a, int64_t max_q)
+{
+    const int G = a.H_q / a.kv.H_kv;
+    if (a.d != kD || (a.kv_dtype != QSA_BF16 && a.kv_dtype != QSA_E4M3)) return false;
+    if (a.kv_dtype == QSA_E4M3 && (a.kv.ld_k % 16 || a.kv.ld_v % 16)) return false;
+    // a fragment holds all heads of a KV head; fp32 queries come in several terms of one
+    if (G > (a.q_dtype == QSA_F32 ? 16 : 32)) return false;
+    return a.q_dtype == QSA_F32 || max_q * G <= 64;
+}
+
+size_t dense_decode_workspace()
+{
+    return kMaxCtas * sizeof(Split) + (size_t)2 * kMaxCtas * partial_floats(32, kD) * sizeof(float);
+}
+
+cudaError_t launch_dense_decode(const DenseArgs &a, int64_t max_q, void *workspace, cudaStream_t st)
+{
+    const int G = a.H_q / a.kv.H_kv;
+    const bool e8 = a.kv_dtype == QSA_E4M3;
+    if (a.q_dtype == QSA_F32)
+        return e8 ? run<true, 1, float, 2>(a, workspace, st) : run<false, 1, float, 3>(a, workspace, st);
+    // one fragment while it holds every new token of a sequence
+    if (G <= 16 && max_q <= 16 / G)
+        return e8 ? run<true, 1, __nv_bfloat16, 1>(a, workspace, st)
+                  : run<false, 1, __nv_bfloat16, 1>(a, workspace, st);
+    return e8 ? run<true, 2, __nv_bfloat16, 1>(a, workspace, st)
+              : run<false, 2, __nv_bfloat16, 1>(a, workspace, st);
+}
+
+}  // namespace qsa

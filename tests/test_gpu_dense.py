@@ -4,6 +4,12 @@ draft verification, against the 64-bit forms of dense_reference.
 Tolerances.  With A = sum_j softmax_j |v_j| (computed in 64 bits), an output is off by at most
   A * (2 * ds + (n + 64) * 2^-24)      fp32 sums over d dims and n cells, ds the logits' error
   + A * 2^-8 or 2^-11                  weights rounded to bf16 or fp16 (tensor-core forms)
+  + 2^-25 * max_j(softmax_j u_j) * sum_j |v_j| / u_j     fp16 weights below fp16's normal range:
+                                       on e4m3 cells a weight multiplies the code v_j / u_j,
+                                       u_j = 2^e_j, so it carries u_j; its unit is no larger than
+                                       the row's largest softmax_j u_j (the kernel's reference is
+                                       some cell's own value), and fp16's spacing there is at most
+                                       2^-24 of the unit, half of it the rounding
   + 2^-8 |out|                         the bf16 output's own rounding
 with ds = (d + 16) * 2^-24 * scale * max sum|q||k| (d products summed in fp32, a scaling and the
 exponential's few units in the last place)."""
@@ -51,7 +57,7 @@ class Pool:
         rows = n_pages * page
         K = torch.full((rows, H * d + pad_k), float("nan"), device=DEV)
         V = torch.full((rows, H * d), float("nan"), device=DEV)
-        self.k, self.v = [], []
+        self.k, self.v, self.units = [], [], []
         for i, n in enumerate(lens):
             r = self.rows(table[i], np.arange(n))
             x = rng.standard_normal((2, n, H, d)).astype(np.float32)
@@ -72,6 +78,11 @@ class Pool:
             k, v = self.values(i, np.arange(n))
             self.k.append(k)
             self.v.append(v)
+            if dtype == E4M3:
+                e = Ve[self.rows(table[i], np.arange(n))].cpu().numpy().astype(float) - 127
+                self.units.append(2.0 ** e)
+            else:
+                self.units.append(None)
         self.kv_len = i32(lens)
 
     def rows(self, table_row, pos):
@@ -91,7 +102,7 @@ class Pool:
         return out
 
 
-def tolerance(q, k, v, first, scale, causal, want, q_dtype, kv_dtype):
+def tolerance(q, k, v, first, scale, causal, want, q_dtype, kv_dtype, units=None):
     n, d = max(k.shape[0], 1), q.shape[-1]
     A = ref.attend(q, k, np.abs(v), first, scale, causal)[0]
     qk = np.abs(q).sum(-1).max() * (np.abs(k).max() if k.size else 0.0)
@@ -100,15 +111,38 @@ def tolerance(q, k, v, first, scale, causal, want, q_dtype, kv_dtype):
     rel = 2 * ds + (n + 64) * 2.0 ** -24
     if q_dtype == BF16:
         rel += 2.0 ** -11 if kv_dtype == E4M3 else 2.0 ** -8
+    if kv_dtype == E4M3 and k.shape[0]:
+        if units is None:  # rows as the cache writes them
+            top = np.abs(v).max(-1)
+            units = 2.0 ** np.clip(np.ceil(np.log2(np.maximum(top, 1e-300) / 448.0)), -100, 100)
+        A = A + 2.0 ** -25 / rel * small_weights(q, k, v, units, first, scale, causal)
     tol = A * rel + (2.0 ** -8 * np.abs(want) if q_dtype == BF16 else 0.0) + 1e-30
     return tol, ds + (n + 64) * 2.0 ** -24
 
 
-def check_attention(got, lse, q, k, v, first, scale, causal, q_dtype, kv_dtype):
+def small_weights(q, k, v, units, first, scale, causal):
+    """max_j(softmax_j u_j) * sum_j |v_j| / u_j over the cells each row sees."""
+    m, H_q, d = q.shape
+    n, H_kv = k.shape[:2]
+    out = np.zeros((m, H_q, d))
+    for h in range(H_q):
+        g = h * H_kv // H_q
+        s = scale * (q[:, h] @ k[:, g].T)
+        if causal:
+            s = np.where(np.arange(n)[None] > first + np.arange(m)[:, None], -np.inf, s)
+        top = s.max(-1, keepdims=True)
+        p = np.exp(s - np.where(np.isfinite(top), top, 0.0))
+        p = p / np.maximum(p.sum(-1, keepdims=True), 1e-300)
+        codes = (p > 0).astype(float) @ (np.abs(v[:, g]) / units[:, g, None])
+        out[:, h] = (p * units[None, :, g]).max(-1, keepdims=True) * codes
+    return out
+
+
+def check_attention(got, lse, q, k, v, first, scale, causal, q_dtype, kv_dtype, units=None):
     if q.shape[0] == 0:
         return
     want, wl = ref.attend(q, k, v, first, scale, causal)
-    tol, tl = tolerance(q, k, v, first, scale, causal, want, q_dtype, kv_dtype)
+    tol, tl = tolerance(q, k, v, first, scale, causal, want, q_dtype, kv_dtype, units)
     err = np.abs(got - want)
     assert np.isfinite(got).all()
     assert (err <= tol).all(), f"out off by {err.max():.3g}, {(err / tol).max():.3g} of the bound"
@@ -143,7 +177,7 @@ def run_paged(pool, news, H_q, q_dtype, seed, causal=True, pad=3, max_q=None, sc
         a, b = cu[s], cu[s + 1]
         check_attention(o[a:b], l[a:b], qn[a:b], pool.k[s], pool.v[s], pool.lens[s] - m, scale,
                         causal, q_dtype, {v: k for k, v in {BF16: 1, F32: 0, E4M3: 2}.items()}.get(
-                            pool.cache._struct.dtype))
+                            pool.cache._struct.dtype), pool.units[s])
     assert (o[cu[-1]:] == -7).all() and (l[cu[-1]:] == -7).all()
     return out, lse
 
@@ -349,7 +383,7 @@ def test_cells_not_seen_do_not_matter(bad, kv_dtype):
         a, first = cu[s], lens[s] - news[s]
         clean = hit[s] - first  # tokens before it do not see the cell
         check_attention(o[a:a + clean], l[a:a + clean], qn[a:a + clean], pool.k[s][:hit[s]], pool.v[s][:hit[s]],
-                        first, 0.1, True, BF16, kv_dtype)
+                        first, 0.1, True, BF16, kv_dtype, None if kv_dtype == BF16 else pool.units[s][:hit[s]])
         assert np.isnan(o[a + clean:cu[s + 1]]).all()
 
 
