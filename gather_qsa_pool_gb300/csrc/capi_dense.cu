@@ -81,6 +81,11 @@ qsa_status run_attn(const DenseArgs &a, int64_t max_q, void *workspace, size_t w
             return QSA_ERR_INVALID_ARG;
         return from_cuda(launch_dense_decode(a, max_q, workspace, st));
     }
+    if (dense_tc_ok(a)) {
+        if (!workspace || !aligned(workspace, 256) || workspace_bytes < dense_tc_workspace())
+            return QSA_ERR_INVALID_ARG;
+        return launch_dense_tc(a, workspace, st);
+    }
     return from_cuda(launch_dense_attn(a, st));
 }
 
@@ -88,7 +93,8 @@ qsa_status run_attn(const DenseArgs &a, int64_t max_q, void *workspace, size_t w
 size_t attn_workspace(int64_t n_tok, int64_t n_seq, int H_q, int H_kv, int d)
 {
     if (n_tok <= 0 || n_seq <= 0 || H_q < 1 || H_kv < 1 || d < 1) return 0;
-    return dense_decode_workspace();
+    const size_t x = dense_decode_workspace(), y = dense_tc_workspace();
+    return x > y ? x : y;
 }
 
 }  // namespace

@@ -128,14 +128,45 @@ __device__ __forceinline__ int item_tiles(const WorkShape &w, int len, int cells
     return n > 0 ? (n + w.kt - 1) / w.kt : 1;
 }
 
+__device__ __forceinline__ int64_t floor_div(int64_t a, int64_t b)
+{
+    return a >= 0 ? a / b : -((-a + b - 1) / b);
+}
+
+// Tiles of the row tiles before t (t <= the last row tile) of one KV head of a sequence.  A row
+// tile i < t sees c = cells - len + (i + 1) rt cells: one tile if that is none, else
+// floor((c - 1) / kt) + 1; the sum has a closed form when one of rt and kt divides the other
+// (1, 2, 4 ... heads per KV head) and is a loop otherwise.
+__device__ __forceinline__ int64_t tiles_before(const WorkShape &w, int len, int cells, int t)
+{
+    if (!w.causal || w.kt == 0) return (int64_t)t * item_tiles(w, len, cells, 0);
+    const int64_t base = (int64_t)cells - len;
+    int64_t i0 = base < 0 ? -base / w.rt : 0;  // row tiles that see nothing
+    if (i0 > t) i0 = t;
+    const int64_t B = base + w.rt - 1;
+    int64_t sum = t;
+    if (w.rt % w.kt == 0) {
+        const int64_t n = t - i0;
+        sum += n * floor_div(B, w.kt) + (w.rt / w.kt) * (n * (i0 + t - 1) / 2);
+    } else if (w.kt % w.rt == 0) {
+        const int64_t r = w.kt / w.rt, v0 = floor_div(B, w.rt);
+        // F(n) = sum of floor(v / r) over 0 <= v < n
+        const int64_t n1 = v0 + t, n0 = v0 + i0, q1 = n1 / r, q0 = n0 / r;
+        if (t > i0)
+            sum += (r * (q1 * (q1 - 1) / 2) + q1 * (n1 - q1 * r)) -
+                   (r * (q0 * (q0 - 1) / 2) + q0 * (n0 - q0 * r));
+    } else {
+        sum = 0;
+        for (int i = 0; i < t; ++i) sum += item_tiles(w, len, cells, i);
+    }
+    return sum;
+}
+
 // Tiles of one KV head of a sequence.
 __device__ __forceinline__ int64_t seq_tiles(const WorkShape &w, int len, int cells)
 {
     const int nt = (len + w.rt - 1) / w.rt;
-    if (!w.causal || w.kt == 0) return (int64_t)nt * item_tiles(w, len, cells, 0);
-    int64_t sum = 0;
-    for (int t = 0; t < nt; ++t) sum += item_tiles(w, len, cells, t);
-    return sum;
+    return nt == 0 ? 0 : tiles_before(w, len, cells, nt - 1) + item_tiles(w, len, cells, nt - 1);
 }
 
 struct WorkItem {
@@ -193,20 +224,16 @@ __device__ __forceinline__ WorkItem work_find(const SeqView &sv, const WorkShape
             const int64_t per_head = stot / w.H_kv;
             it.s = s0 + j;
             it.g = (int32_t)((x - sbase) / per_head);
-            int64_t at = sbase + it.g * per_head;
-            const int nt = (len + w.rt - 1) / w.rt;
-            int t = 0;
-            if (w.kt == 0) {
-                t = (int)(x - at);
-                at = x;
-            }
-            for (; w.kt != 0 && t < nt - 1; ++t) {
-                const int n = item_tiles(w, len, cells, t);
-                if (x < at + n) break;
-                at += n;
+            const int64_t at = sbase + it.g * per_head;
+            // the last row tile that does not begin behind x
+            int t = 0, hi = (len + w.rt - 1) / w.rt;
+            while (hi - t > 1) {
+                const int mid = (t + hi) >> 1;
+                if (tiles_before(w, len, cells, mid) <= x - at) t = mid;
+                else hi = mid;
             }
             it.t = t;
-            it.start = at;
+            it.start = at + tiles_before(w, len, cells, t);
             it.tiles = item_tiles(w, len, cells, t);
             return it;
         }
@@ -267,5 +294,10 @@ cudaError_t launch_dense_attn(const DenseArgs &a, cudaStream_t st);
 bool dense_decode_ok(const DenseArgs &a, int64_t max_q);
 size_t dense_decode_workspace();
 cudaError_t launch_dense_decode(const DenseArgs &a, int64_t max_q, void *workspace, cudaStream_t st);
+
+// Many query rows on the tensor cores: bf16 queries, d 128.
+bool dense_tc_ok(const DenseArgs &a);
+size_t dense_tc_workspace();
+qsa_status launch_dense_tc(const DenseArgs &a, void *workspace, cudaStream_t st);
 
 }  // namespace qsa

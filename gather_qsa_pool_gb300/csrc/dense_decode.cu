@@ -19,7 +19,7 @@
 // Fragments: a thread loads 16 contiguous bytes of a key row and uses them as the k indices it
 // is due (the query's fragments are permuted alike), so e4m3 codes go from shared memory to
 // registers to fp16 (exact) without a shuffle; values of two keys are interleaved by byte
-// permutes.  An item's parts in several CTAs are joined by a second kernel, one CTA per row.
+// permutes.  An item's parts in several CTAs are joined by a second kernel (dense_join.cuh).
 //
 // fp32 queries are carried as three bf16 terms (24 significant bits) on a bf16 cache and as two
 // fp16 terms (22 bits, scaled by the row's largest magnitude) on an e4m3 cache, and so are the
@@ -27,7 +27,7 @@
 // their weights are rounded to 16 bits as the bf16 output does not keep more.
 #include <cuda_fp8.h>
 
-#include "dense.cuh"
+#include "dense_join.cuh"
 #include "mma_frag.cuh"
 
 namespace qsa {
@@ -146,11 +146,6 @@ __device__ __forceinline__ uint32_t v_off(int r, int c)
     const int x = E8 ? (((r >> 1) & 3) << 1) : (r & 7);
     return (uint32_t)r * Shape<E8>::kRowBytes + (uint32_t)((c ^ x) << 4);
 }
-
-struct Split {         // what the joining kernel needs of an item cut into parts
-    int32_t s, g, t;   // s < 0: none
-    int32_t parts;
-};
 
 // Value of a cell that may be infinite or NaN, as its row's sum sees it.
 template <bool E8>
@@ -691,83 +686,6 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
     }
 }
 
-// ------------------------------------------------------------------ joining the parts
-// One CTA per row of an item that was cut: its parts are the second record of the CTA where the
-// item begins and the first records of the CTAs after it.  Eight warps take every eighth part.
-template <typename TQ>
-__global__ void __launch_bounds__(256)
-dense_join_kernel(const Split *__restrict__ splits, const float *__restrict__ partial, int rows_max,
-                  const SeqView sv, int rt, int G, int H_q, int d, TQ *__restrict__ out,
-                  float *__restrict__ lse)
-{
-    __shared__ float red_m[8], red_l[8];
-    __shared__ float4 red_o[8][32];
-    pdl_wait();
-    QSA_AFTER_WAIT(splits);
-    QSA_AFTER_WAIT(partial);
-    SeqView sw = sv;
-    QSA_AFTER_WAIT(sw.cu);
-    pdl_trigger();
-    const int c = blockIdx.x, r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Split sp = splits[c];
-    if (sp.s < 0) return;
-    int64_t t0;
-    int len;
-    seq_tokens(sw, sp.s, t0, len);
-    const int tok = sp.t * rt + r / G;
-    if (tok >= len || r >= rt * G) return;
-    const int64_t rec = partial_floats(rows_max, d);
-    float m = -INFINITY, l = 0.0f;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int k = warp; k < sp.parts; k += 8) {
-        const float *p = partial + (2 * (int64_t)(c + k) + (k == 0 ? 1 : 0)) * rec;
-        const float pm = p[r], pl = p[rows_max + r];
-        const float4 po = *reinterpret_cast<const float4 *>(p + 2 * rows_max + (int64_t)r * d + 4 * lane);
-        const float mn = fmaxf(m, pm), u = mn == -INFINITY ? 0.0f : mn;
-        const float a = m == -INFINITY ? 1.0f : exp2f(m - u);   // an unset side is zero or NaN
-        const float b = pm == -INFINITY ? 1.0f : exp2f(pm - u);
-        l = l * a + pl * b;
-        o.x = o.x * a + po.x * b;
-        o.y = o.y * a + po.y * b;
-        o.z = o.z * a + po.z * b;
-        o.w = o.w * a + po.w * b;
-        m = mn;
-    }
-    if (lane == 0) {
-        red_m[warp] = m;
-        red_l[warp] = l;
-    }
-    red_o[warp][lane] = o;
-    __syncthreads();
-    if (warp != 0) return;
-    float M = -INFINITY, L = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) M = fmaxf(M, red_m[w]);
-    const float u = M == -INFINITY ? 0.0f : M;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-    for (int w = 0; w < 8; ++w) {
-        const float a = red_m[w] == -INFINITY ? 1.0f : exp2f(red_m[w] - u);
-        const float4 p = red_o[w][lane];
-        L += red_l[w] * a;
-        v.x += p.x * a;
-        v.y += p.y * a;
-        v.z += p.z * a;
-        v.w += p.w * a;
-    }
-    const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);
-    const int h = sp.g * G + r % G;
-    TQ *dst = out + ((t0 + tok) * H_q + h) * (int64_t)d + 4 * lane;
-    if constexpr (sizeof(TQ) == 2) {
-        *reinterpret_cast<uint2 *>(dst) =
-            make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
-    } else {
-        *reinterpret_cast<float4 *>(dst) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-    }
-    if (lane == 0 && lse) lse[(t0 + tok) * H_q + h] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
-}
-
 constexpr int kMaxCtas = 2 * kTargetSMs;
 
 int decode_ctas()
@@ -795,9 +713,7 @@ cudaError_t run(const DenseArgs &a, void *workspace, cudaStream_t st)
                a.sv, ws, static_cast<const TQ *>(a.q), a.ld_q, a.H_q, a.scale * kLog2e,
                static_cast<TQ *>(a.out), a.lse, partial, splits);
     if (e != cudaSuccess) return e;
-    return launch(dense_join_kernel<TQ>, dim3((unsigned)ctas, (unsigned)(ws.rt * G)), dim3(256), 0, st, 1,
-                  (const Split *)splits, (const float *)partial, 16 * MT, a.sv, ws.rt, G, a.H_q, kD,
-                  static_cast<TQ *>(a.out), a.lse);
+    return launch_dense_join<TQ, 8>(splits, partial, ctas, 16 * MT, ws.rt, a, st);
 }
 
 }  // namespace
