@@ -42,6 +42,10 @@ __device__ __forceinline__ void load8(const __nv_bfloat16 *p, float *x)
     }
 }
 
+// The views below hold plain pointers (not __restrict__): a load through one is an ordinary load,
+// which the compiler does not move before a kernel's wait for its predecessor, so the kernels
+// read the views where they lie, in the parameters.
+
 // Keys and values as the attention kernels see them.  table != NULL: a paged pool, the cell at
 // position p of sequence s lives in row table[s][p >> page_shift] << page_shift | (p & mask).
 // table == NULL: packed sequences, the cell is row cu[s] + p.
@@ -108,6 +112,8 @@ __device__ __forceinline__ int64_t cell_row(const KvView &kv, int s, int64_t fir
 struct WorkShape {
     int32_t rt;      // query tokens per row tile
     int32_t kt;      // cells per tile; 0: every item is one tile (work that is not cut)
+    int32_t over;    // what an item costs besides its tiles, in tiles: the list has that many
+                     // places without a tile before each item's first
     int32_t H_kv;
     int32_t causal;
 };
@@ -162,20 +168,22 @@ __device__ __forceinline__ int64_t tiles_before(const WorkShape &w, int len, int
     return sum;
 }
 
-// Tiles of one KV head of a sequence.
-__device__ __forceinline__ int64_t seq_tiles(const WorkShape &w, int len, int cells)
+// Places of one KV head of a sequence.
+__device__ __forceinline__ int64_t seq_places(const WorkShape &w, int len, int cells)
 {
     const int nt = (len + w.rt - 1) / w.rt;
-    return nt == 0 ? 0 : tiles_before(w, len, cells, nt - 1) + item_tiles(w, len, cells, nt - 1);
+    return nt == 0 ? 0
+                   : tiles_before(w, len, cells, nt - 1) + item_tiles(w, len, cells, nt - 1) +
+                         (int64_t)nt * w.over;
 }
 
 struct WorkItem {
     int32_t s, g, t;        // sequence, KV head, row tile
-    int64_t start;          // its first tile in the list
+    int64_t start;          // its first place in the list; its tiles begin `over` places on
     int32_t tiles;
 };
 
-// Total tiles of the list; all 32 lanes call it and get the same value.
+// Total places of the list; all 32 lanes call it and get the same value.
 __device__ __forceinline__ int64_t work_total(const SeqView &sv, const WorkShape &w)
 {
     const int lane = threadIdx.x & 31;
@@ -184,14 +192,14 @@ __device__ __forceinline__ int64_t work_total(const SeqView &sv, const WorkShape
         int64_t t0;
         int len;
         seq_tokens(sv, s, t0, len);
-        sum += seq_tiles(w, len, seq_cells(sv, s, len));
+        sum += seq_places(w, len, seq_cells(sv, s, len));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     return sum * w.H_kv;
 }
 
-// The item that holds tile x of the list (0 <= x < work_total); all 32 lanes call it.
+// The item that holds place x of the list (0 <= x < work_total); all 32 lanes call it.
 __device__ __forceinline__ WorkItem work_find(const SeqView &sv, const WorkShape &w, int64_t x)
 {
     const int lane = threadIdx.x & 31;
@@ -205,7 +213,7 @@ __device__ __forceinline__ WorkItem work_find(const SeqView &sv, const WorkShape
             int64_t t0;
             seq_tokens(sv, s, t0, len);
             cells = seq_cells(sv, s, len);
-            mine = seq_tiles(w, len, cells) * w.H_kv;
+            mine = seq_places(w, len, cells) * w.H_kv;
         }
         int64_t incl = mine;
 #pragma unroll
@@ -229,11 +237,11 @@ __device__ __forceinline__ WorkItem work_find(const SeqView &sv, const WorkShape
             int t = 0, hi = (len + w.rt - 1) / w.rt;
             while (hi - t > 1) {
                 const int mid = (t + hi) >> 1;
-                if (tiles_before(w, len, cells, mid) <= x - at) t = mid;
+                if (tiles_before(w, len, cells, mid) + (int64_t)mid * w.over <= x - at) t = mid;
                 else hi = mid;
             }
             it.t = t;
-            it.start = at + tiles_before(w, len, cells, t);
+            it.start = at + tiles_before(w, len, cells, t) + (int64_t)t * w.over;
             it.tiles = item_tiles(w, len, cells, t);
             return it;
         }
@@ -251,7 +259,7 @@ __device__ __forceinline__ bool work_next(const SeqView &sv, const WorkShape &w,
     seq_tokens(sv, it.s, t0, len);
     int cells = seq_cells(sv, it.s, len);
     const int nt = (len + w.rt - 1) / w.rt;
-    it.start += it.tiles;
+    it.start += it.tiles + w.over;
     if (++it.t >= nt) {
         it.t = 0;
         if (++it.g >= w.H_kv) {

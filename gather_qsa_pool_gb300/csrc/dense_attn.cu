@@ -57,13 +57,6 @@ dense_attn_kernel(KvView kv, SeqView sv, WorkShape ws, const TQ *__restrict__ q,
     __shared__ int bad_s;
     pdl_wait();
     QSA_AFTER_WAIT(q);
-    QSA_AFTER_WAIT(sv.cu);
-    QSA_AFTER_WAIT(sv.kv_len);
-    QSA_AFTER_WAIT(kv.table);
-    QSA_AFTER_WAIT(kv.K);
-    QSA_AFTER_WAIT(kv.V);
-    QSA_AFTER_WAIT(kv.K_exp);
-    QSA_AFTER_WAIT(kv.V_exp);
     pdl_trigger();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = H_q / kv.H_kv;
@@ -205,6 +198,7 @@ cudaError_t run(const DenseArgs &a, cudaStream_t st)
     ws.kt = 0;
     ws.H_kv = a.kv.H_kv;
     ws.causal = a.causal;
+    ws.over = 0;
     const size_t smem = dense_smem(a.d);
     cudaError_t e = ensure_kernel_attrs<dense_attn_kernel<TQ, TK>>(smem);
     if (e != cudaSuccess) return e;

@@ -8,10 +8,12 @@
 // Shape: one persistent CTA per SM takes an equal share of the flattened list of (sequence, KV
 // head, row tile) items in tiles of 128 cells (dense.cuh).  A row tile is two groups of 128 rows
 // (query tokens x heads of one KV head, so the heads of a group read each K and V tile once).
-// Warps 0-3 and 4-7 are the two groups' softmax, one thread per row; warp 8 issues the MMAs;
-// warp 9 stages K and V tiles by TMA (one box per page, 128-byte swizzle) into a ring of
-// 32 KB stages; warps 12-15 see to the tiles where some row does not see some cell, and turn e4m3
-// cells into bf16.
+// Warps 0-15 are the softmax: eight per group, each row shared by two threads that take 64 cells
+// each (four warps per scheduler: with one thread per row, 128 logits in registers and half the
+// warps, the chain logits -> maximum -> exponentials -> weights left the tensor cores idle for
+// half the time).  Warp 16 issues the MMAs; warp 17 stages queries, K and V tiles by TMA (one box
+// per page, 128-byte swizzle), K and V into a ring of 32 KB stages; warps 18 and 19 see to the
+// tiles where some row does not see some cell.
 //   tensor memory (512 columns): S of group A, S of group B (128 fp32 columns each; a row's
 //   weights P overwrite its own S as bf16, 64 columns), O of A and of B (128 each).
 // Per tile the tensor cores run O_A += P_A V, S_A = Q_A K', O_B += P_B V, S_B = Q_B K' (K' the
@@ -34,7 +36,9 @@ namespace {
 constexpr int kD = 128;
 constexpr int kM = 128;                  // rows of a group
 constexpr int kN = 128;                  // cells of a tile
-constexpr int kThreads = 512;
+constexpr int kSoftWarps = 16, kMmaWarp = 16, kLoadWarp = 17, kAuxWarp = 18, kAuxWarps = 2;
+constexpr int kThreads = 32 * (kAuxWarp + kAuxWarps);
+constexpr int kOver = 4;                 // an item's fixed cost in tiles
 constexpr uint32_t kHalf = 128 * 128;    // 16 KB: 128 rows x 64 dims of bf16
 constexpr uint32_t kTileB = 2 * kHalf;   // 32 KB: a K or V tile, or a group's queries
 constexpr uint32_t kTmemCols = 512;
@@ -48,9 +52,10 @@ constexpr int kStages = 5;
 
 struct Bars {
     uint64_t full[kStages], empty[kStages], raw[kStages];
-    uint64_t s_full[2], p_full[2], q_ready[2], drain;
+    uint64_t s_full[2], p_full[2], o_full[2], q_full[2], q_free[2], drain;
     uint32_t tmem, pad;
     int32_t odd[kSlots], bad[kSlots];  // number + 1 of the part that set it
+    float row[2][kM];                  // exchanged by the two threads of a row
 };
 
 __host__ __device__ constexpr size_t tc_smem()
@@ -61,6 +66,33 @@ __host__ __device__ constexpr size_t tc_smem()
 __device__ __forceinline__ void mbar_arrive_n(uint64_t *bar, uint32_t n)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
+
+__device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
+                                         uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// Barrier of the two warps that share 32 rows; `id` from 1.
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+// The same, with the OR of `v` over the 64 threads.
+__device__ __forceinline__ bool pair_or(int id, bool v)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, c;\n\t"
+        "setp.ne.u32 c, %1, 0;\n\t"
+        "bar.red.or.pred p, %2, 64, c;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(id)
+        : "memory");
+    return r != 0;
 }
 
 // One box of a 2D tensor map: 64 bf16 columns from x, the map's box rows from y.
@@ -93,7 +125,7 @@ __device__ __forceinline__ void tmem_wait_ld(float *v)
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < 128; ++i) asm volatile("" : "+f"(v[i]));
+    for (int i = 0; i < 64; ++i) asm volatile("" : "+f"(v[i]));
 }
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
@@ -127,9 +159,9 @@ struct Parts {
 
     __device__ __forceinline__ void set(const KvView &kv, const SeqView &sv, const WorkShape &w)
     {
-        tile0 = (int)(x - it.start);
-        const int64_t end = it.start + it.tiles;
-        tile1 = (int)((end < x1 ? end : x1) - it.start);
+        const int64_t first = it.start + w.over;
+        tile0 = x > first ? (int)(x - first) : 0;
+        tile1 = x1 > first ? (int)min((int64_t)it.tiles, x1 - first) : 0;
         seq_tokens(sv, it.s, t0, len);
         cells = seq_cells(sv, it.s, len);
         fits = cells_fit(kv, cells);
@@ -138,12 +170,15 @@ struct Parts {
         toks = min(w.rt, len - tok0);
         pos0 = w.causal ? cells - len + tok0 : cells - 1;
     }
+    // The next part that has tiles.
     __device__ __forceinline__ bool next(const KvView &kv, const SeqView &sv, const WorkShape &w)
     {
-        x = it.start + tile1;
         ++n;
-        if (x >= x1 || !work_next(sv, w, it)) return false;
-        set(kv, sv, w);
+        do {
+            x = it.start + w.over + it.tiles;
+            if (x >= x1 || !work_next(sv, w, it)) return false;
+            set(kv, sv, w);
+        } while (tile1 <= tile0);
         return true;
     }
     // cells behind pos0 (and behind n_see) are not seen by every row
@@ -151,11 +186,10 @@ struct Parts {
 };
 
 __global__ void __launch_bounds__(kThreads, 1)
-dense_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
-                const KvView kv_, const SeqView sv_, const WorkShape ws, int box_rows,
-                const __nv_bfloat16 *__restrict__ q_, int64_t ld_q, int H_q, float scale_log2,
-                uint32_t q_and, uint32_t q_xor, __nv_bfloat16 *__restrict__ out,
-                float *__restrict__ lse, float *__restrict__ partial, Split *__restrict__ splits,
+dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
+                const __grid_constant__ CUtensorMap mapV, const KvView kv, const SeqView sv,
+                const WorkShape ws, int box_rows, int H_q, float scale_log2,
+                __nv_bfloat16 *__restrict__ out, float *__restrict__ lse, float *__restrict__ partial, Split *__restrict__ splits,
                 const WaitCtl wc)
 {
     extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -165,31 +199,24 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
     Bars &bars = *reinterpret_cast<Bars *>(ring + (size_t)kStages * kTileB);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    KvView kv = kv_;
-    SeqView sv = sv_;
-    const __nv_bfloat16 *q = q_;
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&bars.full[s], 4);
+            mbar_init(&bars.full[s], kAuxWarps);
             mbar_init(&bars.empty[s], 1);
             mbar_init(&bars.raw[s], 1);
         }
         for (int g = 0; g < 2; ++g) {
             mbar_init(&bars.s_full[g], 1);
-            mbar_init(&bars.p_full[g], 4);
-            mbar_init(&bars.q_ready[g], 4);
+            mbar_init(&bars.p_full[g], kSoftWarps / 2);
+            mbar_init(&bars.o_full[g], 1);
+            mbar_init(&bars.q_full[g], 1);
+            mbar_init(&bars.q_free[g], 1);
         }
         mbar_init(&bars.drain, 1);
         for (int i = 0; i < kSlots; ++i) bars.odd[i] = bars.bad[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     pdl_wait();
-    QSA_AFTER_WAIT(q);
-    QSA_AFTER_WAIT(sv.cu);
-    QSA_AFTER_WAIT(sv.kv_len);
-    QSA_AFTER_WAIT(kv.table);
-    QSA_AFTER_WAIT(kv.K);
-    QSA_AFTER_WAIT(kv.V);
     pdl_trigger();
 
     Parts p;
@@ -202,8 +229,12 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
     if (p.x >= p.x1) return;
     p.it = work_find(sv, ws, p.x);
     p.set(kv, sv, ws);
+    if (p.tile1 <= p.tile0) {  // only places without a tile
+        --p.n;
+        if (!p.next(kv, sv, ws)) return;
+    }
 
-    if (warp == 8) {
+    if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&bars.tmem)),
                      "r"(kTmemCols)
@@ -217,13 +248,11 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
     const int G = H_q / kv.H_kv;
     const int rt2 = ws.rt / 2;  // tokens of a group
     bool ok = true;
-    // registers: 512 threads x 128 at launch = 256 x 192 + 256 x 64; the softmax holds a row of
-    // 128 logits
-    if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp == 8) {
-        // ---- MMA issue (lane 0)
-        if (lane == 0) {
+    // registers: 640 threads x 96 at launch = 512 x 104 + 128 x 64
+    if (warp >= kSoftWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (warp == kMmaWarp && lane == 0) {
+            // ---- MMA issue
             constexpr uint32_t id_s = idesc_m128(kN, false), id_o = idesc_m128(kD, true);
             const uint64_t dk0 = desc_kmajor_sw128(smem_u32(ring));
             const uint64_t dv0 = desc_mnmajor_sw128(smem_u32(ring), kHalf);
@@ -246,28 +275,30 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                                  (!first || k) ? 1u : 0u);
             };
             uint32_t n = 0, np[2] = {0, 0}, nq[2] = {0, 0};  // stages, weights, queries so far
+            auto stage_ready = [&](uint32_t i) {
+                return mbar_wait(&bars.full[i % kStages], (i / kStages) & 1u, wc.limit_ns);
+            };
             do {
                 const int tiles = p.tile1 - p.tile0;
                 const bool two = p.toks > rt2;  // group B has rows
-                auto stage_ready = [&](uint32_t i) {
-                    return mbar_wait(&bars.full[i % kStages], (i / kStages) & 1u, wc.limit_ns);
-                };
-                ok = stage_ready(n) && mbar_wait(&bars.q_ready[0], nq[0]++ & 1u, wc.limit_ns);
+                ok = stage_ready(n) && mbar_wait(&bars.q_full[0], nq[0]++ & 1u, wc.limit_ns);
                 if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 mma_s(0, (int)(n % kStages));
                 umma_commit(&bars.s_full[0]);
+                if (tiles == 1) umma_commit(&bars.q_free[0]);
                 if (two) {
-                    ok = mbar_wait(&bars.q_ready[1], nq[1]++ & 1u, wc.limit_ns);
+                    ok = mbar_wait(&bars.q_full[1], nq[1]++ & 1u, wc.limit_ns);
                     if (!ok) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     mma_s(1, (int)(n % kStages));
                     umma_commit(&bars.s_full[1]);
+                    if (tiles == 1) umma_commit(&bars.q_free[1]);
                 }
                 umma_commit(&bars.empty[n % kStages]);
                 for (int t = 0; t < tiles; ++t) {
                     const uint32_t iv = n + 2 * (uint32_t)t + 1, ik = iv + 1;
-                    const bool more = t + 1 < tiles;
+                    const bool more = t + 1 < tiles, last_s = t + 2 == tiles;
                     ok = stage_ready(iv) && mbar_wait(&bars.p_full[0], np[0]++ & 1u, wc.limit_ns);
                     if (!ok) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -277,8 +308,11 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                         if (!ok) break;
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                         mma_s(0, (int)(ik % kStages));
+                        umma_commit(&bars.s_full[0]);
+                        if (last_s) umma_commit(&bars.q_free[0]);
+                    } else {
+                        umma_commit(&bars.o_full[0]);
                     }
-                    umma_commit(&bars.s_full[0]);
                     if (two) {
                         ok = mbar_wait(&bars.p_full[1], np[1]++ & 1u, wc.limit_ns);
                         if (!ok) break;
@@ -286,230 +320,260 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                         mma_o(1, (int)(iv % kStages), t == 0);
                     }
                     umma_commit(&bars.empty[iv % kStages]);
-                    if (more) {
-                        if (two) mma_s(1, (int)(ik % kStages));
-                        umma_commit(&bars.empty[ik % kStages]);
+                    if (two && more) {
+                        mma_s(1, (int)(ik % kStages));
+                        umma_commit(&bars.s_full[1]);
+                        if (last_s) umma_commit(&bars.q_free[1]);
+                    } else if (two) {
+                        umma_commit(&bars.o_full[1]);
                     }
-                    if (two) umma_commit(&bars.s_full[1]);
+                    if (more) umma_commit(&bars.empty[ik % kStages]);
                 }
                 n += 2 * (uint32_t)tiles;
             } while (ok && p.next(kv, sv, ws));
             // every MMA issued has completed before the tensor memory is freed
             umma_commit(&bars.drain);
             if (!mbar_wait(&bars.drain, 0)) ok = false;
-        }
-        __syncwarp();
-    } else if (warp == 9) {
-        // ---- K and V tiles: box b of a tile is box_rows cells, by lane b
-        const int boxes = kN / box_rows;
-        uint32_t n = 0;
-        uint32_t edge_last = 0, raw_phase = 0, used = 0;  // bits by stage
-        do {
-            for (int t = p.tile0; ok && t < p.tile1; ++t) {
-                const int j = t * kN + lane * box_rows;
-                int64_t row = -2;
-                if (lane < boxes && j < p.n_see) row = cell_row(kv, p.it.s, p.t0, j);
-                const uint32_t go = __ballot_sync(0xffffffffu, row >= 0);
-                if (__any_sync(0xffffffffu, row == -1) && lane == 0)
-                    *reinterpret_cast<volatile int32_t *>(&bars.bad[p.n % kSlots]) = p.n + 1;
-                for (int half = 0; half < 2; ++half, ++n) {  // K, then V
-                    const int s = (int)(n % kStages);
-                    if (n >= kStages &&
-                        !warp_wait(&bars.empty[s], ((n / kStages) - 1) & 1u, wc.limit_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    const bool edge = half == 1 && p.edge(t);
-                    uint64_t *bar = edge ? &bars.raw[s] : &bars.full[s];
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(bar, (uint32_t)__popc(go) * (uint32_t)box_rows * 256u);
-                        if (!edge) mbar_arrive_n(bar, 3);
-                    }
-                    used |= 1u << s;
-                    edge_last = edge ? edge_last | (1u << s) : edge_last & ~(1u << s);
-                    if (edge) raw_phase ^= 1u << s;
-                    __syncwarp();
-                    if (row >= 0) {
-                        const uint32_t dst =
-                            smem_u32(ring) + (uint32_t)s * kTileB + (uint32_t)(lane * box_rows) * 128;
-                        const CUtensorMap *map = half ? &mapV : &mapK;
-                        tma_box(dst, map, p.it.g * kD, (int)row, bar);
-                        tma_box(dst + kHalf, map, p.it.g * kD + 64, (int)row, bar);
-                    }
-                }
-            }
-        } while (ok && p.next(kv, sv, ws));
-        // every copy issued has landed before the CTA may leave (a stage's earlier copies landed
-        // before it was used again)
-        if (lane == 0) {
-            for (int s = 0; s < kStages; ++s) {
-                if (!((used >> s) & 1u)) continue;
-                bool done;
-                if ((edge_last >> s) & 1u) {
-                    done = mbar_wait(&bars.raw[s], ((raw_phase >> s) & 1u) ^ 1u);
-                } else {
-                    // the last use of stage s: the largest i < n with i % kStages == s
-                    const uint32_t i = n - 1 - ((n - 1 - (uint32_t)s) % kStages);
-                    done = mbar_wait(&bars.full[s], (i / kStages) & 1u);
-                }
-                if (!done) ok = false;
-            }
-        }
-        __syncwarp();
-    } else if (warp >= 12) {
-        // ---- V tiles in which some row does not see some cell: values of cells that no row
-        // sees become zero (their weight is zero, but zero times an infinity is not), and so do
-        // infinities and NaN of cells that only some rows see; the epilogue adds those
-        const int aux = warp - 12;
-        uint32_t n = 0, raw_phase = 0;
-        do {
-            for (int t = p.tile0; ok && t < p.tile1; ++t, n += 2) {
-                if (!p.edge(t)) continue;
-                const int s = (int)((n + 1) % kStages);
-                if (!warp_wait(&bars.raw[s], (raw_phase >> s) & 1u, wc.limit_ns)) {
-                    ok = false;
-                    break;
-                }
-                raw_phase ^= 1u << s;
-                unsigned char *tile = ring + (size_t)s * kTileB;
-                const int r0 = max(0, p.pos0 + 1 - t * kN), r1 = p.n_see - t * kN;
-                bool here = false;
-                // 16 chunks of 16 bytes a row: two rows a turn
-                for (int r = r0 + 2 * aux + (lane >> 4); r < kN; r += 8) {
-                    const int c = lane & 15;
-                    uint4 *w = reinterpret_cast<uint4 *>(tile + (c >> 3) * kHalf + r * 128 +
-                                                         (((c & 7) ^ (r & 7)) << 4));
-                    if (r >= r1) {
-                        *w = make_uint4(0u, 0u, 0u, 0u);
-                        continue;
-                    }
-                    uint4 v = *w;
-                    uint32_t *u = reinterpret_cast<uint32_t *>(&v);
-                    bool any = false;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t m = __vcmpeq2(u[k] & 0x7f807f80u, 0x7f807f80u);
-                        any |= m != 0;
-                        u[k] &= ~m;
-                    }
-                    if (any) *w = v;
-                    here |= any;
-                }
-                if (here) *reinterpret_cast<volatile int32_t *>(&bars.odd[p.n % kSlots]) = p.n + 1;
-                // written by this warp (generic proxy), read by the tensor cores (async proxy)
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.full[s]);
-            }
-        } while (ok && p.next(kv, sv, ws));
-    }
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
-        // ---- softmax of group gi, one thread per row
-        const int gi = warp >> 2, quarter = warp & 3;
-        const int r = quarter * 32 + lane;
-        const uint32_t lrow = (uint32_t)(quarter * 32) << 16;
-        const uint32_t colS = tmem + lrow + col_s(gi), colO = tmem + lrow + col_o(gi);
-        uint32_t cs = 0;  // completed waits on s_full
-        do {
-            const int tok = gi * rt2 + r / G;  // of the item
-            const bool live = r < rt2 * G && tok < p.toks;
-            const bool group = gi == 0 || p.toks > rt2;
-            const int last = live ? (ws.causal ? p.pos0 + tok : p.cells - 1) : -1;
-            const int first_pos = p.pos0 + (ws.causal ? gi * rt2 : 0);  // every row sees up to here
-            if (ok && group) {
-                // this warp's rows of the queries, two per turn, into the swizzled tile
-                const int c = lane & 15;
-#pragma unroll 4
-                for (int i = 0; i < 16; ++i) {
-                    const int rr = quarter * 32 + 2 * i + (lane >> 4);
-                    const int tk = gi * rt2 + rr / G;
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (rr < rt2 * G && tk < p.toks) {
-                        v = *reinterpret_cast<const uint4 *>(
-                            q + (p.t0 + p.tok0 + tk) * ld_q + (int64_t)(p.it.g * G + rr % G) * kD + c * 8);
-                        v.x = (v.x & q_and) ^ q_xor;
-                        v.y = (v.y & q_and) ^ q_xor;
-                        v.z = (v.z & q_and) ^ q_xor;
-                        v.w = (v.w & q_and) ^ q_xor;
-                    }
-                    *reinterpret_cast<uint4 *>(sQ + (uint32_t)gi * kTileB + (uint32_t)(c >> 3) * kHalf +
-                                               rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = v;
-                }
-                // written by this warp (generic proxy), read by the tensor cores (async proxy)
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.q_ready[gi]);
-            }
-            float m = -INFINITY, l = 0.0f;
-            for (int t = p.tile0; ok && group && t < p.tile1; ++t) {
-                if (!warp_wait(&bars.s_full[gi], cs & 1u, wc.limit_ns)) {
-                    ok = false;
-                    break;
-                }
-                ++cs;
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                float x[kN];
-#pragma unroll
-                for (int c = 0; c < kN; c += 32) tmem_ld32_async(colS + (uint32_t)c, x + c);
-                tmem_wait_ld(x);
-                if (t * kN + kN - 1 > first_pos) {
-                    const int lim = last - t * kN;  // cells up to lim are seen
-#pragma unroll
-                    for (int e = 0; e < kN; ++e) x[e] = e <= lim ? x[e] : -INFINITY;
-                }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int e = 0; e < kN; e += 8) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], fmaxf(x[e + 2 * k], x[e + 2 * k + 1]));
-                }
-                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2;
-                const bool move = mt > m + kMove;  // also the first finite maximum
-                if (__any_sync(0xffffffffu, move)) {
-                    const float alpha = move ? ex2_approx(m - mt) : 1.0f;
-                    if (move) {
-                        l *= alpha;
-                        m = mt;
-                    }
-                    // s_full follows this group's last product with V: o may be rescaled
-                    if (t > p.tile0) {
-#pragma unroll 1
-                        for (int c = 0; c < kD; c += 32) {
-                            float o[32];
-                            tmem_ld32(colO + (uint32_t)c, o);
-                            uint32_t ou[32];
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) ou[e] = __float_as_uint(o[e] * alpha);
-                            tmem_st32(colO + (uint32_t)c, ou);
+        } else if (warp == kLoadWarp) {
+            // ---- queries, K and V tiles: box b of a tile is box_rows cells, by lane b
+            const int boxes = kN / box_rows;
+            uint32_t n = 0, nq[2] = {0, 0};
+            uint32_t edge_last = 0, raw_phase = 0, used = 0;  // bits by stage
+            do {
+                for (int t = p.tile0; ok && t < p.tile1; ++t) {
+                    const int j = t * kN + lane * box_rows;
+                    int64_t row = -2;
+                    if (lane < boxes && j < p.n_see) row = cell_row(kv, p.it.s, p.t0, j);
+                    const uint32_t go = __ballot_sync(0xffffffffu, row >= 0);
+                    if (__any_sync(0xffffffffu, row == -1) && lane == 0)
+                        *reinterpret_cast<volatile int32_t *>(&bars.bad[p.n % kSlots]) = p.n + 1;
+                    for (int half = 0; ok && half < 2; ++half) {  // K, then V
+                        const int s = (int)(n % kStages);
+                        if (n >= kStages &&
+                            !warp_wait(&bars.empty[s], ((n / kStages) - 1) & 1u, wc.limit_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        const bool edge = half == 1 && p.edge(t);
+                        uint64_t *bar = edge ? &bars.raw[s] : &bars.full[s];
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(bar, (uint32_t)__popc(go) * (uint32_t)box_rows * 256u);
+                            if (!edge) mbar_arrive_n(bar, kAuxWarps - 1);
+                        }
+                        used |= 1u << s;
+                        edge_last = edge ? edge_last | (1u << s) : edge_last & ~(1u << s);
+                        if (edge) raw_phase ^= 1u << s;
+                        ++n;
+                        __syncwarp();
+                        if (row >= 0) {
+                            const uint32_t dst =
+                                smem_u32(ring) + (uint32_t)s * kTileB + (uint32_t)(lane * box_rows) * 128;
+                            const CUtensorMap *map = half ? &mapV : &mapK;
+                            tma_box(dst, map, p.it.g * kD, (int)row, bar);
+                            tma_box(dst + kHalf, map, p.it.g * kD + 64, (int)row, bar);
+                        }
+                        if (half == 0 && t == p.tile0) {
+                            // this part's queries, once the last part's logits are done with theirs
+                            for (int g = 0; g < (p.toks > rt2 ? 2 : 1); ++g) {
+                                if (nq[g] > 0 && !warp_wait(&bars.q_free[g], (nq[g] - 1) & 1u, wc.limit_ns)) {
+                                    ok = false;
+                                    break;
+                                }
+                                ++nq[g];
+                                if (lane == 0) {
+                                    mbar_arrive_expect_tx(&bars.q_full[g], (uint32_t)(rt2 * G) * 256u);
+                                    const uint32_t dst = smem_u32(sQ) + (uint32_t)g * kTileB;
+                                    const int tok = (int)p.t0 + p.tok0 + g * rt2;
+                                    tma_box3(dst, &mapQ, 0, p.it.g * G, tok, &bars.q_full[g]);
+                                    tma_box3(dst + kHalf, &mapQ, 64, p.it.g * G, tok, &bars.q_full[g]);
+                                }
+                                __syncwarp();
+                            }
                         }
                     }
                 }
-                const float mu = m == -INFINITY ? 0.0f : m;
-                const float2 sc = make_float2(scale_log2, scale_log2), mm = make_float2(-mu, -mu);
-                float2 ls[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t w[32];
-#pragma unroll
-                    for (int e = 0; e < 64; e += 2) {
-                        float2 v = fma2(make_float2(x[64 * h + e], x[64 * h + e + 1]), sc, mm);
-                        v.x = ex2_approx(v.x);
-                        v.y = ex2_approx(v.y);
-                        ls[(e >> 1) & 1] = add2(ls[(e >> 1) & 1], v);
-                        w[e / 2] = pack_bf16(v.x, v.y);
-                    }
-                    tmem_st32(colS + (uint32_t)(32 * h), w);
+            } while (ok && p.next(kv, sv, ws));
+            // every copy issued has landed before the CTA may leave (a stage's earlier copies
+            // landed before it was used again)
+            if (lane == 0) {
+                for (int s = 0; s < kStages; ++s) {
+                    if (!((used >> s) & 1u)) continue;
+                    // the last use of stage s: the largest i < n with i % kStages == s
+                    const uint32_t i = n - 1 - ((n - 1 - (uint32_t)s) % kStages);
+                    const bool done = (edge_last >> s) & 1u
+                                          ? mbar_wait(&bars.raw[s], ((raw_phase >> s) & 1u) ^ 1u)
+                                          : mbar_wait(&bars.full[s], (i / kStages) & 1u);
+                    if (!done) ok = false;
                 }
-                l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
-                tmem_wait_st();
-                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.p_full[gi]);
+                for (int g = 0; g < 2; ++g)
+                    if (nq[g] > 0 && !mbar_wait(&bars.q_full[g], (nq[g] - 1) & 1u)) ok = false;
+            }
+        } else if (warp >= kAuxWarp) {
+            // ---- V tiles in which some row does not see some cell: values of cells that no row
+            // sees become zero (their weight is zero, but zero times an infinity is not), and so
+            // do infinities and NaN of cells that only some rows see; the epilogue adds those
+            const int aux = warp - kAuxWarp;
+            uint32_t n = 0, raw_phase = 0;
+            do {
+                for (int t = p.tile0; ok && t < p.tile1; ++t, n += 2) {
+                    if (!p.edge(t)) continue;
+                    const int s = (int)((n + 1) % kStages);
+                    if (!warp_wait(&bars.raw[s], (raw_phase >> s) & 1u, wc.limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    raw_phase ^= 1u << s;
+                    unsigned char *tile = ring + (size_t)s * kTileB;
+                    const int r0 = max(0, p.pos0 + 1 - t * kN), r1 = p.n_see - t * kN;
+                    bool here = false;
+                    // 16 chunks of 16 bytes a row: two rows a turn
+                    for (int r = r0 + 2 * aux + (lane >> 4); r < kN; r += 2 * kAuxWarps) {
+                        const int c = lane & 15;
+                        uint4 *w = reinterpret_cast<uint4 *>(tile + (c >> 3) * kHalf + r * 128 +
+                                                             (((c & 7) ^ (r & 7)) << 4));
+                        if (r >= r1) {
+                            *w = make_uint4(0u, 0u, 0u, 0u);
+                            continue;
+                        }
+                        uint4 v = *w;
+                        uint32_t *u = reinterpret_cast<uint32_t *>(&v);
+                        bool any = false;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t m = __vcmpeq2(u[k] & 0x7f807f80u, 0x7f807f80u);
+                            any |= m != 0;
+                            u[k] &= ~m;
+                        }
+                        if (any) *w = v;
+                        here |= any;
+                    }
+                    if (here) *reinterpret_cast<volatile int32_t *>(&bars.odd[p.n % kSlots]) = p.n + 1;
+                    // written by this warp (generic proxy), read by the tensor cores (async proxy)
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.full[s]);
+                }
+            } while (ok && p.next(kv, sv, ws));
+        }
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        // ---- softmax of group gi: row r by two threads, cells 64 hf .. 64 hf + 63 of each tile.
+        // The two warps of a row stay in step (pair barriers): what one of them cannot wait for
+        // any more, both give up.
+        const int gi = warp >> 3, hf = (warp >> 2) & 1, quarter = warp & 3;
+        const int r = quarter * 32 + lane;
+        const int pair = 1 + gi * 4 + quarter;
+        const uint32_t lrow = (uint32_t)(quarter * 32) << 16;
+        const uint32_t colS = tmem + lrow + col_s(gi), colO = tmem + lrow + col_o(gi) + 64 * hf;
+        float *const swap = &bars.row[gi][r];
+        uint32_t cs = 0, co = 0;  // waits on s_full, o_full so far
+        do {
+            const int tok = gi * rt2 + r / G;  // of the item
+            const bool group = gi == 0 || p.toks > rt2;
+            const bool live = r < rt2 * G && tok < p.toks;
+            float m = -INFINITY, l = 0.0f;
+            {
+                const int last = live ? (ws.causal ? p.pos0 + tok : p.cells - 1) : -1;
+                const int first_pos = p.pos0 + (ws.causal ? gi * rt2 : 0);  // all rows see up to here
+                for (int t = p.tile0; ok && group && t < p.tile1; ++t) {
+                    bool here = warp_wait(&bars.s_full[gi], cs & 1u, wc.limit_ns);
+                    ++cs;
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    float x[64];
+                    tmem_ld32_async(colS + 64u * hf, x);
+                    tmem_ld32_async(colS + 64u * hf + 32u, x + 32);
+                    tmem_wait_ld(x);
+                    if (t * kN + kN - 1 > first_pos) {
+                        const int lim = last - t * kN - 64 * hf;  // cells up to lim are seen
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) x[e] = e <= lim ? x[e] : -INFINITY;
+                    }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int e = 0; e < 64; e += 8) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], fmaxf(x[e + 2 * k], x[e + 2 * k + 1]));
+                    }
+                    float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2;
+                    // (the barrier also says that both threads hold their logits: either may
+                    // write its weights over them)
+                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                    if (pair_or(pair, !here || mt > m + kMove)) {
+                        // the row's maximum from both; NaN says that a wait gave up
+                        if (hf) *swap = here ? mt : NAN;
+                        pair_sync(pair);
+                        if (!hf) {
+                            const float other = *swap;
+                            here = here && other == other;
+                            mt = fmaxf(mt, other);
+                            *swap = here ? mt : NAN;
+                        }
+                        pair_sync(pair);
+                        if (hf) mt = *swap;
+                        if (hf) here = mt == mt;
+                        // a maximum over logits is no NaN (fmaxf leaves them out); a quarter of a
+                        // row block gives up as a whole
+                        if (!__all_sync(0xffffffffu, here)) {
+                            ok = false;
+                            break;
+                        }
+                        const bool move = mt > m + kMove;  // also the first finite maximum
+                        const float alpha = move ? ex2_approx(m - mt) : 1.0f;
+                        if (move) {
+                            l *= alpha;
+                            m = mt;
+                        }
+                        // s_full follows this group's last product with V: o may be rescaled
+                        if (t > p.tile0 && __any_sync(0xffffffffu, move)) {
+#pragma unroll 1
+                            for (int c = 0; c < 64; c += 16) {
+                                float o[16];
+                                tmem_ld16(colO + (uint32_t)c, o);
+                                uint32_t ou[16];
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) ou[e] = __float_as_uint(o[e] * alpha);
+                                tmem_st16(colO + (uint32_t)c, ou);
+                            }
+                        }
+                    }
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const float mu = m == -INFINITY ? 0.0f : m;
+                    const float2 sc = make_float2(scale_log2, scale_log2), mm = make_float2(-mu, -mu);
+                    float2 ls[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float2 v = fma2(make_float2(x[32 * h + e], x[32 * h + e + 1]), sc, mm);
+                            v.x = ex2_approx(v.x);
+                            v.y = ex2_approx(v.y);
+                            ls[(e >> 1) & 1] = add2(ls[(e >> 1) & 1], v);
+                            w[e / 2] = pack_bf16(v.x, v.y);
+                        }
+                        tmem_st16(colS + (uint32_t)(32 * hf + 16 * h), w);
+                    }
+                    l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+                    tmem_wait_st();
+                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.p_full[gi]);
+                }
             }
             if (ok && group) {
-                if (warp_wait(&bars.s_full[gi], cs & 1u, wc.limit_ns)) ++cs;
-                else ok = false;
+                bool here = warp_wait(&bars.o_full[gi], co & 1u, wc.limit_ns);
+                ++co;
+                here = !pair_or(pair, !here);
+                if (hf) *swap = l;
+                pair_sync(pair);
+                if (!hf) {
+                    l += *swap;
+                    *swap = l;
+                }
+                pair_sync(pair);
+                if (hf) l = *swap;
+                if (!here) ok = false;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             }
             // ---- the part's result: finished rows, or a record to be joined
@@ -525,7 +589,7 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 const int rr = gi * kM + r;
                 const int64_t at = ((p.t0 + p.tok0 + tok) * H_q + p.it.g * G + r % G);
 #pragma unroll 1
-                for (int c = 0; c < kD; c += 32) {
+                for (int c = 0; c < 64; c += 32) {
                     float o[32];
                     if (ok) {
                         tmem_ld32(colO + (uint32_t)c, o);
@@ -535,12 +599,13 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                     }
                     if (!live) continue;
                     if (odd && ok) {
-                        const int to = min(min(last, p.n_see - 1), p.tile1 * kN - 1);
+                        const int see = ws.causal ? p.pos0 + tok : p.cells - 1;
+                        const int to = min(min(see, p.n_see - 1), p.tile1 * kN - 1);
                         for (int j = max(p.pos0 + 1, p.tile0 * kN); j <= to; ++j) {
                             const int64_t row = cell_row(kv, p.it.s, p.t0, j);
                             if (row < 0) continue;
                             const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(kv.V) +
-                                                     row * kv.ld_v + (int64_t)p.it.g * kD + c;
+                                                     row * kv.ld_v + (int64_t)p.it.g * kD + 64 * hf + c;
 #pragma unroll
                             for (int e = 0; e < 32; ++e) {
                                 const float f = __bfloat162float(v[e]);
@@ -549,7 +614,7 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                         }
                     }
                     if (whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(out + at * kD + c);
+                        uint4 *dst = reinterpret_cast<uint4 *>(out + at * kD + 64 * hf + c);
 #pragma unroll
                         for (int e = 0; e < 32; e += 8)
                             dst[e / 8] = make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv),
@@ -557,13 +622,13 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                                                     pack_bf16(o[e + 4] * inv, o[e + 5] * inv),
                                                     pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
                     } else {
-                        float4 *dst = reinterpret_cast<float4 *>(rec + 4 * kM + (int64_t)rr * kD + c);
+                        float4 *dst = reinterpret_cast<float4 *>(rec + 4 * kM + (int64_t)rr * kD + 64 * hf + c);
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
                             dst[e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                     }
                 }
-                if (live) {
+                if (live && hf == 0) {
                     if (whole) {
                         if (lse) lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
                     } else {
@@ -574,7 +639,7 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             }
             if (starts && !ends && tid == 0) {
-                const int64_t c1 = (p.it.start + p.it.tiles - 1) / per;
+                const int64_t c1 = (p.it.start + ws.over + p.it.tiles - 1) / per;
                 Split sp = {p.it.s, p.it.g, p.it.t, (int32_t)(c1 - blockIdx.x) + 1};
                 splits[blockIdx.x] = sp;
             }
@@ -585,7 +650,7 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    if (warp == 8)
+    if (warp == kMmaWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                      "r"(kTmemCols)
                      : "memory");
@@ -625,6 +690,20 @@ bool make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t width, int
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries [n_tok][H_q][128]: boxes of 64 values x G heads x as many tokens as fill a group.
+bool make_query_map(CUtensorMap *m, const void *q, int64_t n_tok, int H_q, int64_t ld_q, int G)
+{
+    const EncodeTiledFn fn = encode_tiled();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)H_q, (cuuint64_t)n_tok};
+    const cuuint64_t strides[2] = {(cuuint64_t)kD * 2, (cuuint64_t)ld_q * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(kM / G)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 constexpr int kMaxCtas = kTargetSMs;
 
 }  // namespace
@@ -632,8 +711,9 @@ constexpr int kMaxCtas = kTargetSMs;
 bool dense_tc_ok(const DenseArgs &a)
 {
     const int G = a.H_q / a.kv.H_kv;
-    return a.d == kD && a.q_dtype == QSA_BF16 && a.kv_dtype == QSA_BF16 && G <= kM && a.pool_rows > 0 &&
-           a.pool_rows <= 0x7fffffffLL;
+    // (the softmax takes its maximum over unscaled logits: a positive scale)
+    return a.d == kD && a.q_dtype == QSA_BF16 && a.kv_dtype == QSA_BF16 && G <= kM && a.scale > 0.0f &&
+           a.pool_rows > 0 && a.pool_rows <= 0x7fffffffLL;
 }
 
 size_t dense_tc_workspace()
@@ -646,9 +726,10 @@ qsa_status launch_dense_tc(const DenseArgs &a, void *workspace, cudaStream_t st)
     const int G = a.H_q / a.kv.H_kv;
     const int page = 1 << a.kv.page_shift;
     const int box_rows = a.kv.table && page < kN ? page : kN;
-    CUtensorMap mk, mv;
+    CUtensorMap mq, mk, mv;
     const int64_t width = (int64_t)a.kv.H_kv * kD;
-    if (!make_map(&mk, a.kv.K, a.pool_rows, width, a.kv.ld_k, box_rows) ||
+    if (!make_query_map(&mq, a.q, a.sv.n_tok, a.H_q, a.ld_q, G) ||
+        !make_map(&mk, a.kv.K, a.pool_rows, width, a.kv.ld_k, box_rows) ||
         !make_map(&mv, a.kv.V, a.pool_rows, width, a.kv.ld_v, box_rows))
         return QSA_ERR_CUDA;
     WorkShape ws;
@@ -656,18 +737,15 @@ qsa_status launch_dense_tc(const DenseArgs &a, void *workspace, cudaStream_t st)
     ws.kt = kN;
     ws.H_kv = a.kv.H_kv;
     ws.causal = a.causal;
+    ws.over = kOver;
     if (ensure_kernel_attrs<dense_tc_kernel>(tc_smem()) != cudaSuccess) return QSA_ERR_CUDA;
     int ctas = device_sm_count();
     if (ctas > kMaxCtas) ctas = kMaxCtas;
     Split *splits = static_cast<Split *>(workspace);
     float *partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + kMaxCtas * sizeof(Split));
-    // the softmax takes a positive scale; a negative one turns the queries' signs, zero clears them
-    const float scale = a.scale == 0.0f ? 1.0f : fabsf(a.scale);
-    const uint32_t q_and = a.scale == 0.0f ? 0u : 0xffffffffu, q_xor = a.scale < 0.0f ? 0x80008000u : 0u;
-    cudaError_t e = launch(dense_tc_kernel, dim3((unsigned)ctas), dim3(kThreads), tc_smem(), st, 1, mk, mv, a.kv,
-                           a.sv, ws, box_rows, static_cast<const __nv_bfloat16 *>(a.q), a.ld_q, a.H_q,
-                           scale * kLog2e, q_and, q_xor, static_cast<__nv_bfloat16 *>(a.out), a.lse, partial,
-                           splits, current_wait_ctl());
+    cudaError_t e = launch(dense_tc_kernel, dim3((unsigned)ctas), dim3(kThreads), tc_smem(), st, 1, mq, mk, mv,
+                           a.kv, a.sv, ws, box_rows, a.H_q, a.scale * kLog2e,
+                           static_cast<__nv_bfloat16 *>(a.out), a.lse, partial, splits, current_wait_ctl());
     if (e != cudaSuccess) return QSA_ERR_CUDA;
     e = launch_dense_join<__nv_bfloat16, 1>(splits, partial, ctas, 2 * kM, kM / G, a, st);
     return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;

@@ -186,26 +186,17 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
 
     pdl_wait();
     const TQ *qp = q;
-    KvView kw = kv;
-    SeqView sw = sv;
     QSA_AFTER_WAIT(qp);
-    QSA_AFTER_WAIT(sw.cu);
-    QSA_AFTER_WAIT(sw.kv_len);
-    QSA_AFTER_WAIT(kw.table);
-    QSA_AFTER_WAIT(kw.K);
-    QSA_AFTER_WAIT(kw.V);
-    QSA_AFTER_WAIT(kw.K_exp);
-    QSA_AFTER_WAIT(kw.V_exp);
     pdl_trigger();
 
-    const int64_t total = work_total(sw, ws);
+    const int64_t total = work_total(sv, ws);
     const int64_t per = (total + gridDim.x - 1) / gridDim.x;
     const int64_t x0 = (int64_t)blockIdx.x * per;
     const int64_t x1 = x0 + per < total ? x0 + per : total;
     if (tid == 0) splits[blockIdx.x].s = -1;
     if (x0 >= x1) return;
-    const int G = H_q / kw.H_kv;
-    WorkItem it = work_find(sw, ws, x0);
+    const int G = H_q / kv.H_kv;
+    WorkItem it = work_find(sv, ws, x0);
     int64_t x = x0;
     for (;;) {
         const int64_t item_end = it.start + it.tiles;
@@ -214,9 +205,9 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
         const bool starts = tile0 == 0, ends = tile1 == it.tiles;
         int64_t t0;
         int len;
-        seq_tokens(sw, it.s, t0, len);
-        const int cells = seq_cells(sw, it.s, len);
-        const bool fits = cells_fit(kw, cells);
+        seq_tokens(sv, it.s, t0, len);
+        const int cells = seq_cells(sv, it.s, len);
+        const bool fits = cells_fit(kv, cells);
         const int n_see = fits ? item_cells(ws, len, cells, it.t) : 0;
         const int tok0 = it.t * ws.rt;
         const int rows = min(ws.rt, len - tok0) * G;
@@ -310,7 +301,7 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
         auto row_of = [&](int tile) -> int64_t {
             const int p = tile * ws.kt + warp * S::kKeys + my_key;
             if (tile >= tile1 || p >= n_see) return -2;  // not there: zeros
-            const int64_t row = cell_row(kw, it.s, t0, p);
+            const int64_t row = cell_row(kv, it.s, t0, p);
             bad |= row < 0;
             return row;
         };
@@ -318,16 +309,16 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
         auto load_exps = [&](int64_t row) {
             float2 f = make_float2(0.0f, 0.0f);
             if (row >= 0) {
-                const int ek = (int)kw.K_exp[row * kw.H_kv + it.g] - kExpBias;
-                const int ev = (int)kw.V_exp[row * kw.H_kv + it.g] - kExpBias;
+                const int ek = (int)kv.K_exp[row * kv.H_kv + it.g] - kExpBias;
+                const int ev = (int)kv.V_exp[row * kv.H_kv + it.g] - kExpBias;
                 f.x = two_to(min(max(ek, kExpMin), kExpMax)) * scale_log2;
                 f.y = (float)min(max(ev, kExpMin), kExpMax);
             }
             return f;
         };
-        const unsigned char *Kb = static_cast<const unsigned char *>(kw.K) + (int64_t)it.g * S::kRowBytes;
-        const unsigned char *Vb = static_cast<const unsigned char *>(kw.V) + (int64_t)it.g * S::kRowBytes;
-        const int64_t ldk_b = kw.ld_k * (E8 ? 1 : 2), ldv_b = kw.ld_v * (E8 ? 1 : 2);
+        const unsigned char *Kb = static_cast<const unsigned char *>(kv.K) + (int64_t)it.g * S::kRowBytes;
+        const unsigned char *Vb = static_cast<const unsigned char *>(kv.V) + (int64_t)it.g * S::kRowBytes;
+        const int64_t ldk_b = kv.ld_k * (E8 ? 1 : 2), ldv_b = kv.ld_v * (E8 ? 1 : 2);
         auto issue = [&](int stage, int64_t row) {
             constexpr int kChunks = S::kRowBytes / 16, kAt = 32 / kChunks;
             const uint32_t st = smem_u32(ring + stage * 2 * kTile);
@@ -648,9 +639,9 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
             if (odd_s) {
                 const int to = min(n_see - 1, ws.causal ? pos0 + r / G : cells - 1);
                 for (int j = max(pos0 + 1, tile0 * ws.kt); j <= to && j < tile1 * ws.kt; ++j) {
-                    const int64_t row = cell_row(kw, it.s, t0, j);
+                    const int64_t row = cell_row(kv, it.s, t0, j);
                     if (row >= 0)
-                        for (int k = 0; k < 4; ++k) v[k] += odd_value<E8>(kw, row, it.g, c + k);
+                        for (int k = 0; k < 4; ++k) v[k] += odd_value<E8>(kv, row, it.g, c + k);
                 }
             }
             if (nan_out) sum = NAN;
@@ -682,7 +673,7 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
         }
         x = it.start + tile1;
         if (x >= x1) break;
-        if (!work_next(sw, ws, it)) break;
+        if (!work_next(sv, ws, it)) break;
     }
 }
 
@@ -703,6 +694,7 @@ cudaError_t run(const DenseArgs &a, void *workspace, cudaStream_t st)
     ws.kt = kWarps * Shape<E8>::kKeys;
     ws.H_kv = a.kv.H_kv;
     ws.causal = a.causal;
+    ws.over = 0;
     constexpr size_t smem = decode_smem<E8, MT, NT>();
     cudaError_t e = ensure_kernel_attrs<dense_decode_kernel<E8, MT, TQ, NT>>(smem);
     if (e != cudaSuccess) return e;

@@ -31,8 +31,6 @@ dense_join_kernel(const Split *__restrict__ splits, const float *__restrict__ pa
     pdl_wait();
     QSA_AFTER_WAIT(splits);
     QSA_AFTER_WAIT(partial);
-    SeqView sw = sv;
-    QSA_AFTER_WAIT(sw.cu);
     pdl_trigger();
     const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part = warp % kParts;
@@ -40,7 +38,7 @@ dense_join_kernel(const Split *__restrict__ splits, const float *__restrict__ pa
     if (sp.s < 0) return;
     int64_t t0;
     int len;
-    seq_tokens(sw, sp.s, t0, len);
+    seq_tokens(sv, sp.s, t0, len);
     const int64_t rec = partial_floats(rows_max, kD);
     const int r = blockIdx.y * kRows + warp / kParts;
     const int tok = sp.t * rt + (r >> 7) * group + (r & 127) / G;

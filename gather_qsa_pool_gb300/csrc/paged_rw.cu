@@ -88,9 +88,6 @@ paged_write_kernel(const TS *__restrict__ k, const TS *__restrict__ v, int64_t l
     pdl_wait();
     QSA_AFTER_WAIT(k);
     QSA_AFTER_WAIT(v);
-    QSA_AFTER_WAIT(sv.cu);
-    QSA_AFTER_WAIT(sv.kv_len);
-    QSA_AFTER_WAIT(kv.table);
     pdl_trigger();
     const int lanes = 1 << lanes_log2;  // lanes of a row; those beyond d / 8 idle
     const int64_t gt = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
@@ -156,11 +153,6 @@ paged_read_kernel(KvView kv, int H, int d, const int32_t *__restrict__ seq,
     QSA_AFTER_WAIT(kv_len);
     QSA_AFTER_WAIT(pos);
     QSA_AFTER_WAIT(n_cells);
-    QSA_AFTER_WAIT(kv.table);
-    QSA_AFTER_WAIT(kv.K);
-    QSA_AFTER_WAIT(kv.V);
-    QSA_AFTER_WAIT(kv.K_exp);
-    QSA_AFTER_WAIT(kv.V_exp);
     pdl_trigger();
     const int lane = threadIdx.x & 31;
     const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
