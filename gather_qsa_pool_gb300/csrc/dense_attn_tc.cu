@@ -95,6 +95,40 @@ __device__ __forceinline__ bool pair_or(int id, bool v)
     return r != 0;
 }
 
+// mbar_wait and warp_wait for this kernel's many waiting warps: the hardware may suspend the
+// thread up to 20 us a try (sixteen softmax warps that poll take issue slots from those that
+// compute).
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns)
+{
+    if (limit_ns == 0) return false;
+    const uint32_t a = smem_u32(bar);
+    uint64_t t0 = 0;
+    for (uint32_t i = 0;; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(a), "r"(parity), "r"(20000u)
+            : "memory");
+        if (done) return true;
+        if ((i & 15) == 0) {
+            const uint64_t t = global_ns();
+            if (t0 == 0) t0 = t;
+            else if (t - t0 > limit_ns) return false;
+        }
+    }
+}
+__device__ __forceinline__ bool bar_wait_warp(uint64_t *bar, uint32_t parity, uint64_t limit_ns)
+{
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0) ok = bar_wait(bar, parity, limit_ns);
+    ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+    __syncwarp();
+    return ok;
+}
+
 // One box of a 2D tensor map: 64 bf16 columns from x, the map's box rows from y.
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar)
 {
@@ -198,7 +232,8 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
     unsigned char *ring = sQ + 2 * kTileB;
     Bars &bars = *reinterpret_cast<Bars *>(ring + (size_t)kStages * kTileB);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform, as the compiler sees it
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&bars.full[s], kAuxWarps);
@@ -251,8 +286,9 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
     // registers: 640 threads x 96 at launch = 512 x 104 + 128 x 64
     if (warp >= kSoftWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        if (warp == kMmaWarp && lane == 0) {
-            // ---- MMA issue
+        if (warp == kMmaWarp) {
+            // ---- MMA issue (all lanes walk, one issues)
+            const uint32_t lead = elect_leader();
             constexpr uint32_t id_s = idesc_m128(kN, false), id_o = idesc_m128(kD, true);
             const uint64_t dk0 = desc_kmajor_sw128(smem_u32(ring));
             const uint64_t dv0 = desc_mnmajor_sw128(smem_u32(ring), kHalf);
@@ -263,43 +299,43 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
 #pragma unroll
                 for (int k = 0; k < kD / 16; ++k) {
                     const uint32_t off = ((uint32_t)(k >> 2) * kHalf + (uint32_t)(k & 3) * 32) >> 4;
-                    umma_m128_ss(tmem + col_s(g), dq0 + (((uint32_t)g * kTileB) >> 4) + off,
-                                 dk0 + (((uint32_t)st * kTileB) >> 4) + off, id_s, k ? 1u : 0u);
+                    umma_m128_ss_lead(tmem + col_s(g), dq0 + (((uint32_t)g * kTileB) >> 4) + off,
+                                 dk0 + (((uint32_t)st * kTileB) >> 4) + off, id_s, k ? 1u : 0u, lead);
                 }
             };
             auto mma_o = [&](int g, int st, bool first) {
 #pragma unroll
                 for (int k = 0; k < kN / 16; ++k)
-                    umma_m128_ta(tmem + col_o(g), tmem + col_s(g) + (uint32_t)k * 8,
+                    umma_m128_ta_lead(tmem + col_o(g), tmem + col_s(g) + (uint32_t)k * 8,
                                  dv0 + (((uint32_t)st * kTileB + (uint32_t)k * 2048) >> 4), id_o,
-                                 (!first || k) ? 1u : 0u);
+                                 (!first || k) ? 1u : 0u, lead);
             };
             uint32_t n = 0, np[2] = {0, 0}, nq[2] = {0, 0};  // stages, weights, queries so far
             auto stage_ready = [&](uint32_t i) {
-                return mbar_wait(&bars.full[i % kStages], (i / kStages) & 1u, wc.limit_ns);
+                return bar_wait(&bars.full[i % kStages], (i / kStages) & 1u, wc.limit_ns);
             };
             do {
                 const int tiles = p.tile1 - p.tile0;
                 const bool two = p.toks > rt2;  // group B has rows
-                ok = stage_ready(n) && mbar_wait(&bars.q_full[0], nq[0]++ & 1u, wc.limit_ns);
+                ok = stage_ready(n) && bar_wait(&bars.q_full[0], nq[0]++ & 1u, wc.limit_ns);
                 if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 mma_s(0, (int)(n % kStages));
-                umma_commit(&bars.s_full[0]);
-                if (tiles == 1) umma_commit(&bars.q_free[0]);
+                umma_commit_lead(&bars.s_full[0], lead);
+                if (tiles == 1) umma_commit_lead(&bars.q_free[0], lead);
                 if (two) {
-                    ok = mbar_wait(&bars.q_full[1], nq[1]++ & 1u, wc.limit_ns);
+                    ok = bar_wait(&bars.q_full[1], nq[1]++ & 1u, wc.limit_ns);
                     if (!ok) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     mma_s(1, (int)(n % kStages));
-                    umma_commit(&bars.s_full[1]);
-                    if (tiles == 1) umma_commit(&bars.q_free[1]);
+                    umma_commit_lead(&bars.s_full[1], lead);
+                    if (tiles == 1) umma_commit_lead(&bars.q_free[1], lead);
                 }
-                umma_commit(&bars.empty[n % kStages]);
+                umma_commit_lead(&bars.empty[n % kStages], lead);
                 for (int t = 0; t < tiles; ++t) {
                     const uint32_t iv = n + 2 * (uint32_t)t + 1, ik = iv + 1;
                     const bool more = t + 1 < tiles, last_s = t + 2 == tiles;
-                    ok = stage_ready(iv) && mbar_wait(&bars.p_full[0], np[0]++ & 1u, wc.limit_ns);
+                    ok = stage_ready(iv) && bar_wait(&bars.p_full[0], np[0]++ & 1u, wc.limit_ns);
                     if (!ok) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     mma_o(0, (int)(iv % kStages), t == 0);
@@ -308,31 +344,31 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
                         if (!ok) break;
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                         mma_s(0, (int)(ik % kStages));
-                        umma_commit(&bars.s_full[0]);
-                        if (last_s) umma_commit(&bars.q_free[0]);
+                        umma_commit_lead(&bars.s_full[0], lead);
+                        if (last_s) umma_commit_lead(&bars.q_free[0], lead);
                     } else {
-                        umma_commit(&bars.o_full[0]);
+                        umma_commit_lead(&bars.o_full[0], lead);
                     }
                     if (two) {
-                        ok = mbar_wait(&bars.p_full[1], np[1]++ & 1u, wc.limit_ns);
+                        ok = bar_wait(&bars.p_full[1], np[1]++ & 1u, wc.limit_ns);
                         if (!ok) break;
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                         mma_o(1, (int)(iv % kStages), t == 0);
                     }
-                    umma_commit(&bars.empty[iv % kStages]);
+                    umma_commit_lead(&bars.empty[iv % kStages], lead);
                     if (two && more) {
                         mma_s(1, (int)(ik % kStages));
-                        umma_commit(&bars.s_full[1]);
-                        if (last_s) umma_commit(&bars.q_free[1]);
+                        umma_commit_lead(&bars.s_full[1], lead);
+                        if (last_s) umma_commit_lead(&bars.q_free[1], lead);
                     } else if (two) {
-                        umma_commit(&bars.o_full[1]);
+                        umma_commit_lead(&bars.o_full[1], lead);
                     }
-                    if (more) umma_commit(&bars.empty[ik % kStages]);
+                    if (more) umma_commit_lead(&bars.empty[ik % kStages], lead);
                 }
                 n += 2 * (uint32_t)tiles;
             } while (ok && p.next(kv, sv, ws));
             // every MMA issued has completed before the tensor memory is freed
-            umma_commit(&bars.drain);
+            umma_commit_lead(&bars.drain, lead);
             if (!mbar_wait(&bars.drain, 0)) ok = false;
         } else if (warp == kLoadWarp) {
             // ---- queries, K and V tiles: box b of a tile is box_rows cells, by lane b
@@ -350,7 +386,7 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
                     for (int half = 0; ok && half < 2; ++half) {  // K, then V
                         const int s = (int)(n % kStages);
                         if (n >= kStages &&
-                            !warp_wait(&bars.empty[s], ((n / kStages) - 1) & 1u, wc.limit_ns)) {
+                            !bar_wait_warp(&bars.empty[s], ((n / kStages) - 1) & 1u, wc.limit_ns)) {
                             ok = false;
                             break;
                         }
@@ -375,7 +411,7 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
                         if (half == 0 && t == p.tile0) {
                             // this part's queries, once the last part's logits are done with theirs
                             for (int g = 0; g < (p.toks > rt2 ? 2 : 1); ++g) {
-                                if (nq[g] > 0 && !warp_wait(&bars.q_free[g], (nq[g] - 1) & 1u, wc.limit_ns)) {
+                                if (nq[g] > 0 && !bar_wait_warp(&bars.q_free[g], (nq[g] - 1) & 1u, wc.limit_ns)) {
                                     ok = false;
                                     break;
                                 }
@@ -418,7 +454,7 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
                 for (int t = p.tile0; ok && t < p.tile1; ++t, n += 2) {
                     if (!p.edge(t)) continue;
                     const int s = (int)((n + 1) % kStages);
-                    if (!warp_wait(&bars.raw[s], (raw_phase >> s) & 1u, wc.limit_ns)) {
+                    if (!bar_wait_warp(&bars.raw[s], (raw_phase >> s) & 1u, wc.limit_ns)) {
                         ok = false;
                         break;
                     }
@@ -477,7 +513,7 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
                 const int last = live ? (ws.causal ? p.pos0 + tok : p.cells - 1) : -1;
                 const int first_pos = p.pos0 + (ws.causal ? gi * rt2 : 0);  // all rows see up to here
                 for (int t = p.tile0; ok && group && t < p.tile1; ++t) {
-                    bool here = warp_wait(&bars.s_full[gi], cs & 1u, wc.limit_ns);
+                    bool here = bar_wait_warp(&bars.s_full[gi], cs & 1u, wc.limit_ns);
                     ++cs;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     float x[64];
@@ -562,7 +598,7 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
                 }
             }
             if (ok && group) {
-                bool here = warp_wait(&bars.o_full[gi], co & 1u, wc.limit_ns);
+                bool here = bar_wait_warp(&bars.o_full[gi], co & 1u, wc.limit_ns);
                 ++co;
                 here = !pair_or(pair, !here);
                 if (hf) *swap = l;
