@@ -15,7 +15,8 @@
 // per page, 128-byte swizzle), K and V into a ring of 32 KB stages; warps 18 and 19 see to the
 // tiles where some row does not see some cell.
 //   tensor memory (512 columns): S of group A, S of group B (128 fp32 columns each; a row's
-//   weights P overwrite its own S as bf16, 64 columns), O of A and of B (128 each).
+//   weights P overwrite its own S as bf16, each thread's 64 over its own logits), O of A and of B
+//   (128 each).
 // Per tile the tensor cores run O_A += P_A V, S_A = Q_A K', O_B += P_B V, S_B = Q_B K' (K' the
 // next tile's keys): while one group's weights are computed the other group's products run.
 // One thread issues them all, in the order in which they use S and P.
@@ -122,11 +123,7 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, uint64_
 }
 __device__ __forceinline__ bool bar_wait_warp(uint64_t *bar, uint32_t parity, uint64_t limit_ns)
 {
-    bool ok = true;
-    if ((threadIdx.x & 31) == 0) ok = bar_wait(bar, parity, limit_ns);
-    ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-    __syncwarp();
-    return ok;
+    return __all_sync(0xffffffffu, bar_wait(bar, parity, limit_ns)) != 0;
 }
 
 // One box of a 2D tensor map: 64 bf16 columns from x, the map's box rows from y.
@@ -306,7 +303,7 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
             auto mma_o = [&](int g, int st, bool first) {
 #pragma unroll
                 for (int k = 0; k < kN / 16; ++k)
-                    umma_m128_ta_lead(tmem + col_o(g), tmem + col_s(g) + (uint32_t)k * 8,
+                    umma_m128_ta_lead(tmem + col_o(g), tmem + col_s(g) + (uint32_t)(k >> 2) * 64 + (uint32_t)(k & 3) * 8,
                                  dv0 + (((uint32_t)st * kTileB + (uint32_t)k * 2048) >> 4), id_o,
                                  (!first || k) ? 1u : 0u, lead);
             };
@@ -525,6 +522,29 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
 #pragma unroll
                         for (int e = 0; e < 64; ++e) x[e] = e <= lim ? x[e] : -INFINITY;
                     }
+                    // the weights relative to the reference as it stands, over this thread's own
+                    // logits; the maximum, meanwhile, says whether they may stay
+                    float2 ls[2];
+                    const float2 sc = make_float2(scale_log2, scale_log2);
+                    auto weights = [&]() {
+                        const float mu = m == -INFINITY ? 0.0f : m;
+                        const float2 mm = make_float2(-mu, -mu);
+                        ls[0] = ls[1] = make_float2(0.0f, 0.0f);
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int e = 0; e < 16; e += 2) {
+                                float2 v = fma2(make_float2(x[16 * h + e], x[16 * h + e + 1]), sc, mm);
+                                v.x = ex2_approx(v.x);
+                                v.y = ex2_approx(v.y);
+                                ls[(e >> 1) & 1] = add2(ls[(e >> 1) & 1], v);
+                                w[e / 2] = pack_bf16(v.x, v.y);
+                            }
+                            tmem_st8(colS + (uint32_t)(64 * hf + 8 * h), w);
+                        }
+                    };
+                    weights();
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                     for (int e = 0; e < 64; e += 8) {
@@ -532,9 +552,6 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
                         for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], fmaxf(x[e + 2 * k], x[e + 2 * k + 1]));
                     }
                     float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2;
-                    // (the barrier also says that both threads hold their logits: either may
-                    // write its weights over them)
-                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                     if (pair_or(pair, !here || mt > m + kMove)) {
                         // the row's maximum from both; NaN says that a wait gave up
                         if (hf) *swap = here ? mt : NAN;
@@ -572,23 +589,7 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
                                 tmem_st16(colO + (uint32_t)c, ou);
                             }
                         }
-                    }
-                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const float mu = m == -INFINITY ? 0.0f : m;
-                    const float2 sc = make_float2(scale_log2, scale_log2), mm = make_float2(-mu, -mu);
-                    float2 ls[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            float2 v = fma2(make_float2(x[32 * h + e], x[32 * h + e + 1]), sc, mm);
-                            v.x = ex2_approx(v.x);
-                            v.y = ex2_approx(v.y);
-                            ls[(e >> 1) & 1] = add2(ls[(e >> 1) & 1], v);
-                            w[e / 2] = pack_bf16(v.x, v.y);
-                        }
-                        tmem_st16(colS + (uint32_t)(32 * hf + 16 * h), w);
+                        weights();
                     }
                     l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
                     tmem_wait_st();
