@@ -13,7 +13,8 @@
 // warps, the chain logits -> maximum -> exponentials -> weights left the tensor cores idle for
 // half the time).  Warp 16 issues the MMAs; warp 17 stages queries, K and V tiles by TMA (one box
 // per page, 128-byte swizzle), K and V into a ring of 32 KB stages; warps 18 and 19 see to the
-// tiles where some row does not see some cell.
+// tiles where some row does not see some cell (e4m3 cells: six warps that also turn codes into
+// bf16).
 //   tensor memory (512 columns): S of group A, S of group B (128 fp32 columns each; a row's
 //   weights P overwrite its own S as bf16, each thread's 64 over its own logits), O of A and of B
 //   (128 each).
@@ -37,8 +38,7 @@ namespace {
 constexpr int kD = 128;
 constexpr int kM = 128;                  // rows of a group
 constexpr int kN = 128;                  // cells of a tile
-constexpr int kSoftWarps = 16, kMmaWarp = 16, kLoadWarp = 17, kAuxWarp = 18, kAuxWarps = 2;
-constexpr int kThreads = 32 * (kAuxWarp + kAuxWarps);
+constexpr int kSoftWarps = 16, kMmaWarp = 16, kLoadWarp = 17, kAuxWarp = 18;
 constexpr int kOver = 4;                 // an item's fixed cost in tiles
 constexpr uint32_t kHalf = 128 * 128;    // 16 KB: 128 rows x 64 dims of bf16
 constexpr uint32_t kTileB = 2 * kHalf;   // 32 KB: a K or V tile, or a group's queries
@@ -49,20 +49,37 @@ constexpr int kSlots = 8;                // parts whose flags are kept
 __host__ __device__ constexpr uint32_t col_s(int g) { return g ? 128u : 0u; }
 __host__ __device__ constexpr uint32_t col_o(int g) { return g ? 384u : 256u; }
 
-constexpr int kStages = 5;
+constexpr int kMaxStages = 5;
+
+// What differs between caches.  bf16: five stages, two warps for the tiles with a causal edge.
+// e4m3: four stages of bf16 filled by six warps from two raw 16 KB tiles.
+// Registers: 640 x 96 at launch = 512 x 104 + 128 x 64; 768 x 80 = 512 x 96 + 256 x 48.
+template <bool E8>
+struct Cfg {
+    static constexpr int kStages = E8 ? 4 : 5;
+    static constexpr int kAuxWarps = E8 ? 6 : 2;
+    static constexpr int kThreads = 32 * (kAuxWarp + kAuxWarps);
+};
+constexpr uint32_t kRawTile = 128 * 128;  // 16 KB: 128 cells of codes
+constexpr int kAuxBar = 9;                // named barrier of the converting warps
 
 struct Bars {
-    uint64_t full[kStages], empty[kStages], raw[kStages];
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t raw[kMaxStages];                        // bf16: copies of a stage with an edge
+    uint64_t raw_full[2], raw_empty[2];              // e4m3: raw tiles
     uint64_t s_full[2], p_full[2], o_full[2], q_full[2], q_free[2], drain;
     uint32_t tmem, pad;
     int32_t odd[kSlots], bad[kSlots];  // number + 1 of the part that set it
+    uint8_t exps[2][kN];               // e4m3: exponents of a raw tile's cells
     float row[2][kM];                  // exchanged by the two threads of a row
 };
 
+template <bool E8>
 __host__ __device__ constexpr size_t tc_smem()
 {
-    return 1024 + 2 * kTileB + (size_t)kStages * kTileB + sizeof(Bars);
+    return 1024 + 2 * kTileB + (size_t)Cfg<E8>::kStages * kTileB + (E8 ? 2 * kRawTile : 0) + sizeof(Bars);
 }
+static_assert(tc_smem<false>() <= 227 * 1024 && tc_smem<true>() <= 227 * 1024, "shared memory of one CTA");
 
 __device__ __forceinline__ void mbar_arrive_n(uint64_t *bar, uint32_t n)
 {
@@ -216,18 +233,21 @@ struct Parts {
     __device__ __forceinline__ bool edge(int t) const { return t * kN + kN - 1 > pos0; }
 };
 
-__global__ void __launch_bounds__(kThreads, 1)
+template <bool E8>
+__global__ void __launch_bounds__(Cfg<E8>::kThreads, 1)
 dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                 const __grid_constant__ CUtensorMap mapV, const KvView kv, const SeqView sv,
                 const WorkShape ws, int box_rows, int H_q, float scale_log2,
                 __nv_bfloat16 *__restrict__ out, float *__restrict__ lse, float *__restrict__ partial, Split *__restrict__ splits,
                 const WaitCtl wc)
 {
+    constexpr int kStages = Cfg<E8>::kStages, kAuxWarps = Cfg<E8>::kAuxWarps;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     unsigned char *sQ = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);  // [group][dim half]
     unsigned char *ring = sQ + 2 * kTileB;
-    Bars &bars = *reinterpret_cast<Bars *>(ring + (size_t)kStages * kTileB);
+    unsigned char *raw_tiles = ring + (size_t)kStages * kTileB;  // e4m3: two
+    Bars &bars = *reinterpret_cast<Bars *>(raw_tiles + (E8 ? 2 * kRawTile : 0));
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform, as the compiler sees it
@@ -243,6 +263,10 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
             mbar_init(&bars.o_full[g], 1);
             mbar_init(&bars.q_full[g], 1);
             mbar_init(&bars.q_free[g], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bars.raw_full[s], 1);
+            mbar_init(&bars.raw_empty[s], kAuxWarps);
         }
         mbar_init(&bars.drain, 1);
         for (int i = 0; i < kSlots; ++i) bars.odd[i] = bars.bad[i] = 0;
@@ -280,9 +304,9 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
     const int G = H_q / kv.H_kv;
     const int rt2 = ws.rt / 2;  // tokens of a group
     bool ok = true;
-    // registers: 640 threads x 96 at launch = 512 x 104 + 128 x 64
     if (warp >= kSoftWarps) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if constexpr (E8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == kMmaWarp) {
             // ---- MMA issue (all lanes walk, one issues)
             const uint32_t lead = elect_leader();
@@ -381,29 +405,47 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
                     if (__any_sync(0xffffffffu, row == -1) && lane == 0)
                         *reinterpret_cast<volatile int32_t *>(&bars.bad[p.n % kSlots]) = p.n + 1;
                     for (int half = 0; ok && half < 2; ++half) {  // K, then V
-                        const int s = (int)(n % kStages);
-                        if (n >= kStages &&
-                            !bar_wait_warp(&bars.empty[s], ((n / kStages) - 1) & 1u, wc.limit_ns)) {
-                            ok = false;
-                            break;
-                        }
-                        const bool edge = half == 1 && p.edge(t);
-                        uint64_t *bar = edge ? &bars.raw[s] : &bars.full[s];
-                        if (lane == 0) {
-                            mbar_arrive_expect_tx(bar, (uint32_t)__popc(go) * (uint32_t)box_rows * 256u);
-                            if (!edge) mbar_arrive_n(bar, kAuxWarps - 1);
-                        }
-                        used |= 1u << s;
-                        edge_last = edge ? edge_last | (1u << s) : edge_last & ~(1u << s);
-                        if (edge) raw_phase ^= 1u << s;
-                        ++n;
-                        __syncwarp();
-                        if (row >= 0) {
-                            const uint32_t dst =
-                                smem_u32(ring) + (uint32_t)s * kTileB + (uint32_t)(lane * box_rows) * 128;
-                            const CUtensorMap *map = half ? &mapV : &mapK;
-                            tma_box(dst, map, p.it.g * kD, (int)row, bar);
-                            tma_box(dst + kHalf, map, p.it.g * kD + 64, (int)row, bar);
+                        const CUtensorMap *map = half ? &mapV : &mapK;
+                        if constexpr (E8) {
+                            const int s = (int)(n & 1u);
+                            if (n >= 2 &&
+                                !bar_wait_warp(&bars.raw_empty[s], ((n >> 1) - 1) & 1u, wc.limit_ns)) {
+                                ok = false;
+                                break;
+                            }
+                            if (lane == 0)
+                                mbar_arrive_expect_tx(&bars.raw_full[s],
+                                                      (uint32_t)__popc(go) * (uint32_t)box_rows * 128u);
+                            ++n;
+                            __syncwarp();
+                            if (row >= 0)
+                                tma_box(smem_u32(raw_tiles) + (uint32_t)s * kRawTile +
+                                            (uint32_t)(lane * box_rows) * 128,
+                                        map, p.it.g * kD, (int)row, &bars.raw_full[s]);
+                        } else {
+                            const int s = (int)(n % kStages);
+                            if (n >= kStages &&
+                                !bar_wait_warp(&bars.empty[s], ((n / kStages) - 1) & 1u, wc.limit_ns)) {
+                                ok = false;
+                                break;
+                            }
+                            const bool edge = half == 1 && p.edge(t);
+                            uint64_t *bar = edge ? &bars.raw[s] : &bars.full[s];
+                            if (lane == 0) {
+                                mbar_arrive_expect_tx(bar, (uint32_t)__popc(go) * (uint32_t)box_rows * 256u);
+                                if (!edge) mbar_arrive_n(bar, kAuxWarps - 1);
+                            }
+                            used |= 1u << s;
+                            edge_last = edge ? edge_last | (1u << s) : edge_last & ~(1u << s);
+                            if (edge) raw_phase ^= 1u << s;
+                            ++n;
+                            __syncwarp();
+                            if (row >= 0) {
+                                const uint32_t dst =
+                                    smem_u32(ring) + (uint32_t)s * kTileB + (uint32_t)(lane * box_rows) * 128;
+                                tma_box(dst, map, p.it.g * kD, (int)row, bar);
+                                tma_box(dst + kHalf, map, p.it.g * kD + 64, (int)row, bar);
+                            }
                         }
                         if (half == 0 && t == p.tile0) {
                             // this part's queries, once the last part's logits are done with theirs
@@ -429,7 +471,11 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
             // every copy issued has landed before the CTA may leave (a stage's earlier copies
             // landed before it was used again)
             if (lane == 0) {
-                for (int s = 0; s < kStages; ++s) {
+                for (int s = 0; E8 && s < 2; ++s) {
+                    const uint32_t uses = (n + 1 - (uint32_t)s) >> 1;
+                    if (uses > 0 && !mbar_wait(&bars.raw_full[s], (uses - 1) & 1u)) ok = false;
+                }
+                for (int s = 0; !E8 && s < kStages; ++s) {
                     if (!((used >> s) & 1u)) continue;
                     // the last use of stage s: the largest i < n with i % kStages == s
                     const uint32_t i = n - 1 - ((n - 1 - (uint32_t)s) % kStages);
@@ -441,7 +487,92 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
                 for (int g = 0; g < 2; ++g)
                     if (nq[g] > 0 && !mbar_wait(&bars.q_full[g], (nq[g] - 1) & 1u)) ok = false;
             }
-        } else if (warp >= kAuxWarp) {
+        } else if (E8 && warp >= kAuxWarp) {
+            // ---- e4m3 cells to bf16: value = code * 2^e, exact.  The six warps take a raw tile
+            // 16 codes a lane at a time; the exponents of the next tile are on their way meanwhile
+            // (lane l of warps 0-3: cell 32 warp + l).  In V tiles with an edge, what not every
+            // row sees is treated as below.
+            const int aux = warp - kAuxWarp, at = aux * 32 + lane;
+            uint32_t n = 0;
+            auto load_exp = [&](int tile, bool is_v) -> uint32_t {
+                const int j = tile * kN + at;
+                if (at >= kN || tile >= p.tile1 || j >= p.n_see) return kExpBias;
+                const int64_t row = cell_row(kv, p.it.s, p.t0, j);
+                return row >= 0 ? (is_v ? kv.V_exp : kv.K_exp)[row * kv.H_kv + p.it.g] : kExpBias;
+            };
+            do {
+                uint32_t ex = load_exp(p.tile0, false);
+                for (int t = p.tile0; ok && t < p.tile1; ++t) {
+                    for (int half = 0; ok && half < 2; ++half, ++n) {
+                        const int s = (int)(n & 1u), st = (int)(n % kStages);
+                        if (at < kN) bars.exps[s][at] = (uint8_t)ex;
+                        bool here = bar_wait_warp(&bars.raw_full[s], (n >> 1) & 1u, wc.limit_ns);
+                        if (here && n >= kStages)
+                            here = bar_wait_warp(&bars.empty[st], ((n / kStages) - 1) & 1u, wc.limit_ns);
+                        // the exponents are there, and every warp is done with the other buffer's;
+                        // a wait that gave up ends all six warps' work
+                        uint32_t fail;
+                        asm volatile(
+                            "{\n\t.reg .pred p, c;\n\t"
+                            "setp.ne.u32 c, %1, 0;\n\t"
+                            "bar.red.or.pred p, %2, %3, c;\n\t"
+                            "selp.u32 %0, 1, 0, p;\n\t}"
+                            : "=r"(fail)
+                            : "r"((uint32_t)!here), "n"(kAuxBar), "n"(32 * Cfg<true>::kAuxWarps)
+                            : "memory");
+                        if (fail) {
+                            ok = false;
+                            break;
+                        }
+                        ex = load_exp(t + half, half == 0);
+                        const bool edge = half == 1 && p.edge(t);
+                        const int r0 = edge ? max(0, p.pos0 + 1 - t * kN) : kN, r1 = p.n_see - t * kN;
+                        const unsigned char *src = raw_tiles + (size_t)s * kRawTile;
+                        unsigned char *dst = ring + (size_t)st * kTileB;
+                        bool odd = false;
+#pragma unroll 2
+                        for (int i = at; i < kN * 8; i += 32 * kAuxWarps) {
+                            const int r = i >> 3, c = i & 7;
+                            uint4 v = *reinterpret_cast<const uint4 *>(src + i * 16);
+                            uint32_t *u = reinterpret_cast<uint32_t *>(&v);
+                            if (r >= r0) {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const uint32_t m = __vcmpeq4(u[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                    odd |= m != 0 && r < r1;
+                                    u[k] = r < r1 ? u[k] & ~m : 0u;
+                                }
+                            }
+                            const float f = two_to(min(max((int)bars.exps[s][r] - kExpBias, kExpMin), kExpMax));
+                            uint32_t o[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+                                    (__nv_fp8x2_storage_t)(u[k >> 1] >> (16 * (k & 1))), __NV_E4M3);
+                                const float2 x = __half22float2(__half2(h));
+                                o[k] = pack_bf16(x.x * f, x.y * f);
+                            }
+                            // chunks 2c, 2c + 1 of the row; lanes of the upper dim half in the
+                            // other order, as both halves lie on the same banks
+                            unsigned char *w = dst + (c >> 2) * kHalf + r * 128;
+                            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]);
+                            const uint4 hi = make_uint4(o[4], o[5], o[6], o[7]);
+                            const int first = 2 * (c & 3) + (c >> 2), second = first ^ 1;
+                            *reinterpret_cast<uint4 *>(w + ((first ^ (r & 7)) << 4)) = c >> 2 ? hi : lo;
+                            *reinterpret_cast<uint4 *>(w + ((second ^ (r & 7)) << 4)) = c >> 2 ? lo : hi;
+                        }
+                        if (odd) *reinterpret_cast<volatile int32_t *>(&bars.odd[p.n % kSlots]) = p.n + 1;
+                        // written by this warp (generic proxy), read by the tensor cores (async proxy)
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&bars.raw_empty[s]);
+                            mbar_arrive(&bars.full[st]);
+                        }
+                    }
+                }
+            } while (ok && p.next(kv, sv, ws));
+        } else if (!E8 && warp >= kAuxWarp) {
             // ---- V tiles in which some row does not see some cell: values of cells that no row
             // sees become zero (their weight is zero, but zero times an infinity is not), and so
             // do infinities and NaN of cells that only some rows see; the epilogue adds those
@@ -490,7 +621,8 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
         }
         __syncwarp();
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        if constexpr (E8) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
         // ---- softmax of group gi: row r by two threads, cells 64 hf .. 64 hf + 63 of each tile.
         // The two warps of a row stay in step (pair barriers): what one of them cannot wait for
         // any more, both give up.
@@ -641,12 +773,15 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
                         for (int j = max(p.pos0 + 1, p.tile0 * kN); j <= to; ++j) {
                             const int64_t row = cell_row(kv, p.it.s, p.t0, j);
                             if (row < 0) continue;
-                            const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(kv.V) +
-                                                     row * kv.ld_v + (int64_t)p.it.g * kD + 64 * hf + c;
+                            const int64_t v0 = row * kv.ld_v + (int64_t)p.it.g * kD + 64 * hf + c;
 #pragma unroll
                             for (int e = 0; e < 32; ++e) {
-                                const float f = __bfloat162float(v[e]);
-                                if (!isfinite(f)) o[e] += f;
+                                if constexpr (E8) {
+                                    if ((static_cast<const uint8_t *>(kv.V)[v0 + e] & 0x7f) == 0x7f) o[e] = NAN;
+                                } else {
+                                    const float f = __bfloat162float(static_cast<const __nv_bfloat16 *>(kv.V)[v0 + e]);
+                                    if (!isfinite(f)) o[e] += f;
+                                }
                             }
                         }
                     }
@@ -712,19 +847,21 @@ EncodeTiledFn encode_tiled()
     return fn;
 }
 
-// Rows of `width` bf16 values at a stride of ld: boxes of 64 values x box_rows rows in the
-// 128-byte swizzle, zeros behind the last row.
-bool make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t width, int64_t ld, int box_rows)
+// Rows of `width` values at a stride of ld.  bf16: boxes of 64 values x box_rows rows in the
+// 128-byte swizzle; e4m3: boxes of 128 codes x box_rows rows, row after row.  Zeros behind the last
+// row.
+bool make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t width, int64_t ld, int box_rows, bool e8)
 {
     const EncodeTiledFn fn = encode_tiled();
     if (!fn) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * (e8 ? 1 : 2)};
+    const cuuint32_t box[2] = {e8 ? 128u : 64u, (cuuint32_t)box_rows};
     const cuuint32_t estr[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return fn(m, e8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+              const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              e8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The queries [n_tok][H_q][128]: boxes of 64 values x G heads x as many tokens as fill a group.
@@ -748,9 +885,12 @@ constexpr int kMaxCtas = kTargetSMs;
 bool dense_tc_ok(const DenseArgs &a)
 {
     const int G = a.H_q / a.kv.H_kv;
-    // (the softmax takes its maximum over unscaled logits: a positive scale)
-    return a.d == kD && a.q_dtype == QSA_BF16 && a.kv_dtype == QSA_BF16 && G <= kM && a.scale > 0.0f &&
-           a.pool_rows > 0 && a.pool_rows <= 0x7fffffffLL;
+    // (a TMA map's strides are multiples of 16 bytes; the softmax takes its maximum over unscaled
+    // logits: a positive scale)
+    const bool cells = a.kv_dtype == QSA_BF16 ||
+                       (a.kv_dtype == QSA_E4M3 && a.kv.ld_k % 16 == 0 && a.kv.ld_v % 16 == 0);
+    return a.d == kD && a.q_dtype == QSA_BF16 && cells && G <= kM && a.scale > 0.0f && a.pool_rows > 0 &&
+           a.pool_rows <= 0x7fffffffLL;
 }
 
 size_t dense_tc_workspace()
@@ -758,7 +898,8 @@ size_t dense_tc_workspace()
     return kMaxCtas * sizeof(Split) + (size_t)2 * kMaxCtas * partial_floats(2 * kM, kD) * sizeof(float);
 }
 
-qsa_status launch_dense_tc(const DenseArgs &a, void *workspace, cudaStream_t st)
+template <bool E8>
+static qsa_status run_tc(const DenseArgs &a, void *workspace, cudaStream_t st)
 {
     const int G = a.H_q / a.kv.H_kv;
     const int page = 1 << a.kv.page_shift;
@@ -766,8 +907,8 @@ qsa_status launch_dense_tc(const DenseArgs &a, void *workspace, cudaStream_t st)
     CUtensorMap mq, mk, mv;
     const int64_t width = (int64_t)a.kv.H_kv * kD;
     if (!make_query_map(&mq, a.q, a.sv.n_tok, a.H_q, a.ld_q, G) ||
-        !make_map(&mk, a.kv.K, a.pool_rows, width, a.kv.ld_k, box_rows) ||
-        !make_map(&mv, a.kv.V, a.pool_rows, width, a.kv.ld_v, box_rows))
+        !make_map(&mk, a.kv.K, a.pool_rows, width, a.kv.ld_k, box_rows, E8) ||
+        !make_map(&mv, a.kv.V, a.pool_rows, width, a.kv.ld_v, box_rows, E8))
         return QSA_ERR_CUDA;
     WorkShape ws;
     ws.rt = 2 * (kM / G);
@@ -775,17 +916,23 @@ qsa_status launch_dense_tc(const DenseArgs &a, void *workspace, cudaStream_t st)
     ws.H_kv = a.kv.H_kv;
     ws.causal = a.causal;
     ws.over = kOver;
-    if (ensure_kernel_attrs<dense_tc_kernel>(tc_smem()) != cudaSuccess) return QSA_ERR_CUDA;
+    constexpr size_t smem = tc_smem<E8>();
+    if (ensure_kernel_attrs<dense_tc_kernel<E8>>(smem) != cudaSuccess) return QSA_ERR_CUDA;
     int ctas = device_sm_count();
     if (ctas > kMaxCtas) ctas = kMaxCtas;
     Split *splits = static_cast<Split *>(workspace);
     float *partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + kMaxCtas * sizeof(Split));
-    cudaError_t e = launch(dense_tc_kernel, dim3((unsigned)ctas), dim3(kThreads), tc_smem(), st, 1, mq, mk, mv,
-                           a.kv, a.sv, ws, box_rows, a.H_q, a.scale * kLog2e,
+    cudaError_t e = launch(dense_tc_kernel<E8>, dim3((unsigned)ctas), dim3(Cfg<E8>::kThreads), smem, st, 1, mq,
+                           mk, mv, a.kv, a.sv, ws, box_rows, a.H_q, a.scale * kLog2e,
                            static_cast<__nv_bfloat16 *>(a.out), a.lse, partial, splits, current_wait_ctl());
     if (e != cudaSuccess) return QSA_ERR_CUDA;
     e = launch_dense_join<__nv_bfloat16, 1>(splits, partial, ctas, 2 * kM, kM / G, a, st);
     return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
+}
+
+qsa_status launch_dense_tc(const DenseArgs &a, void *workspace, cudaStream_t st)
+{
+    return a.kv_dtype == QSA_E4M3 ? run_tc<true>(a, workspace, st) : run_tc<false>(a, workspace, st);
 }
 
 }  // namespace qsa
