@@ -403,6 +403,23 @@ class _PagedCacheStruct(ctypes.Structure):
                 ("page_size", _int)]
 
 
+# The calls below are made once per layer and step, many of them on tensors that take the GPU a few
+# microseconds: their checks are plain comparisons, and messages are made only when one fails.
+
+_torch = None
+_raw_stream_of = None
+
+
+def _use_torch():
+    """torch, imported on first use (this module itself loads without it)."""
+    global _torch, _raw_stream_of
+    import torch
+
+    _torch = torch
+    _raw_stream_of = torch._C._cuda_getCurrentRawStream
+    return torch
+
+
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
@@ -413,38 +430,53 @@ def _dp(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream(stream):
-    import torch
-
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
-
-
-def _need_i32(name, t, *shape):
-    """An int32 CUDA tensor with contiguous rows and at least the given shape (None: any)."""
-    import torch
-
-    ok = (t.dtype == torch.int32 and t.is_cuda and t.dim() == len(shape)
-          and all(w is None or n >= w for n, w in zip(t.shape, shape))
-          and (t.numel() <= 1 or t.stride(-1) == 1))
-    _need(ok, f"{name}: an int32 CUDA tensor of shape {shape} or more is wanted, "
-              f"got {t.dtype} {tuple(t.shape)}")
+def _raw_stream(stream, device):
+    """The stream's handle: `stream`, or the current stream of the current device, on which the
+    tensors must be."""
+    if stream is not None:
+        return stream.cuda_stream
+    here = _torch._C._cuda_getDevice()
+    if device.index != here:
+        raise ValueError(f"tensors on {device}, but the current device is cuda:{here}")
+    return _raw_stream_of(here)
 
 
-def _need_table(table, n_seq):
-    _need_i32("table", table, n_seq, None)
-    _need(table.is_contiguous(), "table: packed [n_seq][pages]")
+def _bad_i32(name, t, shape):
+    raise ValueError(f"{name}: a packed int32 CUDA tensor of shape {shape} or more is wanted, "
+                     f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _i32_vector(name, t, n):
+    """int32, on the GPU, contiguous, n entries or more; its address."""
+    if t.dtype is not _torch.int32 or not t.is_cuda or t.dim() != 1 or t.shape[0] < n or \
+            not t.is_contiguous():
+        _bad_i32(name, t, (n,))
+    return t.data_ptr()
+
+
+def _i32_table(t, n_seq):
+    if t.dtype is not _torch.int32 or not t.is_cuda or t.dim() != 2 or t.shape[0] < n_seq or \
+            not t.is_contiguous():
+        _bad_i32("table", t, (n_seq, "pages"))
+    return t.data_ptr()
 
 
 def _head_rows(name, t, H, d):
     """[n][H][d] (or [n][H*d]) rows whose heads are contiguous; the stride between rows."""
-    n = t.shape[0] if t.dim() > 1 else 0
-    width = t.shape[1] * t.shape[2] if t.dim() == 3 else (t.shape[1] if t.dim() == 2 else -1)
-    ok = t.is_cuda and width == H * d and (t.stride(-1) == 1 or n == 0)
-    if ok and t.dim() == 3:
-        ok = t.shape[2] == d and (H == 1 or t.stride(1) == d or n == 0)
-    _need(ok, f"{name}: a CUDA tensor of shape [n][{H}][{d}] with contiguous rows is wanted, "
-              f"got {tuple(t.shape)} with strides {tuple(t.stride())}")
-    return t.stride(0) if n > 1 else H * d
+    if t.is_cuda:
+        shape, stride = t.shape, t.stride()
+        if len(shape) == 3 and shape[1] == H and shape[2] == d:
+            if shape[0] == 0:
+                return H * d
+            if (stride[2] == 1 or d == 1) and (stride[1] == d or H == 1):
+                return stride[0] if shape[0] > 1 else H * d
+        elif len(shape) == 2 and shape[1] == H * d:
+            if shape[0] == 0:
+                return H * d
+            if stride[1] == 1:
+                return stride[0] if shape[0] > 1 else H * d
+    raise ValueError(f"{name}: a CUDA tensor of shape [n][{H}][{d}] with contiguous rows is wanted, "
+                     f"got {tuple(t.shape)} with strides {tuple(t.stride())} on {t.device}")
 
 
 class PagedCache:
@@ -453,8 +485,7 @@ class PagedCache:
     exponent bytes K_exp, V_exp [n_pages * page_size][H_kv] uint8.  Holds the tensors."""
 
     def __init__(self, K, V, page_size, K_exp=None, V_exp=None):
-        import torch
-
+        torch = _use_torch()
         if K.dim() == 4:
             K, V = K.flatten(0, 1), V.flatten(0, 1)
             if K_exp is not None:
@@ -483,18 +514,20 @@ class PagedCache:
 def paged_write(cache, table, cu_q, kv_len, k, v, stream=None):
     """qsa_paged_write: rows k, v [n_tok][H_kv][d] (float32 or bfloat16) of the new tokens into
     the pages of their sequences (table [n_seq][>= pages], cu_q [n_seq + 1], kv_len [n_seq])."""
-    n_seq = kv_len.shape[0]
-    _need_table(table, n_seq)
-    _need_i32("cu_q", cu_q, n_seq + 1)
-    _need_i32("kv_len", kv_len, None)
+    n_seq, n_tok = kv_len.shape[0], k.shape[0]
+    tb, cu, kl = (_i32_table(table, n_seq), _i32_vector("cu_q", cu_q, n_seq + 1),
+                  _i32_vector("kv_len", kv_len, 0))
     ld_k = _head_rows("k", k, cache.H_kv, cache.d)
     ld_v = _head_rows("v", v, cache.H_kv, cache.d)
-    _need(k.shape[0] == v.shape[0] and k.dtype == v.dtype, "k and v: one type and length")
-    if k.shape[0] == 0:
+    if v.shape[0] != n_tok or v.dtype is not k.dtype:
+        raise ValueError("k and v: one type and length")
+    if n_tok == 0:
         return  # an empty tensor has no address
-    _check("qsa_paged_write", load().qsa_paged_write(
-        cache._ref, _dp(table), table.shape[1], n_seq, _dp(cu_q), _dp(kv_len), _dp(k), _dp(v),
-        _dtype(k), k.shape[0], ld_k, ld_v, _raw_stream(stream)))
+    st = load().qsa_paged_write(
+        cache._ref, tb, table.shape[1], n_seq, cu, kl, k.data_ptr(), v.data_ptr(), _dtype(k), n_tok,
+        ld_k, ld_v, _raw_stream(stream, k.device))
+    if st:
+        raise QSAError("qsa_paged_write", st)
 
 
 def paged_read(cache, table, kv_len, n_cells, max_cells, K_out, V_out, pos=None, seq=None,
@@ -502,40 +535,35 @@ def paged_read(cache, table, kv_len, n_cells, max_cells, K_out, V_out, pos=None,
     """qsa_paged_read: the listed cells (pos [n_list][max_cells], or the first n_cells[i] of each
     sequence) as values, K_out / V_out [n_list][max_cells][H_kv][d] float32 or bfloat16."""
     n_seq, n_list = kv_len.shape[0], n_cells.shape[0]
-    _need_table(table, n_seq)
-    _need_i32("kv_len", kv_len, None)
-    _need_i32("n_cells", n_cells, None)
-    if pos is not None:
-        _need_i32("pos", pos, n_list, max_cells)
-        _need(pos.shape[1] == max_cells and pos.is_contiguous(), "pos: packed [n_list][max_cells]")
+    tb, kl, nc = (_i32_table(table, n_seq), _i32_vector("kv_len", kv_len, 0),
+                  _i32_vector("n_cells", n_cells, 0))
+    if pos is not None and (pos.dtype is not _torch.int32 or not pos.is_cuda or
+                            tuple(pos.shape) != (n_list, max_cells) or not pos.is_contiguous()):
+        _bad_i32("pos", pos, (n_list, max_cells))
     if seq is not None:
-        _need_i32("seq", seq, n_list)
-    else:
-        _need(n_list <= n_seq, "n_cells: one list per sequence unless seq is given")
+        _i32_vector("seq", seq, n_list)
+    elif n_list > n_seq:
+        raise ValueError("n_cells: one list per sequence unless seq is given")
     size = n_list * max_cells * cache.H_kv * cache.d
     for t in (K_out, V_out):
-        _need(t.is_cuda and t.is_contiguous() and t.numel() >= size,
-              "K_out and V_out: packed [n_list][max_cells][H_kv][d]")
-    _need(K_out.dtype == V_out.dtype, "K_out and V_out: one type")
+        if not t.is_cuda or not t.is_contiguous() or t.numel() < size or t.dtype is not K_out.dtype:
+            raise ValueError("K_out and V_out: packed [n_list][max_cells][H_kv][d] of one type")
     if size == 0:
         return
-    _check("qsa_paged_read", load().qsa_paged_read(
-        cache._ref, _dp(table), table.shape[1], n_seq, _dp(kv_len), _dp(seq), _dp(pos),
-        _dp(n_cells), n_list, max_cells, _dp(K_out), _dp(V_out), _dtype(K_out),
-        _raw_stream(stream)))
+    st = load().qsa_paged_read(
+        cache._ref, tb, table.shape[1], n_seq, kl, _dp(seq), _dp(pos), nc, n_list, max_cells,
+        K_out.data_ptr(), V_out.data_ptr(), _dtype(K_out), _raw_stream(stream, K_out.device))
+    if st:
+        raise QSAError("qsa_paged_read", st)
 
 
-def _attn_buffers(q, out, lse, H_q, d):
-    n_tok = q.shape[0]
-    ld_q = _head_rows("q", q, H_q, d)
-    _need(out.is_cuda and out.dtype == q.dtype and out.is_contiguous() and out.numel() == n_tok * H_q * d,
-          "out: packed, of q's type and shape")
-    if lse is not None:
-        import torch
-
-        _need(lse.is_cuda and lse.dtype == torch.float32 and lse.is_contiguous()
-              and lse.numel() == n_tok * H_q, "lse: packed float32 [n_tok][H_q]")
-    return n_tok, ld_q
+def _attn_outputs(q, out, lse, n_tok, H_q, d):
+    if out.dtype is not q.dtype or not out.is_cuda or not out.is_contiguous() or \
+            out.numel() != n_tok * H_q * d:
+        raise ValueError("out: packed, of q's type and shape")
+    if lse is not None and (lse.dtype is not _torch.float32 or not lse.is_cuda or
+                            not lse.is_contiguous() or lse.numel() != n_tok * H_q):
+        raise ValueError("lse: packed float32 [n_tok][H_q]")
 
 
 def paged_attn_workspace_size(n_tok, n_seq, max_q, H_q, H_kv, d) -> int:
@@ -547,19 +575,21 @@ def paged_attn(cache, table, cu_q, kv_len, q, out, scale, max_q, causal=True, ls
     """qsa_paged_attn: q [n_tok][H_q][d] (float32 or bfloat16) of the new tokens over the cells
     of their sequences; out like q, lse [n_tok][H_q] float32.  workspace:
     paged_attn_workspace_size() bytes of device memory."""
-    n_seq = kv_len.shape[0]
-    H_q = q.shape[1] if q.dim() == 3 else q.shape[-1] // cache.d
-    _need_table(table, n_seq)
-    _need_i32("cu_q", cu_q, n_seq + 1)
-    _need_i32("kv_len", kv_len, None)
-    n_tok, ld_q = _attn_buffers(q, out, lse, H_q, cache.d)
+    n_seq, n_tok, d = kv_len.shape[0], q.shape[0], cache.d
+    H_q = q.shape[1] if q.dim() == 3 else q.shape[-1] // d
+    tb, cu, kl = (_i32_table(table, n_seq), _i32_vector("cu_q", cu_q, n_seq + 1),
+                  _i32_vector("kv_len", kv_len, 0))
+    ld_q = _head_rows("q", q, H_q, d)
+    _attn_outputs(q, out, lse, n_tok, H_q, d)
     if n_tok == 0:
         return
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check("qsa_paged_attn", load().qsa_paged_attn(
-        cache._ref, _dp(table), table.shape[1], n_seq, _dp(cu_q), _dp(kv_len), _dp(q),
-        _dtype(q), n_tok, max_q, ld_q, H_q, scale, int(bool(causal)), _dp(out), _dp(lse),
-        _dp(workspace), ws_bytes, _raw_stream(stream)))
+    st = load().qsa_paged_attn(
+        cache._ref, tb, table.shape[1], n_seq, cu, kl, q.data_ptr(), _dtype(q), n_tok, max_q, ld_q,
+        H_q, scale, 1 if causal else 0, out.data_ptr(), _dp(lse), _dp(workspace), ws_bytes,
+        _raw_stream(stream, q.device))
+    if st:
+        raise QSAError("qsa_paged_attn", st)
 
 
 def prompt_attn_workspace_size(n_tok, n_seq, H_q, H_kv, d) -> int:
@@ -570,54 +600,70 @@ def prompt_attn(q, k, v, cu_seq, out, scale, causal=True, lse=None, workspace=No
     """qsa_prompt_attn: packed prompts q [n_tok][H_q][d], k, v [n_tok][H_kv][d] (float32 or
     bfloat16), sequence s at tokens cu_seq[s] .. cu_seq[s+1] - 1; out like q, lse [n_tok][H_q]
     float32.  workspace: prompt_attn_workspace_size() bytes of device memory."""
-    _need(q.dim() == 3 and k.dim() == 3 and v.dim() == 3, "q, k, v: [n_tok][heads][d]")
-    H_q, H_kv, d = q.shape[1], k.shape[1], q.shape[2]
-    _need_i32("cu_seq", cu_seq, 1)
-    n_tok, ld_q = _attn_buffers(q, out, lse, H_q, d)
-    ld_k, ld_v = _head_rows("k", k, H_kv, d), _head_rows("v", v, H_kv, d)
-    _need(k.shape[0] == n_tok and v.shape[0] == n_tok and k.dtype == q.dtype == v.dtype,
-          "q, k, v: one type and length")
+    if _torch is None:
+        _use_torch()
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k, v: [n_tok][heads][d]")
+    n_tok, H_q, d = q.shape
+    H_kv = k.shape[1]
+    cu = _i32_vector("cu_seq", cu_seq, 1)
+    ld_q, ld_k, ld_v = (_head_rows("q", q, H_q, d), _head_rows("k", k, H_kv, d),
+                        _head_rows("v", v, H_kv, d))
+    if k.shape[0] != n_tok or v.shape[0] != n_tok or k.dtype is not q.dtype or v.dtype is not q.dtype:
+        raise ValueError("q, k, v: one type and length")
+    _attn_outputs(q, out, lse, n_tok, H_q, d)
     if n_tok == 0:
         return
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check("qsa_prompt_attn", load().qsa_prompt_attn(
-        _dp(q), _dp(k), _dp(v), _dtype(q), n_tok, ld_q, ld_k, ld_v, _dp(cu_seq),
-        cu_seq.shape[0] - 1, H_q, H_kv, d, scale, int(bool(causal)), _dp(out), _dp(lse),
-        _dp(workspace), ws_bytes, _raw_stream(stream)))
+    st = load().qsa_prompt_attn(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype(q), n_tok, ld_q, ld_k, ld_v, cu,
+        cu_seq.shape[0] - 1, H_q, H_kv, d, scale, 1 if causal else 0, out.data_ptr(), _dp(lse),
+        _dp(workspace), ws_bytes, _raw_stream(stream, q.device))
+    if st:
+        raise QSAError("qsa_prompt_attn", st)
+
+
+def _prob_rows(name, t, n_seq, n, vocab):
+    """float32 [n_seq][n][vocab] with every row at one stride from the one before; the stride."""
+    if t.dtype is _torch.float32 and t.is_cuda and tuple(t.shape) == (n_seq, n, vocab):
+        if n == 0 or n_seq == 0:
+            return vocab
+        s = t.stride()
+        ld = s[1] if n > 1 else (s[0] if n_seq > 1 else vocab)
+        if (s[2] == 1 or vocab == 1) and (n_seq == 1 or s[0] == n * ld):
+            return ld
+    raise ValueError(f"{name}: float32 [{n_seq}][{n}][{vocab}] on the GPU with contiguous rows at one "
+                     f"stride is wanted, got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+
+
+def _packed(name, t, dtype, shape):
+    if t.dtype is not dtype or not t.is_cuda or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: packed {dtype} {shape} on the GPU")
+    return t.data_ptr()
 
 
 def draft_verify(target, draft, tokens, u, tokens_out, n_accepted, n_draft=None, stream=None):
     """qsa_draft_verify: target [n_seq][max_draft + 1][vocab] and draft [n_seq][max_draft][vocab]
     (or None) fp32 probabilities, tokens [n_seq][max_draft] and n_draft [n_seq] int32, u
     [n_seq][max_draft + 1] fp32; tokens_out [n_seq][max_draft + 1] and n_accepted [n_seq] int32."""
-    import torch
-
-    _need(target.dim() == 3, "target: [n_seq][max_draft + 1][vocab]")
+    if _torch is None:
+        _use_torch()
+    if target.dim() != 3 or target.shape[1] < 1:
+        raise ValueError("target: [n_seq][max_draft + 1][vocab]")
     n_seq, n_rows, vocab = target.shape
     max_draft = n_rows - 1
-    _need(max_draft >= 0, "target: [n_seq][max_draft + 1][vocab]")
-
-    def rows(name, t, n):
-        _need(t.is_cuda and t.dtype == torch.float32 and tuple(t.shape) == (n_seq, n, vocab)
-              and (t.stride(2) == 1 or vocab == 1 or t.numel() == 0),
-              f"{name}: float32 [{n_seq}][{n}][{vocab}] with contiguous rows")
-        if n == 0 or n_seq == 0:
-            return vocab
-        ld = t.stride(1) if n > 1 else (t.stride(0) if n_seq > 1 else vocab)
-        _need(n_seq == 1 or t.stride(0) == n * ld, f"{name}: rows at one stride")
-        return ld
-
-    ld_t = rows("target", target, n_rows)
-    ld_d = rows("draft", draft, max_draft) if draft is not None else 0
-    for name, t, shape in (("tokens", tokens, (n_seq, max_draft)),
-                           ("tokens_out", tokens_out, (n_seq, n_rows)),
-                           ("n_accepted", n_accepted, (n_seq,))):
-        _need(t.is_cuda and t.dtype == torch.int32 and tuple(t.shape) == shape
-              and t.is_contiguous(), f"{name}: packed int32 {shape}")
-    if n_draft is not None:
-        _need_i32("n_draft", n_draft, n_seq)
-    _need(u.is_cuda and u.dtype == torch.float32 and tuple(u.shape) == (n_seq, n_rows)
-          and u.is_contiguous(), f"u: packed float32 ({n_seq}, {n_rows})")
-    _check("qsa_draft_verify", load().qsa_draft_verify(
-        _dp(target), ld_t, _dp(draft), ld_d, _dp(tokens), _dp(n_draft), _dp(u), n_seq, max_draft,
-        vocab, _dp(tokens_out), _dp(n_accepted), _raw_stream(stream)))
+    i32, f32 = _torch.int32, _torch.float32
+    ld_t = _prob_rows("target", target, n_seq, n_rows, vocab)
+    ld_d = 0 if draft is None else _prob_rows("draft", draft, n_seq, max_draft, vocab)
+    tk, to, na, uu = (_packed("tokens", tokens, i32, (n_seq, max_draft)),
+                      _packed("tokens_out", tokens_out, i32, (n_seq, n_rows)),
+                      _packed("n_accepted", n_accepted, i32, (n_seq,)),
+                      _packed("u", u, f32, (n_seq, n_rows)))
+    nd = None if n_draft is None else _i32_vector("n_draft", n_draft, n_seq)
+    if n_seq == 0:
+        return
+    st = load().qsa_draft_verify(
+        target.data_ptr(), ld_t, _dp(draft), ld_d, tk, nd, uu, n_seq, max_draft, vocab, to, na,
+        _raw_stream(stream, target.device))
+    if st:
+        raise QSAError("qsa_draft_verify", st)

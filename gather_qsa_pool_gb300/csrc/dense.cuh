@@ -134,9 +134,16 @@ __device__ __forceinline__ int item_tiles(const WorkShape &w, int len, int cells
     return n > 0 ? (n + w.kt - 1) / w.kt : 1;
 }
 
+// a / b, b > 0, with one 32-bit division where that is enough.
+__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b)
+{
+    if (((uint64_t)a | (uint64_t)b) >> 32 == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
+}
+
 __device__ __forceinline__ int64_t floor_div(int64_t a, int64_t b)
 {
-    return a >= 0 ? a / b : -((-a + b - 1) / b);
+    return a >= 0 ? div_pos(a, b) : -div_pos(-a + b - 1, b);
 }
 
 // Tiles of the row tiles before t (t <= the last row tile) of one KV head of a sequence.  A row
@@ -147,7 +154,7 @@ __device__ __forceinline__ int64_t tiles_before(const WorkShape &w, int len, int
 {
     if (!w.causal || w.kt == 0) return (int64_t)t * item_tiles(w, len, cells, 0);
     const int64_t base = (int64_t)cells - len;
-    int64_t i0 = base < 0 ? -base / w.rt : 0;  // row tiles that see nothing
+    int64_t i0 = base < 0 ? div_pos(-base, w.rt) : 0;  // row tiles that see nothing
     if (i0 > t) i0 = t;
     const int64_t B = base + w.rt - 1;
     int64_t sum = t;
@@ -157,7 +164,7 @@ __device__ __forceinline__ int64_t tiles_before(const WorkShape &w, int len, int
     } else if (w.kt % w.rt == 0) {
         const int64_t r = w.kt / w.rt, v0 = floor_div(B, w.rt);
         // F(n) = sum of floor(v / r) over 0 <= v < n
-        const int64_t n1 = v0 + t, n0 = v0 + i0, q1 = n1 / r, q0 = n0 / r;
+        const int64_t n1 = v0 + t, n0 = v0 + i0, q1 = div_pos(n1, r), q0 = div_pos(n0, r);
         if (t > i0)
             sum += (r * (q1 * (q1 - 1) / 2) + q1 * (n1 - q1 * r)) -
                    (r * (q0 * (q0 - 1) / 2) + q0 * (n0 - q0 * r));
@@ -179,75 +186,106 @@ __device__ __forceinline__ int64_t seq_places(const WorkShape &w, int len, int c
 
 struct WorkItem {
     int32_t s, g, t;        // sequence, KV head, row tile
-    int64_t start;          // its first place in the list; its tiles begin `over` places on
     int32_t tiles;
+    int64_t start;          // its first place in the list; its tiles begin `over` places on
+    int64_t index;          // its number
 };
 
-// Total places of the list; all 32 lanes call it and get the same value.
-__device__ __forceinline__ int64_t work_total(const SeqView &sv, const WorkShape &w)
+// Places and items of one sequence.
+__device__ __forceinline__ void seq_work(const SeqView &sv, const WorkShape &w, int s, int64_t &places,
+                                         int64_t &items, int &len, int &cells)
 {
-    const int lane = threadIdx.x & 31;
-    int64_t sum = 0;
-    for (int s = lane; s < sv.n_seq; s += 32) {
-        int64_t t0;
-        int len;
-        seq_tokens(sv, s, t0, len);
-        sum += seq_places(w, len, seq_cells(sv, s, len));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    return sum * w.H_kv;
+    places = items = 0;
+    len = cells = 0;
+    if (s >= sv.n_seq) return;
+    int64_t t0;
+    seq_tokens(sv, s, t0, len);
+    cells = seq_cells(sv, s, len);
+    places = seq_places(w, len, cells) * w.H_kv;
+    items = (int64_t)((len + w.rt - 1) / w.rt) * w.H_kv;
 }
 
-// The item that holds place x of the list (0 <= x < work_total); all 32 lanes call it.
-__device__ __forceinline__ WorkItem work_find(const SeqView &sv, const WorkShape &w, int64_t x)
+__device__ __forceinline__ int64_t warp_sum_i64(int64_t v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// The item that holds place x of the list, among 32 sequences from s0 on whose lanes have their
+// work (base, items before them: of the sequences before s0); false if it lies behind them.
+__device__ __forceinline__ bool work_among(const WorkShape &w, int64_t x, int s0, int64_t mine, int64_t items,
+                                           int len, int cells, int64_t &base, int64_t &before, WorkItem &it)
 {
     const int lane = threadIdx.x & 31;
-    int64_t base = 0;
-    WorkItem it = {0, 0, 0, 0, 1};
-    for (int s0 = 0; s0 < sv.n_seq; s0 += 32) {
-        const int s = s0 + lane;
-        int64_t mine = 0;
-        int len = 0, cells = 0;
-        if (s < sv.n_seq) {
-            int64_t t0;
-            seq_tokens(sv, s, t0, len);
-            cells = seq_cells(sv, s, len);
-            mine = seq_places(w, len, cells) * w.H_kv;
-        }
-        int64_t incl = mine;
+    int64_t incl = mine, inc_items = items;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o), u = __shfl_up_sync(0xffffffffu, inc_items, o);
+        if (lane >= o) {
+            incl += v;
+            inc_items += u;
         }
-        const bool in = x < base + incl;
-        const uint32_t hit = __ballot_sync(0xffffffffu, in);
-        if (hit) {
-            const int j = __ffs(hit) - 1;  // the first lane whose prefix passes x
-            const int64_t sbase = base + __shfl_sync(0xffffffffu, incl - mine, j);
-            const int64_t stot = __shfl_sync(0xffffffffu, mine, j);
-            len = __shfl_sync(0xffffffffu, len, j);
-            cells = __shfl_sync(0xffffffffu, cells, j);
-            const int64_t per_head = stot / w.H_kv;
-            it.s = s0 + j;
-            it.g = (int32_t)((x - sbase) / per_head);
-            const int64_t at = sbase + it.g * per_head;
-            // the last row tile that does not begin behind x
-            int t = 0, hi = (len + w.rt - 1) / w.rt;
-            while (hi - t > 1) {
-                const int mid = (t + hi) >> 1;
-                if (tiles_before(w, len, cells, mid) + (int64_t)mid * w.over <= x - at) t = mid;
-                else hi = mid;
-            }
-            it.t = t;
-            it.start = at + tiles_before(w, len, cells, t) + (int64_t)t * w.over;
-            it.tiles = item_tiles(w, len, cells, t);
-            return it;
-        }
-        base += __shfl_sync(0xffffffffu, incl, 31);
     }
-    return it;
+    const uint32_t hit = __ballot_sync(0xffffffffu, x < base + incl);
+    if (!hit) {
+        base += __shfl_sync(0xffffffffu, incl, 31);
+        before += __shfl_sync(0xffffffffu, inc_items, 31);
+        return false;
+    }
+    const int j = __ffs(hit) - 1;  // the first lane whose prefix passes x
+    const int64_t sbase = base + __shfl_sync(0xffffffffu, incl - mine, j);
+    const int64_t stot = __shfl_sync(0xffffffffu, mine, j);
+    const int64_t first_item = before + __shfl_sync(0xffffffffu, inc_items - items, j);
+    len = __shfl_sync(0xffffffffu, len, j);
+    cells = __shfl_sync(0xffffffffu, cells, j);
+    const int64_t per_head = div_pos(stot, w.H_kv);
+    it.s = s0 + j;
+    it.g = (int32_t)div_pos(x - sbase, per_head);
+    const int64_t at = sbase + it.g * per_head;
+    // the last row tile that does not begin behind x
+    const int nt = (len + w.rt - 1) / w.rt;
+    int t = 0, hi = nt;
+    while (hi - t > 1) {
+        const int mid = (t + hi) >> 1;
+        if (tiles_before(w, len, cells, mid) + (int64_t)mid * w.over <= x - at) t = mid;
+        else hi = mid;
+    }
+    it.t = t;
+    it.start = t == 0 ? at : at + tiles_before(w, len, cells, t) + (int64_t)t * w.over;
+    it.tiles = item_tiles(w, len, cells, t);
+    it.index = first_item + (int64_t)it.g * nt + t;
+    return true;
+}
+
+// The share of CTA `cta` of `ctas`: places [x0, x1) of the list, and the item at x0.  False when
+// there is none.  All 32 lanes of a warp call it and get the same values.
+__device__ __forceinline__ bool work_share(const SeqView &sv, const WorkShape &w, int cta, int ctas, int64_t &per,
+                                           int64_t &x0, int64_t &x1, WorkItem &it)
+{
+    const int lane = threadIdx.x & 31;
+    int64_t mine, items, total;
+    int len, cells;
+    seq_work(sv, w, lane, mine, items, len, cells);
+    total = mine;
+    for (int s = 32 + lane; s < sv.n_seq; s += 32) {
+        int64_t m, i;
+        int l, c;
+        seq_work(sv, w, s, m, i, l, c);
+        total += m;
+    }
+    total = warp_sum_i64(total);
+    per = div_pos(total + ctas - 1, ctas);
+    x0 = cta * per;
+    x1 = x0 + per < total ? x0 + per : total;
+    if (x0 >= x1) return false;
+    int64_t base = 0, before = 0;
+    if (work_among(w, x0, 0, mine, items, len, cells, base, before, it)) return true;
+    for (int s0 = 32; s0 < sv.n_seq; s0 += 32) {
+        seq_work(sv, w, s0 + lane, mine, items, len, cells);
+        if (work_among(w, x0, s0, mine, items, len, cells, base, before, it)) return true;
+    }
+    return false;
 }
 
 // The item after `it` in the list (its sequence's length and cells are looked up again).
@@ -260,6 +298,7 @@ __device__ __forceinline__ bool work_next(const SeqView &sv, const WorkShape &w,
     int cells = seq_cells(sv, it.s, len);
     const int nt = (len + w.rt - 1) / w.rt;
     it.start += it.tiles + w.over;
+    ++it.index;
     if (++it.t >= nt) {
         it.t = 0;
         if (++it.g >= w.H_kv) {

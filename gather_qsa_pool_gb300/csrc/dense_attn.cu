@@ -61,8 +61,10 @@ dense_attn_kernel(KvView kv, SeqView sv, WorkShape ws, const TQ *__restrict__ q,
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = H_q / kv.H_kv;
     if (warp == 0) {
-        WorkItem it = {-1, 0, 0, 0, 0};
-        if ((int64_t)blockIdx.x < work_total(sv, ws)) it = work_find(sv, ws, blockIdx.x);
+        // one place per item, one item per CTA
+        WorkItem it;
+        int64_t per, x0, x1;
+        if (!work_share(sv, ws, blockIdx.x, gridDim.x, per, x0, x1, it)) it.s = -1;
         if (lane == 0) {
             item_s = it;
             bad_s = 0;

@@ -239,7 +239,7 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
                 const __grid_constant__ CUtensorMap mapV, const KvView kv, const SeqView sv,
                 const WorkShape ws, int box_rows, int H_q, float scale_log2,
                 __nv_bfloat16 *__restrict__ out, float *__restrict__ lse, float *__restrict__ partial, Split *__restrict__ splits,
-                const WaitCtl wc)
+                int by_item, const WaitCtl wc)
 {
     constexpr int kStages = Cfg<E8>::kStages, kAuxWarps = Cfg<E8>::kAuxWarps;
     extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -276,14 +276,10 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
     pdl_trigger();
 
     Parts p;
-    const int64_t total = work_total(sv, ws);
-    const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-    p.x = (int64_t)blockIdx.x * per;
-    p.x1 = p.x + per < total ? p.x + per : total;
+    int64_t per;
     p.n = 0;
-    if (tid == 0) splits[blockIdx.x].s = -1;
-    if (p.x >= p.x1) return;
-    p.it = work_find(sv, ws, p.x);
+    if (!by_item && tid == 0) splits[blockIdx.x].s = -1;
+    if (!work_share(sv, ws, blockIdx.x, gridDim.x, per, p.x, p.x1, p.it)) return;
     p.set(kv, sv, ws);
     if (p.tile1 <= p.tile0) {  // only places without a tile
         --p.n;
@@ -810,11 +806,9 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
                 }
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             }
-            if (starts && !ends && tid == 0) {
-                const int64_t c1 = (p.it.start + ws.over + p.it.tiles - 1) / per;
-                Split sp = {p.it.s, p.it.g, p.it.t, (int32_t)(c1 - blockIdx.x) + 1};
-                splits[blockIdx.x] = sp;
-            }
+            if (starts && tid == 0)
+                note_split(splits, by_item, p.it, ends,
+                           div_pos(p.it.start + ws.over + p.it.tiles - 1, per));
         } while (p.next(kv, sv, ws));
     }
 
@@ -924,9 +918,10 @@ static qsa_status run_tc(const DenseArgs &a, void *workspace, cudaStream_t st)
     float *partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + kMaxCtas * sizeof(Split));
     cudaError_t e = launch(dense_tc_kernel<E8>, dim3((unsigned)ctas), dim3(Cfg<E8>::kThreads), smem, st, 1, mq,
                            mk, mv, a.kv, a.sv, ws, box_rows, a.H_q, a.scale * kLog2e,
-                           static_cast<__nv_bfloat16 *>(a.out), a.lse, partial, splits, current_wait_ctl());
+                           static_cast<__nv_bfloat16 *>(a.out), a.lse, partial, splits, (int)join_by_item(a, ws.rt, ctas),
+                           current_wait_ctl());
     if (e != cudaSuccess) return QSA_ERR_CUDA;
-    e = launch_dense_join<__nv_bfloat16, 1>(splits, partial, ctas, 2 * kM, kM / G, a, st);
+    e = launch_dense_join<__nv_bfloat16>(splits, partial, ctas, 2 * kM, kM / G, a, st);
     return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
 }
 

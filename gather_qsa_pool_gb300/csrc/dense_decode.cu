@@ -168,7 +168,8 @@ template <bool E8, int MT, typename TQ, int NT>
 __global__ void __launch_bounds__(kThreads, 2)
 dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const TQ *__restrict__ q,
                     int64_t ld_q, int H_q, float scale_log2, TQ *__restrict__ out,
-                    float *__restrict__ lse, float *__restrict__ partial, Split *__restrict__ splits)
+                    float *__restrict__ lse, float *__restrict__ partial, Split *__restrict__ splits,
+                    int by_item)
 {
     using S = Shape<E8>;
     constexpr int kRows = 16 * MT;
@@ -189,15 +190,11 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
     QSA_AFTER_WAIT(qp);
     pdl_trigger();
 
-    const int64_t total = work_total(sv, ws);
-    const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-    const int64_t x0 = (int64_t)blockIdx.x * per;
-    const int64_t x1 = x0 + per < total ? x0 + per : total;
-    if (tid == 0) splits[blockIdx.x].s = -1;
-    if (x0 >= x1) return;
+    int64_t per, x, x1;
+    WorkItem it;
     const int G = H_q / kv.H_kv;
-    WorkItem it = work_find(sv, ws, x0);
-    int64_t x = x0;
+    if (!by_item && tid == 0) splits[blockIdx.x].s = -1;
+    if (!work_share(sv, ws, blockIdx.x, gridDim.x, per, x, x1, it)) return;
     for (;;) {
         const int64_t item_end = it.start + it.tiles;
         const int tile0 = (int)(x - it.start);
@@ -666,11 +663,7 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
                 }
             }
         }
-        if (starts && !ends && tid == 0) {
-            const int64_t c1 = (item_end - 1) / per;  // the CTA of the item's last tile
-            Split sp = {it.s, it.g, it.t, (int32_t)(c1 - blockIdx.x) + 1};
-            splits[blockIdx.x] = sp;
-        }
+        if (starts && tid == 0) note_split(splits, by_item, it, ends, div_pos(item_end - 1, per));
         x = it.start + tile1;
         if (x >= x1) break;
         if (!work_next(sv, ws, it)) break;
@@ -703,9 +696,9 @@ cudaError_t run(const DenseArgs &a, void *workspace, cudaStream_t st)
     float *partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + kMaxCtas * sizeof(Split));
     e = launch(dense_decode_kernel<E8, MT, TQ, NT>, dim3((unsigned)ctas), dim3(kThreads), smem, st, 1, a.kv,
                a.sv, ws, static_cast<const TQ *>(a.q), a.ld_q, a.H_q, a.scale * kLog2e,
-               static_cast<TQ *>(a.out), a.lse, partial, splits);
+               static_cast<TQ *>(a.out), a.lse, partial, splits, (int)join_by_item(a, ws.rt, ctas));
     if (e != cudaSuccess) return e;
-    return launch_dense_join<TQ, 8>(splits, partial, ctas, 16 * MT, ws.rt, a, st);
+    return launch_dense_join<TQ>(splits, partial, ctas, 16 * MT, ws.rt, a, st);
 }
 
 }  // namespace

@@ -9,12 +9,30 @@
 
 namespace qsa {
 
-// An item cut into parts, at the CTA where it begins: its parts are that CTA's second record and
-// the first records of the CTAs after it.
+// An item cut into parts: they are the second record of the CTA where it begins and the first
+// records of the CTAs after it.
 struct Split {
-    int32_t s, g, t;   // sequence (below 0: no item), KV head, row tile
+    int32_t s, g, t;   // sequence (below 0: not cut), KV head, row tile
+    int32_t cta;       // where it begins
     int32_t parts;
+    int32_t pad[3];
 };
+
+// A split's place in the list: the item's number while there are no more items than CTAs (few items
+// in many parts: the joining kernel then has work for every CTA it launches), else the CTA where it
+// begins (a CTA begins at most one item that it does not end).
+inline bool join_by_item(const DenseArgs &a, int rt, int ctas)
+{
+    return ((a.sv.n_tok + rt - 1) / rt + a.sv.n_seq) * a.kv.H_kv <= ctas;
+}
+
+// Called once for each item, by the CTA where it begins.
+__device__ __forceinline__ void note_split(Split *splits, int by_item, const WorkItem &it, bool whole, int64_t last_cta)
+{
+    if (whole && !by_item) return;  // (a CTA's entry was cleared at its start)
+    Split sp = {whole ? -1 : it.s, it.g, it.t, (int32_t)blockIdx.x, (int32_t)(last_cta - blockIdx.x) + 1, {0, 0, 0}};
+    splits[by_item ? it.index : (int64_t)blockIdx.x] = sp;
+}
 
 // One warp per part and row: kParts warps take every kParts-th part of a row (many parts: a long
 // context's few rows), 8 / kParts rows at a time.  A record's rows lie in groups of 128, `group`
@@ -22,7 +40,7 @@ struct Split {
 template <typename TQ, int kParts>
 __global__ void __launch_bounds__(256)
 dense_join_kernel(const Split *__restrict__ splits, const float *__restrict__ partial, int rows_max,
-                  const SeqView sv, int rt, int group, int G, int H_q, TQ *__restrict__ out,
+                  const SeqView sv, int rt, int group, int H_kv, int G, int by_item, TQ *__restrict__ out,
                   float *__restrict__ lse)
 {
     constexpr int kD = 128, kRows = 8 / kParts;
@@ -32,10 +50,22 @@ dense_join_kernel(const Split *__restrict__ splits, const float *__restrict__ pa
     QSA_AFTER_WAIT(splits);
     QSA_AFTER_WAIT(partial);
     pdl_trigger();
-    const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int part = warp % kParts;
-    const Split sp = splits[c];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int part = warp % kParts, H_q = H_kv * G;
+    if (by_item) {
+        // fewer items than the host could tell have no entry
+        int64_t items = 0;
+        for (int s = lane; s < sv.n_seq; s += 32) {
+            int64_t t0;
+            int len;
+            seq_tokens(sv, s, t0, len);
+            items += (len + rt - 1) / rt;
+        }
+        if ((int64_t)blockIdx.x >= warp_sum_i64(items) * H_kv) return;
+    }
+    const Split sp = splits[blockIdx.x];
     if (sp.s < 0) return;
+    const int c = sp.cta;
     int64_t t0;
     int len;
     seq_tokens(sv, sp.s, t0, len);
@@ -99,17 +129,29 @@ dense_join_kernel(const Split *__restrict__ splits, const float *__restrict__ pa
     if (lane == 0 && lse) lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-// ctas: CTAs of the attention kernel; group: tokens of a record's 128 rows (of all its rows where
-// it has fewer).
 template <typename TQ, int kParts>
-cudaError_t launch_dense_join(const Split *splits, const float *partial, int ctas, int rows_max, int group,
-                              const DenseArgs &a, cudaStream_t st)
+cudaError_t launch_join(const Split *splits, const float *partial, int entries, int by_item, int rows_max, int group,
+                        const DenseArgs &a, cudaStream_t st)
 {
     const int G = a.H_q / a.kv.H_kv, rt = rows_max > 128 ? 2 * group : group;
     constexpr int kRows = 8 / kParts;
-    return launch(dense_join_kernel<TQ, kParts>, dim3((unsigned)ctas, (unsigned)((rows_max + kRows - 1) / kRows)),
-                  dim3(256), 0, st, 1, splits, partial, rows_max, a.sv, rt, group, G, a.H_q,
-                  static_cast<TQ *>(a.out), a.lse);
+    return launch(dense_join_kernel<TQ, kParts>,
+                  dim3((unsigned)entries, (unsigned)((rows_max + kRows - 1) / kRows)), dim3(256), 0, st, 1, splits,
+                  partial, rows_max, a.sv, rt, group, a.kv.H_kv, G, by_item, static_cast<TQ *>(a.out), a.lse);
+}
+
+// ctas: CTAs of the attention kernel; group: tokens of a record's 128 rows (of all its rows where
+// it has fewer).  As many warps on a row as the items have parts, about.
+template <typename TQ>
+cudaError_t launch_dense_join(const Split *splits, const float *partial, int ctas, int rows_max, int group,
+                              const DenseArgs &a, cudaStream_t st)
+{
+    const int rt = rows_max > 128 ? 2 * group : group;
+    if (!join_by_item(a, rt, ctas)) return launch_join<TQ, 1>(splits, partial, ctas, 0, rows_max, group, a, st);
+    const int items = (int)(((a.sv.n_tok + rt - 1) / rt + a.sv.n_seq) * a.kv.H_kv);
+    if (items * 12 <= ctas) return launch_join<TQ, 8>(splits, partial, items, 1, rows_max, group, a, st);
+    if (items * 3 <= ctas) return launch_join<TQ, 2>(splits, partial, items, 1, rows_max, group, a, st);
+    return launch_join<TQ, 1>(splits, partial, items, 1, rows_max, group, a, st);
 }
 
 }  // namespace qsa

@@ -59,21 +59,155 @@ __device__ __forceinline__ double warp_sum_f64(double v)
 }
 
 struct Row {
-    const float *p, *q;  // q == NULL: no draft row
+    const float *p, *q;  // q == NULL: the plain weights p
     int skip;            // index whose weight is 0 (the refused token of a draft without rows)
+    __device__ __forceinline__ void weight(float pv, float qv, int64_t i, float &d, float &e) const
+    {
+        if (q) {
+            weight_of(pv, qv, d, e);
+        } else {
+            d = pv > 0.0f && i != skip ? pv : 0.0f;
+            e = 0.0f;
+        }
+    }
 };
 
-__device__ __forceinline__ void row_weight(const Row &r, int64_t i, int64_t vocab, bool difference,
-                                           float &d, float &e)
+// Sum of the warp's chunks [c0, c1) of the row's weights; every lane gets it.
+__device__ __forceinline__ double slice_sum(const Row &row, int64_t c0, int64_t c1, int64_t vocab, bool vec)
 {
-    d = e = 0.0f;
-    if (i >= vocab) return;
-    const float p = r.p[i];
-    if (difference && r.q) {
-        weight_of(p, r.q[i], d, e);
-    } else if (!(difference && i == r.skip)) {
-        d = p > 0.0f ? p : 0.0f;
+    const int lane = threadIdx.x & 31;
+    float ws = 0.0f, wc = 0.0f;
+    auto take = [&](float p, float q, int64_t i) {
+        float d, e;
+        row.weight(p, q, i, d, e);
+        add_pair(ws, wc, d);
+        wc = __fadd_rn(wc, e);
+    };
+    if (vec) {  // the vocabulary is a multiple of 4, rows are 16-byte aligned
+        for (int64_t c = c0; c < c1; c += 4) {
+            float4 p[4], q[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int64_t i = (c + u) * kChunk + 4 * lane;
+                const bool on = c + u < c1 && i < vocab;
+                p[u] = q[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (on) p[u] = *reinterpret_cast<const float4 *>(row.p + i);
+                if (on && row.q) q[u] = *reinterpret_cast<const float4 *>(row.q + i);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int64_t i = (c + u) * kChunk + 4 * lane;
+                take(p[u].x, q[u].x, i);
+                take(p[u].y, q[u].y, i + 1);
+                take(p[u].z, q[u].z, i + 2);
+                take(p[u].w, q[u].w, i + 3);
+            }
+        }
+    } else {
+        const int64_t end = min(c1 * kChunk, vocab);
+        for (int64_t i0 = c0 * kChunk + lane; i0 < end; i0 += 256) {
+            float p[8], q[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int64_t i = i0 + 32 * u;
+                p[u] = i < end ? row.p[i] : 0.0f;
+                q[u] = row.q && i < end ? row.q[i] : 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) take(p[u], q[u], i0 + 32 * u);
+        }
     }
+    return warp_sum_f64((double)ws + (double)wc);
+}
+
+// The first index of the warp's chunks [c0, c1) whose running sum, from `base` on, passes x; the
+// last positive weight where none does; -1 without any.  find_last: only the latter.
+__device__ __forceinline__ int64_t slice_find(const Row &row, int64_t c0, int64_t c1, int64_t vocab, double base,
+                                              double x, bool find_last)
+{
+    const int lane = threadIdx.x & 31;
+    int64_t last = -1;
+    for (int64_t cb = c0; cb < c1; cb += 4) {
+        float p[4][4], q[4][4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t i = (cb + u) * kChunk + 4 * lane + k;
+                const bool on = cb + u < c1 && i < vocab;
+                p[u][k] = on ? row.p[i] : 0.0f;
+                q[u][k] = on && row.q ? row.q[i] : 0.0f;
+            }
+#pragma unroll 1
+        for (int u = 0; u < 4 && cb + u < c1; ++u) {
+            const int64_t i0 = (cb + u) * kChunk;
+            // the lane's four weights and their sum as a pair
+            float d[4], e[4], s = 0.0f, c = 0.0f;
+            int pos = -1;  // the lane's last positive weight
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                // (index 4 u + k by selects: the arrays stay in registers)
+                const float pk = u == 0 ? p[0][k] : u == 1 ? p[1][k] : u == 2 ? p[2][k] : p[3][k];
+                const float qk = u == 0 ? q[0][k] : u == 1 ? q[1][k] : u == 2 ? q[2][k] : q[3][k];
+                row.weight(pk, qk, i0 + 4 * lane + k, d[k], e[k]);
+                if (d[k] > 0.0f) pos = k;
+                add_pair(s, c, d[k]);
+                c = __fadd_rn(c, e[k]);
+            }
+            const uint32_t any = __ballot_sync(0xffffffffu, pos >= 0);
+            if (any) {
+                const int j = 31 - __clz(any);
+                last = i0 + 4 * j + __shfl_sync(0xffffffffu, pos, j);
+            }
+            if (find_last) continue;
+            const double sum = (double)s + (double)c;
+            double incl = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const double v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            const uint32_t b = __ballot_sync(0xffffffffu, pos >= 0 && base + incl > x);
+            if (b) {
+                const int j = __ffs(b) - 1;  // the lane whose weights pass x
+                int hit = pos;
+                if (lane == j) {
+                    double run = base + (incl - sum);
+                    hit = -1;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        run += (double)d[k] + (double)e[k];
+                        if (hit < 0 && d[k] > 0.0f && run > x) hit = k;
+                    }
+                    if (hit < 0) hit = pos;
+                }
+                return i0 + 4 * j + __shfl_sync(0xffffffffu, hit, j);
+            }
+            base += __shfl_sync(0xffffffffu, incl, 31);
+        }
+    }
+    return last;
+}
+
+// First of `n` sums (n <= 32, lane i holds v) whose running sum passes x, and the sum before it;
+// -1 when none does.  last: the last positive one.
+__device__ __forceinline__ int first_over(double v, int n, double start, double x, double &before, int &last)
+{
+    const int lane = threadIdx.x & 31;
+    if (lane >= n) v = 0.0;
+    double incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
+    }
+    const uint32_t pos = __ballot_sync(0xffffffffu, v > 0.0);
+    const uint32_t b = __ballot_sync(0xffffffffu, v > 0.0 && start + incl > x);
+    last = pos ? 31 - __clz(pos) : -1;
+    if (!b) return -1;
+    const int j = __ffs(b) - 1;
+    before = start + __shfl_sync(0xffffffffu, incl - v, j);
+    return j;
 }
 
 __global__ void __launch_bounds__(kThreads)
@@ -83,8 +217,8 @@ draft_verify_kernel(const float *__restrict__ target, int64_t ld_t, const float 
                     int max_draft, int64_t vocab, int vec, int32_t *__restrict__ tokens_out,
                     int32_t *__restrict__ n_accepted)
 {
-    __shared__ double warp_w[kWarps], warp_p[kWarps];       // this CTA's slices: weights, plain p
-    __shared__ double cta_w[kMaxCluster], cta_p[kMaxCluster];  // every CTA's total
+    __shared__ double warp_w[kWarps];        // this CTA's slices
+    __shared__ double cta_w[2][kMaxCluster];  // every CTA's total: of the weights, of the plain row
     __shared__ int taken_s, refused_s;
     cg::cluster_group cl = cg::this_cluster();
     const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
@@ -99,21 +233,24 @@ draft_verify_kernel(const float *__restrict__ target, int64_t ld_t, const float 
     QSA_AFTER_WAIT(u);
     pdl_trigger();
 
-    // ---- how many drafts are taken: the first refusal
+    // ---- how many drafts are taken: the first refusal.  (The first 32 tokens and numbers are
+    // loaded beside n_draft, not behind it.)
     if (warp == 0) {
-        const int n = n_draft ? min(max(n_draft[s], 0), max_draft) : max_draft;
-        int a = n;
+        int n = max_draft, a = max_draft;
         for (int j0 = 0; j0 < n && a == n; j0 += 32) {
             const int j = j0 + lane;
-            bool refuse = false;
-            if (j < n) {
-                const int t = tokens[s * max_draft + j];
-                refuse = true;  // a token outside the vocabulary is refused
-                if (t >= 0 && t < vocab) {
-                    const float p = target[(s * (max_draft + 1) + j) * ld_t + t];
-                    const float q = draft ? draft[(s * max_draft + j) * ld_d + t] : 1.0f;
-                    refuse = !((double)u[s * (max_draft + 1) + j] * (double)q < (double)p);
-                }
+            int t = -1;
+            float uj = 0.0f;
+            if (j < max_draft) {
+                t = tokens[s * max_draft + j];
+                uj = u[s * (max_draft + 1) + j];
+            }
+            if (j0 == 0 && n_draft) a = n = min(max(n_draft[s], 0), max_draft);
+            bool refuse = j < n;  // a token outside the vocabulary is refused
+            if (j < max_draft && t >= 0 && t < vocab) {
+                const float p = target[(s * (max_draft + 1) + j) * ld_t + t];
+                const float q = draft ? draft[(s * max_draft + j) * ld_d + t] : 1.0f;
+                refuse = j < n && !((double)uj * (double)q < (double)p);
             }
             const uint32_t b = __ballot_sync(0xffffffffu, refuse);
             if (b) a = j0 + __ffs(b) - 1;
@@ -126,164 +263,63 @@ draft_verify_kernel(const float *__restrict__ target, int64_t ld_t, const float 
     __syncthreads();
     const int a = taken_s;
     const bool refused = refused_s != 0;
-    Row row;
-    row.p = target + (s * (max_draft + 1) + a) * ld_t;
-    row.q = refused && draft ? draft + (s * max_draft + a) * ld_d : nullptr;
-    row.skip = refused && !draft ? tokens[s * max_draft + a] : -1;
-
-    // ---- sums of this warp's slice: whole chunks of 128 values
     const int64_t chunks = (vocab + kChunk - 1) / kChunk;
     const int64_t per = (chunks + (int64_t)C * kWarps - 1) / ((int64_t)C * kWarps);
     const int64_t c0 = min(((int64_t)rank * kWarps + warp) * per, chunks);
     const int64_t c1 = min(c0 + per, chunks);
-    float ws = 0.0f, wc = 0.0f, ps = 0.0f, pc = 0.0f;
-    auto take = [&](float p, float q, int64_t i) {
-        float d, e = 0.0f;
-        if (row.q) {
-            weight_of(p, q, d, e);
-        } else {
-            d = p > 0.0f && i != row.skip ? p : 0.0f;
-        }
-        add_pair(ws, wc, d);
-        wc = __fadd_rn(wc, e);
-        if (refused) add_pair(ps, pc, p > 0.0f ? p : 0.0f);
-    };
-    if (vec) {
-#pragma unroll 4
-        for (int64_t c = c0; c < c1; ++c) {
-            const int64_t i = c * kChunk + 4 * lane;
-            if (i >= vocab) continue;  // vec: the vocabulary is a multiple of 4
-            const float4 p = *reinterpret_cast<const float4 *>(row.p + i);
-            float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (row.q) q = *reinterpret_cast<const float4 *>(row.q + i);
-            take(p.x, q.x, i);
-            take(p.y, q.y, i + 1);
-            take(p.z, q.z, i + 2);
-            take(p.w, q.w, i + 3);
-        }
-    } else {
-#pragma unroll 4
-        for (int64_t i = c0 * kChunk + lane; i < min(c1 * kChunk, vocab); i += 32)
-            take(row.p[i], row.q ? row.q[i] : 0.0f, i);
-    }
-    const double wsum = warp_sum_f64((double)ws + (double)wc);
-    const double psum = warp_sum_f64((double)ps + (double)pc);
-    if (lane == 0) {
-        warp_w[warp] = wsum;
-        warp_p[warp] = psum;
-    }
-    __syncthreads();
+    const double r = fmin(fmax((double)u[s * (max_draft + 1) + max_draft], 0.0), 1.0);
+    const int turned = refused && !draft ? tokens[s * max_draft + a] : -1;
     cl.barrier_wait(std::move(started));  // every CTA of the cluster runs
-    if (tid == 0) {
-        double tw = 0.0, tp = 0.0;
-        for (int i = 0; i < kWarps; ++i) {
-            tw += warp_w[i];
-            tp += warp_p[i];
-        }
-        for (int c = 0; c < C; ++c) {
-            *cl.map_shared_rank(&cta_w[rank], c) = tw;
-            *cl.map_shared_rank(&cta_p[rank], c) = tp;
-        }
-    }
-    cl.sync();  // after it no CTA touches another's shared memory
 
-    // ---- where the drawn point lies
-    if (warp == 0) {
-        double total = 0.0, before = 0.0;
-        for (int c = 0; c < C; ++c) total += cta_w[c];
-        // nothing left of p - q (the two rows are equal): the token comes from p itself
-        const bool difference = refused && total > 0.0;
-        const double *cta = cta_w, *wsums = warp_w;
-        if (refused && !difference) {
-            cta = cta_p;
-            wsums = warp_p;
-            total = 0.0;
-            for (int c = 0; c < C; ++c) total += cta_p[c];
+    // the weights after a refusal; then, only where they are zero everywhere (the two rows are
+    // equal), the target's row itself
+    for (int plain = refused ? 0 : 1; plain < 2; ++plain) {
+        Row row;
+        row.p = target + (s * (max_draft + 1) + a) * ld_t;
+        row.q = !plain && draft ? draft + (s * max_draft + a) * ld_d : nullptr;
+        row.skip = plain ? -1 : turned;
+        const double mine = slice_sum(row, c0, c1, vocab, vec != 0);
+        if (lane == 0) warp_w[warp] = mine;
+        __syncthreads();
+        if (warp == 0) {
+            const double t = warp_sum_f64(lane < kWarps ? warp_w[lane] : 0.0);
+            if (lane < C) *cl.map_shared_rank(&cta_w[plain][rank], lane) = t;
         }
-        const double r = fmin(fmax((double)u[s * (max_draft + 1) + max_draft], 0.0), 1.0);
-        const double x = r * total;
-        // the first slice whose running sum passes x, else the last one that holds any weight
-        int owner = -1, ow = -1, last_c = -1;
-        double run = 0.0;
-        for (int c = 0; c < C; ++c) {
-            if (cta[c] > 0.0) last_c = c;
-            if (owner < 0 && run + cta[c] > x) {
-                owner = c;
-                before = run;
+        cl.sync();  // after the last turn's no CTA touches another's shared memory
+        double total = 0.0;
+        for (int c = 0; c < C; ++c) total += cta_w[plain][c];
+        if (!plain && !(total > 0.0)) continue;
+        // ---- where the drawn point lies: the CTA, its warp's slice, the index
+        if (warp == 0) {
+            const double x = r * total;
+            double before = 0.0;
+            int last;
+            int owner = first_over(lane < C ? cta_w[plain][lane] : 0.0, C, 0.0, x, before, last);
+            const bool tail = owner < 0;  // rounding at the end: the last weight
+            if (tail) owner = last;
+            if (rank == (owner < 0 ? 0 : owner)) {
+                int token = -1;  // no weight anywhere
+                if (owner >= 0) {
+                    double base = 0.0;
+                    int w = tail ? -1
+                                 : first_over(lane < kWarps ? warp_w[lane] : 0.0, kWarps, before, x, base, last);
+                    const bool end = w < 0;
+                    if (end) {
+                        (void)first_over(lane < kWarps ? warp_w[lane] : 0.0, kWarps, 0.0, INFINITY, base, last);
+                        w = last;
+                    }
+                    if (w >= 0) {
+                        const int64_t d0 = min(((int64_t)rank * kWarps + w) * per, chunks);
+                        token = (int)slice_find(row, d0, min(d0 + per, chunks), vocab, base, x, end);
+                    }
+                }
+                int32_t *to = tokens_out + s * (max_draft + 1);
+                for (int j = lane; j <= max_draft; j += 32)
+                    to[j] = j < a ? tokens[s * max_draft + j] : (j == a ? token : -1);
+                if (lane == 0) n_accepted[s] = a;
             }
-            run += cta[c];
         }
-        if (owner < 0) {
-            owner = last_c;
-            before = INFINITY;  // its last weight
-        }
-        int32_t *to = tokens_out + s * (max_draft + 1);
-        if (rank == (owner < 0 ? 0 : owner)) {
-            int token = -1;  // no weight anywhere
-            if (owner >= 0) {
-                run = before;
-                int last_w = -1;
-                for (int i = 0; i < kWarps; ++i) {
-                    if (wsums[i] > 0.0) last_w = i;
-                    if (ow < 0 && run + wsums[i] > x && wsums[i] > 0.0 && !isinf(run)) {
-                        ow = i;
-                        before = run;
-                    }
-                    run += wsums[i];
-                }
-                if (ow < 0) {
-                    ow = last_w;
-                    before = INFINITY;
-                }
-                const int64_t d0 = min(((int64_t)rank * kWarps + ow) * per, chunks);
-                const int64_t d1 = min(d0 + per, chunks);
-                const bool find_last = isinf(before);
-                double base = find_last ? 0.0 : before;
-                int64_t found = -1, last = -1;
-                for (int64_t c = d0; c < d1 && found < 0; ++c) {
-                    const int64_t i = c * kChunk + 4 * lane;
-                    double w[4], sum = 0.0;
-                    bool any_w[4];
-                    int pos = -1;  // this lane's last positive weight
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float d, e;
-                        row_weight(row, i + k, vocab, difference, d, e);
-                        w[k] = (double)d + (double)e;
-                        any_w[k] = w[k] > 0.0;
-                        if (any_w[k]) pos = k;
-                        sum += w[k];
-                        w[k] = sum;
-                    }
-                    double incl = sum;
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const double v = __shfl_up_sync(0xffffffffu, incl, o);
-                        if (lane >= o) incl += v;
-                    }
-                    const double start = base + (incl - sum);
-                    int hit = 4;
-#pragma unroll
-                    for (int k = 3; k >= 0; --k)
-                        if (any_w[k] && start + w[k] > x && !find_last) hit = k;
-                    const uint32_t b = __ballot_sync(0xffffffffu, hit < 4);
-                    const uint32_t any = __ballot_sync(0xffffffffu, pos >= 0);
-                    if (any) {
-                        const int j = 31 - __clz(any);
-                        last = c * kChunk + 4 * j + __shfl_sync(0xffffffffu, pos, j);
-                    }
-                    if (b) {
-                        const int j = __ffs(b) - 1;
-                        found = c * kChunk + 4 * j + __shfl_sync(0xffffffffu, hit, j);
-                    }
-                    base += __shfl_sync(0xffffffffu, incl, 31);
-                }
-                token = (int)(found >= 0 ? found : last);
-            }
-            for (int j = lane; j <= max_draft; j += 32)
-                to[j] = j < a ? tokens[s * max_draft + j] : (j == a ? token : -1);
-            if (lane == 0) n_accepted[s] = a;
-        }
+        break;
     }
 }
 

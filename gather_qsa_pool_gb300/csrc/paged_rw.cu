@@ -74,11 +74,25 @@ __device__ __forceinline__ int row_exponent(float top)
 }
 
 // ------------------------------------------------------------------ write
-// Eight values per lane, d / 8 lanes per row (a power of two up to 32): a warp holds several
-// rows at once, and a row's largest magnitude is a shuffle over its lanes.  One task is a
-// token's row of K or of V for one KV head; consecutive tasks are consecutive in memory.
-// Bound by the bytes of the rows (a source row read once, its codes written once); with few
-// tokens by the launch.
+// The sequence of token tok: the number of s with cu[s + 1] <= tok, 32 of them at a time.
+__device__ __forceinline__ int token_seq(const SeqView &sv, int64_t tok)
+{
+    const int lane = threadIdx.x & 31;
+    for (int s0 = 0;; s0 += 32) {
+        const int s = s0 + lane;
+        const bool behind = s < sv.n_seq && (int64_t)sv.cu[s + 1] <= tok;
+        const int n = __popc(__ballot_sync(0xffffffffu, behind));
+        if (n < 32) return s0 + n;
+    }
+}
+
+// One warp per token and tensor (K or V): the cell is looked up once, then the row of all KV heads
+// goes through, eight values a lane, d / 8 lanes per head (a power of two of them, up to 32), so a
+// head's largest magnitude is a shuffle over its lanes.  The row's loads do not wait for the
+// look-up.  Bound by the bytes (a source row read once, its codes written once); with few tokens by
+// the launch and the look-up's four dependent loads.
+constexpr int kAhead = 4;  // steps of 256 values whose loads are issued together
+
 template <typename TS, typename TD>
 __global__ void __launch_bounds__(256)
 paged_write_kernel(const TS *__restrict__ k, const TS *__restrict__ v, int64_t ld_k, int64_t ld_v,
@@ -89,58 +103,97 @@ paged_write_kernel(const TS *__restrict__ k, const TS *__restrict__ v, int64_t l
     QSA_AFTER_WAIT(k);
     QSA_AFTER_WAIT(v);
     pdl_trigger();
-    const int lanes = 1 << lanes_log2;  // lanes of a row; those beyond d / 8 idle
-    const int64_t gt = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    const int c = (int)(gt & (lanes - 1));
+    const int lane = threadIdx.x & 31;
+    const int c = lane & ((1 << lanes_log2) - 1);    // this lane's eight values of a head
+    const int heads = 32 >> lanes_log2;              // heads of a step
     const bool on = c * 8 < d;
-    const int64_t n_tasks = sv.n_tok * 2 * H;
-    const int64_t stride = ((int64_t)gridDim.x * blockDim.x) >> lanes_log2;
-    // every lane of a warp makes the same number of turns: the shuffles need all of them
-    const int64_t first = gt >> lanes_log2;
-    const int64_t turns = (n_tasks + stride - 1) / stride;
-    for (int64_t i = 0; i < turns; ++i) {
-        const int64_t task = first + i * stride;
-        const bool live = task < n_tasks;
-        const int64_t tok = live ? task / (2 * H) : 0;
-        const int r = live ? (int)(task - tok * 2 * H) : 0;
-        const bool is_v = r >= H;
-        const int h = is_v ? r - H : r;
-        // the token's sequence: the last s with cu[s] <= tok (binary search)
-        int lo = 0, hi = sv.n_seq;  // answer in [lo, hi)
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if ((int64_t)sv.cu[mid] <= tok) lo = mid;
-            else hi = mid;
-        }
+    const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
+    for (int64_t task = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; task < 2 * sv.n_tok;
+         task += warps) {
+        const int64_t tok = task >> 1;
+        const bool is_v = task & 1;
+        const TS *src = (is_v ? v + tok * ld_v : k + tok * ld_k) + 8 * c;
         int64_t row = -1;
-        if (live) {
-            const int64_t a = sv.cu[lo], b = sv.cu[lo + 1];
-            const int64_t p = (int64_t)sv.kv_len[lo] - (b - tok);
-            if (tok >= a && tok < b && p >= 0 && p < (int64_t)sv.kv_len[lo])
-                row = cell_row(kv, lo, 0, (int)p);
-        }
-        float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-        if (live && on)
-            load8((is_v ? v + tok * ld_v : k + tok * ld_k) + (int64_t)h * d + 8 * c, x);
-        TD *dst = (is_v ? V + row * kv.ld_v : K + row * kv.ld_k) + (int64_t)h * d + 8 * c;
-        if constexpr (sizeof(TD) == 1) {
-            float top = 0.0f;
+        bool known = false;
+        for (int h0 = 0; h0 < H; h0 += heads * kAhead) {
+            float x[kAhead][8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top = fmaxf(top, isfinite(x[j]) ? fabsf(x[j]) : 0.0f);
-            for (int o = lanes >> 1; o > 0; o >>= 1)
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const int e = row_exponent(top);
-            if (row >= 0 && on) *reinterpret_cast<uint2 *>(dst) = encode8(x, two_to(-e));
-            if (row >= 0 && c == 0) (is_v ? V_exp : K_exp)[row * H + h] = (uint8_t)(e + kExpBias);
-        } else {
-            if (row >= 0 && on) store8(dst, x);
+            for (int i = 0; i < kAhead; ++i) {
+                const int h = h0 + i * heads + (lane >> lanes_log2);
+                if (on && h < H) {
+                    load8(src + (int64_t)h * d, x[i]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[i][j] = 0.0f;
+                }
+            }
+            if (!known) {
+                known = true;
+                const int s = token_seq(sv, tok);
+                if (s < sv.n_seq && (int64_t)sv.cu[s] <= tok) {
+                    const int64_t len = sv.kv_len[s], p = len - ((int64_t)sv.cu[s + 1] - tok);
+                    if (p >= 0 && p < len) row = cell_row(kv, s, 0, (int)p);
+                }
+            }
+            if (row < 0) break;  // a token without a cell
+            TD *dst = (is_v ? V + row * kv.ld_v : K + row * kv.ld_k) + 8 * c;
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int h = h0 + i * heads + (lane >> lanes_log2);
+                if constexpr (sizeof(TD) == 1) {
+                    float top = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) top = fmaxf(top, isfinite(x[i][j]) ? fabsf(x[i][j]) : 0.0f);
+                    for (int o = (1 << lanes_log2) >> 1; o > 0; o >>= 1)
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const int e = row_exponent(top);
+                    if (on && h < H) *reinterpret_cast<uint2 *>(dst + (int64_t)h * d) = encode8(x[i], two_to(-e));
+                    if (c == 0 && h < H) (is_v ? V_exp : K_exp)[row * H + h] = (uint8_t)(e + kExpBias);
+                } else {
+                    if (on && h < H) store8(dst + (int64_t)h * d, x[i]);
+                }
+            }
         }
     }
 }
 
 // ------------------------------------------------------------------ read
-// One warp per listed cell, looping over the list: the cell's K and V rows of all KV heads are
-// contiguous, so the lanes stream them 8 values each.  Bound by the bytes.
+// One warp per eight listed cells: eight lanes look the cells up at once, then the warp streams their
+// K and V rows (all KV heads contiguous), eight values a lane, four steps in flight.  Bound by the
+// bytes; with few cells by the look-up's dependent loads and one step's latency.
+constexpr int kGroup = 8;
+
+template <typename T>
+struct Raw8 {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const T *p)
+    {
+        a = reinterpret_cast<const uint4 *>(p)[0];
+        if constexpr (sizeof(T) == 4) b = reinterpret_cast<const uint4 *>(p)[1];
+    }
+    __device__ __forceinline__ void values(float, float *x) const
+    {
+        if constexpr (sizeof(T) == 4) {
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+        } else {
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+    }
+};
+template <>
+struct Raw8<uint8_t> {
+    uint2 a;
+    __device__ __forceinline__ void load(const uint8_t *p) { a = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void values(float mul, float *x) const { decode8(a, mul, x); }
+};
+
 template <typename TS, typename TD>
 __global__ void __launch_bounds__(256)
 paged_read_kernel(KvView kv, int H, int d, const int32_t *__restrict__ seq,
@@ -157,32 +210,57 @@ paged_read_kernel(KvView kv, int H, int d, const int32_t *__restrict__ seq,
     const int lane = threadIdx.x & 31;
     const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
     const int hd = H * d;
-    for (int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; w < n_list * max_cells;
-         w += warps) {
-        const int64_t i = w / max_cells, j = w - i * max_cells;
-        if (j >= (int64_t)n_cells[i]) continue;
-        const int64_t s = seq ? (int64_t)seq[i] : i;
-        int64_t row = -1;
-        if (s >= 0 && s < n_seq) {
-            const int64_t p = pos ? (int64_t)pos[w] : j;
-            if (p >= 0 && p < (int64_t)kv_len[s]) row = cell_row(kv, (int)s, 0, (int)p);
+    const int64_t groups = (max_cells + kGroup - 1) / kGroup;  // of a list
+    const TS *K = static_cast<const TS *>(kv.K), *V = static_cast<const TS *>(kv.V);
+    for (int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; w < n_list * groups; w += warps) {
+        const int64_t i = div_pos(w, groups), j0 = (w - i * groups) * kGroup;
+        const int64_t many = min((int64_t)n_cells[i], max_cells);
+        const int n = (int)min((int64_t)kGroup, many - j0);
+        if (n <= 0) continue;
+        int32_t mine = -1;  // pool row of cell j0 + lane
+        if (lane < n) {
+            const int64_t s = seq ? (int64_t)seq[i] : i;
+            const int64_t p = pos ? (int64_t)pos[i * max_cells + j0 + lane] : j0 + lane;
+            if (s >= 0 && s < n_seq && p >= 0 && p < (int64_t)kv_len[s])
+                mine = (int32_t)cell_row(kv, (int)s, 0, (int)p);
         }
-        const TS *K = static_cast<const TS *>(kv.K), *V = static_cast<const TS *>(kv.V);
-        for (int e = 8 * lane; e < 2 * hd; e += 256) {
-            const bool is_v = e >= hd;
-            const int at = is_v ? e - hd : e;
-            float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-            if (row >= 0) {
-                const TS *src = (is_v ? V + row * kv.ld_v : K + row * kv.ld_k) + at;
-                if constexpr (sizeof(TS) == 1) {
-                    const int b = (is_v ? kv.V_exp : kv.K_exp)[row * H + at / d];
-                    const int ex = min(max(b - kExpBias, kExpMin), kExpMax);
-                    decode8(*reinterpret_cast<const uint2 *>(src), two_to(ex), x);
-                } else {
-                    load8(src, x);
+        // steps of 256 values: cell, then K and V; the tail of a row is masked
+        const int per = (hd + 255) >> 8, steps = n * 2 * per;
+        int cell = 0, part = 0;  // of the next step to load
+        for (int s0 = 0; s0 < steps; s0 += 4) {
+            Raw8<TS> raw[4];
+            float mul[4];
+            int64_t to[4];
+            bool here[4], is_v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int32_t row = __shfl_sync(0xffffffffu, mine, cell);
+                is_v[u] = part >= per;
+                const int e = ((is_v[u] ? part - per : part) << 8) + 8 * lane;
+                here[u] = s0 + u < steps && e < hd;
+                to[u] = (i * max_cells + j0 + cell) * hd + e;
+                mul[u] = 0.0f;  // a cell that is not there: zeros
+                if constexpr (sizeof(TS) == 1) raw[u].a = make_uint2(0u, 0u);
+                else raw[u].a = make_uint4(0u, 0u, 0u, 0u);
+                if constexpr (sizeof(TS) == 4) raw[u].b = make_uint4(0u, 0u, 0u, 0u);
+                if (here[u] && row >= 0) {
+                    raw[u].load((is_v[u] ? V + row * kv.ld_v : K + row * kv.ld_k) + e);
+                    if constexpr (sizeof(TS) == 1)
+                        mul[u] = two_to(min(max((int)(is_v[u] ? kv.V_exp : kv.K_exp)[(int64_t)row * H + e / d] -
+                                                    kExpBias, kExpMin), kExpMax));
+                }
+                if (++part == 2 * per) {
+                    part = 0;
+                    cell = cell + 1 < n ? cell + 1 : cell;
                 }
             }
-            store8((is_v ? V_out : K_out) + w * hd + at, x);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (!here[u]) continue;
+                float x[8];
+                raw[u].values(mul[u], x);
+                store8((is_v[u] ? V_out : K_out) + to[u], x);
+            }
         }
     }
 }
@@ -193,9 +271,8 @@ cudaError_t write_to(const void *k, const void *v, int64_t ld_k, int64_t ld_v, i
 {
     int lanes_log2 = 0;
     while ((8 << lanes_log2) < d) ++lanes_log2;
-    const int64_t threads = sv.n_tok * 2 * kv.H_kv << lanes_log2;
-    int64_t grid = (threads + 255) / 256;
-    const int64_t most = (int64_t)device_sm_count() * 16;
+    int64_t grid = (2 * sv.n_tok + 7) / 8;
+    const int64_t most = (int64_t)device_sm_count() * 8;
     if (grid > most) grid = most;
     const TS *ks = static_cast<const TS *>(k), *vs = static_cast<const TS *>(v);
     uint8_t *ke = const_cast<uint8_t *>(kv.K_exp), *ve = const_cast<uint8_t *>(kv.V_exp);
@@ -220,7 +297,7 @@ cudaError_t read_to(const KvView &kv, int d, const int32_t *seq, const int32_t *
                     const int32_t *pos, const int32_t *n_cells, int64_t n_list, int64_t max_cells,
                     void *K_out, void *V_out, cudaStream_t st)
 {
-    int64_t grid = (n_list * max_cells + 7) / 8;
+    int64_t grid = (n_list * ((max_cells + kGroup - 1) / kGroup) + 7) / 8;
     const int64_t most = (int64_t)device_sm_count() * 8;
     if (grid > most) grid = most;
     return launch(paged_read_kernel<TS, TD>, dim3((unsigned)grid), dim3(256), 0, st, 1, kv, kv.H_kv, d,
