@@ -127,10 +127,10 @@ __device__ __forceinline__ int64_t slice_find(const Row &row, int64_t c0, int64_
 {
     const int lane = threadIdx.x & 31;
     int64_t last = -1;
-    for (int64_t cb = c0; cb < c1; cb += 4) {
-        float p[4][4], q[4][4];
+    for (int64_t cb = c0; cb < c1; cb += 2) {
+        float p[2][4], q[2][4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int64_t i = (cb + u) * kChunk + 4 * lane + k;
@@ -139,16 +139,14 @@ __device__ __forceinline__ int64_t slice_find(const Row &row, int64_t c0, int64_
                 q[u][k] = on && row.q ? row.q[i] : 0.0f;
             }
 #pragma unroll 1
-        for (int u = 0; u < 4 && cb + u < c1; ++u) {
+        for (int u = 0; u < 2 && cb + u < c1; ++u) {
             const int64_t i0 = (cb + u) * kChunk;
             // the lane's four weights and their sum as a pair
             float d[4], e[4], s = 0.0f, c = 0.0f;
             int pos = -1;  // the lane's last positive weight
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                // (index 4 u + k by selects: the arrays stay in registers)
-                const float pk = u == 0 ? p[0][k] : u == 1 ? p[1][k] : u == 2 ? p[2][k] : p[3][k];
-                const float qk = u == 0 ? q[0][k] : u == 1 ? q[1][k] : u == 2 ? q[2][k] : q[3][k];
+                const float pk = u ? p[1][k] : p[0][k], qk = u ? q[1][k] : q[0][k];
                 row.weight(pk, qk, i0 + 4 * lane + k, d[k], e[k]);
                 if (d[k] > 0.0f) pos = k;
                 add_pair(s, c, d[k]);
@@ -210,7 +208,7 @@ __device__ __forceinline__ int first_over(double v, int n, double start, double 
     return j;
 }
 
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 draft_verify_kernel(const float *__restrict__ target, int64_t ld_t, const float *__restrict__ draft,
                     int64_t ld_d, const int32_t *__restrict__ tokens,
                     const int32_t *__restrict__ n_draft, const float *__restrict__ u,
@@ -219,7 +217,7 @@ draft_verify_kernel(const float *__restrict__ target, int64_t ld_t, const float 
 {
     __shared__ double warp_w[kWarps];        // this CTA's slices
     __shared__ double cta_w[2][kMaxCluster];  // every CTA's total: of the weights, of the plain row
-    __shared__ int taken_s, refused_s;
+    __shared__ int taken_s, refused_s, empty_s;
     cg::cluster_group cl = cg::this_cluster();
     const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
     const int64_t s = blockIdx.x / C;
@@ -267,7 +265,7 @@ draft_verify_kernel(const float *__restrict__ target, int64_t ld_t, const float 
     const int64_t per = (chunks + (int64_t)C * kWarps - 1) / ((int64_t)C * kWarps);
     const int64_t c0 = min(((int64_t)rank * kWarps + warp) * per, chunks);
     const int64_t c1 = min(c0 + per, chunks);
-    const double r = fmin(fmax((double)u[s * (max_draft + 1) + max_draft], 0.0), 1.0);
+    const float r = fminf(fmaxf(u[s * (max_draft + 1) + max_draft], 0.0f), 1.0f);
     const int turned = refused && !draft ? tokens[s * max_draft + a] : -1;
     cl.barrier_wait(std::move(started));  // every CTA of the cluster runs
 
@@ -287,11 +285,15 @@ draft_verify_kernel(const float *__restrict__ target, int64_t ld_t, const float 
         }
         cl.sync();  // after the last turn's no CTA touches another's shared memory
         double total = 0.0;
-        for (int c = 0; c < C; ++c) total += cta_w[plain][c];
-        if (!plain && !(total > 0.0)) continue;
+        if (warp == 0) total = warp_sum_f64(lane < C ? cta_w[plain][lane] : 0.0);
+        if (!plain) {  // (every CTA comes to the same answer)
+            if (tid == 0) empty_s = !(total > 0.0);
+            __syncthreads();
+            if (empty_s) continue;
+        }
         // ---- where the drawn point lies: the CTA, its warp's slice, the index
         if (warp == 0) {
-            const double x = r * total;
+            const double x = (double)r * total;
             double before = 0.0;
             int last;
             int owner = first_over(lane < C ? cta_w[plain][lane] : 0.0, C, 0.0, x, before, last);
@@ -332,10 +334,10 @@ cudaError_t launch_draft_verify(const float *target, int64_t ld_t, const float *
 {
     const bool vec = vocab % 4 == 0 && ld_t % 4 == 0 && (!draft || ld_d % 4 == 0) &&
                      ((reinterpret_cast<uintptr_t>(target) | reinterpret_cast<uintptr_t>(draft)) & 15) == 0;
-    // CTAs per sequence: until the sequences fill the GPU twice, and while a warp still has more
-    // than one chunk of the row
+    // CTAs per sequence: as many as run at once (two per SM), while a warp still has more than one
+    // chunk of the row
     int c = 1;
-    while (c < kMaxCluster && n_seq * c < 2 * (int64_t)device_sm_count() &&
+    while (c < kMaxCluster && n_seq * 2 * c <= 2 * (int64_t)device_sm_count() &&
            vocab > (int64_t)c * kWarps * kChunk)
         c *= 2;
     return launch(draft_verify_kernel, dim3((unsigned)(n_seq * c)), dim3(kThreads), 0, st, c, target,

@@ -86,17 +86,15 @@ __device__ __forceinline__ int token_seq(const SeqView &sv, int64_t tok)
     }
 }
 
-// One warp per token and tensor (K or V): the cell is looked up once, then the row of all KV heads
-// goes through, eight values a lane, d / 8 lanes per head (a power of two of them, up to 32), so a
-// head's largest magnitude is a shuffle over its lanes.  The row's loads do not wait for the
-// look-up.  Bound by the bytes (a source row read once, its codes written once); with few tokens by
-// the launch and the look-up's four dependent loads.
-constexpr int kAhead = 4;  // steps of 256 values whose loads are issued together
-
+// One warp per `group` consecutive tokens: its lanes look their cells up at once, then the warp takes
+// the tokens' K and V rows of all KV heads, eight values a lane, d / 8 lanes per head (a power of two
+// of them, up to 32), so a head's largest magnitude is a shuffle over its lanes; four steps' loads
+// are in flight.  Bound by the bytes (a source row read once, its codes written once); with few
+// tokens by the launch and the look-up's dependent loads.
 template <typename TS, typename TD>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(128)
 paged_write_kernel(const TS *__restrict__ k, const TS *__restrict__ v, int64_t ld_k, int64_t ld_v,
-                   int H, int d, int lanes_log2, SeqView sv, KvView kv, TD *K, TD *V,
+                   int H, int d, int lanes_log2, int group, SeqView sv, KvView kv, TD *K, TD *V,
                    uint8_t *K_exp, uint8_t *V_exp)
 {
     pdl_wait();
@@ -106,51 +104,65 @@ paged_write_kernel(const TS *__restrict__ k, const TS *__restrict__ v, int64_t l
     const int lane = threadIdx.x & 31;
     const int c = lane & ((1 << lanes_log2) - 1);    // this lane's eight values of a head
     const int heads = 32 >> lanes_log2;              // heads of a step
+    const int per = (H + heads - 1) / heads;         // steps of a row
     const bool on = c * 8 < d;
     const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-    for (int64_t task = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; task < 2 * sv.n_tok;
-         task += warps) {
-        const int64_t tok = task >> 1;
-        const bool is_v = task & 1;
-        const TS *src = (is_v ? v + tok * ld_v : k + tok * ld_k) + 8 * c;
-        int64_t row = -1;
-        bool known = false;
-        for (int h0 = 0; h0 < H; h0 += heads * kAhead) {
-            float x[kAhead][8];
+    const int64_t groups = (sv.n_tok + group - 1) / group;
+    for (int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; w < groups; w += warps) {
+        const int64_t tok0 = w * group;
+        const int n = (int)min((int64_t)group, sv.n_tok - tok0);
+        int32_t mine = -1;  // pool row of token tok0 + lane
+        const int first = token_seq(sv, tok0);
+        if (lane < n) {
+            const int64_t tok = tok0 + lane;
+            int s = first;
+            while (s < sv.n_seq && (int64_t)sv.cu[s + 1] <= tok) ++s;
+            if (s < sv.n_seq && (int64_t)sv.cu[s] <= tok) {
+                const int64_t len = sv.kv_len[s], p = len - ((int64_t)sv.cu[s + 1] - tok);
+                if (p >= 0 && p < len) mine = (int32_t)cell_row(kv, s, 0, (int)p);
+            }
+        }
+        const int steps = n * 2 * per;
+        int at = 0, part = 0;  // of the next step to load: token, then K and V
+        for (int s0 = 0; s0 < steps; s0 += 4) {
+            float x[4][8];
+            int tk[4], pt[4];
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const int h = h0 + i * heads + (lane >> lanes_log2);
-                if (on && h < H) {
-                    load8(src + (int64_t)h * d, x[i]);
+            for (int u = 0; u < 4; ++u) {
+                tk[u] = at;
+                pt[u] = part;
+                const bool is_v = part >= per;
+                const int h = (is_v ? part - per : part) * heads + (lane >> lanes_log2);
+                if (s0 + u < steps && on && h < H) {
+                    load8((is_v ? v + (tok0 + at) * ld_v : k + (tok0 + at) * ld_k) + (int64_t)h * d + 8 * c, x[u]);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[i][j] = 0.0f;
+                    for (int j = 0; j < 8; ++j) x[u][j] = 0.0f;
+                }
+                if (++part == 2 * per) {
+                    part = 0;
+                    at = at + 1 < n ? at + 1 : at;
                 }
             }
-            if (!known) {
-                known = true;
-                const int s = token_seq(sv, tok);
-                if (s < sv.n_seq && (int64_t)sv.cu[s] <= tok) {
-                    const int64_t len = sv.kv_len[s], p = len - ((int64_t)sv.cu[s + 1] - tok);
-                    if (p >= 0 && p < len) row = cell_row(kv, s, 0, (int)p);
-                }
-            }
-            if (row < 0) break;  // a token without a cell
-            TD *dst = (is_v ? V + row * kv.ld_v : K + row * kv.ld_k) + 8 * c;
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const int h = h0 + i * heads + (lane >> lanes_log2);
+            for (int u = 0; u < 4; ++u) {
+                const int32_t row = __shfl_sync(0xffffffffu, mine, tk[u]);
+                const bool is_v = pt[u] >= per;
+                const int h = (is_v ? pt[u] - per : pt[u]) * heads + (lane >> lanes_log2);
+                const bool here = s0 + u < steps && row >= 0 && h < H;
+                TD *dst = (is_v ? V + row * kv.ld_v : K + row * kv.ld_k) + (int64_t)h * d + 8 * c;
                 if constexpr (sizeof(TD) == 1) {
                     float top = 0.0f;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) top = fmaxf(top, isfinite(x[i][j]) ? fabsf(x[i][j]) : 0.0f);
+                    for (int j = 0; j < 8; ++j) top = fmaxf(top, isfinite(x[u][j]) ? fabsf(x[u][j]) : 0.0f);
                     for (int o = (1 << lanes_log2) >> 1; o > 0; o >>= 1)
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                     const int e = row_exponent(top);
-                    if (on && h < H) *reinterpret_cast<uint2 *>(dst + (int64_t)h * d) = encode8(x[i], two_to(-e));
-                    if (c == 0 && h < H) (is_v ? V_exp : K_exp)[row * H + h] = (uint8_t)(e + kExpBias);
+                    if (here && on) *reinterpret_cast<uint2 *>(dst) = encode8(x[u], two_to(-e));
+                    if (here && c == 0)
+                        (is_v ? V_exp : K_exp)[(int64_t)row * H + h] = (uint8_t)(e + kExpBias);
                 } else {
-                    if (on && h < H) store8(dst + (int64_t)h * d, x[i]);
+                    if (here && on) store8(dst, x[u]);
                 }
             }
         }
@@ -158,10 +170,9 @@ paged_write_kernel(const TS *__restrict__ k, const TS *__restrict__ v, int64_t l
 }
 
 // ------------------------------------------------------------------ read
-// One warp per eight listed cells: eight lanes look the cells up at once, then the warp streams their
+// One warp per `group` listed cells: its lanes look the cells up at once, then the warp streams their
 // K and V rows (all KV heads contiguous), eight values a lane, four steps in flight.  Bound by the
 // bytes; with few cells by the look-up's dependent loads and one step's latency.
-constexpr int kGroup = 8;
 
 template <typename T>
 struct Raw8 {
@@ -195,8 +206,8 @@ struct Raw8<uint8_t> {
 };
 
 template <typename TS, typename TD>
-__global__ void __launch_bounds__(256)
-paged_read_kernel(KvView kv, int H, int d, const int32_t *__restrict__ seq,
+__global__ void __launch_bounds__(128)
+paged_read_kernel(KvView kv, int H, int d, int group, const int32_t *__restrict__ seq,
                   const int32_t *__restrict__ kv_len, int64_t n_seq, const int32_t *__restrict__ pos,
                   const int32_t *__restrict__ n_cells, int64_t n_list, int64_t max_cells,
                   TD *__restrict__ K_out, TD *__restrict__ V_out)
@@ -210,20 +221,20 @@ paged_read_kernel(KvView kv, int H, int d, const int32_t *__restrict__ seq,
     const int lane = threadIdx.x & 31;
     const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
     const int hd = H * d;
-    const int64_t groups = (max_cells + kGroup - 1) / kGroup;  // of a list
+    const int64_t groups = (max_cells + group - 1) / group;  // of a list
     const TS *K = static_cast<const TS *>(kv.K), *V = static_cast<const TS *>(kv.V);
     for (int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; w < n_list * groups; w += warps) {
-        const int64_t i = div_pos(w, groups), j0 = (w - i * groups) * kGroup;
+        const int64_t i = div_pos(w, groups), j0 = (w - i * groups) * group;
+        // (the list's entry is loaded beside its length, not behind it)
+        const int64_t s = seq ? (int64_t)seq[i] : i;
+        int64_t p = -1;
+        if (lane < group && j0 + lane < max_cells) p = pos ? (int64_t)pos[i * max_cells + j0 + lane] : j0 + lane;
+        const int32_t len = s >= 0 && s < n_seq ? kv_len[s] : 0;
         const int64_t many = min((int64_t)n_cells[i], max_cells);
-        const int n = (int)min((int64_t)kGroup, many - j0);
+        const int n = (int)min((int64_t)group, many - j0);
         if (n <= 0) continue;
         int32_t mine = -1;  // pool row of cell j0 + lane
-        if (lane < n) {
-            const int64_t s = seq ? (int64_t)seq[i] : i;
-            const int64_t p = pos ? (int64_t)pos[i * max_cells + j0 + lane] : j0 + lane;
-            if (s >= 0 && s < n_seq && p >= 0 && p < (int64_t)kv_len[s])
-                mine = (int32_t)cell_row(kv, (int)s, 0, (int)p);
-        }
+        if (lane < n && p >= 0 && p < (int64_t)len) mine = (int32_t)cell_row(kv, (int)s, 0, (int)p);
         // steps of 256 values: cell, then K and V; the tail of a row is masked
         const int per = (hd + 255) >> 8, steps = n * 2 * per;
         int cell = 0, part = 0;  // of the next step to load
@@ -265,30 +276,38 @@ paged_read_kernel(KvView kv, int H, int d, const int32_t *__restrict__ seq,
     }
 }
 
+// Rows a warp looks up together: as many as leave sixteen warps per SM, one to eight.
+int rows_group(int64_t rows)
+{
+    const int64_t per = rows / ((int64_t)device_sm_count() * 16);
+    return per >= 8 ? 8 : (per >= 4 ? 4 : (per >= 2 ? 2 : 1));
+}
+
 template <typename TS>
 cudaError_t write_to(const void *k, const void *v, int64_t ld_k, int64_t ld_v, int d, const SeqView &sv,
                      const KvView &kv, qsa_dtype cache_dtype, cudaStream_t st)
 {
     int lanes_log2 = 0;
     while ((8 << lanes_log2) < d) ++lanes_log2;
-    int64_t grid = (2 * sv.n_tok + 7) / 8;
-    const int64_t most = (int64_t)device_sm_count() * 8;
+    const int group = rows_group(sv.n_tok);
+    int64_t grid = ((sv.n_tok + group - 1) / group + 3) / 4;
+    const int64_t most = (int64_t)device_sm_count() * 16;
     if (grid > most) grid = most;
     const TS *ks = static_cast<const TS *>(k), *vs = static_cast<const TS *>(v);
     uint8_t *ke = const_cast<uint8_t *>(kv.K_exp), *ve = const_cast<uint8_t *>(kv.V_exp);
     void *K = const_cast<void *>(kv.K), *V = const_cast<void *>(kv.V);
-    const dim3 g((unsigned)grid), b(256);
+    const dim3 g((unsigned)grid), b(128);
     switch (cache_dtype) {
         case QSA_E4M3:
             return launch(paged_write_kernel<TS, uint8_t>, g, b, 0, st, 1, ks, vs, ld_k, ld_v, kv.H_kv, d,
-                          lanes_log2, sv, kv, static_cast<uint8_t *>(K), static_cast<uint8_t *>(V), ke, ve);
+                          lanes_log2, group, sv, kv, static_cast<uint8_t *>(K), static_cast<uint8_t *>(V), ke, ve);
         case QSA_BF16:
             return launch(paged_write_kernel<TS, __nv_bfloat16>, g, b, 0, st, 1, ks, vs, ld_k, ld_v,
-                          kv.H_kv, d, lanes_log2, sv, kv, static_cast<__nv_bfloat16 *>(K),
+                          kv.H_kv, d, lanes_log2, group, sv, kv, static_cast<__nv_bfloat16 *>(K),
                           static_cast<__nv_bfloat16 *>(V), ke, ve);
         default:
             return launch(paged_write_kernel<TS, float>, g, b, 0, st, 1, ks, vs, ld_k, ld_v, kv.H_kv, d,
-                          lanes_log2, sv, kv, static_cast<float *>(K), static_cast<float *>(V), ke, ve);
+                          lanes_log2, group, sv, kv, static_cast<float *>(K), static_cast<float *>(V), ke, ve);
     }
 }
 
@@ -297,10 +316,11 @@ cudaError_t read_to(const KvView &kv, int d, const int32_t *seq, const int32_t *
                     const int32_t *pos, const int32_t *n_cells, int64_t n_list, int64_t max_cells,
                     void *K_out, void *V_out, cudaStream_t st)
 {
-    int64_t grid = (n_list * ((max_cells + kGroup - 1) / kGroup) + 7) / 8;
-    const int64_t most = (int64_t)device_sm_count() * 8;
+    const int group = rows_group(n_list * max_cells);
+    int64_t grid = (n_list * ((max_cells + group - 1) / group) + 3) / 4;
+    const int64_t most = (int64_t)device_sm_count() * 16;
     if (grid > most) grid = most;
-    return launch(paged_read_kernel<TS, TD>, dim3((unsigned)grid), dim3(256), 0, st, 1, kv, kv.H_kv, d,
+    return launch(paged_read_kernel<TS, TD>, dim3((unsigned)grid), dim3(128), 0, st, 1, kv, kv.H_kv, d, group,
                   seq, kv_len, n_seq, pos, n_cells, n_list, max_cells, static_cast<TD *>(K_out),
                   static_cast<TD *>(V_out));
 }
