@@ -7,7 +7,8 @@
 // sums and weights stay within 2^8 of the largest and the common tile needs no reduction across
 // lanes, one vote only.  On e4m3 cells v_j = c_j 2^e_j; the weight that multiplies the code is
 // 2^(s_j + e_j - mx) with a reference of its own, so that the fp16 weights keep their bits on
-// the cells that matter for o whatever the rows' exponents are.
+// the cells that matter for o whatever the rows' exponents are; the sum l then adds 2^-e_j times it (and,
+// where exponents lie more than 2^50 from one, exponentials of the logits alone).
 //
 // Shape: a CTA of four warps takes a share of the flattened list of (sequence, KV head, row
 // tile) items (dense.cuh), equal for every CTA, whatever the lengths: ragged batches stay
@@ -35,11 +36,21 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStages = 3;
 constexpr int kD = 128;
 constexpr uint32_t kTile = 4096;                 // bytes of K (and of V) of a warp's stage
 constexpr float kMove = 8.0f;                    // move the reference past 2^8 growth
-constexpr float kHuge = 3.0e38f;
+// Exponents of e4m3 rows within 2^+-50 of one: their sums are taken from the weights (2^(x - mx)
+// times 2^-e stays far from fp32's ends); beyond it they get exponentials of their own.
+constexpr float kFar = 50.0f;
+
+// Stages of a warp's ring and CTAs per SM: a warp is a long chain of dependent instructions (a tile
+// takes it over a thousand cycles whatever the memory does), so the more of them the better, as far
+// as registers go: 64 accumulators a lane allow twelve warps, 128 of them eight.
+template <int MT, int NT>
+struct Plan {
+    static constexpr int kCtas = MT == 1 && NT == 1 ? 3 : 2;
+    static constexpr int kStages = MT == 1 && NT == 1 ? 2 : 3;
+};
 
 template <bool E8>
 struct Shape {
@@ -56,8 +67,8 @@ __host__ __device__ constexpr size_t q_bytes()
 template <bool E8, int MT, int NT>
 __host__ __device__ constexpr size_t decode_smem()
 {
-    return (size_t)kWarps * kStages * 2 * kTile + q_bytes<E8, MT, NT>() +
-           (E8 ? (size_t)kWarps * kStages * 32 * 8 : 0);
+    return (size_t)kWarps * Plan<MT, NT>::kStages * 2 * kTile + q_bytes<E8, MT, NT>() +
+           (E8 ? (size_t)kWarps * Plan<MT, NT>::kStages * 32 * 16 : 0);
 }
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool on)
@@ -165,24 +176,24 @@ __device__ __forceinline__ float odd_value(const KvView &kv, int64_t row, int g,
 // E8: e4m3 cells (else bf16).  MT: 16-row fragments of an item's rows.  TQ: type of q and out;
 // NT: 16-bit terms of a query or weight.
 template <bool E8, int MT, typename TQ, int NT>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, (Plan<MT, NT>::kCtas))
 dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const TQ *__restrict__ q,
-                    int64_t ld_q, int H_q, float scale_log2, TQ *__restrict__ out,
+                    int64_t ld_q, int H_q, float scale_log2, float q_sign, TQ *__restrict__ out,
                     float *__restrict__ lse, float *__restrict__ partial, Split *__restrict__ splits,
                     int by_item)
 {
     using S = Shape<E8>;
-    constexpr int kRows = 16 * MT;
+    constexpr int kRows = 16 * MT, kStages = Plan<MT, NT>::kStages;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int bad_s, odd_s;
-    __shared__ float red_m[kWarps][kRows], red_l[kWarps][kRows], q_scale_s[kRows];
+    __shared__ float red_m[kWarps][kRows], red_l[kWarps][kRows], top_s[MT];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g8 = lane >> 2, c4 = lane & 3;
     unsigned char *ring = smem + (size_t)warp * kStages * 2 * kTile;
     uint4 *qf = reinterpret_cast<uint4 *>(smem + (size_t)kWarps * kStages * 2 * kTile);
-    // factor of the logit and exponent of the value, per cell of a stage (E8)
-    float2 *exps = reinterpret_cast<float2 *>(reinterpret_cast<unsigned char *>(qf) + q_bytes<E8, MT, NT>()) +
+    // per cell of a stage (E8): factor of the logit, exponent e of the value, 2^-e
+    float4 *exps = reinterpret_cast<float4 *>(reinterpret_cast<unsigned char *>(qf) + q_bytes<E8, MT, NT>()) +
                    warp * kStages * 32;
 
     pdl_wait();
@@ -190,6 +201,7 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
     QSA_AFTER_WAIT(qp);
     pdl_trigger();
 
+    const float inv_scale = 1.0f / scale_log2;
     int64_t per, x, x1;
     WorkItem it;
     const int G = H_q / kv.H_kv;
@@ -215,42 +227,61 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
         if (tid == 0) bad_s = odd_s = 0;
         // ---- the query's fragments: lane's rows g8 and g8 + 8 of each fragment, k permuted as
         // the key rows are read (thread c4 holds 16 contiguous bytes of each block)
-        float q_back[MT][2];  // what the rows' logits are multiplied by
+        float q_back = 1.0f;  // what undoes the queries' scaling
         {
             constexpr int E = E8 ? 16 : 8;       // dims of a thread in a block
             constexpr int kBlocks = kD / (4 * E);
-            for (int mt = warp; mt < MT; mt += kWarps) {
+            const int mt = warp;
+            auto load_row = [&](int hf, float *xa) {
+                const int r = mt * 16 + g8 + 8 * hf;
+                const TQ *src =
+                    qp + (t0 + tok0 + r / G) * ld_q + (int64_t)(it.g * G + r % G) * kD + c4 * E;
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+                    for (int e = 0; e < E; e += 8) {
+                        if (r < rows) {
+                            load8(src + b * 4 * E + e, xa + b * E + e);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) xa[b * E + e + k] = 0.0f;
+                        }
+                    }
+            };
+            float mul = q_sign;
+            if constexpr (E8) {
+                // fp16 holds the queries once the tile's largest magnitude is below 2^8: one power
+                // of two for all rows, as a row 2^20 times smaller than another keeps 2^-13 of its
+                // own largest value and has logits that much smaller
+                if (mt < MT) {
+                    float top = 0.0f;
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        float xa[kBlocks * E];
+                        load_row(hf, xa);
+#pragma unroll
+                        for (int e = 0; e < kBlocks * E; ++e)
+                            if (isfinite(xa[e])) top = fmaxf(top, fabsf(xa[e]));
+                    }
+                    top = warp_max(top);
+                    if (lane == 0) top_s[mt] = top;
+                }
+                __syncthreads();
+                float top = top_s[0];
+#pragma unroll
+                for (int i = 1; i < MT; ++i) top = fmaxf(top, top_s[i]);
+                const int ex = (int)(__float_as_uint(top) >> 23) - 127;
+                const int sh = top > 0.0f ? min(max(7 - ex, -120), 100) : 0;
+                q_back = two_to(-sh);
+                mul = q_sign * two_to(sh);
+            }
+            if (mt < MT) {
                 float xa[2][kBlocks * E];
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-                    const int r = mt * 16 + g8 + 8 * hf;
-                    const TQ *src =
-                        qp + (t0 + tok0 + r / G) * ld_q + (int64_t)(it.g * G + r % G) * kD + c4 * E;
+                    load_row(hf, xa[hf]);
 #pragma unroll
-                    for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-                        for (int e = 0; e < E; e += 8) {
-                            if (r < rows) {
-                                load8(src + b * 4 * E + e, &xa[hf][b * E + e]);
-                            } else {
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) xa[hf][b * E + e + k] = 0.0f;
-                            }
-                        }
-                    if constexpr (E8) {
-                        // fp16 holds the row once its largest magnitude is below 2^8
-                        float top = 0.0f;
-#pragma unroll
-                        for (int e = 0; e < kBlocks * E; ++e) top = fmaxf(top, fabsf(xa[hf][e]));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                        const int ex = top > 0.0f && top < kHuge ? (int)(__float_as_uint(top) >> 23) - 127 : 0;
-                        const int sh = min(max(7 - ex, -100), 100);
-                        const float mul = two_to(sh);
-#pragma unroll
-                        for (int e = 0; e < kBlocks * E; ++e) xa[hf][e] *= mul;
-                        q_scale_s[r] = two_to(-sh);
-                    }
+                    for (int e = 0; e < kBlocks * E; ++e) xa[hf][e] *= mul;
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -266,11 +297,6 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
             }
         }
         __syncthreads();
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-                q_back[mt][hf] = E8 ? q_scale_s[mt * 16 + g8 + 8 * hf] : 1.0f;
         int last[MT][2];  // the last cell each row sees
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -280,6 +306,8 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
                 last[mt][hf] = r < rows ? (ws.causal ? pos0 + r / G : cells - 1) : -1;
             }
 
+        // mx: the rows' reference; l: the sums in its units.  E8 with exponents far apart (wide):
+        // l in units of ms, a reference of the logits alone.
         float o[MT][16][4];
         float ms[MT][2], mx[MT][2], l[MT][2];
 #pragma unroll
@@ -291,53 +319,73 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
             ms[mt][0] = ms[mt][1] = mx[mt][0] = mx[mt][1] = -INFINITY;
             l[mt][0] = l[mt][1] = 0.0f;
         }
+        bool wide = false;
 
-        // ---- the ring: row_next is the pool row of this lane's cell of the tile to be issued
+        // ---- the ring: a tile's cells are looked up two turns before its copies are issued (p_next,
+        // entry_next: this lane's cell of the next tile to issue, and its page)
         const int my_key = lane < S::kKeys ? lane : 0;
         bool bad = false, odd = false;
-        auto row_of = [&](int tile) -> int64_t {
+        int32_t p_next = -1, entry_next = -1;
+        auto look_up = [&](int tile) {
             const int p = tile * ws.kt + warp * S::kKeys + my_key;
-            if (tile >= tile1 || p >= n_see) return -2;  // not there: zeros
-            const int64_t row = cell_row(kv, it.s, t0, p);
-            bad |= row < 0;
-            return row;
-        };
-        float2 pend = make_float2(0.0f, 0.0f);
-        auto load_exps = [&](int64_t row) {
-            float2 f = make_float2(0.0f, 0.0f);
-            if (row >= 0) {
-                const int ek = (int)kv.K_exp[row * kv.H_kv + it.g] - kExpBias;
-                const int ev = (int)kv.V_exp[row * kv.H_kv + it.g] - kExpBias;
-                f.x = two_to(min(max(ek, kExpMin), kExpMax)) * scale_log2;
-                f.y = (float)min(max(ev, kExpMin), kExpMax);
+            p_next = tile < tile1 && p < n_see ? p : -1;
+            if (kv.table && p_next >= 0) {
+                const int64_t j = p >> kv.page_shift;
+                entry_next = j < kv.ld_table ? kv.table[(int64_t)it.s * kv.ld_table + j] : -1;
             }
-            return f;
         };
-        const unsigned char *Kb = static_cast<const unsigned char *>(kv.K) + (int64_t)it.g * S::kRowBytes;
-        const unsigned char *Vb = static_cast<const unsigned char *>(kv.V) + (int64_t)it.g * S::kRowBytes;
-        const int64_t ldk_b = kv.ld_k * (E8 ? 1 : 2), ldv_b = kv.ld_v * (E8 ? 1 : 2);
-        auto issue = [&](int stage, int64_t row) {
-            constexpr int kChunks = S::kRowBytes / 16, kAt = 32 / kChunks;
+        auto row_next = [&]() -> int32_t {
+            if (p_next < 0) return -1;  // not there: zeros
+            if (!kv.table) return (int32_t)t0 + p_next;
+            if ((uint32_t)entry_next >= (uint32_t)kv.n_pages) {
+                bad = true;
+                return -1;
+            }
+            return (entry_next << kv.page_shift) | (p_next & ((1 << kv.page_shift) - 1));
+        };
+        int pend_k = kExpBias, pend_v = kExpBias;
+        auto load_exps = [&](int32_t row) {
+            if (row >= 0) {
+                pend_k = kv.K_exp[(int64_t)row * kv.H_kv + it.g];
+                pend_v = kv.V_exp[(int64_t)row * kv.H_kv + it.g];
+            }
+        };
+        const float key_scale = scale_log2 * q_back;
+        auto keep_exps = [&](int stage) {
+            const int ek = min(max(pend_k - kExpBias, kExpMin), kExpMax);
+            const int ev = min(max(pend_v - kExpBias, kExpMin), kExpMax);
+            exps[stage * 32 + lane] = make_float4(two_to(ek) * key_scale, (float)ev, two_to(-ev), 0.0f);
+        };
+        constexpr int kChunks = S::kRowBytes / 16, kAt = 32 / kChunks;
+        const int cc = lane & (kChunks - 1), r0 = lane / kChunks;
+        const unsigned char *Kl =
+            static_cast<const unsigned char *>(kv.K) + (int64_t)it.g * S::kRowBytes + cc * 16;
+        const unsigned char *Vl =
+            static_cast<const unsigned char *>(kv.V) + (int64_t)it.g * S::kRowBytes + cc * 16;
+        const int ldk_b = (int)kv.ld_k * (E8 ? 1 : 2), ldv_b = (int)kv.ld_v * (E8 ? 1 : 2);
+        auto issue = [&](int stage, int32_t row) {
             const uint32_t st = smem_u32(ring + stage * 2 * kTile);
-            const int c = lane & (kChunks - 1), r0 = lane / kChunks;
 #pragma unroll
             for (int i = 0; i < S::kKeys / kAt; ++i) {
                 const int r = r0 + kAt * i;
-                const int64_t rr = __shfl_sync(0xffffffffu, row, r);
+                const int32_t rr = __shfl_sync(0xffffffffu, row, r);
                 const bool on = rr >= 0;
                 const int64_t at = on ? rr : 0;
-                cp16(st + k_off<E8>(r, c), Kb + at * ldk_b + c * 16, on);
-                cp16(st + kTile + v_off<E8>(r, c), Vb + at * ldv_b + c * 16, on);
+                cp16(st + k_off<E8>(r, cc), Kl + at * ldk_b, on);
+                cp16(st + kTile + v_off<E8>(r, cc), Vl + at * ldv_b, on);
             }
         };
-        int64_t row_next = row_of(tile0);
+        look_up(tile0);
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) {
-            const int64_t row = row_next;
-            row_next = row_of(tile0 + i + 1);
+            const int32_t row = row_next();
+            look_up(tile0 + i + 1);
             if (tile0 + i < tile1) {
                 issue(i, row);
-                if constexpr (E8) exps[i * 32 + lane] = load_exps(row);
+                if constexpr (E8) {
+                    load_exps(row);
+                    keep_exps(i);
+                }
             }
             cp_commit();
         }
@@ -346,16 +394,16 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
             cp_wait<kStages - 2>();
             __syncwarp();
             const unsigned char *sk = ring + slot * 2 * kTile, *sv_ = sk + kTile;
-            const float2 *ex = exps + slot * 32;
+            const float4 *ex = exps + slot * 32;
             const int j0 = tile * ws.kt + warp * S::kKeys;
             // ---- issue the tile kStages - 1 ahead into the stage read in the last turn
             {
                 const int nslot = slot == 0 ? kStages - 1 : slot - 1;
-                const int64_t row = row_next;
-                row_next = row_of(tile + kStages);
+                const int32_t row = row_next();
+                look_up(tile + kStages);
                 if (tile + kStages - 1 < tile1) {
                     issue(nslot, row);
-                    if constexpr (E8) pend = load_exps(row);
+                    if constexpr (E8) load_exps(row);
                 }
                 cp_commit();
             }
@@ -420,63 +468,83 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
                             }
                     }
                 }
-                // ---- scaled to log2 units, masked; the references move when they have to
-                float ev[S::kGroups * 2][2];
+                // ---- masked, and the references moved where they have to: on bf16 cells the raw
+                // logit is compared, on e4m3 cells x = logit + e in log2 units takes its place
+                bool far = false;
+                if constexpr (E8) {
+#pragma unroll
+                    for (int n = 0; n < S::kGroups * 2; ++n) {
+                        const float4 f0 = ex[8 * n + 2 * c4], f1 = ex[8 * n + 2 * c4 + 1];
+                        far |= fabsf(f0.y) > kFar || fabsf(f1.y) > kFar;
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                            for (int hf = 0; hf < 2; ++hf) {
+                                s[mt][n][2 * hf] = fmaf(s[mt][n][2 * hf], f0.x, f0.y);
+                                s[mt][n][2 * hf + 1] = fmaf(s[mt][n][2 * hf + 1], f1.x, f1.y);
+                            }
+                    }
+                }
+                if (edge) {
+#pragma unroll
+                    for (int n = 0; n < S::kGroups * 2; ++n)
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (j0 + 8 * n + 2 * c4 + (i & 1) > last[mt][i >> 1]) s[mt][n][i] = -INFINITY;
+                }
                 bool move = false;
 #pragma unroll
-                for (int n = 0; n < S::kGroups * 2; ++n) {
-                    float f0 = scale_log2, f1 = scale_log2;
-                    ev[n][0] = ev[n][1] = 0.0f;
-                    if constexpr (E8) {
-                        const float4 f = *reinterpret_cast<const float4 *>(&ex[8 * n + 2 * c4]);
-                        f0 = f.x;
-                        ev[n][0] = f.y;
-                        f1 = f.z;
-                        ev[n][1] = f.w;
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        // (-inf before the first cell: any finite logit moves it)
+                        const float over = E8 ? mx[mt][hf] + kMove : (mx[mt][hf] + kMove) * inv_scale;
+#pragma unroll
+                        for (int n = 0; n < S::kGroups * 2; ++n)
+                            move |= fmaxf(s[mt][n][2 * hf], s[mt][n][2 * hf + 1]) > over;
                     }
-                    const int j = j0 + 8 * n + 2 * c4;
+                if constexpr (E8) {
+                    if (!wide && __any_sync(0xffffffffu, far)) {
+                        wide = true;  // so far l is in units of mx
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
+                        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            const float a = s[mt][n][2 * hf] * (f0 * q_back[mt][hf]);
-                            const float b = s[mt][n][2 * hf + 1] * (f1 * q_back[mt][hf]);
-                            s[mt][n][2 * hf] = edge && j > last[mt][hf] ? -INFINITY : a;
-                            s[mt][n][2 * hf + 1] = edge && j + 1 > last[mt][hf] ? -INFINITY : b;
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const float v = s[mt][n][2 * hf + e];
-                                move |= v > ms[mt][hf] + kMove;
-                                if constexpr (E8) move |= v + ev[n][e] > mx[mt][hf] + kMove;
-                            }
-                        }
+                            for (int hf = 0; hf < 2; ++hf) ms[mt][hf] = mx[mt][hf];
                     }
+                    move |= wide;
                 }
                 if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf) {
-                            float a = ms[mt][hf], b = mx[mt][hf];
+                            float b = mx[mt][hf], a = ms[mt][hf];
 #pragma unroll
                             for (int n = 0; n < S::kGroups * 2; ++n)
 #pragma unroll
                                 for (int e = 0; e < 2; ++e) {
-                                    a = fmaxf(a, s[mt][n][2 * hf + e]);
-                                    if constexpr (E8) b = fmaxf(b, s[mt][n][2 * hf + e] + ev[n][e]);
+                                    const float v = s[mt][n][2 * hf + e];
+                                    b = fmaxf(b, E8 ? v : v * scale_log2);
+                                    if constexpr (E8) {
+                                        if (wide) a = fmaxf(a, v - ex[8 * n + 2 * c4 + e].y);
+                                    }
                                 }
-                            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-                            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-                            const float al = a == -INFINITY ? 1.0f : ex2(ms[mt][hf] - a);
-                            ms[mt][hf] = a;
-                            l[mt][hf] *= al;
-                            float ao = al;
+                            b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 1));
+                            b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 2));
+                            const float ao = b == -INFINITY ? 1.0f : ex2(mx[mt][hf] - b);
+                            mx[mt][hf] = b;
+                            float al = ao;
                             if constexpr (E8) {
-                                b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 1));
-                                b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 2));
-                                ao = b == -INFINITY ? 1.0f : ex2(mx[mt][hf] - b);
-                                mx[mt][hf] = b;
+                                if (wide) {
+                                    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+                                    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+                                    al = a == -INFINITY ? 1.0f : ex2(ms[mt][hf] - a);
+                                    ms[mt][hf] = a;
+                                }
                             }
+                            l[mt][hf] *= al;
 #pragma unroll
                             for (int n = 0; n < 16; ++n) {
                                 o[mt][n][2 * hf] *= ao;
@@ -488,22 +556,48 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
 #pragma unroll
                 for (int kg = 0; kg < S::kGroups; ++kg) {
                     uint32_t a[MT][NT][4];
+                    float2 iv[2];  // 2^-e of this thread's cells
+                    if constexpr (E8) {
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            const float4 *f = ex + 8 * (2 * kg + n) + 2 * c4;
+                            iv[n] = make_float2(f[0].z, f[1].z);
+                        }
+                    }
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
                         float w[2][2][2];  // [n tile][row half][cell]
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf) {
-                            const float us = ms[mt][hf] == -INFINITY ? 0.0f : ms[mt][hf];
                             const float ux = mx[mt][hf] == -INFINITY ? 0.0f : mx[mt][hf];
 #pragma unroll
                             for (int n = 0; n < 2; ++n)
 #pragma unroll
                                 for (int e = 0; e < 2; ++e) {
                                     const float v = s[mt][2 * kg + n][2 * hf + e];
-                                    const float p = ex2(v - us);
-                                    l[mt][hf] += p;
-                                    w[n][hf][e] = E8 ? ex2(v + ev[2 * kg + n][e] - ux) : p;
+                                    const float p = ex2(E8 ? v - ux : fmaf(v, scale_log2, -ux));
+                                    w[n][hf][e] = p;
+                                    if constexpr (E8) {
+                                        const float g = e ? iv[n].y : iv[n].x;
+                                        if (!wide) l[mt][hf] = fmaf(p, g, l[mt][hf]);
+                                    } else {
+                                        l[mt][hf] += p;
+                                    }
                                 }
+                        }
+                        if constexpr (E8) {
+                            if (wide) {
+#pragma unroll
+                                for (int hf = 0; hf < 2; ++hf) {
+                                    const float us = ms[mt][hf] == -INFINITY ? 0.0f : ms[mt][hf];
+#pragma unroll
+                                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                                        for (int e = 0; e < 2; ++e)
+                                            l[mt][hf] += ex2(s[mt][2 * kg + n][2 * hf + e] -
+                                                             ex[8 * (2 * kg + n) + 2 * c4 + e].y - us);
+                                }
+                            }
                         }
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
@@ -565,7 +659,7 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
             }
             if constexpr (E8) {
                 const int nslot = slot == 0 ? kStages - 1 : slot - 1;
-                if (tile + kStages - 1 < tile1) exps[nslot * 32 + lane] = pend;
+                if (tile + kStages - 1 < tile1) keep_exps(nslot);
             }
             __syncwarp();
             slot = slot == kStages - 1 ? 0 : slot + 1;
@@ -574,7 +668,13 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
         if (__any_sync(0xffffffffu, bad) && lane == 0) bad_s = 1;
         if (__any_sync(0xffffffffu, odd) && lane == 0) odd_s = 1;
 
-        // ---- join the four warps: o in units of the logits' reference
+        // ---- join the four warps: o in units of the sums' reference
+        if (!E8 || !wide) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) ms[mt][hf] = mx[mt][hf];
+        }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -600,8 +700,7 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
                 const int r = mt * 16 + g8 + 8 * hf;
                 const float m = fmaxf(fmaxf(red_m[0][r], red_m[1][r]), fmaxf(red_m[2][r], red_m[3][r]));
                 const float u = m == -INFINITY ? 0.0f : m;
-                const float f = E8 ? (mx[mt][hf] == -INFINITY ? 0.0f : exp2f(mx[mt][hf] - u))
-                                   : (ms[mt][hf] == -INFINITY ? 0.0f : exp2f(ms[mt][hf] - u));
+                const float f = mx[mt][hf] == -INFINITY ? 0.0f : exp2f(mx[mt][hf] - u);
                 float *dst = ob + (size_t)(warp * kRows + r) * kPitch;
 #pragma unroll
                 for (int n = 0; n < 16; ++n)
@@ -670,11 +769,11 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
     }
 }
 
-constexpr int kMaxCtas = 2 * kTargetSMs;
+constexpr int kMaxCtas = 3 * kTargetSMs;
 
-int decode_ctas()
+int decode_ctas(int per_sm)
 {
-    const int n = 2 * device_sm_count();
+    const int n = per_sm * device_sm_count();
     return n < kMaxCtas ? n : kMaxCtas;
 }
 
@@ -688,14 +787,17 @@ cudaError_t run(const DenseArgs &a, void *workspace, cudaStream_t st)
     ws.H_kv = a.kv.H_kv;
     ws.causal = a.causal;
     ws.over = 0;
+    // the kernel takes a positive scale: a negative one turns the queries' signs, zero clears them
+    const float scale = (a.scale == 0.0f ? 1.0f : fabsf(a.scale)) * kLog2e;
+    const float q_sign = a.scale == 0.0f ? 0.0f : (a.scale < 0.0f ? -1.0f : 1.0f);
     constexpr size_t smem = decode_smem<E8, MT, NT>();
     cudaError_t e = ensure_kernel_attrs<dense_decode_kernel<E8, MT, TQ, NT>>(smem);
     if (e != cudaSuccess) return e;
-    const int ctas = decode_ctas();
+    const int ctas = decode_ctas(Plan<MT, NT>::kCtas);
     Split *splits = static_cast<Split *>(workspace);
     float *partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + kMaxCtas * sizeof(Split));
     e = launch(dense_decode_kernel<E8, MT, TQ, NT>, dim3((unsigned)ctas), dim3(kThreads), smem, st, 1, a.kv,
-               a.sv, ws, static_cast<const TQ *>(a.q), a.ld_q, a.H_q, a.scale * kLog2e,
+               a.sv, ws, static_cast<const TQ *>(a.q), a.ld_q, a.H_q, scale, q_sign,
                static_cast<TQ *>(a.out), a.lse, partial, splits, (int)join_by_item(a, ws.rt, ctas));
     if (e != cudaSuccess) return e;
     return launch_dense_join<TQ>(splits, partial, ctas, 16 * MT, ws.rt, a, st);
@@ -708,6 +810,7 @@ bool dense_decode_ok(const DenseArgs &a, int64_t max_q)
     const int G = a.H_q / a.kv.H_kv;
     if (a.d != kD || (a.kv_dtype != QSA_BF16 && a.kv_dtype != QSA_E4M3)) return false;
     if (a.kv_dtype == QSA_E4M3 && (a.kv.ld_k % 16 || a.kv.ld_v % 16)) return false;
+    if (a.kv.ld_k > (1 << 28) || a.kv.ld_v > (1 << 28)) return false;  // strides in 32 bits
     // a fragment holds all heads of a KV head; fp32 queries come in several terms of one
     if (G > (a.q_dtype == QSA_F32 ? 16 : 32)) return false;
     return a.q_dtype == QSA_F32 || max_q * G <= 64;

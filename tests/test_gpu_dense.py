@@ -3,7 +3,9 @@ draft verification, against the 64-bit forms of dense_reference.
 
 Tolerances.  With A = sum_j softmax_j |v_j| (computed in 64 bits), an output is off by at most
   A * (2 * ds + (n + 64) * 2^-24)      fp32 sums over d dims and n cells, ds the logits' error
-  + A * 2^-8 or 2^-11                  weights rounded to bf16 or fp16 (tensor-core forms)
+  + A * 2^-8                           weights rounded to bf16 (the tensor-core forms for bf16
+                                       queries: bf16 cells at any number of rows, e4m3 cells at
+                                       many; with few rows on e4m3 cells they are fp16, 2^-11)
   + 2^-25 * max_j(softmax_j u_j) * sum_j |v_j| / u_j     fp16 weights below fp16's normal range:
                                        on e4m3 cells a weight multiplies the code v_j / u_j,
                                        u_j = 2^e_j, so it carries u_j; its unit is no larger than
@@ -110,7 +112,7 @@ def tolerance(q, k, v, first, scale, causal, want, q_dtype, kv_dtype, units=None
     ds = (d + 16) * 2.0 ** -24 * abs(scale) * qk * 2  # sum|q||k| <= |q||k| (2: cancellation inside)
     rel = 2 * ds + (n + 64) * 2.0 ** -24
     if q_dtype == BF16:
-        rel += 2.0 ** -11 if kv_dtype == E4M3 else 2.0 ** -8
+        rel += 2.0 ** -8
     if kv_dtype == E4M3 and k.shape[0]:
         if units is None:  # rows as the cache writes them
             top = np.abs(v).max(-1)
@@ -335,6 +337,51 @@ def test_large_logits_and_scales(news, kv_dtype):
     pool = Pool([150, 700], 2, 128, 32, kv_dtype, seed=10)
     run_paged(pool, [news, news], 16, BF16, seed=11, scale=8.0)
     run_paged(pool, [news, news], 16, BF16, seed=12, scale=0.0)
+
+
+@pytest.mark.parametrize("news", [1, 4, 7, 60])
+@pytest.mark.parametrize("q_dtype", [BF16, F32])
+def test_exponents_far_apart(news, q_dtype):
+    """e4m3 values whose rows' exponents span the whole range, all the large ones in one part of
+    the sequence, and rows of zeros (the smallest exponent)."""
+    pool = Pool([300, 700], 2, 128, 32, E4M3, seed=20)
+    rng = np.random.default_rng(21)
+    for s in (0, 1):
+        rows = pool.rows(pool.table[s].cpu().numpy(), np.arange(pool.lens[s]))
+        e = rng.choice([27, 60, 90, 120, 127, 150], (len(rows), 2))
+        e[200:] = rng.choice([27, 127, 200, 227], (len(rows) - 200, 2)) if s else e[200:]
+        pool.Ve[rows] = torch.from_numpy(e.astype(np.uint8)).to(DEV)
+        pool.V.view(torch.uint8)[rows[10:20]] = 0
+        pool.v[s] = pool.values(s, np.arange(pool.lens[s]))[1]
+        pool.units[s] = 2.0 ** (e.astype(float) - 127)
+    run_paged(pool, [news, news], 16, q_dtype, seed=22)
+
+
+def test_every_code_comes_back_exactly():
+    """One cell: the output is its value, for each of the 256 codes, whichever kernel runs."""
+    for news, ex in ((1, 127), (3, 40), (40, 127), (40, 215), (40, 27)):
+        K = torch.zeros(2 * 8, 1, 128, device=DEV).to(E4M3)
+        V = torch.zeros(2 * 8, 1, 128, dtype=torch.uint8, device=DEV)
+        V[0, 0], V[8, 0] = torch.arange(128, device=DEV), torch.arange(128, 256, device=DEV)
+        e = torch.full((16, 1), ex, dtype=torch.uint8, device=DEV)
+        cache = qsa.PagedCache(K, V.view(E4M3), 8, K_exp=e, V_exp=e)
+        q = torch.randn(2 * news, 4, 128, device=DEV).to(BF16)
+        out = torch.zeros_like(q)
+        ws = torch.zeros(max(16, qsa.paged_attn_workspace_size(2 * news, 2, news, 4, 1, 128)), dtype=torch.uint8, device=DEV)
+        qsa.paged_attn(cache, i32([[0], [1]]), i32([0, news, 2 * news]), i32([1, 1]), q, out, 0.1, news, causal=False, workspace=ws)
+        want = ref.e4m3_values() * 2.0 ** (ex - 127)
+        got = out.double().cpu().numpy()
+        for s in (0, 1):
+            for i in (0, news - 1):
+                for h in range(4):
+                    np.testing.assert_array_equal(got[s * news + i, h], want[128 * s:128 * s + 128])
+
+
+@pytest.mark.parametrize("kv_dtype", [BF16, E4M3])
+@pytest.mark.parametrize("news", [1, 4, 60])
+def test_negative_scale(news, kv_dtype):
+    pool = Pool([150, 300], 2, 128, 32, kv_dtype, seed=23)
+    run_paged(pool, [news, news], 16, BF16, seed=24, scale=-0.2)
 
 
 @pytest.mark.parametrize("kv_dtype", [BF16, E4M3])
