@@ -288,6 +288,22 @@ __device__ __forceinline__ bool work_share(const SeqView &sv, const WorkShape &w
     return false;
 }
 
+// The same with item number `cta` whole, for work of few, short items: the list is its own.
+__device__ __forceinline__ bool work_item(const SeqView &sv, const WorkShape &w, int cta, int ctas, int64_t &per,
+                                          int64_t &x0, int64_t &x1, WorkItem &it)
+{
+    WorkShape one = w;
+    one.kt = one.over = 0;
+    if (!work_share(sv, one, cta, ctas, per, x0, x1, it)) return false;
+    int64_t t0;
+    int len;
+    seq_tokens(sv, it.s, t0, len);
+    it.tiles = item_tiles(w, len, seq_cells(sv, it.s, len), it.t);
+    it.start = x0 = 0;
+    x1 = per = w.over + it.tiles;
+    return true;
+}
+
 // The item after `it` in the list (its sequence's length and cells are looked up again).
 // Returns false past the end.  All 32 lanes call it with the same item.
 __device__ __forceinline__ bool work_next(const SeqView &sv, const WorkShape &w, WorkItem &it)

@@ -40,6 +40,7 @@ constexpr int kM = 128;                  // rows of a group
 constexpr int kN = 128;                  // cells of a tile
 constexpr int kSoftWarps = 16, kMmaWarp = 16, kLoadWarp = 17, kAuxWarp = 18;
 constexpr int kOver = 4;                 // an item's fixed cost in tiles
+constexpr int kWholeTiles = 8;           // items of no more tiles are not cut where each has a CTA
 constexpr uint32_t kHalf = 128 * 128;    // 16 KB: 128 rows x 64 dims of bf16
 constexpr uint32_t kTileB = 2 * kHalf;   // 32 KB: a K or V tile, or a group's queries
 constexpr uint32_t kTmemCols = 512;
@@ -61,7 +62,8 @@ struct Cfg {
     static constexpr int kThreads = 32 * (kAuxWarp + kAuxWarps);
 };
 constexpr uint32_t kRawTile = 128 * 128;  // 16 KB: 128 cells of codes
-constexpr int kAuxBar = 9;                // named barrier of the converting warps
+constexpr int kTeamWarps = 3;             // warps that convert K tiles, and V tiles
+constexpr int kAuxBar = 9;                // their named barriers: 9, 10
 
 struct Bars {
     uint64_t full[kMaxStages], empty[kMaxStages];
@@ -70,7 +72,7 @@ struct Bars {
     uint64_t s_full[2], p_full[2], o_full[2], q_full[2], q_free[2], drain;
     uint32_t tmem, pad;
     int32_t odd[kSlots], bad[kSlots];  // number + 1 of the part that set it
-    uint8_t exps[2][kN];               // e4m3: exponents of a raw tile's cells
+    uint8_t exps[2][2][kN];            // e4m3: exponents of the cells of K and V tiles, two turns
     float row[2][kM];                  // exchanged by the two threads of a row
 };
 
@@ -194,6 +196,15 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
     return d;
 }
 
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return d;
+}
+
 // The CTA's share of the list, part by part; every role walks the same parts.
 struct Parts {
     WorkItem it;
@@ -239,7 +250,7 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
                 const __grid_constant__ CUtensorMap mapV, const KvView kv, const SeqView sv,
                 const WorkShape ws, int box_rows, int H_q, float scale_log2,
                 __nv_bfloat16 *__restrict__ out, float *__restrict__ lse, float *__restrict__ partial, Split *__restrict__ splits,
-                int by_item, const WaitCtl wc)
+                int by_item, int whole_items, const WaitCtl wc)
 {
     constexpr int kStages = Cfg<E8>::kStages, kAuxWarps = Cfg<E8>::kAuxWarps;
     extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -253,7 +264,7 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform, as the compiler sees it
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&bars.full[s], kAuxWarps);
+            mbar_init(&bars.full[s], E8 ? kTeamWarps : kAuxWarps);
             mbar_init(&bars.empty[s], 1);
             mbar_init(&bars.raw[s], 1);
         }
@@ -266,7 +277,7 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bars.raw_full[s], 1);
-            mbar_init(&bars.raw_empty[s], kAuxWarps);
+            mbar_init(&bars.raw_empty[s], kTeamWarps);
         }
         mbar_init(&bars.drain, 1);
         for (int i = 0; i < kSlots; ++i) bars.odd[i] = bars.bad[i] = 0;
@@ -279,7 +290,11 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
     int64_t per;
     p.n = 0;
     if (!by_item && tid == 0) splits[blockIdx.x].s = -1;
-    if (!work_share(sv, ws, blockIdx.x, gridDim.x, per, p.x, p.x1, p.it)) return;
+    if (whole_items) {
+        if (!work_item(sv, ws, blockIdx.x, gridDim.x, per, p.x, p.x1, p.it)) return;
+    } else if (!work_share(sv, ws, blockIdx.x, gridDim.x, per, p.x, p.x1, p.it)) {
+        return;
+    }
     p.set(kv, sv, ws);
     if (p.tile1 <= p.tile0) {  // only places without a tile
         --p.n;
@@ -484,87 +499,96 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
                     if (nq[g] > 0 && !mbar_wait(&bars.q_full[g], (nq[g] - 1) & 1u)) ok = false;
             }
         } else if (E8 && warp >= kAuxWarp) {
-            // ---- e4m3 cells to bf16: value = code * 2^e, exact.  The six warps take a raw tile
-            // 16 codes a lane at a time; the exponents of the next tile are on their way meanwhile
-            // (lane l of warps 0-3: cell 32 warp + l).  In V tiles with an edge, what not every
-            // row sees is treated as below.
-            const int aux = warp - kAuxWarp, at = aux * 32 + lane;
-            uint32_t n = 0;
-            auto load_exp = [&](int tile, bool is_v) -> uint32_t {
-                const int j = tile * kN + at;
-                if (at >= kN || tile >= p.tile1 || j >= p.n_see) return kExpBias;
-                const int64_t row = cell_row(kv, p.it.s, p.t0, j);
-                return row >= 0 ? (is_v ? kv.V_exp : kv.K_exp)[row * kv.H_kv + p.it.g] : kExpBias;
+            // ---- e4m3 cells to bf16: value = code * 2^e, exact.  Three warps take the K tiles, three
+            // the V tiles; the exponents of a team's next tile are on their way meanwhile.  In V tiles
+            // with an edge, what not every row sees is treated as below.
+            const int team = (warp - kAuxWarp) / kTeamWarps;  // K tiles, V tiles
+            const int at = (warp - kAuxWarp - team * kTeamWarps) * 32 + lane;
+            const uint8_t *const exp_of = team ? kv.V_exp : kv.K_exp;
+            uint32_t turn = 0;
+            uint32_t ex[2];  // exponents of cells at and at + 96 of the next tile
+            auto load_exps = [&](int tile) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int c = at + 32 * kTeamWarps * i, j = tile * kN + c;
+                    ex[i] = kExpBias;
+                    if (c < kN && tile < p.tile1 && j < p.n_see) {
+                        const int64_t row = cell_row(kv, p.it.s, p.t0, j);
+                        if (row >= 0) ex[i] = exp_of[row * kv.H_kv + p.it.g];
+                    }
+                }
             };
             do {
-                uint32_t ex = load_exp(p.tile0, false);
-                for (int t = p.tile0; ok && t < p.tile1; ++t) {
-                    for (int half = 0; ok && half < 2; ++half, ++n) {
-                        const int s = (int)(n & 1u), st = (int)(n % kStages);
-                        if (at < kN) bars.exps[s][at] = (uint8_t)ex;
-                        bool here = bar_wait_warp(&bars.raw_full[s], (n >> 1) & 1u, wc.limit_ns);
-                        if (here && n >= kStages)
-                            here = bar_wait_warp(&bars.empty[st], ((n / kStages) - 1) & 1u, wc.limit_ns);
-                        // the exponents are there, and every warp is done with the other buffer's;
-                        // a wait that gave up ends all six warps' work
-                        uint32_t fail;
-                        asm volatile(
-                            "{\n\t.reg .pred p, c;\n\t"
-                            "setp.ne.u32 c, %1, 0;\n\t"
-                            "bar.red.or.pred p, %2, %3, c;\n\t"
-                            "selp.u32 %0, 1, 0, p;\n\t}"
-                            : "=r"(fail)
-                            : "r"((uint32_t)!here), "n"(kAuxBar), "n"(32 * Cfg<true>::kAuxWarps)
-                            : "memory");
-                        if (fail) {
-                            ok = false;
-                            break;
-                        }
-                        ex = load_exp(t + half, half == 0);
-                        const bool edge = half == 1 && p.edge(t);
-                        const int r0 = edge ? max(0, p.pos0 + 1 - t * kN) : kN, r1 = p.n_see - t * kN;
-                        const unsigned char *src = raw_tiles + (size_t)s * kRawTile;
-                        unsigned char *dst = ring + (size_t)st * kTileB;
-                        bool odd = false;
+                load_exps(p.tile0);
+                for (int t = p.tile0; t < p.tile1; ++t, ++turn) {
+                    const uint32_t n = 2 * turn + (uint32_t)team;  // raw tile `team`, stage n
+                    const int st = (int)(n % kStages);
+                    uint8_t *const exps = bars.exps[team][turn & 1u];
+                    exps[at] = (uint8_t)ex[0];
+                    if (at + 32 * kTeamWarps < kN) exps[at + 32 * kTeamWarps] = (uint8_t)ex[1];
+                    bool here = bar_wait_warp(&bars.raw_full[team], turn & 1u, wc.limit_ns);
+                    if (here && n >= kStages)
+                        here = bar_wait_warp(&bars.empty[st], ((n / kStages) - 1) & 1u, wc.limit_ns);
+                    // the exponents are there (the other buffer is free: every warp of the team is past
+                    // the last turn); a wait that gave up ends the whole team's work
+                    uint32_t fail;
+                    asm volatile(
+                        "{\n\t.reg .pred p, c;\n\t"
+                        "setp.ne.u32 c, %1, 0;\n\t"
+                        "bar.red.or.pred p, %2, %3, c;\n\t"
+                        "selp.u32 %0, 1, 0, p;\n\t}"
+                        : "=r"(fail)
+                        : "r"((uint32_t)!here), "r"(kAuxBar + team), "n"(32 * kTeamWarps)
+                        : "memory");
+                    if (fail) {
+                        ok = false;
+                        break;
+                    }
+                    load_exps(t + 1);
+                    const bool edge = team && p.edge(t);
+                    const int e0 = edge ? max(0, p.pos0 + 1 - t * kN) : kN, e1 = p.n_see - t * kN;
+                    const unsigned char *src = raw_tiles + (size_t)team * kRawTile;
+                    unsigned char *dst = ring + (size_t)st * kTileB;
+                    bool odd = false;
+                    // lane's 16 codes c of rows r, r + 12, ...: chunks 2 c and 2 c + 1 of the bf16 row; the
+                    // lanes of the upper dim half write them in the other order, as both halves lie on
+                    // the same banks
+                    const int c = at & 7;
+                    unsigned char *const w = dst + (c >> 2) * kHalf;
+                    const int first = 2 * (c & 3) + (c >> 2), second = first ^ 1;
 #pragma unroll 2
-                        for (int i = at; i < kN * 8; i += 32 * kAuxWarps) {
-                            const int r = i >> 3, c = i & 7;
-                            uint4 v = *reinterpret_cast<const uint4 *>(src + i * 16);
-                            uint32_t *u = reinterpret_cast<uint32_t *>(&v);
-                            if (r >= r0) {
+                    for (int r = at >> 3; r < kN; r += 4 * kTeamWarps) {
+                        uint4 v = *reinterpret_cast<const uint4 *>(src + r * 128 + c * 16);
+                        uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                        if (r >= e0) {
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    const uint32_t m = __vcmpeq4(u[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                                    odd |= m != 0 && r < r1;
-                                    u[k] = r < r1 ? u[k] & ~m : 0u;
-                                }
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t m = __vcmpeq4(u[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                odd |= m != 0 && r < e1;
+                                u[k] = r < e1 ? u[k] & ~m : 0u;
                             }
-                            const float f = two_to(min(max((int)bars.exps[s][r] - kExpBias, kExpMin), kExpMax));
-                            uint32_t o[8];
+                        }
+                        const float f = two_to(min(max((int)exps[r] - kExpBias, kExpMin), kExpMax));
+                        uint32_t o[8];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-                                    (__nv_fp8x2_storage_t)(u[k >> 1] >> (16 * (k & 1))), __NV_E4M3);
-                                const float2 x = __half22float2(__half2(h));
-                                o[k] = pack_bf16(x.x * f, x.y * f);
-                            }
-                            // chunks 2c, 2c + 1 of the row; lanes of the upper dim half in the
-                            // other order, as both halves lie on the same banks
-                            unsigned char *w = dst + (c >> 2) * kHalf + r * 128;
-                            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]);
-                            const uint4 hi = make_uint4(o[4], o[5], o[6], o[7]);
-                            const int first = 2 * (c & 3) + (c >> 2), second = first ^ 1;
-                            *reinterpret_cast<uint4 *>(w + ((first ^ (r & 7)) << 4)) = c >> 2 ? hi : lo;
-                            *reinterpret_cast<uint4 *>(w + ((second ^ (r & 7)) << 4)) = c >> 2 ? lo : hi;
+                        for (int k = 0; k < 8; ++k) {
+                            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+                                (__nv_fp8x2_storage_t)(u[k >> 1] >> (16 * (k & 1))), __NV_E4M3);
+                            const float2 x = mul2(__half22float2(__half2(h)), make_float2(f, f));
+                            o[k] = pack_bf16(x.x, x.y);
                         }
-                        if (odd) *reinterpret_cast<volatile int32_t *>(&bars.odd[p.n % kSlots]) = p.n + 1;
-                        // written by this warp (generic proxy), read by the tensor cores (async proxy)
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(&bars.raw_empty[s]);
-                            mbar_arrive(&bars.full[st]);
-                        }
+                        const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]);
+                        const uint4 hi = make_uint4(o[4], o[5], o[6], o[7]);
+                        *reinterpret_cast<uint4 *>(w + r * 128 + ((first ^ (r & 7)) << 4)) = c >> 2 ? hi : lo;
+                        *reinterpret_cast<uint4 *>(w + r * 128 + ((second ^ (r & 7)) << 4)) = c >> 2 ? lo : hi;
+                    }
+                    if (odd) *reinterpret_cast<volatile int32_t *>(&bars.odd[p.n % kSlots]) = p.n + 1;
+                    // written by this warp (generic proxy), read by the tensor cores (async proxy)
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&bars.raw_empty[team]);
+                        mbar_arrive(&bars.full[st]);
                     }
                 }
             } while (ok && p.next(kv, sv, ws));
@@ -806,7 +830,7 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
                 }
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             }
-            if (starts && tid == 0)
+            if (starts && tid == 0 && !whole_items)
                 note_split(splits, by_item, p.it, ends,
                            div_pos(p.it.start + ws.over + p.it.tiles - 1, per));
         } while (p.next(kv, sv, ws));
@@ -916,12 +940,18 @@ static qsa_status run_tc(const DenseArgs &a, void *workspace, cudaStream_t st)
     if (ctas > kMaxCtas) ctas = kMaxCtas;
     Split *splits = static_cast<Split *>(workspace);
     float *partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + kMaxCtas * sizeof(Split));
+    // few items of few tiles, as far as the host knows: a CTA each, and nothing to join (a prompt of
+    // 777 tokens, 8 / 2 heads: 17 us instead of 31)
+    const int64_t items = ((a.sv.n_tok + ws.rt - 1) / ws.rt + a.sv.n_seq) * a.kv.H_kv;
+    const int64_t cells = a.kv.table ? a.kv.ld_table << a.kv.page_shift : a.sv.n_tok;
+    const bool whole = items <= ctas && cells <= kWholeTiles * kN;
+    if (whole) ctas = (int)items;
     cudaError_t e = launch(dense_tc_kernel<E8>, dim3((unsigned)ctas), dim3(Cfg<E8>::kThreads), smem, st, 1, mq,
                            mk, mv, a.kv, a.sv, ws, box_rows, a.H_q, a.scale * kLog2e,
-                           static_cast<__nv_bfloat16 *>(a.out), a.lse, partial, splits, (int)join_by_item(a, ws.rt, ctas),
-                           current_wait_ctl());
-    if (e != cudaSuccess) return QSA_ERR_CUDA;
-    e = launch_dense_join<__nv_bfloat16>(splits, partial, ctas, 2 * kM, kM / G, a, st);
+                           static_cast<__nv_bfloat16 *>(a.out), a.lse, partial, splits,
+                           (int)join_by_item(a, ws.rt, ctas), (int)whole, current_wait_ctl());
+    if (e == cudaSuccess && !whole)
+        e = launch_dense_join<__nv_bfloat16>(splits, partial, ctas, 2 * kM, kM / G, a, st);
     return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
 }
 

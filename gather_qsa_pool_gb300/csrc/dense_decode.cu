@@ -225,6 +225,63 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
 
         __syncthreads();  // the previous part's shared memory is free
         if (tid == 0) bad_s = odd_s = 0;
+        // ---- the ring (its first copies are under way before the queries are looked at): a tile's cells are looked up two turns before its copies are issued (p_next,
+        // entry_next: this lane's cell of the next tile to issue, and its page)
+        const int my_key = lane < S::kKeys ? lane : 0;
+        bool bad = false, odd = false;
+        int32_t p_next = -1, entry_next = -1;
+        auto look_up = [&](int tile) {
+            const int p = tile * ws.kt + warp * S::kKeys + my_key;
+            p_next = tile < tile1 && p < n_see ? p : -1;
+            if (kv.table && p_next >= 0) {
+                const int64_t j = p >> kv.page_shift;
+                entry_next = j < kv.ld_table ? kv.table[(int64_t)it.s * kv.ld_table + j] : -1;
+            }
+        };
+        auto row_next = [&]() -> int32_t {
+            if (p_next < 0) return -1;  // not there: zeros
+            if (!kv.table) return (int32_t)t0 + p_next;
+            if ((uint32_t)entry_next >= (uint32_t)kv.n_pages) {
+                bad = true;
+                return -1;
+            }
+            return (entry_next << kv.page_shift) | (p_next & ((1 << kv.page_shift) - 1));
+        };
+        int pend_k[kStages - 1], pend_v[kStages - 1];  // exponents on their way
+        auto load_exps = [&](int32_t row, int i) {
+            pend_k[i] = row >= 0 ? kv.K_exp[(int64_t)row * kv.H_kv + it.g] : kExpBias;
+            pend_v[i] = row >= 0 ? kv.V_exp[(int64_t)row * kv.H_kv + it.g] : kExpBias;
+        };
+        constexpr int kChunks = S::kRowBytes / 16, kAt = 32 / kChunks;
+        const int cc = lane & (kChunks - 1), r0 = lane / kChunks;
+        const unsigned char *Kl =
+            static_cast<const unsigned char *>(kv.K) + (int64_t)it.g * S::kRowBytes + cc * 16;
+        const unsigned char *Vl =
+            static_cast<const unsigned char *>(kv.V) + (int64_t)it.g * S::kRowBytes + cc * 16;
+        const int ldk_b = (int)kv.ld_k * (E8 ? 1 : 2), ldv_b = (int)kv.ld_v * (E8 ? 1 : 2);
+        auto issue = [&](int stage, int32_t row) {
+            const uint32_t st = smem_u32(ring + stage * 2 * kTile);
+#pragma unroll
+            for (int i = 0; i < S::kKeys / kAt; ++i) {
+                const int r = r0 + kAt * i;
+                const int32_t rr = __shfl_sync(0xffffffffu, row, r);
+                const bool on = rr >= 0;
+                const int64_t at = on ? rr : 0;
+                cp16(st + k_off<E8>(r, cc), Kl + at * ldk_b, on);
+                cp16(st + kTile + v_off<E8>(r, cc), Vl + at * ldv_b, on);
+            }
+        };
+        look_up(tile0);
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) {
+            const int32_t row = row_next();
+            look_up(tile0 + i + 1);
+            if (tile0 + i < tile1) {
+                issue(i, row);
+                if constexpr (E8) load_exps(row, i);
+            }
+            cp_commit();
+        }
         // ---- the query's fragments: lane's rows g8 and g8 + 8 of each fragment, k permuted as
         // the key rows are read (thread c4 holds 16 contiguous bytes of each block)
         float q_back = 1.0f;  // what undoes the queries' scaling
@@ -297,6 +354,17 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
             }
         }
         __syncthreads();
+        const float key_scale = scale_log2 * q_back;
+        auto keep_exps = [&](int stage, int i) {
+            const int ek = min(max(pend_k[i] - kExpBias, kExpMin), kExpMax);
+            const int ev = min(max(pend_v[i] - kExpBias, kExpMin), kExpMax);
+            exps[stage * 32 + lane] = make_float4(two_to(ek) * key_scale, (float)ev, two_to(-ev), 0.0f);
+        };
+        if constexpr (E8) {
+#pragma unroll
+            for (int i = 0; i < kStages - 1; ++i)
+                if (tile0 + i < tile1) keep_exps(i, i);
+        }
         int last[MT][2];  // the last cell each row sees
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -321,74 +389,6 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
         }
         bool wide = false;
 
-        // ---- the ring: a tile's cells are looked up two turns before its copies are issued (p_next,
-        // entry_next: this lane's cell of the next tile to issue, and its page)
-        const int my_key = lane < S::kKeys ? lane : 0;
-        bool bad = false, odd = false;
-        int32_t p_next = -1, entry_next = -1;
-        auto look_up = [&](int tile) {
-            const int p = tile * ws.kt + warp * S::kKeys + my_key;
-            p_next = tile < tile1 && p < n_see ? p : -1;
-            if (kv.table && p_next >= 0) {
-                const int64_t j = p >> kv.page_shift;
-                entry_next = j < kv.ld_table ? kv.table[(int64_t)it.s * kv.ld_table + j] : -1;
-            }
-        };
-        auto row_next = [&]() -> int32_t {
-            if (p_next < 0) return -1;  // not there: zeros
-            if (!kv.table) return (int32_t)t0 + p_next;
-            if ((uint32_t)entry_next >= (uint32_t)kv.n_pages) {
-                bad = true;
-                return -1;
-            }
-            return (entry_next << kv.page_shift) | (p_next & ((1 << kv.page_shift) - 1));
-        };
-        int pend_k = kExpBias, pend_v = kExpBias;
-        auto load_exps = [&](int32_t row) {
-            if (row >= 0) {
-                pend_k = kv.K_exp[(int64_t)row * kv.H_kv + it.g];
-                pend_v = kv.V_exp[(int64_t)row * kv.H_kv + it.g];
-            }
-        };
-        const float key_scale = scale_log2 * q_back;
-        auto keep_exps = [&](int stage) {
-            const int ek = min(max(pend_k - kExpBias, kExpMin), kExpMax);
-            const int ev = min(max(pend_v - kExpBias, kExpMin), kExpMax);
-            exps[stage * 32 + lane] = make_float4(two_to(ek) * key_scale, (float)ev, two_to(-ev), 0.0f);
-        };
-        constexpr int kChunks = S::kRowBytes / 16, kAt = 32 / kChunks;
-        const int cc = lane & (kChunks - 1), r0 = lane / kChunks;
-        const unsigned char *Kl =
-            static_cast<const unsigned char *>(kv.K) + (int64_t)it.g * S::kRowBytes + cc * 16;
-        const unsigned char *Vl =
-            static_cast<const unsigned char *>(kv.V) + (int64_t)it.g * S::kRowBytes + cc * 16;
-        const int ldk_b = (int)kv.ld_k * (E8 ? 1 : 2), ldv_b = (int)kv.ld_v * (E8 ? 1 : 2);
-        auto issue = [&](int stage, int32_t row) {
-            const uint32_t st = smem_u32(ring + stage * 2 * kTile);
-#pragma unroll
-            for (int i = 0; i < S::kKeys / kAt; ++i) {
-                const int r = r0 + kAt * i;
-                const int32_t rr = __shfl_sync(0xffffffffu, row, r);
-                const bool on = rr >= 0;
-                const int64_t at = on ? rr : 0;
-                cp16(st + k_off<E8>(r, cc), Kl + at * ldk_b, on);
-                cp16(st + kTile + v_off<E8>(r, cc), Vl + at * ldv_b, on);
-            }
-        };
-        look_up(tile0);
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) {
-            const int32_t row = row_next();
-            look_up(tile0 + i + 1);
-            if (tile0 + i < tile1) {
-                issue(i, row);
-                if constexpr (E8) {
-                    load_exps(row);
-                    keep_exps(i);
-                }
-            }
-            cp_commit();
-        }
         int slot = 0;
         for (int tile = tile0; tile < tile1; ++tile) {
             cp_wait<kStages - 2>();
@@ -403,7 +403,7 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
                 look_up(tile + kStages);
                 if (tile + kStages - 1 < tile1) {
                     issue(nslot, row);
-                    if constexpr (E8) load_exps(row);
+                    if constexpr (E8) load_exps(row, 0);
                 }
                 cp_commit();
             }
@@ -659,7 +659,7 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
             }
             if constexpr (E8) {
                 const int nslot = slot == 0 ? kStages - 1 : slot - 1;
-                if (tile + kStages - 1 < tile1) keep_exps(nslot);
+                if (tile + kStages - 1 < tile1) keep_exps(nslot, 0);
             }
             __syncwarp();
             slot = slot == kStages - 1 ? 0 : slot + 1;
@@ -813,7 +813,10 @@ bool dense_decode_ok(const DenseArgs &a, int64_t max_q)
     if (a.kv.ld_k > (1 << 28) || a.kv.ld_v > (1 << 28)) return false;  // strides in 32 bits
     // a fragment holds all heads of a KV head; fp32 queries come in several terms of one
     if (G > (a.q_dtype == QSA_F32 ? 16 : 32)) return false;
-    return a.q_dtype == QSA_F32 || max_q * G <= 64;
+    // rows beyond one fragment of bf16 cells (two of e4m3 cells) are the 128-row kernel's: 64
+    // sequences of up to 8,000 cells, 32 / 4 heads, bf16: 2 tokens 113 us here and 121 there, 3
+    // tokens 127 and 122, 8 tokens 224 and 128; e4m3: 4 tokens 135 and 258
+    return a.q_dtype == QSA_F32 || max_q * G <= (a.kv_dtype == QSA_E4M3 ? 32 : 16);
 }
 
 size_t dense_decode_workspace()
@@ -827,12 +830,10 @@ cudaError_t launch_dense_decode(const DenseArgs &a, int64_t max_q, void *workspa
     const bool e8 = a.kv_dtype == QSA_E4M3;
     if (a.q_dtype == QSA_F32)
         return e8 ? run<true, 1, float, 2>(a, workspace, st) : run<false, 1, float, 3>(a, workspace, st);
+    if (!e8) return run<false, 1, __nv_bfloat16, 1>(a, workspace, st);
     // one fragment while it holds every new token of a sequence
-    if (G <= 16 && max_q <= 16 / G)
-        return e8 ? run<true, 1, __nv_bfloat16, 1>(a, workspace, st)
-                  : run<false, 1, __nv_bfloat16, 1>(a, workspace, st);
-    return e8 ? run<true, 2, __nv_bfloat16, 1>(a, workspace, st)
-              : run<false, 2, __nv_bfloat16, 1>(a, workspace, st);
+    if (G <= 16 && max_q <= 16 / G) return run<true, 1, __nv_bfloat16, 1>(a, workspace, st);
+    return run<true, 2, __nv_bfloat16, 1>(a, workspace, st);
 }
 
 }  // namespace qsa

@@ -92,7 +92,7 @@ __device__ __forceinline__ int token_seq(const SeqView &sv, int64_t tok)
 // are in flight.  Bound by the bytes (a source row read once, its codes written once); with few
 // tokens by the launch and the look-up's dependent loads.
 template <typename TS, typename TD>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(128, 8)
 paged_write_kernel(const TS *__restrict__ k, const TS *__restrict__ v, int64_t ld_k, int64_t ld_v,
                    int H, int d, int lanes_log2, int group, SeqView sv, KvView kv, TD *K, TD *V,
                    uint8_t *K_exp, uint8_t *V_exp)
@@ -206,7 +206,7 @@ struct Raw8<uint8_t> {
 };
 
 template <typename TS, typename TD>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(128, 8)
 paged_read_kernel(KvView kv, int H, int d, int group, const int32_t *__restrict__ seq,
                   const int32_t *__restrict__ kv_len, int64_t n_seq, const int32_t *__restrict__ pos,
                   const int32_t *__restrict__ n_cells, int64_t n_list, int64_t max_cells,
@@ -276,10 +276,10 @@ paged_read_kernel(KvView kv, int H, int d, int group, const int32_t *__restrict_
     }
 }
 
-// Rows a warp looks up together: as many as leave sixteen warps per SM, one to eight.
+// Rows a warp looks up together: as many as leave 32 warps per SM, one to eight.
 int rows_group(int64_t rows)
 {
-    const int64_t per = rows / ((int64_t)device_sm_count() * 16);
+    const int64_t per = rows / ((int64_t)device_sm_count() * 32);
     return per >= 8 ? 8 : (per >= 4 ? 4 : (per >= 2 ? 2 : 1));
 }
 
