@@ -72,52 +72,81 @@ struct Row {
     }
 };
 
+// The packed forms of the above: two indices at a time.
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b)  // a + (-1) b: one rounding, as a - b
+{
+    float2 d, n = make_float2(-1.0f, -1.0f);
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(b)), "l"(reinterpret_cast<uint64_t &>(n)),
+          "l"(reinterpret_cast<uint64_t &>(a)));
+    return d;
+}
+
 // Sum of the warp's chunks [c0, c1) of the row's weights; every lane gets it.
 __device__ __forceinline__ double slice_sum(const Row &row, int64_t c0, int64_t c1, int64_t vocab, bool vec)
 {
     const int lane = threadIdx.x & 31;
-    float ws = 0.0f, wc = 0.0f;
-    auto take = [&](float p, float q, int64_t i) {
-        float d, e;
-        row.weight(p, q, i, d, e);
-        add_pair(ws, wc, d);
-        wc = __fadd_rn(wc, e);
+    float2 s = make_float2(0.0f, 0.0f), c = make_float2(0.0f, 0.0f);
+    auto take = [&](float2 p, float2 q, int64_t i) {
+        float2 d = p, e = make_float2(0.0f, 0.0f);
+        if (row.q) {
+            d = sub2(p, q);
+            const float2 b = sub2(d, p);
+            e = sub2(sub2(p, sub2(d, b)), add2(q, b));
+        }
+        const bool x = d.x > 0.0f && i != row.skip, y = d.y > 0.0f && i + 1 != row.skip;
+        d.x = x ? d.x : 0.0f;
+        d.y = y ? d.y : 0.0f;
+        e.x = x ? e.x : 0.0f;
+        e.y = y ? e.y : 0.0f;
+        const float2 t = add2(s, d), b = sub2(t, s);
+        c = add2(c, add2(add2(sub2(s, sub2(t, b)), sub2(d, b)), e));
+        s = t;
     };
     if (vec) {  // the vocabulary is a multiple of 4, rows are 16-byte aligned
-        for (int64_t c = c0; c < c1; c += 4) {
+        for (int64_t c_ = c0; c_ < c1; c_ += 4) {
             float4 p[4], q[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int64_t i = (c + u) * kChunk + 4 * lane;
-                const bool on = c + u < c1 && i < vocab;
+                const int64_t i = (c_ + u) * kChunk + 4 * lane;
+                const bool on = c_ + u < c1 && i < vocab;
                 p[u] = q[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 if (on) p[u] = *reinterpret_cast<const float4 *>(row.p + i);
                 if (on && row.q) q[u] = *reinterpret_cast<const float4 *>(row.q + i);
             }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int64_t i = (c + u) * kChunk + 4 * lane;
-                take(p[u].x, q[u].x, i);
-                take(p[u].y, q[u].y, i + 1);
-                take(p[u].z, q[u].z, i + 2);
-                take(p[u].w, q[u].w, i + 3);
+                const int64_t i = (c_ + u) * kChunk + 4 * lane;
+                take(make_float2(p[u].x, p[u].y), make_float2(q[u].x, q[u].y), i);
+                take(make_float2(p[u].z, p[u].w), make_float2(q[u].z, q[u].w), i + 2);
             }
         }
     } else {
         const int64_t end = min(c1 * kChunk, vocab);
-        for (int64_t i0 = c0 * kChunk + lane; i0 < end; i0 += 256) {
-            float p[8], q[8];
+        for (int64_t i0 = c0 * kChunk + 2 * lane; i0 < end; i0 += 256) {
+            float2 p[4], q[4];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int64_t i = i0 + 32 * u;
-                p[u] = i < end ? row.p[i] : 0.0f;
-                q[u] = row.q && i < end ? row.q[i] : 0.0f;
+            for (int u = 0; u < 4; ++u) {
+                const int64_t i = i0 + 64 * u;
+                p[u].x = i < end ? row.p[i] : 0.0f;
+                p[u].y = i + 1 < end ? row.p[i + 1] : 0.0f;
+                q[u].x = row.q && i < end ? row.q[i] : 0.0f;
+                q[u].y = row.q && i + 1 < end ? row.q[i + 1] : 0.0f;
             }
 #pragma unroll
-            for (int u = 0; u < 8; ++u) take(p[u], q[u], i0 + 32 * u);
+            for (int u = 0; u < 4; ++u) take(p[u], q[u], i0 + 64 * u);
         }
     }
-    return warp_sum_f64((double)ws + (double)wc);
+    return warp_sum_f64(((double)s.x + (double)s.y) + ((double)c.x + (double)c.y));
 }
 
 // The first index of the warp's chunks [c0, c1) whose running sum, from `base` on, passes x; the

@@ -34,18 +34,73 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float *x)
     *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Eight e4m3 codes of x * 2^-e (inv = 2^-e), packed little-endian.
-__device__ __forceinline__ uint2 encode8(const float *x, float inv)
-{
-    uint32_t w[2] = {0u, 0u};
+// Eight consecutive source values as they lie in memory.
+template <typename T>
+struct Src8;
+template <>
+struct Src8<float> {
+    uint32_t w[8];
+    __device__ __forceinline__ void clear()
+    {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float y0 = x[2 * i] * inv, y1 = x[2 * i + 1] * inv;
-        // infinities become NaN (0 * inf); the conversion clamps finite values to 448
-        y0 = isfinite(x[2 * i]) ? y0 : NAN;
-        y1 = isfinite(x[2 * i + 1]) ? y1 : NAN;
-        const uint32_t c = __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3);
-        w[i >> 1] |= c << (16 * (i & 1));
+        for (int i = 0; i < 8; ++i) w[i] = 0u;
+    }
+    __device__ __forceinline__ void load(const float *p)
+    {
+        const uint4 a = reinterpret_cast<const uint4 *>(p)[0], b = reinterpret_cast<const uint4 *>(p)[1];
+        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+    }
+    __device__ __forceinline__ float at(int i) const { return __uint_as_float(w[i]); }
+    // the largest magnitude, as bits (an order of its own: NaN and infinities come out on top)
+    __device__ __forceinline__ uint32_t top() const
+    {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
+        return m;
+    }
+};
+template <>
+struct Src8<__nv_bfloat16> {
+    uint32_t w[4];
+    __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0u; }
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p)
+    {
+        const uint4 a = *reinterpret_cast<const uint4 *>(p);
+        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    }
+    __device__ __forceinline__ float at(int i) const
+    {
+        return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    }
+    __device__ __forceinline__ uint32_t top() const
+    {
+        const uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                    __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+        return max(m & 0xffff0000u, m << 16);
+    }
+};
+constexpr uint32_t kInfBits = 0x7f800000u;
+
+// Eight e4m3 codes of x * 2^-e (inv = 2^-e), packed little-endian; the conversion clamps finite
+// values to 448 and keeps NaN.  all: every value is finite; else infinities become NaN too.
+template <typename T>
+__device__ __forceinline__ uint2 encode8(const Src8<T> &x, float inv, bool all)
+{
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        float y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = x.at(4 * i + j) * inv;
+        if (!all) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = isfinite(x.at(4 * i + j)) ? y[j] : NAN;
+        }
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
+        w[i] = __byte_perm(lo, hi, 0x5410);
     }
     return make_uint2(w[0], w[1]);
 }
@@ -63,11 +118,10 @@ __device__ __forceinline__ void decode8(uint2 c, float mul, float *x)
     }
 }
 
-// Exponent of a row from its largest finite magnitude.
-__device__ __forceinline__ int row_exponent(float top)
+// Exponent of a row from the bits of its largest finite magnitude.
+__device__ __forceinline__ int row_exponent(uint32_t u)
 {
     // top = m * 2^x with m in [1, 2): top <= 448 * 2^e = 1.75 * 2^(e + 8)
-    const uint32_t u = __float_as_uint(top);
     const int x = (int)(u >> 23) - 127;  // subnormals and zero give -127: clamped below
     const int e = x - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
     return min(max(e, kExpMin), kExpMax);
@@ -125,7 +179,7 @@ paged_write_kernel(const TS *__restrict__ k, const TS *__restrict__ v, int64_t l
         const int steps = n * 2 * per;
         int at = 0, part = 0;  // of the next step to load: token, then K and V
         for (int s0 = 0; s0 < steps; s0 += 4) {
-            float x[4][8];
+            Src8<TS> x[4];
             int tk[4], pt[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
@@ -133,12 +187,9 @@ paged_write_kernel(const TS *__restrict__ k, const TS *__restrict__ v, int64_t l
                 pt[u] = part;
                 const bool is_v = part >= per;
                 const int h = (is_v ? part - per : part) * heads + (lane >> lanes_log2);
-                if (s0 + u < steps && on && h < H) {
-                    load8((is_v ? v + (tok0 + at) * ld_v : k + (tok0 + at) * ld_k) + (int64_t)h * d + 8 * c, x[u]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[u][j] = 0.0f;
-                }
+                x[u].clear();
+                if (s0 + u < steps && on && h < H)
+                    x[u].load((is_v ? v + (tok0 + at) * ld_v : k + (tok0 + at) * ld_k) + h * d + 8 * c);
                 if (++part == 2 * per) {
                     part = 0;
                     at = at + 1 < n ? at + 1 : at;
@@ -150,19 +201,29 @@ paged_write_kernel(const TS *__restrict__ k, const TS *__restrict__ v, int64_t l
                 const bool is_v = pt[u] >= per;
                 const int h = (is_v ? pt[u] - per : pt[u]) * heads + (lane >> lanes_log2);
                 const bool here = s0 + u < steps && row >= 0 && h < H;
-                TD *dst = (is_v ? V + row * kv.ld_v : K + row * kv.ld_k) + (int64_t)h * d + 8 * c;
+                TD *dst = (is_v ? V + row * kv.ld_v : K + row * kv.ld_k) + h * d + 8 * c;
                 if constexpr (sizeof(TD) == 1) {
-                    float top = 0.0f;
+                    uint32_t top = x[u].top();
+                    const bool all = !__any_sync(0xffffffffu, top >= kInfBits);
+                    if (!all) {  // some value of the step is no number: the finite ones decide
+                        top = 0;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) top = fmaxf(top, isfinite(x[u][j]) ? fabsf(x[u][j]) : 0.0f);
+                        for (int j = 0; j < 8; ++j) {
+                            const uint32_t b = __float_as_uint(x[u].at(j)) & 0x7fffffffu;
+                            top = b < kInfBits ? max(top, b) : top;
+                        }
+                    }
                     for (int o = (1 << lanes_log2) >> 1; o > 0; o >>= 1)
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
                     const int e = row_exponent(top);
-                    if (here && on) *reinterpret_cast<uint2 *>(dst) = encode8(x[u], two_to(-e));
+                    if (here && on) *reinterpret_cast<uint2 *>(dst) = encode8(x[u], two_to(-e), all);
                     if (here && c == 0)
                         (is_v ? V_exp : K_exp)[(int64_t)row * H + h] = (uint8_t)(e + kExpBias);
                 } else {
-                    if (here && on) store8(dst, x[u]);
+                    float f[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) f[j] = x[u].at(j);
+                    if (here && on) store8(dst, f);
                 }
             }
         }
@@ -171,43 +232,53 @@ paged_write_kernel(const TS *__restrict__ k, const TS *__restrict__ v, int64_t l
 
 // ------------------------------------------------------------------ read
 // One warp per `group` listed cells: its lanes look the cells up at once, then the warp streams their
-// K and V rows (all KV heads contiguous), eight values a lane, four steps in flight.  Bound by the
-// bytes; with few cells by the look-up's dependent loads and one step's latency.
-
-template <typename T>
-struct Raw8 {
-    uint4 a, b;
+// K and V rows (all KV heads contiguous), kVec values a lane, four steps in flight.  With eight codes
+// a lane the instructions of the conversion bound it (72% of issue slots at 74 us for whole sequences
+// of 61,789 cells); with sixteen (d a multiple of 16) the bytes do.  With few cells: the look-up's
+// dependent loads and one step's latency.
+template <typename T, int kVec>
+struct Raw {
+    static constexpr int kWords = (int)sizeof(T) * kVec / 4;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0u;
+    }
     __device__ __forceinline__ void load(const T *p)
     {
-        a = reinterpret_cast<const uint4 *>(p)[0];
-        if constexpr (sizeof(T) == 4) b = reinterpret_cast<const uint4 *>(p)[1];
-    }
-    __device__ __forceinline__ void values(float, float *x) const
-    {
-        if constexpr (sizeof(T) == 4) {
-            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+        if constexpr (kWords == 2) {
+            const uint2 a = *reinterpret_cast<const uint2 *>(p);
+            w[0] = a.x; w[1] = a.y;
         } else {
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[2 * i] = __uint_as_float(w[i] << 16);
-                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            for (int i = 0; i < kWords; i += 4) {
+                const uint4 a = reinterpret_cast<const uint4 *>(p)[i / 4];
+                w[i] = a.x; w[i + 1] = a.y; w[i + 2] = a.z; w[i + 3] = a.w;
             }
         }
     }
-};
-template <>
-struct Raw8<uint8_t> {
-    uint2 a;
-    __device__ __forceinline__ void load(const uint8_t *p) { a = *reinterpret_cast<const uint2 *>(p); }
-    __device__ __forceinline__ void values(float mul, float *x) const { decode8(a, mul, x); }
+    // values 8 i .. 8 i + 7, times mul where they are codes
+    __device__ __forceinline__ void eight(int i, float mul, float *x) const
+    {
+        if constexpr (sizeof(T) == 1) {
+            decode8(make_uint2(w[2 * i], w[2 * i + 1]), mul, x);
+        } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[2 * j] = __uint_as_float(w[4 * i + j] << 16);
+                x[2 * j + 1] = __uint_as_float(w[4 * i + j] & 0xffff0000u);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(w[8 * i + j]);
+        }
+    }
 };
 
-template <typename TS, typename TD>
+template <typename TS, typename TD, int kVec>
 __global__ void __launch_bounds__(128, 8)
-paged_read_kernel(KvView kv, int H, int d, int group, const int32_t *__restrict__ seq,
+paged_read_kernel(KvView kv, int H, int d, int d_log2, int group, const int32_t *__restrict__ seq,
                   const int32_t *__restrict__ kv_len, int64_t n_seq, const int32_t *__restrict__ pos,
                   const int32_t *__restrict__ n_cells, int64_t n_list, int64_t max_cells,
                   TD *__restrict__ K_out, TD *__restrict__ V_out)
@@ -218,6 +289,7 @@ paged_read_kernel(KvView kv, int H, int d, int group, const int32_t *__restrict_
     QSA_AFTER_WAIT(pos);
     QSA_AFTER_WAIT(n_cells);
     pdl_trigger();
+    constexpr int kStep = 32 * kVec;
     const int lane = threadIdx.x & 31;
     const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
     const int hd = H * d;
@@ -235,30 +307,31 @@ paged_read_kernel(KvView kv, int H, int d, int group, const int32_t *__restrict_
         if (n <= 0) continue;
         int32_t mine = -1;  // pool row of cell j0 + lane
         if (lane < n && p >= 0 && p < (int64_t)len) mine = (int32_t)cell_row(kv, (int)s, 0, (int)p);
-        // steps of 256 values: cell, then K and V; the tail of a row is masked
-        const int per = (hd + 255) >> 8, steps = n * 2 * per;
+        // a step: kStep values of a cell's K or V row
+        const int per = (hd + kStep - 1) / kStep, steps = n * 2 * per;
         int cell = 0, part = 0;  // of the next step to load
         for (int s0 = 0; s0 < steps; s0 += 4) {
-            Raw8<TS> raw[4];
+            Raw<TS, kVec> raw[4];
             float mul[4];
-            int64_t to[4];
-            bool here[4], is_v[4];
+            TD *to[4];  // NULL: nothing of this lane's
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int32_t row = __shfl_sync(0xffffffffu, mine, cell);
-                is_v[u] = part >= per;
-                const int e = ((is_v[u] ? part - per : part) << 8) + 8 * lane;
-                here[u] = s0 + u < steps && e < hd;
-                to[u] = (i * max_cells + j0 + cell) * hd + e;
+                const bool is_v = part >= per;
+                const int e = (is_v ? part - per : part) * kStep + kVec * lane;
+                to[u] = nullptr;
                 mul[u] = 0.0f;  // a cell that is not there: zeros
-                if constexpr (sizeof(TS) == 1) raw[u].a = make_uint2(0u, 0u);
-                else raw[u].a = make_uint4(0u, 0u, 0u, 0u);
-                if constexpr (sizeof(TS) == 4) raw[u].b = make_uint4(0u, 0u, 0u, 0u);
-                if (here[u] && row >= 0) {
-                    raw[u].load((is_v[u] ? V + row * kv.ld_v : K + row * kv.ld_k) + e);
-                    if constexpr (sizeof(TS) == 1)
-                        mul[u] = two_to(min(max((int)(is_v[u] ? kv.V_exp : kv.K_exp)[(int64_t)row * H + e / d] -
-                                                    kExpBias, kExpMin), kExpMax));
+                raw[u].clear();
+                if (s0 + u < steps && e < hd) {
+                    to[u] = (is_v ? V_out : K_out) + (i * max_cells + j0 + cell) * hd + e;
+                    if (row >= 0) {
+                        raw[u].load((is_v ? V + row * kv.ld_v : K + row * kv.ld_k) + e);
+                        if constexpr (sizeof(TS) == 1) {
+                            const int h = d_log2 >= 0 ? e >> d_log2 : e / d;
+                            mul[u] = two_to(min(max((int)(is_v ? kv.V_exp : kv.K_exp)[(int64_t)row * H + h] -
+                                                        kExpBias, kExpMin), kExpMax));
+                        }
+                    }
                 }
                 if (++part == 2 * per) {
                     part = 0;
@@ -267,10 +340,13 @@ paged_read_kernel(KvView kv, int H, int d, int group, const int32_t *__restrict_
             }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                if (!here[u]) continue;
-                float x[8];
-                raw[u].values(mul[u], x);
-                store8((is_v[u] ? V_out : K_out) + to[u], x);
+                if (!to[u]) continue;
+#pragma unroll
+                for (int k = 0; k < kVec / 8; ++k) {
+                    float x[8];
+                    raw[u].eight(k, mul[u], x);
+                    store8(to[u] + 8 * k, x);
+                }
             }
         }
     }
@@ -311,18 +387,34 @@ cudaError_t write_to(const void *k, const void *v, int64_t ld_k, int64_t ld_v, i
     }
 }
 
-template <typename TS, typename TD>
-cudaError_t read_to(const KvView &kv, int d, const int32_t *seq, const int32_t *kv_len, int64_t n_seq,
-                    const int32_t *pos, const int32_t *n_cells, int64_t n_list, int64_t max_cells,
-                    void *K_out, void *V_out, cudaStream_t st)
+template <typename TS, typename TD, int kVec>
+cudaError_t read_vec(const KvView &kv, int d, const int32_t *seq, const int32_t *kv_len, int64_t n_seq,
+                     const int32_t *pos, const int32_t *n_cells, int64_t n_list, int64_t max_cells,
+                     void *K_out, void *V_out, cudaStream_t st)
 {
     const int group = rows_group(n_list * max_cells);
     int64_t grid = (n_list * ((max_cells + group - 1) / group) + 3) / 4;
     const int64_t most = (int64_t)device_sm_count() * 16;
     if (grid > most) grid = most;
-    return launch(paged_read_kernel<TS, TD>, dim3((unsigned)grid), dim3(128), 0, st, 1, kv, kv.H_kv, d, group,
-                  seq, kv_len, n_seq, pos, n_cells, n_list, max_cells, static_cast<TD *>(K_out),
-                  static_cast<TD *>(V_out));
+    int d_log2 = -1;
+    for (int i = 3; i <= 8; ++i)
+        if (d == 1 << i) d_log2 = i;
+    return launch(paged_read_kernel<TS, TD, kVec>, dim3((unsigned)grid), dim3(128), 0, st, 1, kv, kv.H_kv, d,
+                  d_log2, group, seq, kv_len, n_seq, pos, n_cells, n_list, max_cells,
+                  static_cast<TD *>(K_out), static_cast<TD *>(V_out));
+}
+
+template <typename TS, typename TD>
+cudaError_t read_to(const KvView &kv, int d, const int32_t *seq, const int32_t *kv_len, int64_t n_seq,
+                    const int32_t *pos, const int32_t *n_cells, int64_t n_list, int64_t max_cells,
+                    void *K_out, void *V_out, cudaStream_t st)
+{
+    if constexpr (sizeof(TS) == 1) {
+        // sixteen codes of one head, 16-byte aligned
+        if (d % 16 == 0 && kv.ld_k % 16 == 0 && kv.ld_v % 16 == 0)
+            return read_vec<TS, TD, 16>(kv, d, seq, kv_len, n_seq, pos, n_cells, n_list, max_cells, K_out, V_out, st);
+    }
+    return read_vec<TS, TD, 8>(kv, d, seq, kv_len, n_seq, pos, n_cells, n_list, max_cells, K_out, V_out, st);
 }
 
 }  // namespace
