@@ -82,7 +82,8 @@ int qsa_version(void);
  * Kernels that stage data with asynchronous copies or run tcgen05 tensor-core work wait on
  * shared-memory barriers: the attention kernels of qsa_sparse_attn (bf16, 128-dim, 8 query
  * heads per KV head; the many-query form; the latent form), qsa_sparse_attn_union,
- * qsa_mask_sparse_attn and qsa_decode_step / its host-fed and plan forms, and the tensor-core
+ * qsa_mask_sparse_attn and qsa_decode_step / its host-fed and plan forms, the tensor-core form of
+ * qsa_paged_attn and qsa_prompt_attn (QSA_BF16 queries, d 128), and the tensor-core
  * score contraction of qsa_index_score (QSA_PREC_BF16_TC).  No wait is unbounded.  When a
  * wait inside a kernel's pipeline lasts longer than pipeline_limit_ns, the kernel stores
  * QSA_ERR_TIMEOUT into *status_out (when status_out is not NULL), stops issuing work, waits
@@ -743,8 +744,9 @@ qsa_status qsa_paged_read(const qsa_paged_cache *cache, const int32_t *table, in
  *   out[i][h][:] = sum_j softmax_j(scale * q[i][h] . K[j][g]) V[j][g][:]
  *   lse_out[i][h] = log(sum_j exp(scale * q[i][h] . K[j][g]))   (natural log; optional)
  * A token that sees no cell (p < 0) gives out = 0, lse = -inf.  Cells a token does not see do
- * not enter its result, whatever they hold.  A sequence longer than its table row, or with a
- * page outside the pool among its visible cells, gives out = NaN and lse = NaN.
+ * not enter its result, whatever they hold.  A sequence longer than its table row gives out = NaN
+ * and lse = NaN, and so does a token that sees a cell on a page outside the pool (the sequence's
+ * other tokens may then be NaN too).
  *
  *   q        [n_tok][H_q][d] of type q_dtype (QSA_F32 or QSA_BF16), ld_q elements between tokens
  *   out      [n_tok][H_q][d] packed, of type q_dtype;  lse_out [n_tok][H_q] fp32 or NULL
@@ -753,9 +755,12 @@ qsa_status qsa_paged_read(const qsa_paged_cache *cache, const int32_t *table, in
  *   workspace  qsa_paged_attn_workspace_size() bytes, 256-byte aligned, for the parts of rows
  *            whose cells are shared out; its contents do not matter, and calls that may run at
  *            the same time need one each
- * All sums, the softmax and the output accumulate in fp32.  With a QSA_BF16 query the tensor
- * cores take the softmax weights in 16 bits (bf16 on a bf16 cache, fp16 on an e4m3 one); with a
- * QSA_F32 query the arithmetic is fp32 throughout.
+ * All sums, the softmax statistics and the output are held in fp32.  With d = 128 and a QSA_BF16
+ * or QSA_E4M3 pool the products run on the tensor cores: QSA_BF16 queries with the softmax weights
+ * rounded to 16 bits (bf16, or fp16 for a few tokens on a QSA_E4M3 pool), QSA_F32 queries (up to
+ * 16 heads per KV head) with queries and weights as sums of three bf16 terms on a QSA_BF16 pool
+ * (24 bits) and of two fp16 terms on a QSA_E4M3 pool (22 bits).  Other shapes, and QSA_BF16
+ * chunks with scale <= 0, take fp32 arithmetic on the CUDA cores, which is right but slower.
  * Errors: INVALID_ARG for null pointers, sizes < 0, H_q not a multiple of H_kv, ld_q < H_q*d, a
  * misaligned pointer (q and out 16 bytes, rows of q a multiple of 16 bytes), a workspace smaller
  * than required; UNSUPPORTED for n_seq, n_tok or their work beyond 2^31 - 1 rows.
