@@ -76,6 +76,11 @@ qsa_status run_attn(const DenseArgs &a, int64_t max_q, void *workspace, size_t w
 {
     const int64_t items = (a.sv.n_tok + a.sv.n_seq) * (int64_t)a.kv.H_kv;
     if (items > kMaxInt || (int64_t)a.H_q * a.d > (1 << 24)) return QSA_ERR_UNSUPPORTED;
+    if (dense_few_ok(a, max_q)) {
+        if (!workspace || !aligned(workspace, 256) || workspace_bytes < dense_few_workspace())
+            return QSA_ERR_INVALID_ARG;
+        return launch_dense_few(a, max_q, workspace, st);
+    }
     if (dense_decode_ok(a, max_q)) {
         if (!workspace || !aligned(workspace, 256) || workspace_bytes < dense_decode_workspace())
             return QSA_ERR_INVALID_ARG;

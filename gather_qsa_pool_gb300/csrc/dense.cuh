@@ -358,6 +358,11 @@ bool dense_decode_ok(const DenseArgs &a, int64_t max_q);
 size_t dense_decode_workspace();
 cudaError_t launch_dense_decode(const DenseArgs &a, int64_t max_q, void *workspace, cudaStream_t st);
 
+// The same with bf16 queries on the tcgen05 tensor cores, up to 32 rows (tokens x heads of a KV head).
+bool dense_few_ok(const DenseArgs &a, int64_t max_q);
+size_t dense_few_workspace();
+qsa_status launch_dense_few(const DenseArgs &a, int64_t max_q, void *workspace, cudaStream_t st);
+
 // Many query rows on the tensor cores: bf16 queries, d 128.
 bool dense_tc_ok(const DenseArgs &a);
 size_t dense_tc_workspace();

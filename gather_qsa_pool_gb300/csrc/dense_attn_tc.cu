@@ -645,8 +645,8 @@ static qsa_status run_tc(const DenseArgs &a, void *workspace, cudaStream_t st)
     CUtensorMap mq, mk, mv;
     const int64_t width = (int64_t)a.kv.H_kv * kD;
     if (!make_query_map(&mq, a.q, a.sv.n_tok, a.H_q, a.ld_q, G) ||
-        !make_map(&mk, a.kv.K, a.pool_rows, width, a.kv.ld_k, box_rows, E8) ||
-        !make_map(&mv, a.kv.V, a.pool_rows, width, a.kv.ld_v, box_rows, E8))
+        !make_map(&mk, a.kv.K, a.pool_rows, width, a.kv.ld_k, box_rows, E8, !E8) ||
+        !make_map(&mv, a.kv.V, a.pool_rows, width, a.kv.ld_v, box_rows, E8, !E8))
         return QSA_ERR_CUDA;
     WorkShape ws;
     ws.rt = 2 * (kM / G);

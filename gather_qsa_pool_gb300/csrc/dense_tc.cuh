@@ -1,6 +1,6 @@
-// dense_tc.cuh -- pieces of the tcgen05 attention over every visible cell (dense_attn_tc.cu): tiles and
-// their TMA maps, bounded waits, packed arithmetic, e4m3 tiles turned into bf16, the walk over a CTA's
-// parts.  Only the library's own .cu files include this header.
+// dense_tc.cuh -- what the tcgen05 kernels of the attention over every visible cell share
+// (dense_attn_tc.cu, dense_few_tc.cu): tiles and their TMA maps, bounded waits, packed arithmetic, the
+// walk over a CTA's parts.  Only the library's own .cu files include this header.
 #pragma once
 
 #include <cuda.h>
@@ -175,10 +175,11 @@ inline EncodeTiledFn encode_tiled()
     return fn;
 }
 
-// Rows of `width` values at a stride of ld.  bf16: boxes of 64 values x box_rows rows in the
-// 128-byte swizzle; e4m3: boxes of 128 codes x box_rows rows, row after row.  Zeros behind the last
-// row.
-inline bool make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t width, int64_t ld, int box_rows, bool e8)
+// Rows of `width` values at a stride of ld, in boxes of 128 bytes (64 bf16 values or 128 codes) x
+// box_rows rows, in the 128-byte swizzle or row after row.  Zeros behind the last row.  L2 fetches a
+// head's row and no more (with 256 bytes of codes the other heads' come along and go again: 570 MB
+// instead of 420 for 411 MB of cells).
+inline bool make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t width, int64_t ld, int box_rows, bool e8, bool swizzle)
 {
     const EncodeTiledFn fn = encode_tiled();
     if (!fn) return false;
@@ -188,8 +189,8 @@ inline bool make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t wid
     const cuuint32_t estr[2] = {1, 1};
     return fn(m, e8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
               const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              e8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+              e8 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Every tensor-memory load of this thread so far has arrived; the N values pass through it, so that no

@@ -19,8 +19,8 @@ __device__ __forceinline__ uint64_t desc_kmajor_sw128(uint32_t saddr)
     return d;
 }
 
-// MN-major operand, 128-byte swizzle: each 128-byte row holds 64 consecutive N elements of
-// one k; the next 64 N elements start `mn_stride` bytes on (leading byte offset); the next
+// MN-major operand, 128-byte swizzle: each 128-byte row holds 64 consecutive M or N elements (128 of
+// 8 bits) of one k; the next of them start `mn_stride` bytes on (leading byte offset); the next
 // 8 k rows 1024 bytes on (stride byte offset).
 __device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t saddr, uint32_t mn_stride)
 {
@@ -38,6 +38,14 @@ __device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t saddr, uint32_t 
 __host__ __device__ constexpr uint32_t idesc_m128(int n, bool b_mn, bool f16 = false)
 {
     return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (b_mn ? (1u << 16) : 0u) |
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+// Instruction descriptor, kind::f8f6f4: fp32 accumulator, A e4m3, B e5m2, M 128, the given N, A or B
+// MN-major where said.
+__host__ __device__ constexpr uint32_t idesc_f8_m128(int n, bool a_mn, bool b_mn)
+{
+    return (1u << 4) | (1u << 10) | (a_mn ? (1u << 15) : 0u) | (b_mn ? (1u << 16) : 0u) |
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
@@ -96,6 +104,18 @@ __device__ __forceinline__ void umma_m128_ss_lead(uint32_t d_tmem, uint64_t a_de
         "setp.ne.b32 p, %4, 0;\n\t"
         "setp.ne.b32 e, %5, 0;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+// The same for 8-bit operands (kind::f8f6f4, types as the instruction descriptor says).
+__device__ __forceinline__ void umma_m128_f8_ss_lead(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                     uint32_t idesc, uint32_t accumulate, uint32_t leader)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
         : "memory");
 }
