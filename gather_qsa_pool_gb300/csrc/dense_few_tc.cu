@@ -37,11 +37,12 @@
 namespace qsa {
 namespace {
 
-constexpr int kSoftWarps = 16, kMmaWarp = 16, kLoadWarp = 17, kAuxWarp = 19, kAuxWarps = 2;
+constexpr int kGroups = 2;      // of softmax warps, four each: a cell of a tile to a thread
+constexpr int kSoftWarps = 4 * kGroups, kMmaWarp = kSoftWarps, kLoadWarp = kMmaWarp + 1, kAuxWarp = kLoadWarp + 2;
+constexpr int kAuxWarps = 2;
 constexpr int kThreads = 32 * (kAuxWarp + kAuxWarps);
-constexpr int kOver = 2;        // an item's fixed cost in tiles
-constexpr int kMaxStages = 10, kMaxGroups = 4;
-constexpr int kBarVote = 1, kBarAll = 5, kBarAux = 6, kBarFirst = 7;  // named barriers: 1-4 the groups'
+constexpr int kMaxStages = 10;
+constexpr int kBarVote = 1, kBarAll = 3, kBarAux = 4, kBarFirst = 5;  // named barriers: 1, 2 the groups'
 constexpr float kUnset = 3.0e38f;  // -m of a row that has seen nothing: any logit moves it
 // Exponents of V beyond this: the sum takes an exponential of its own (2^(x - m) times 2^-ve could
 // start from a weight that is zero).
@@ -49,18 +50,15 @@ constexpr int kFar = 50;
 
 template <bool E8, int NR>
 struct Few {
-    // 32 rows: two groups, a cell's rows shared by two threads; 16 rows: four groups, a cell a thread
-    static constexpr int kGroups = NR == 32 ? 2 : 4, kSplit = NR == 32 ? 2 : 1;
-    static constexpr int kLanes = 128 * kSplit;                // threads of a group
-    static constexpr int kOwn = NR / kSplit;                   // rows of a thread
     static constexpr int kTerms = E8 ? 3 : 1;
     static constexpr int kCols = kTerms * NR;                  // columns of S' and O'
     static constexpr uint32_t kStage = E8 ? kRawTile : kTileB;
     static constexpr uint32_t kQBytes = NR * 128 * (E8 ? 3 : 2);
     static constexpr uint32_t kPBytes = kN * 128;              // a cell's weights: 128 bytes, in part used
     // stages of K, of V
-    static constexpr int kOfK = E8 ? (NR == 32 ? 5 : 4) : 2, kOfV = E8 ? (NR == 32 ? 5 : 4) : (NR == 32 ? 3 : 2);
+    static constexpr int kOfK = E8 ? 5 : 2, kOfV = E8 ? 5 : 3;
     static constexpr int kStages = kOfK + kOfV;
+    static constexpr int kOver = E8 ? 7 : 4;                   // an item's fixed cost in tiles
     static constexpr uint32_t kStride = kCols <= 16 ? 16 : (kCols <= 32 ? 32 : (kCols <= 64 ? 64 : 128));
     static constexpr uint32_t kTmem = 2 * kGroups * kStride;
     // the weights' range: at most 2^kTop where m was set, 2^kMost before it moves (bf16: any; fp16 terms:
@@ -71,14 +69,14 @@ struct Few {
 struct Bars {
     uint64_t full[kMaxStages], empty[kMaxStages], raw[kMaxStages];  // of K's stages, then V's
     uint64_t part_full[kSlots];
-    uint64_t s_full[kMaxGroups], p_full[kMaxGroups], o_full[kMaxGroups], q_full[2], q_free[2], drain;
+    uint64_t s_full[kGroups], p_full[kGroups], o_full[kGroups], q_full[2], q_free[2], drain;
     uint32_t tmem, pad;
     int32_t odd[kSlots], bad[kSlots];  // number + 1 of the part that set it
     float qs[kSlots];                  // what the part's queries were divided by
     uint32_t qmax[2][8];
-    alignas(16) float nm[kMaxGroups][32], mref[kMaxGroups][32];  // -m, m of a group's rows
-    float2 al[kMaxGroups][32], fac[kMaxGroups][32];  // factors 2^x as two, each in range
-    float red[kMaxGroups][4][32], sum[kMaxGroups][4][32];
+    alignas(16) float nm[kGroups][32], mref[kGroups][32];  // -m, m of a group's rows
+    float2 al[kGroups][32], fac[kGroups][32];  // factors 2^x as two, each in range
+    float red[kGroups][4][32], sum[kGroups][4][32];
     float inv[32];
     int32_t see[32];                   // last cell of a row
     int64_t at[32];                    // place of a row's results, -1: none
@@ -92,7 +90,7 @@ template <bool E8, int NR>
 __host__ __device__ constexpr size_t few_smem()
 {
     using F = Few<E8, NR>;
-    return 1024 + (size_t)F::kStages * F::kStage + F::kGroups * F::kPBytes + 2 * F::kQBytes + sizeof(Bars);
+    return 1024 + (size_t)F::kStages * F::kStage + kGroups * F::kPBytes + 2 * F::kQBytes + sizeof(Bars);
 }
 static_assert(few_smem<false, 16>() <= 227 * 1024 && few_smem<true, 16>() <= 227 * 1024 &&
                   few_smem<false, 32>() <= 227 * 1024 && few_smem<true, 32>() <= 227 * 1024,
@@ -137,14 +135,14 @@ __device__ __forceinline__ void tmem_ld_async(uint32_t taddr, float *v)
     else tmem_ld4_async(taddr, v);
 }
 
-// 16 values of each lane reduced over the warp's lanes: lane i returns value i % 16.  A step halves the
-// values that a lane holds.
-template <bool Max>
-__device__ __forceinline__ float col_reduce(float *v)
+// N values (16 or 32) of each lane reduced over the warp's lanes: lane i returns value i % N.  A step halves
+// the values that a lane holds.
+template <bool Max, int N>
+__device__ __forceinline__ float col_reduce(float (&v)[N])
 {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int h = 8; h > 0; h >>= 1) {
+    for (int h = N / 2; h > 0; h >>= 1) {
         const bool up = lane & h;
 #pragma unroll
         for (int i = 0; i < h; ++i) {
@@ -153,8 +151,11 @@ __device__ __forceinline__ float col_reduce(float *v)
             v[i] = Max ? fmaxf(keep, got) : keep + got;
         }
     }
-    const float got = __shfl_xor_sync(0xffffffffu, v[0], 16);
-    return Max ? fmaxf(v[0], got) : v[0] + got;
+    if constexpr (N == 16) {
+        const float got = __shfl_xor_sync(0xffffffffu, v[0], 16);
+        v[0] = Max ? fmaxf(v[0], got) : v[0] + got;
+    }
+    return v[0];
 }
 
 // A cell's page entry, loaded some tiles ahead and not looked at until then (packed rows: none), and
@@ -321,7 +322,7 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
                  Split *__restrict__ splits, int by_item, const WaitCtl wc)
 {
     using F = Few<E8, NR>;
-    constexpr int kStages = F::kStages, kGroups = F::kGroups, kLanes = F::kLanes, kOwn = F::kOwn;
+    constexpr int kStages = F::kStages;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     unsigned char *ring = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -339,7 +340,7 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
         }
         for (int g = 0; g < kGroups; ++g) {
             mbar_init(&bars.s_full[g], 1);
-            mbar_init(&bars.p_full[g], kLanes / 32);
+            mbar_init(&bars.p_full[g], 4);
             mbar_init(&bars.o_full[g], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -453,7 +454,7 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
             if (!ok) break;
             if (tiles <= kGroups) umma_commit_lead(&bars.q_free[buf], lead);
             for (int t = 0; t < tiles; ++t) {
-                const int g = t & (kGroups - 1);
+                const int g = t % kGroups;
                 const int st = F::kOfK + (int)(nv % F::kOfV);
                 ok = v_ready(nv) && bar_wait(&bars.p_full[g], (np >> g) & 1u, wc.limit_ns);
                 if (!ok) break;
@@ -596,10 +597,9 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
         } while (more);
         __syncwarp();
     } else {
-        // ---- weights: this thread's cell is number r of every tile of group g, its rows from h0 on
-        const int g = warp / (kLanes / 32), quarter = warp & 3, r = quarter * 32 + lane;
-        const int h0 = F::kSplit == 1 ? 0 : ((warp >> 2) & 1) * kOwn;
-        const uint32_t colS = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)g * F::kStride + (uint32_t)h0;
+        // ---- weights: this thread's cell is number r of every tile of group g
+        const int g = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+        const uint32_t colS = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)g * F::kStride;
         unsigned char *const prow = sP + (size_t)g * F::kPBytes + r * 128;
         uint32_t waits = 0;  // bit 0, 1: the phase of s_full, o_full
         if (tid < NR * 8) {
@@ -613,23 +613,23 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
         do {
             const Parts &p = bars.part[n % kSlots];
             const int tiles = p.tile1 - p.tile0, mine = (tiles + kGroups - 1 - g) / kGroups;
-            float l[kOwn];
+            float l[NR];
 #pragma unroll
-            for (int c = 0; c < kOwn; ++c) l[c] = 0.0f;
+            for (int c = 0; c < NR; ++c) l[c] = 0.0f;
             // (row r of the group: one thread's, here and where it moves)
-            const bool keeper = r < kOwn;
+            const bool keeper = r < NR;
             if (keeper) {
-                bars.mref[g][h0 + r] = -INFINITY;
-                bars.nm[g][h0 + r] = kUnset;
+                bars.mref[g][r] = -INFINITY;
+                bars.nm[g][r] = kUnset;
             }
-            named_sync<kLanes>(kBarVote + g);
+            named_sync<128>(kBarVote + g);
             // e4m3: the page of this group's next cell
             PageAhead ahead = {0, -1};
             auto look = [&](int k) {
                 ahead.load(kv, p, k < mine, (int64_t)(p.tile0 + kGroups * k + g) * kN + r);
             };
             if constexpr (E8) look(0);
-            const float *nm = &bars.nm[g][h0];
+            const float *nm = bars.nm[g];
             for (int k = 0; ok && k < mine; ++k) {
                 const int t = p.tile0 + kGroups * k + g;
                 // e4m3: the exponents, on their way while the logits are (the copies' warp had them brought
@@ -657,45 +657,46 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
                     far = __any_sync(0xffffffffu, abs(ve) > kFar);
                 }
                 // the logits in log2 units (e4m3: with the exponent of the cell's values)
-                float v[kOwn];
+                float v[NR];
+                constexpr int kStep = 8;  // columns of a term loaded together
                 auto logits = [&]() {
                     const float2 k2 = make_float2(ks, ks), v2 = make_float2(vs, vs);
 #pragma unroll
-                    for (int half = 0; half < kOwn; half += 8) {  // (a term's sixteen at once take too many registers)
-                        float x[F::kTerms * 8];
+                    for (int at = 0; at < NR; at += kStep) {
+                        float x[F::kTerms * kStep];
 #pragma unroll
                         for (int i = 0; i < F::kTerms; ++i)
-                            tmem_ld_async<8>(colS + (uint32_t)(i * NR + half), x + i * 8);
-                        tmem_wait_ld<F::kTerms * 8>(x);
+                            tmem_ld_async<kStep>(colS + (uint32_t)(i * NR + at), x + i * kStep);
+                        tmem_wait_ld<F::kTerms * kStep>(x);
 #pragma unroll
-                        for (int c = 0; c < 8; c += 2) {
+                        for (int c = 0; c < kStep; c += 2) {
                             float2 y = make_float2(x[c], x[c + 1]);
                             if constexpr (E8) {
-                                y = add2(y, add2(make_float2(x[8 + c], x[9 + c]), make_float2(x[16 + c], x[17 + c])));
+                                y = add2(y, add2(make_float2(x[kStep + c], x[kStep + c + 1]), make_float2(x[2 * kStep + c], x[2 * kStep + c + 1])));
                                 y = fma2(y, k2, v2);
                             } else {
                                 y = mul2(y, k2);
                             }
-                            v[half + c] = y.x;
-                            v[half + c + 1] = y.y;
+                            v[at + c] = y.x;
+                            v[at + c + 1] = y.y;
                         }
                     }
                     if (p.edge(t)) {
                         const int64_t j = (int64_t)t * kN + r;
                         // the first row that sees cell j
-                        const int c0 = (j >= p.n_see ? NR : (ws.causal && j > p.pos0 ? (int)(j - p.pos0) * G : 0)) - h0;
+                        const int c0 = j >= p.n_see ? NR : (ws.causal && j > p.pos0 ? (int)(j - p.pos0) * G : 0);
 #pragma unroll
-                        for (int c = 0; c < kOwn; ++c) v[c] = c >= c0 ? v[c] : -INFINITY;
+                        for (int c = 0; c < NR; ++c) v[c] = c >= c0 ? v[c] : -INFINITY;
                     }
                 };
                 // the weights relative to the references as they stand, in fp32 and as 16-bit pairs, whose
                 // maximum says whether they may stay
-                uint32_t h[kOwn / 2];
+                uint32_t h[NR / 2];
                 uint32_t most;
                 auto weights = [&]() {
                     most = 0;
 #pragma unroll
-                    for (int c = 0; c < kOwn; c += 4) {
+                    for (int c = 0; c < NR; c += 4) {
                         const float4 m4 = *reinterpret_cast<const float4 *>(nm + c);
                         const float2 a0 = add2(make_float2(v[c], v[c + 1]), make_float2(m4.x, m4.y));
                         const float2 a1 = add2(make_float2(v[c + 2], v[c + 3]), make_float2(m4.z, m4.w));
@@ -721,55 +722,57 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
                     }
                 };
                 logits();
-                weights();
-                bool move;
-                if constexpr (E8) {
-                    const float2 x = __half22float2(reinterpret_cast<const __half2 &>(most));
-                    move = fmaxf(x.x, x.y) > F::kMost;
-                } else {
-                    move = fmaxf(__uint_as_float(most << 16), __uint_as_float(most & 0xffff0000u)) > F::kMost;
+                bool move = k == 0;  // a part's first tile sets the references
+                if (k > 0) {
+                    weights();
+                    if constexpr (E8) {
+                        const float2 x = __half22float2(reinterpret_cast<const __half2 &>(most));
+                        move = fmaxf(x.x, x.y) > F::kMost;
+                    } else {
+                        move = fmaxf(__uint_as_float(most << 16), __uint_as_float(most & 0xffff0000u)) > F::kMost;
+                    }
+                    move = named_or<128>(kBarVote + g, move || !here);
                 }
-                if (named_or<kLanes>(kBarVote + g, move || !here)) {
-                    if (named_or<kLanes>(kBarVote + g, !here)) {
+                if (move) {
+                    if (named_or<128>(kBarVote + g, !here)) {
                         ok = false;
                         break;
                     }
                     // ---- the references move
-                    logits();
+                    if (k > 0) logits();
                     const int tid = thread_again(), lane = tid & 31, quarter = (tid >> 5) & 3;
                     const uint32_t colO = tmem + ((uint32_t)(quarter * 32) << 16) + kGroups * F::kStride;
                     {
                         const float cm = col_reduce<true>(v);
-                        if (lane < kOwn) bars.red[g][quarter][h0 + lane] = cm;
+                        if (lane < NR) bars.red[g][quarter][lane] = cm;
                     }
-                    named_sync<kLanes>(kBarVote + g);
+                    named_sync<128>(kBarVote + g);
                     if (keeper) {
-                        const int c = h0 + r;
-                        const float m = bars.mref[g][c];
-                        const float top = fmaxf(fmaxf(bars.red[g][0][c], bars.red[g][1][c]),
-                                                fmaxf(bars.red[g][2][c], bars.red[g][3][c]));
+                        const float m = bars.mref[g][r];
+                        const float top = fmaxf(fmaxf(bars.red[g][0][r], bars.red[g][1][r]),
+                                                fmaxf(bars.red[g][2][r], bars.red[g][3][r]));
                         float2 f = make_float2(1.0f, 1.0f);
                         // (of a row whose weights may stay, a little more room does no harm)
                         const float mn = ceilf(top) - F::kTop;
                         if (mn > m) {
                             if (m != -INFINITY) f = two_factors(m - mn);
-                            bars.mref[g][c] = mn;
-                            bars.nm[g][c] = -mn;
+                            bars.mref[g][r] = mn;
+                            bars.nm[g][r] = -mn;
                         }
-                        bars.al[g][c] = f;
+                        bars.al[g][r] = f;
                     }
-                    named_sync<kLanes>(kBarVote + g);
+                    named_sync<128>(kBarVote + g);
                     if (k > 0) {
 #pragma unroll
-                        for (int c = 0; c < kOwn; ++c) {
-                            const float2 f = bars.al[g][h0 + c];
+                        for (int c = 0; c < NR; ++c) {
+                            const float2 f = bars.al[g][c];
                             l[c] = l[c] * f.x * f.y;
                         }
                         // s_full follows this group's last product with V: o may be rescaled
 #pragma unroll 1
-                        for (int i = 0; i < 2 * F::kTerms; ++i) {
-                            const int c = h0 + 8 * (i & 1);
-                            const uint32_t at = colO + (uint32_t)g * F::kStride + (uint32_t)((i >> 1) * NR + c);
+                        for (int i = 0; i < NR / 8 * F::kTerms; ++i) {
+                            const int c = 8 * (i % (NR / 8));
+                            const uint32_t at = colO + (uint32_t)g * F::kStride + (uint32_t)(i / (NR / 8) * NR + c);
                             float o[8];
                             tmem_ld8_async(at, o);
                             tmem_wait_ld<8>(o);
@@ -788,7 +791,7 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
                 }
                 // ---- their sum, and their terms for the product
 #pragma unroll
-                for (int c = 0; c < kOwn; c += 2) {
+                for (int c = 0; c < NR; c += 2) {
                     float2 s2 = make_float2(l[c], l[c + 1]);
                     const float2 w2 = make_float2(v[c], v[c + 1]);
                     if constexpr (E8) {
@@ -801,10 +804,9 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
                 }
                 if constexpr (E8) {
 #pragma unroll
-                    for (int c = 0; c < kOwn / 2; ++c) h[c] = (h[c] + 0x00020002u) & 0xfffcfffcu;  // nine bits
-                    constexpr int kChunks = kOwn / 16;
-                    const int ch0 = h0 / 16;
-#pragma unroll
+                    for (int c = 0; c < NR / 2; ++c) h[c] = (h[c] + 0x00020002u) & 0xfffcfffcu;  // nine bits
+                    constexpr int kChunks = NR / 16;
+                    #pragma unroll
                     for (int i = 0; i < 3; ++i) {
 #pragma unroll
                         for (int ch = 0; ch < kChunks; ++ch) {
@@ -812,23 +814,23 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 w[e] = __byte_perm(h[8 * ch + 2 * e], h[8 * ch + 2 * e + 1], 0x7531);
-                            *reinterpret_cast<uint4 *>(prow + (((i * (NR / 16) + ch0 + ch) ^ (r & 7)) << 4)) =
+                            *reinterpret_cast<uint4 *>(prow + (((i * kChunks + ch) ^ (r & 7)) << 4)) =
                                 make_uint4(w[0], w[1], w[2], w[3]);
                         }
                         if (i < 2) {
 #pragma unroll
-                            for (int c = 0; c < kOwn / 2; ++c) h[c] = less_upper(h[c]);
+                            for (int c = 0; c < NR / 2; ++c) h[c] = less_upper(h[c]);
                         }
                     }
                     if (far) {
                         logits();
 #pragma unroll
-                        for (int c = 0; c < kOwn; ++c) l[c] += ex2_approx(v[c] - vs + nm[c]);
+                        for (int c = 0; c < NR; ++c) l[c] += ex2_approx(v[c] - vs + nm[c]);
                     }
                 } else {
 #pragma unroll
-                    for (int ch = 0; ch < kOwn / 8; ++ch)
-                        *reinterpret_cast<uint4 *>(prow + ((h0 / 8 + ch) ^ (r & 7)) * 16) =
+                    for (int ch = 0; ch < NR / 8; ++ch)
+                        *reinterpret_cast<uint4 *>(prow + ((ch ^ (r & 7)) << 4)) =
                             make_uint4(h[4 * ch], h[4 * ch + 1], h[4 * ch + 2], h[4 * ch + 3]);
                 }
                 // written by this thread (generic proxy), read by the tensor cores (async proxy)
@@ -843,15 +845,14 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
             // it stays between 2^-123 and 2^83 times the cells.
             constexpr float kLess = E8 ? 30.0f : 0.0f;
             const int tid = thread_again(), lane = tid & 31, warp = tid >> 5;
-            const int g = warp / (kLanes / 32), quarter = warp & 3, r = quarter * 32 + lane;
-            const int h0 = F::kSplit == 1 ? 0 : ((warp >> 2) & 1) * kOwn;
+            const int g = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
             if constexpr (E8) {
 #pragma unroll
-                for (int c = 0; c < kOwn; ++c) l[c] *= 1.0f / (1 << 30);
+                for (int c = 0; c < NR; ++c) l[c] *= 1.0f / (1 << 30);
             }
             {
                 const float cm = col_reduce<false>(l);
-                if (lane < kOwn) bars.sum[g][quarter][h0 + lane] = cm;
+                if (lane < NR) bars.sum[g][quarter][lane] = cm;
             }
             if (ok && mine > 0) {
                 if (!bar_wait_warp(&bars.o_full[g], waits >> 1, wc.limit_ns)) ok = false;
@@ -892,7 +893,7 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
             }
             named_sync<32 * kSoftWarps>(kBarAll);
             // dim r of the rows c0 .. c0 + kRows - 1
-            constexpr int kRows = NR / 4;
+            constexpr int kRows = NR / kGroups;
             const int c0 = (warp >> 2) * kRows;
             const bool odd = ok && *reinterpret_cast<volatile int32_t *>(&bars.odd[n % kSlots]) == n + 1;
             float o[kRows];
@@ -984,7 +985,7 @@ qsa_status run_few(const DenseArgs &a, void *workspace, cudaStream_t st)
     ws.kt = kN;
     ws.H_kv = a.kv.H_kv;
     ws.causal = a.causal;
-    ws.over = kOver;
+    ws.over = F::kOver;
     // the kernel takes a positive scale: a negative one turns the queries' signs, zero clears them
     const float scale = (a.scale == 0.0f ? 1.0f : fabsf(a.scale)) * kLog2e;
     const float q_sign = a.scale == 0.0f ? 0.0f : (a.scale < 0.0f ? -1.0f : 1.0f);
