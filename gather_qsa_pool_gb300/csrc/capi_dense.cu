@@ -84,7 +84,7 @@ qsa_status run_attn(const DenseArgs &a, int64_t max_q, void *workspace, size_t w
     if (dense_decode_ok(a, max_q)) {
         if (!workspace || !aligned(workspace, 256) || workspace_bytes < dense_decode_workspace())
             return QSA_ERR_INVALID_ARG;
-        return from_cuda(launch_dense_decode(a, max_q, workspace, st));
+        return from_cuda(launch_dense_decode(a, workspace, st));
     }
     if (dense_tc_ok(a)) {
         if (!workspace || !aligned(workspace, 256) || workspace_bytes < dense_tc_workspace())
@@ -98,8 +98,8 @@ qsa_status run_attn(const DenseArgs &a, int64_t max_q, void *workspace, size_t w
 size_t attn_workspace(int64_t n_tok, int64_t n_seq, int H_q, int H_kv, int d)
 {
     if (n_tok <= 0 || n_seq <= 0 || H_q < 1 || H_kv < 1 || d < 1) return 0;
-    const size_t x = dense_decode_workspace(), y = dense_tc_workspace();
-    return x > y ? x : y;
+    const size_t x = dense_decode_workspace(), y = dense_tc_workspace(), z = dense_few_workspace();
+    return x > y ? (x > z ? x : z) : (y > z ? y : z);
 }
 
 }  // namespace

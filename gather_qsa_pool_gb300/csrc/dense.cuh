@@ -1,5 +1,5 @@
 // dense.cuh -- shared pieces of the paged key/value cache and of the dense attention over it
-// (paged_rw.cu, dense_attn.cu, dense_decode.cu, dense_attn_tc.cu): the device view of a cache,
+// (paged_rw.cu, dense_attn.cu, dense_decode.cu, dense_few_tc.cu, dense_attn_tc.cu): the device view of a cache,
 // the row of a cell, the packed sequences and the flattened list of work.
 #pragma once
 
@@ -356,9 +356,10 @@ cudaError_t launch_dense_attn(const DenseArgs &a, cudaStream_t st);
 // A few new tokens per sequence (max_q as the host knows it) over bf16 or e4m3 cells, d 128.
 bool dense_decode_ok(const DenseArgs &a, int64_t max_q);
 size_t dense_decode_workspace();
-cudaError_t launch_dense_decode(const DenseArgs &a, int64_t max_q, void *workspace, cudaStream_t st);
+cudaError_t launch_dense_decode(const DenseArgs &a, void *workspace, cudaStream_t st);
 
-// The same with bf16 queries on the tcgen05 tensor cores, up to 32 rows (tokens x heads of a KV head).
+// The same with bf16 queries on the tcgen05 tensor cores, up to 32 rows (tokens x heads of a KV head);
+// short contexts of up to 16 rows it leaves to the above.
 bool dense_few_ok(const DenseArgs &a, int64_t max_q);
 size_t dense_few_workspace();
 qsa_status launch_dense_few(const DenseArgs &a, int64_t max_q, void *workspace, cudaStream_t st);

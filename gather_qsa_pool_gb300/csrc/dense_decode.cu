@@ -1,5 +1,7 @@
-// dense_decode.cu -- attention of a few new tokens per sequence over a long paged (or packed)
-// cache: bound by the one pass over the cells' keys and values.
+// dense_decode.cu -- attention of a few new tokens per sequence over a paged (or packed) cache: fp32
+// queries, and bf16 queries of up to 16 rows over short contexts (longer ones: dense_few_tc.cu).  Bound
+// by latency (one sequence of 2,050 cells, 8 / 2 heads, bf16: 11.9 us with the join), by the
+// instructions of the conversion on long e4m3 contexts.
 //
 // Mathematics: with s_j the logit of cell j in log2 units, a part of a row's cells gives
 // (m, l, o) = (reference, sum 2^(s_j - m), sum 2^(s_j - m) v_j), and parts join by scaling to a
@@ -13,7 +15,7 @@
 // Shape: a CTA of four warps takes a share of the flattened list of (sequence, KV head, row
 // tile) items (dense.cuh), equal for every CTA, whatever the lengths: ragged batches stay
 // balanced and a captured graph follows lengths that change in place.  The rows of an item (new
-// tokens x the heads of its KV head) are one or two 16-row fragments of mma.m16n8k16; these
+// tokens x the heads of its KV head) are one 16-row fragment of mma.m16n8k16; these
 // tensor instructions suffice since 16 rows per 256 or 512 bytes of K and V leave them under a
 // third busy.  Each warp runs its own ring of stages (cp.async, 8 KB each) over its own 16
 // (bf16) or 32 (e4m3) cells of every tile and meets the others only at the end of a part.
@@ -45,11 +47,11 @@ constexpr float kFar = 50.0f;
 
 // Stages of a warp's ring and CTAs per SM: a warp is a long chain of dependent instructions (a tile
 // takes it over a thousand cycles whatever the memory does), so the more of them the better, as far
-// as registers go: 64 accumulators a lane allow twelve warps, 128 of them eight.
-template <int MT, int NT>
+// as registers go: twelve warps with one term of a query, eight with several.
+template <int NT>
 struct Plan {
-    static constexpr int kCtas = MT == 1 && NT == 1 ? 3 : 2;
-    static constexpr int kStages = MT == 1 && NT == 1 ? 2 : 3;
+    static constexpr int kCtas = NT == 1 ? 3 : 2;
+    static constexpr int kStages = NT == 1 ? 2 : 3;
 };
 
 template <bool E8>
@@ -59,16 +61,16 @@ struct Shape {
     static constexpr int kGroups = kKeys / 16;
 };
 
-template <bool E8, int MT, int NT>
+template <int NT>
 __host__ __device__ constexpr size_t q_bytes()
 {
-    return (size_t)MT * NT * 8 * 32 * 16;  // fragments: 8 k steps x 32 lanes x 16 bytes
+    return (size_t)NT * 8 * 32 * 16;  // fragments: 8 k steps x 32 lanes x 16 bytes
 }
-template <bool E8, int MT, int NT>
+template <bool E8, int NT>
 __host__ __device__ constexpr size_t decode_smem()
 {
-    return (size_t)kWarps * Plan<MT, NT>::kStages * 2 * kTile + q_bytes<E8, MT, NT>() +
-           (E8 ? (size_t)kWarps * Plan<MT, NT>::kStages * 32 * 16 : 0);
+    return (size_t)kWarps * Plan<NT>::kStages * 2 * kTile + q_bytes<NT>() +
+           (E8 ? (size_t)kWarps * Plan<NT>::kStages * 32 * 16 : 0);
 }
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool on)
@@ -173,27 +175,27 @@ __device__ __forceinline__ float odd_value(const KvView &kv, int64_t row, int g,
 }
 
 // ------------------------------------------------------------------ the kernel
-// E8: e4m3 cells (else bf16).  MT: 16-row fragments of an item's rows.  TQ: type of q and out;
+// E8: e4m3 cells (else bf16).  TQ: type of q and out;
 // NT: 16-bit terms of a query or weight.
-template <bool E8, int MT, typename TQ, int NT>
-__global__ void __launch_bounds__(kThreads, (Plan<MT, NT>::kCtas))
+template <bool E8, typename TQ, int NT>
+__global__ void __launch_bounds__(kThreads, (Plan<NT>::kCtas))
 dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const TQ *__restrict__ q,
                     int64_t ld_q, int H_q, float scale_log2, float q_sign, TQ *__restrict__ out,
                     float *__restrict__ lse, float *__restrict__ partial, Split *__restrict__ splits,
                     int by_item)
 {
     using S = Shape<E8>;
-    constexpr int kRows = 16 * MT, kStages = Plan<MT, NT>::kStages;
+    constexpr int kRows = 16, kStages = Plan<NT>::kStages;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int bad_s, odd_s;
-    __shared__ float red_m[kWarps][kRows], red_l[kWarps][kRows], top_s[MT];
+    __shared__ float red_m[kWarps][kRows], red_l[kWarps][kRows], top_s;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g8 = lane >> 2, c4 = lane & 3;
     unsigned char *ring = smem + (size_t)warp * kStages * 2 * kTile;
     uint4 *qf = reinterpret_cast<uint4 *>(smem + (size_t)kWarps * kStages * 2 * kTile);
     // per cell of a stage (E8): factor of the logit, exponent e of the value, 2^-e
-    float4 *exps = reinterpret_cast<float4 *>(reinterpret_cast<unsigned char *>(qf) + q_bytes<E8, MT, NT>()) +
+    float4 *exps = reinterpret_cast<float4 *>(reinterpret_cast<unsigned char *>(qf) + q_bytes<NT>()) +
                    warp * kStages * 32;
 
     pdl_wait();
@@ -288,9 +290,8 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
         {
             constexpr int E = E8 ? 16 : 8;       // dims of a thread in a block
             constexpr int kBlocks = kD / (4 * E);
-            const int mt = warp;
             auto load_row = [&](int hf, float *xa) {
-                const int r = mt * 16 + g8 + 8 * hf;
+                const int r = g8 + 8 * hf;
                 const TQ *src =
                     qp + (t0 + tok0 + r / G) * ld_q + (int64_t)(it.g * G + r % G) * kD + c4 * E;
 #pragma unroll
@@ -310,7 +311,7 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
                 // fp16 holds the queries once the tile's largest magnitude is below 2^8: one power
                 // of two for all rows, as a row 2^20 times smaller than another keeps 2^-13 of its
                 // own largest value and has logits that much smaller
-                if (mt < MT) {
+                if (warp == 0) {
                     float top = 0.0f;
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
@@ -321,18 +322,16 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
                             if (isfinite(xa[e])) top = fmaxf(top, fabsf(xa[e]));
                     }
                     top = warp_max(top);
-                    if (lane == 0) top_s[mt] = top;
+                    if (lane == 0) top_s = top;
                 }
                 __syncthreads();
-                float top = top_s[0];
-#pragma unroll
-                for (int i = 1; i < MT; ++i) top = fmaxf(top, top_s[i]);
+                const float top = top_s;
                 const int ex = (int)(__float_as_uint(top) >> 23) - 127;
                 const int sh = top > 0.0f ? min(max(7 - ex, -120), 100) : 0;
                 q_back = two_to(-sh);
                 mul = q_sign * two_to(sh);
             }
-            if (mt < MT) {
+            if (warp == 0) {
                 float xa[2][kBlocks * E];
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
@@ -349,7 +348,7 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
                         f.y = pack16<E8>(xa[1][4 * k], xa[1][4 * k + 1]);
                         f.z = pack16<E8>(xa[0][4 * k + 2], xa[0][4 * k + 3]);
                         f.w = pack16<E8>(xa[1][4 * k + 2], xa[1][4 * k + 3]);
-                        qf[((mt * NT + n) * 8 + k) * 32 + lane] = f;
+                        qf[(n * 8 + k) * 32 + lane] = f;
                     }
             }
         }
@@ -365,28 +364,23 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
             for (int i = 0; i < kStages - 1; ++i)
                 if (tile0 + i < tile1) keep_exps(i, i);
         }
-        int last[MT][2];  // the last cell each row sees
+        int last[2];  // the last cell each row sees
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int r = mt * 16 + g8 + 8 * hf;
-                last[mt][hf] = r < rows ? (ws.causal ? pos0 + r / G : cells - 1) : -1;
-            }
+        for (int hf = 0; hf < 2; ++hf) {
+            const int r = g8 + 8 * hf;
+            last[hf] = r < rows ? (ws.causal ? pos0 + r / G : cells - 1) : -1;
+        }
 
         // mx: the rows' reference; l: the sums in its units.  E8 with exponents far apart (wide):
         // l in units of ms, a reference of the logits alone.
-        float o[MT][16][4];
-        float ms[MT][2], mx[MT][2], l[MT][2];
+        float o[16][4];
+        float ms[2], mx[2], l[2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+        for (int n = 0; n < 16; ++n)
 #pragma unroll
-            for (int n = 0; n < 16; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.0f;
-            ms[mt][0] = ms[mt][1] = mx[mt][0] = mx[mt][1] = -INFINITY;
-            l[mt][0] = l[mt][1] = 0.0f;
-        }
+            for (int e = 0; e < 4; ++e) o[n][e] = 0.0f;
+        ms[0] = ms[1] = mx[0] = mx[1] = -INFINITY;
+        l[0] = l[1] = 0.0f;
         bool wide = false;
 
         int slot = 0;
@@ -435,13 +429,11 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
                     __syncwarp();
                 }
                 // ---- logits: fragments of 16 rows x 8 cells
-                float s[MT][S::kGroups * 2][4];
+                float s[S::kGroups * 2][4];
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int n = 0; n < S::kGroups * 2; ++n)
 #pragma unroll
-                    for (int n = 0; n < S::kGroups * 2; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.0f;
+                    for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
                 constexpr int kBlocks = E8 ? 2 : 4, kStepsPer = 8 / kBlocks;
 #pragma unroll
                 for (int b = 0; b < kBlocks; ++b) {
@@ -452,20 +444,18 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
 #pragma unroll
                     for (int j = 0; j < kStepsPer; ++j) {
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt)
+                        for (int t = 0; t < NT; ++t) {
+                            const uint4 f = qf[(t * 8 + b * kStepsPer + j) * 32 + lane];
+                            const uint32_t a[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-                            for (int t = 0; t < NT; ++t) {
-                                const uint4 f = qf[((mt * NT + t) * 8 + b * kStepsPer + j) * 32 + lane];
-                                const uint32_t a[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-                                for (int n = 0; n < S::kGroups * 2; ++n) {
-                                    const uint32_t w[4] = {kr[n].x, kr[n].y, kr[n].z, kr[n].w};
-                                    if constexpr (E8)
-                                        mma<true>(s[mt][n], a, half_pair(w[j]), half_pair_hi(w[j]));
-                                    else
-                                        mma<false>(s[mt][n], a, w[2 * j], w[2 * j + 1]);
-                                }
+                            for (int n = 0; n < S::kGroups * 2; ++n) {
+                                const uint32_t w[4] = {kr[n].x, kr[n].y, kr[n].z, kr[n].w};
+                                if constexpr (E8)
+                                    mma<true>(s[n], a, half_pair(w[j]), half_pair_hi(w[j]));
+                                else
+                                    mma<false>(s[n], a, w[2 * j], w[2 * j + 1]);
                             }
+                        }
                     }
                 }
                 // ---- masked, and the references moved where they have to: on bf16 cells the raw
@@ -477,85 +467,75 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
                         const float4 f0 = ex[8 * n + 2 * c4], f1 = ex[8 * n + 2 * c4 + 1];
                         far |= fabsf(f0.y) > kFar || fabsf(f1.y) > kFar;
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                            for (int hf = 0; hf < 2; ++hf) {
-                                s[mt][n][2 * hf] = fmaf(s[mt][n][2 * hf], f0.x, f0.y);
-                                s[mt][n][2 * hf + 1] = fmaf(s[mt][n][2 * hf + 1], f1.x, f1.y);
-                            }
+                        for (int hf = 0; hf < 2; ++hf) {
+                            s[n][2 * hf] = fmaf(s[n][2 * hf], f0.x, f0.y);
+                            s[n][2 * hf + 1] = fmaf(s[n][2 * hf + 1], f1.x, f1.y);
+                        }
                     }
                 }
                 if (edge) {
 #pragma unroll
                     for (int n = 0; n < S::kGroups * 2; ++n)
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (j0 + 8 * n + 2 * c4 + (i & 1) > last[mt][i >> 1]) s[mt][n][i] = -INFINITY;
+                        for (int i = 0; i < 4; ++i)
+                            if (j0 + 8 * n + 2 * c4 + (i & 1) > last[i >> 1]) s[n][i] = -INFINITY;
                 }
                 bool move = false;
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int hf = 0; hf < 2; ++hf) {
+                    // (-inf before the first cell: any finite logit moves it)
+                    const float over = E8 ? mx[hf] + kMove : (mx[hf] + kMove) * inv_scale;
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        // (-inf before the first cell: any finite logit moves it)
-                        const float over = E8 ? mx[mt][hf] + kMove : (mx[mt][hf] + kMove) * inv_scale;
-#pragma unroll
-                        for (int n = 0; n < S::kGroups * 2; ++n)
-                            move |= fmaxf(s[mt][n][2 * hf], s[mt][n][2 * hf + 1]) > over;
-                    }
+                    for (int n = 0; n < S::kGroups * 2; ++n)
+                        move |= fmaxf(s[n][2 * hf], s[n][2 * hf + 1]) > over;
+                }
                 if constexpr (E8) {
                     if (!wide && __any_sync(0xffffffffu, far)) {
                         wide = true;  // so far l is in units of mx
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                            for (int hf = 0; hf < 2; ++hf) ms[mt][hf] = mx[mt][hf];
+                        for (int hf = 0; hf < 2; ++hf) ms[hf] = mx[hf];
                     }
                     move |= wide;
                 }
                 if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
+                    for (int hf = 0; hf < 2; ++hf) {
+                        float b = mx[hf], a = ms[hf];
 #pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            float b = mx[mt][hf], a = ms[mt][hf];
+                        for (int n = 0; n < S::kGroups * 2; ++n)
 #pragma unroll
-                            for (int n = 0; n < S::kGroups * 2; ++n)
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const float v = s[mt][n][2 * hf + e];
-                                    b = fmaxf(b, E8 ? v : v * scale_log2);
-                                    if constexpr (E8) {
-                                        if (wide) a = fmaxf(a, v - ex[8 * n + 2 * c4 + e].y);
-                                    }
-                                }
-                            b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 1));
-                            b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 2));
-                            const float ao = b == -INFINITY ? 1.0f : ex2(mx[mt][hf] - b);
-                            mx[mt][hf] = b;
-                            float al = ao;
-                            if constexpr (E8) {
-                                if (wide) {
-                                    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-                                    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-                                    al = a == -INFINITY ? 1.0f : ex2(ms[mt][hf] - a);
-                                    ms[mt][hf] = a;
+                            for (int e = 0; e < 2; ++e) {
+                                const float v = s[n][2 * hf + e];
+                                b = fmaxf(b, E8 ? v : v * scale_log2);
+                                if constexpr (E8) {
+                                    if (wide) a = fmaxf(a, v - ex[8 * n + 2 * c4 + e].y);
                                 }
                             }
-                            l[mt][hf] *= al;
-#pragma unroll
-                            for (int n = 0; n < 16; ++n) {
-                                o[mt][n][2 * hf] *= ao;
-                                o[mt][n][2 * hf + 1] *= ao;
+                        b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 1));
+                        b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 2));
+                        const float ao = b == -INFINITY ? 1.0f : ex2(mx[hf] - b);
+                        mx[hf] = b;
+                        float al = ao;
+                        if constexpr (E8) {
+                            if (wide) {
+                                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+                                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+                                al = a == -INFINITY ? 1.0f : ex2(ms[hf] - a);
+                                ms[hf] = a;
                             }
                         }
+                        l[hf] *= al;
+#pragma unroll
+                        for (int n = 0; n < 16; ++n) {
+                            o[n][2 * hf] *= ao;
+                            o[n][2 * hf + 1] *= ao;
+                        }
+                    }
                 }
                 // ---- weights and their product with the values, 16 cells at a time
 #pragma unroll
                 for (int kg = 0; kg < S::kGroups; ++kg) {
-                    uint32_t a[MT][NT][4];
+                    uint32_t a[NT][4];
                     float2 iv[2];  // 2^-e of this thread's cells
                     if constexpr (E8) {
 #pragma unroll
@@ -564,48 +544,45 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
                             iv[n] = make_float2(f[0].z, f[1].z);
                         }
                     }
+                    float w[2][2][2];  // [n tile][row half][cell]
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        float w[2][2][2];  // [n tile][row half][cell]
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const float ux = mx[hf] == -INFINITY ? 0.0f : mx[hf];
 #pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            const float ux = mx[mt][hf] == -INFINITY ? 0.0f : mx[mt][hf];
+                        for (int n = 0; n < 2; ++n)
 #pragma unroll
-                            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const float v = s[mt][2 * kg + n][2 * hf + e];
-                                    const float p = ex2(E8 ? v - ux : fmaf(v, scale_log2, -ux));
-                                    w[n][hf][e] = p;
-                                    if constexpr (E8) {
-                                        const float g = e ? iv[n].y : iv[n].x;
-                                        if (!wide) l[mt][hf] = fmaf(p, g, l[mt][hf]);
-                                    } else {
-                                        l[mt][hf] += p;
-                                    }
-                                }
-                        }
-                        if constexpr (E8) {
-                            if (wide) {
-#pragma unroll
-                                for (int hf = 0; hf < 2; ++hf) {
-                                    const float us = ms[mt][hf] == -INFINITY ? 0.0f : ms[mt][hf];
-#pragma unroll
-                                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                                        for (int e = 0; e < 2; ++e)
-                                            l[mt][hf] += ex2(s[mt][2 * kg + n][2 * hf + e] -
-                                                             ex[8 * (2 * kg + n) + 2 * c4 + e].y - us);
+                            for (int e = 0; e < 2; ++e) {
+                                const float v = s[2 * kg + n][2 * hf + e];
+                                const float p = ex2(E8 ? v - ux : fmaf(v, scale_log2, -ux));
+                                w[n][hf][e] = p;
+                                if constexpr (E8) {
+                                    const float g = e ? iv[n].y : iv[n].x;
+                                    if (!wide) l[hf] = fmaf(p, g, l[hf]);
+                                } else {
+                                    l[hf] += p;
                                 }
                             }
-                        }
+                    }
+                    if constexpr (E8) {
+                        if (wide) {
 #pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            a[mt][t][0] = pack16<E8>(w[0][0][0], w[0][0][1]);
-                            a[mt][t][1] = pack16<E8>(w[0][1][0], w[0][1][1]);
-                            a[mt][t][2] = pack16<E8>(w[1][0][0], w[1][0][1]);
-                            a[mt][t][3] = pack16<E8>(w[1][1][0], w[1][1][1]);
+                            for (int hf = 0; hf < 2; ++hf) {
+                                const float us = ms[hf] == -INFINITY ? 0.0f : ms[hf];
+#pragma unroll
+                                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e)
+                                        l[hf] += ex2(s[2 * kg + n][2 * hf + e] -
+                                                         ex[8 * (2 * kg + n) + 2 * c4 + e].y - us);
+                            }
                         }
+                    }
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        a[t][0] = pack16<E8>(w[0][0][0], w[0][0][1]);
+                        a[t][1] = pack16<E8>(w[0][1][0], w[0][1][1]);
+                        a[t][2] = pack16<E8>(w[1][0][0], w[1][0][1]);
+                        a[t][3] = pack16<E8>(w[1][1][0], w[1][1][1]);
                     }
                     if constexpr (E8) {
                         // cells 2c4, 2c4 + 1 (and + 8): 8-byte words of their rows, interleaved
@@ -631,12 +608,10 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
                                     const uint32_t d0 = half_pair_hi(lo), d1 = half_pair_hi(hi);
                                     const int n = 8 * i + 4 * hw + 2 * p;
 #pragma unroll
-                                    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                                        for (int t = 0; t < NT; ++t) {
-                                            mma<true>(o[mt][n], a[mt][t], b0, b1);
-                                            mma<true>(o[mt][n + 1], a[mt][t], d0, d1);
-                                        }
+                                    for (int t = 0; t < NT; ++t) {
+                                        mma<true>(o[n], a[t], b0, b1);
+                                        mma<true>(o[n + 1], a[t], d0, d1);
+                                    }
                                 }
                             }
                         }
@@ -647,12 +622,10 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
                             uint32_t b[4];
                             ldsm_x4_t(b, sv_ + v_off<E8>(r, 2 * np + (lane >> 4)));
 #pragma unroll
-                            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                                for (int t = 0; t < NT; ++t) {
-                                    mma<false>(o[mt][2 * np], a[mt][t], b[0], b[1]);
-                                    mma<false>(o[mt][2 * np + 1], a[mt][t], b[2], b[3]);
-                                }
+                            for (int t = 0; t < NT; ++t) {
+                                mma<false>(o[2 * np], a[t], b[0], b[1]);
+                                mma<false>(o[2 * np + 1], a[t], b[2], b[3]);
+                            }
                         }
                     }
                 }
@@ -671,46 +644,40 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
         // ---- join the four warps: o in units of the sums' reference
         if (!E8 || !wide) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) ms[mt][hf] = mx[mt][hf];
+            for (int hf = 0; hf < 2; ++hf) ms[hf] = mx[hf];
         }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                float s = l[mt][hf];
-                s += __shfl_xor_sync(0xffffffffu, s, 1);
-                s += __shfl_xor_sync(0xffffffffu, s, 2);
-                l[mt][hf] = s;
-                if (c4 == 0) {
-                    red_m[warp][mt * 16 + g8 + 8 * hf] = ms[mt][hf];
-                    red_l[warp][mt * 16 + g8 + 8 * hf] = s;
-                }
+        for (int hf = 0; hf < 2; ++hf) {
+            float s = l[hf];
+            s += __shfl_xor_sync(0xffffffffu, s, 1);
+            s += __shfl_xor_sync(0xffffffffu, s, 2);
+            l[hf] = s;
+            if (c4 == 0) {
+                red_m[warp][g8 + 8 * hf] = ms[hf];
+                red_l[warp][g8 + 8 * hf] = s;
             }
+        }
         __syncthreads();  // every warp is done with its ring
         constexpr int kPitch = kD + 4;
         float *ob = reinterpret_cast<float *>(smem);  // [warp][row][kPitch]
         static_assert((size_t)kWarps * kRows * kPitch * 4 <= (size_t)kWarps * kStages * 2 * kTile,
                       "the warps' sums fit over the ring");
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int hf = 0; hf < 2; ++hf) {
+            const int r = g8 + 8 * hf;
+            const float m = fmaxf(fmaxf(red_m[0][r], red_m[1][r]), fmaxf(red_m[2][r], red_m[3][r]));
+            const float u = m == -INFINITY ? 0.0f : m;
+            const float f = mx[hf] == -INFINITY ? 0.0f : exp2f(mx[hf] - u);
+            float *dst = ob + (size_t)(warp * kRows + r) * kPitch;
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int r = mt * 16 + g8 + 8 * hf;
-                const float m = fmaxf(fmaxf(red_m[0][r], red_m[1][r]), fmaxf(red_m[2][r], red_m[3][r]));
-                const float u = m == -INFINITY ? 0.0f : m;
-                const float f = mx[mt][hf] == -INFINITY ? 0.0f : exp2f(mx[mt][hf] - u);
-                float *dst = ob + (size_t)(warp * kRows + r) * kPitch;
+            for (int n = 0; n < 16; ++n)
 #pragma unroll
-                for (int n = 0; n < 16; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        // bf16: dims 8n + 2c4 + e; e4m3: dim 64 (n / 8) + 8 (2 c4 + e) + n % 8
-                        const int dim = E8 ? 64 * (n >> 3) + 8 * (2 * c4 + e) + (n & 7) : 8 * n + 2 * c4 + e;
-                        dst[dim] = o[mt][n][2 * hf + e] * f;
-                    }
-            }
+                for (int e = 0; e < 2; ++e) {
+                    // bf16: dims 8n + 2c4 + e; e4m3: dim 64 (n / 8) + 8 (2 c4 + e) + n % 8
+                    const int dim = E8 ? 64 * (n >> 3) + 8 * (2 * c4 + e) + (n & 7) : 8 * n + 2 * c4 + e;
+                    dst[dim] = o[n][2 * hf + e] * f;
+                }
+        }
         __syncthreads();
         const bool whole = starts && ends;
         const bool nan_out = bad_s != 0 || !fits;
@@ -777,12 +744,12 @@ int decode_ctas(int per_sm)
     return n < kMaxCtas ? n : kMaxCtas;
 }
 
-template <bool E8, int MT, typename TQ, int NT>
+template <bool E8, typename TQ, int NT>
 cudaError_t run(const DenseArgs &a, void *workspace, cudaStream_t st)
 {
     const int G = a.H_q / a.kv.H_kv;
     WorkShape ws;
-    ws.rt = 16 * MT / G;
+    ws.rt = 16 / G;
     ws.kt = kWarps * Shape<E8>::kKeys;
     ws.H_kv = a.kv.H_kv;
     ws.causal = a.causal;
@@ -790,17 +757,17 @@ cudaError_t run(const DenseArgs &a, void *workspace, cudaStream_t st)
     // the kernel takes a positive scale: a negative one turns the queries' signs, zero clears them
     const float scale = (a.scale == 0.0f ? 1.0f : fabsf(a.scale)) * kLog2e;
     const float q_sign = a.scale == 0.0f ? 0.0f : (a.scale < 0.0f ? -1.0f : 1.0f);
-    constexpr size_t smem = decode_smem<E8, MT, NT>();
-    cudaError_t e = ensure_kernel_attrs<dense_decode_kernel<E8, MT, TQ, NT>>(smem);
+    constexpr size_t smem = decode_smem<E8, NT>();
+    cudaError_t e = ensure_kernel_attrs<dense_decode_kernel<E8, TQ, NT>>(smem);
     if (e != cudaSuccess) return e;
-    const int ctas = decode_ctas(Plan<MT, NT>::kCtas);
+    const int ctas = decode_ctas(Plan<NT>::kCtas);
     Split *splits = static_cast<Split *>(workspace);
     float *partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + kMaxCtas * sizeof(Split));
-    e = launch(dense_decode_kernel<E8, MT, TQ, NT>, dim3((unsigned)ctas), dim3(kThreads), smem, st, 1, a.kv,
+    e = launch(dense_decode_kernel<E8, TQ, NT>, dim3((unsigned)ctas), dim3(kThreads), smem, st, 1, a.kv,
                a.sv, ws, static_cast<const TQ *>(a.q), a.ld_q, a.H_q, scale, q_sign,
                static_cast<TQ *>(a.out), a.lse, partial, splits, (int)join_by_item(a, ws.rt, ctas));
     if (e != cudaSuccess) return e;
-    return launch_dense_join<TQ>(splits, partial, ctas, 16 * MT, ws.rt, a, st);
+    return launch_dense_join<TQ>(splits, partial, ctas, 16, ws.rt, a, st);
 }
 
 }  // namespace
@@ -811,29 +778,21 @@ bool dense_decode_ok(const DenseArgs &a, int64_t max_q)
     if (a.d != kD || (a.kv_dtype != QSA_BF16 && a.kv_dtype != QSA_E4M3)) return false;
     if (a.kv_dtype == QSA_E4M3 && (a.kv.ld_k % 16 || a.kv.ld_v % 16)) return false;
     if (a.kv.ld_k > (1 << 28) || a.kv.ld_v > (1 << 28)) return false;  // strides in 32 bits
-    // a fragment holds all heads of a KV head; fp32 queries come in several terms of one
-    if (G > (a.q_dtype == QSA_F32 ? 16 : 32)) return false;
-    // rows beyond one fragment of bf16 cells (two of e4m3 cells) are the 128-row kernel's: 64
-    // sequences of up to 8,000 cells, 32 / 4 heads, bf16: 2 tokens 113 us here and 121 there, 3
-    // tokens 127 and 122, 8 tokens 224 and 128; e4m3: 4 tokens 135 and 258
-    return a.q_dtype == QSA_F32 || max_q * G <= (a.kv_dtype == QSA_E4M3 ? 32 : 16);
+    // a fragment holds all heads of a KV head; fp32 queries come in several terms of one, however many
+    // tokens; bf16 queries beyond one fragment are the tcgen05 kernels'
+    return G <= 16 && (a.q_dtype == QSA_F32 || max_q * G <= 16);
 }
 
 size_t dense_decode_workspace()
 {
-    return kMaxCtas * sizeof(Split) + (size_t)2 * kMaxCtas * partial_floats(32, kD) * sizeof(float);
+    return kMaxCtas * sizeof(Split) + (size_t)2 * kMaxCtas * partial_floats(16, kD) * sizeof(float);
 }
 
-cudaError_t launch_dense_decode(const DenseArgs &a, int64_t max_q, void *workspace, cudaStream_t st)
+cudaError_t launch_dense_decode(const DenseArgs &a, void *workspace, cudaStream_t st)
 {
-    const int G = a.H_q / a.kv.H_kv;
     const bool e8 = a.kv_dtype == QSA_E4M3;
-    if (a.q_dtype == QSA_F32)
-        return e8 ? run<true, 1, float, 2>(a, workspace, st) : run<false, 1, float, 3>(a, workspace, st);
-    if (!e8) return run<false, 1, __nv_bfloat16, 1>(a, workspace, st);
-    // one fragment while it holds every new token of a sequence
-    if (G <= 16 && max_q <= 16 / G) return run<true, 1, __nv_bfloat16, 1>(a, workspace, st);
-    return run<true, 2, __nv_bfloat16, 1>(a, workspace, st);
+    if (a.q_dtype == QSA_F32) return e8 ? run<true, float, 2>(a, workspace, st) : run<false, float, 3>(a, workspace, st);
+    return e8 ? run<true, __nv_bfloat16, 1>(a, workspace, st) : run<false, __nv_bfloat16, 1>(a, workspace, st);
 }
 
 }  // namespace qsa

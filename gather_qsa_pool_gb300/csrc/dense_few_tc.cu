@@ -22,12 +22,19 @@
 // 2^(x - ve), from the weight where |ve| is at most 50.
 //
 // Shape: one persistent CTA per SM, an equal share of the flattened list of (sequence, KV head, row
-// tile) items in tiles of 128 cells (dense.cuh).  Warps 0-15: two or four groups that take the
-// weights of the tiles in turn, each with references, sums and output of its own, joined at the end of
-// a part; warp 16 issues the MMAs, warps 17 and 18 the copies of K and V (rings of 16 or 32 KB stages, one box per page),
-// warps 19 and 20 lay out the next part's queries and see to the tiles where some row does not see some cell.
-// Per tile the tensor cores run O_g += V' P_g and S_g of the group's next tile, while the other groups
-// compute.
+// tile) items in tiles of 128 cells (dense.cuh).  Warps 0-7: two groups that take the weights of the
+// tiles in turn, a cell a thread, each with references, sums and output of its own, joined at the end of
+// a part; warp 8 issues the MMAs, warps 9 and 10 the copies of K and of V (rings of 16 or 32 KB stages,
+// one box per page; one warp for both could not keep up), warps 11 and 12 lay out the next part's
+// queries, look the next part up for the others and see to the tiles where some row does not see some
+// cell.  Per tile the tensor cores run O_g += V' P_g and S_g of the group's next tile, while the other
+// group computes.
+//
+// What bounds it: bf16, the bytes (64 sequences of up to 8,000 cells, 32 / 4 heads, one token: 101 us,
+// 5.4 TB/s; one of 255,181: 95 us).  e4m3, the weights' turn from logits to terms and back to the tensor
+// cores, about 1,500 cycles a tile with two groups in flight where the bytes take 1,000 (48 sequences of
+// up to 16,384 cells, 32 rows: 105 us; 16 rows: 90 us, 4.5 TB/s), and about 10,000 cycles at each end of a
+// part (references, sums and outputs joined, the next part's first loads).
 //
 // Every mbarrier wait is bounded: after one gives up, nothing new is issued, what was issued is waited
 // for, the rows not finished become NaN and the tensor memory is returned.
@@ -376,6 +383,7 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
     }
     if (tid == 0) {
         bars.part[0] = p;
+        mbar_arrive(&bars.part_full[0]);  // (part 8 is its second)
         bars.per = per;
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -1008,11 +1016,20 @@ qsa_status run_few(const DenseArgs &a, void *workspace, cudaStream_t st)
 bool dense_few_ok(const DenseArgs &a, int64_t max_q)
 {
     const int G = a.H_q / a.kv.H_kv;
+    const bool e8 = a.kv_dtype == QSA_E4M3;
     // (a TMA map's strides are multiples of 16 bytes)
-    const bool cells = a.kv_dtype == QSA_BF16 ||
-                       (a.kv_dtype == QSA_E4M3 && a.kv.ld_k % 16 == 0 && a.kv.ld_v % 16 == 0);
-    return a.d == kD && a.q_dtype == QSA_BF16 && cells && G <= 32 && max_q * G <= 32 && a.pool_rows > 0 &&
-           a.pool_rows <= 0x7fffffffLL;
+    if (a.d != kD || a.q_dtype != QSA_BF16 || (!e8 && a.kv_dtype != QSA_BF16) || a.pool_rows <= 0 ||
+        a.pool_rows > 0x7fffffffLL || (e8 && (a.kv.ld_k % 16 || a.kv.ld_v % 16)))
+        return false;
+    if (G > 32 || max_q * G > 32) return false;
+    if (max_q * G > 16) return true;
+    // Up to 16 rows over short contexts are dense_decode.cu's: a part costs more here, a cell less.  By what
+    // the host knows, the most cells a sequence may have, measured there and here (us; one token, 32 / 4
+    // heads or 8 / 2): bf16, one sequence of 2,050 cells 11.9 and 14.2, of 8,000 18.9 and 17.3; e4m3, one
+    // of 8,000 15.9 and 18.7, of 30,000 25.4 and 22.7; 64 of up to 2,050 and 4 KV heads, bf16 48.4 and
+    // 44.9, e4m3 43.5 and 40.5, of up to 500 24.7 and 29.1.
+    const int64_t cells = a.kv.table ? a.kv.ld_table << a.kv.page_shift : a.sv.n_tok;
+    return cells >= (e8 ? 16384 : 4096) || (double)cells * (double)a.sv.n_seq * a.kv.H_kv >= (double)(1 << 18);
 }
 
 size_t dense_few_workspace()
