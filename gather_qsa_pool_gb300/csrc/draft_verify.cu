@@ -15,9 +15,11 @@
 // pairs cost six 32-bit adds each and hide behind the loads.
 //
 // One thread-block cluster per sequence: every CTA decides a itself (a few gathers), sums its
-// slice of the row(s), and the CTA whose slice holds the drawn point scans the slice of the one
-// warp that holds it.  One launch, no workspace, no atomics: the same result every time.  Bound
-// by one pass over one or two rows; with few sequences by the chain token -> gather -> row.
+// slice of the row(s), and the warps of the CTA that holds the drawn point scan, a chunk each, the
+// slice of the one warp that holds it (64 sequences, vocabulary of 131,072: 22.9 us; 31.7 with one
+// warp scanning).  One launch, no workspace, no atomics: the same result every time.  Bound by one
+// pass over one or two rows (10 of the 22.9 us, at the copy bandwidth) and the chain around it:
+// token -> gather -> row, the cluster's barrier, the chunk.
 #include <cooperative_groups.h>
 
 #include "dense.cuh"
@@ -149,73 +151,6 @@ __device__ __forceinline__ double slice_sum(const Row &row, int64_t c0, int64_t 
     return warp_sum_f64(((double)s.x + (double)s.y) + ((double)c.x + (double)c.y));
 }
 
-// The first index of the warp's chunks [c0, c1) whose running sum, from `base` on, passes x; the
-// last positive weight where none does; -1 without any.  find_last: only the latter.
-__device__ __forceinline__ int64_t slice_find(const Row &row, int64_t c0, int64_t c1, int64_t vocab, double base,
-                                              double x, bool find_last)
-{
-    const int lane = threadIdx.x & 31;
-    int64_t last = -1;
-    for (int64_t cb = c0; cb < c1; cb += 2) {
-        float p[2][4], q[2][4];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int64_t i = (cb + u) * kChunk + 4 * lane + k;
-                const bool on = cb + u < c1 && i < vocab;
-                p[u][k] = on ? row.p[i] : 0.0f;
-                q[u][k] = on && row.q ? row.q[i] : 0.0f;
-            }
-#pragma unroll 1
-        for (int u = 0; u < 2 && cb + u < c1; ++u) {
-            const int64_t i0 = (cb + u) * kChunk;
-            // the lane's four weights and their sum as a pair
-            float d[4], e[4], s = 0.0f, c = 0.0f;
-            int pos = -1;  // the lane's last positive weight
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float pk = u ? p[1][k] : p[0][k], qk = u ? q[1][k] : q[0][k];
-                row.weight(pk, qk, i0 + 4 * lane + k, d[k], e[k]);
-                if (d[k] > 0.0f) pos = k;
-                add_pair(s, c, d[k]);
-                c = __fadd_rn(c, e[k]);
-            }
-            const uint32_t any = __ballot_sync(0xffffffffu, pos >= 0);
-            if (any) {
-                const int j = 31 - __clz(any);
-                last = i0 + 4 * j + __shfl_sync(0xffffffffu, pos, j);
-            }
-            if (find_last) continue;
-            const double sum = (double)s + (double)c;
-            double incl = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
-            }
-            const uint32_t b = __ballot_sync(0xffffffffu, pos >= 0 && base + incl > x);
-            if (b) {
-                const int j = __ffs(b) - 1;  // the lane whose weights pass x
-                int hit = pos;
-                if (lane == j) {
-                    double run = base + (incl - sum);
-                    hit = -1;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        run += (double)d[k] + (double)e[k];
-                        if (hit < 0 && d[k] > 0.0f && run > x) hit = k;
-                    }
-                    if (hit < 0) hit = pos;
-                }
-                return i0 + 4 * j + __shfl_sync(0xffffffffu, hit, j);
-            }
-            base += __shfl_sync(0xffffffffu, incl, 31);
-        }
-    }
-    return last;
-}
-
 // First of `n` sums (n <= 32, lane i holds v) whose running sum passes x, and the sum before it;
 // -1 when none does.  last: the last positive one.
 __device__ __forceinline__ int first_over(double v, int n, double start, double x, double &before, int &last)
@@ -237,6 +172,83 @@ __device__ __forceinline__ int first_over(double v, int n, double start, double 
     return j;
 }
 
+// What the warps of a CTA tell one another while they look for the drawn point.
+struct Search {
+    double base, x;     // the sum before the slice, the point
+    int64_t c0, c1;     // the slice's chunks; none when another CTA has it
+    int end;            // the last weight is asked for, whatever x
+    double sum[kWarps];
+    int64_t last[kWarps];
+};
+
+// The first index of the slice whose running sum passes x; the last positive weight where none does;
+// -1 without any.  A chunk a warp, kWarps at a time: returned to the warp that has it, -2 to the others.
+__device__ __forceinline__ int64_t slice_find(const Row &row, Search &f, int64_t vocab)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const double x = f.x;
+    const bool end = f.end != 0;
+    double base = f.base;
+    int64_t last = -1;
+    for (int64_t cb = f.c0; cb < f.c1; cb += kWarps) {
+        const int64_t i0 = (cb + warp) * kChunk + 4 * lane;
+        // the lane's four weights and their sum as a pair
+        float d[4], e[4], s = 0.0f, c = 0.0f;
+        int pos = -1;  // the lane's last positive weight
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const bool on = cb + warp < f.c1 && i0 + k < vocab;
+            const float pk = on ? row.p[i0 + k] : 0.0f, qk = on && row.q ? row.q[i0 + k] : 0.0f;
+            row.weight(pk, qk, i0 + k, d[k], e[k]);
+            if (d[k] > 0.0f) pos = k;
+            add_pair(s, c, d[k]);
+            c = __fadd_rn(c, e[k]);
+        }
+        const double sum = (double)s + (double)c, all = warp_sum_f64(sum);
+        const uint32_t any = __ballot_sync(0xffffffffu, pos >= 0);
+        const int tail = any ? 31 - __clz(any) : 0;
+        const int64_t mine = any ? (cb + warp) * kChunk + 4 * tail + __shfl_sync(0xffffffffu, pos, tail) : -1;
+        if (lane == 0) {
+            f.sum[warp] = all;
+            f.last[warp] = mine;
+        }
+        __syncthreads();
+        double before = base;
+        int lw;
+        const int w = end ? -1 : first_over(lane < kWarps ? f.sum[lane] : 0.0, kWarps, base, x, before, lw);
+        if (w >= 0) {
+            if (warp != w) return -2;
+            double incl = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const double v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            const uint32_t b = __ballot_sync(0xffffffffu, pos >= 0 && before + incl > x);
+            if (!b) return mine;  // (rounding: the chunk's last)
+            const int j = __ffs(b) - 1;  // the lane whose weights pass x
+            int hit = pos;
+            if (lane == j) {
+                double run = before + (incl - sum);
+                hit = -1;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    run += (double)d[k] + (double)e[k];
+                    if (hit < 0 && d[k] > 0.0f && run > x) hit = k;
+                }
+                if (hit < 0) hit = pos;
+            }
+            return (cb + w) * kChunk + 4 * j + __shfl_sync(0xffffffffu, hit, j);
+        }
+        for (int i = 0; i < kWarps; ++i) {
+            base += f.sum[i];
+            last = f.last[i] >= 0 ? f.last[i] : last;
+        }
+        __syncthreads();  // before the next turn's sums
+    }
+    return warp == 0 ? last : -2;
+}
+
 __global__ void __launch_bounds__(kThreads, 2)
 draft_verify_kernel(const float *__restrict__ target, int64_t ld_t, const float *__restrict__ draft,
                     int64_t ld_d, const int32_t *__restrict__ tokens,
@@ -246,7 +258,8 @@ draft_verify_kernel(const float *__restrict__ target, int64_t ld_t, const float 
 {
     __shared__ double warp_w[kWarps];        // this CTA's slices
     __shared__ double cta_w[2][kMaxCluster];  // every CTA's total: of the weights, of the plain row
-    __shared__ int taken_s, refused_s, empty_s;
+    __shared__ int taken_s, refused_s, empty_s, owner_s;
+    __shared__ Search search;
     cg::cluster_group cl = cg::this_cluster();
     const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
     const int64_t s = blockIdx.x / C;
@@ -320,33 +333,40 @@ draft_verify_kernel(const float *__restrict__ target, int64_t ld_t, const float 
             __syncthreads();
             if (empty_s) continue;
         }
-        // ---- where the drawn point lies: the CTA, its warp's slice, the index
+        // ---- where the drawn point lies: the CTA, its warp's slice (warp 0), the index (all its warps)
         if (warp == 0) {
             const double x = (double)r * total;
-            double before = 0.0;
-            int last;
+            double before = 0.0, base = 0.0;
+            int last, w = -1;
             int owner = first_over(lane < C ? cta_w[plain][lane] : 0.0, C, 0.0, x, before, last);
             const bool tail = owner < 0;  // rounding at the end: the last weight
             if (tail) owner = last;
-            if (rank == (owner < 0 ? 0 : owner)) {
-                int token = -1;  // no weight anywhere
-                if (owner >= 0) {
-                    double base = 0.0;
-                    int w = tail ? -1
-                                 : first_over(lane < kWarps ? warp_w[lane] : 0.0, kWarps, before, x, base, last);
-                    const bool end = w < 0;
-                    if (end) {
-                        (void)first_over(lane < kWarps ? warp_w[lane] : 0.0, kWarps, 0.0, INFINITY, base, last);
-                        w = last;
-                    }
-                    if (w >= 0) {
-                        const int64_t d0 = min(((int64_t)rank * kWarps + w) * per, chunks);
-                        token = (int)slice_find(row, d0, min(d0 + per, chunks), vocab, base, x, end);
-                    }
+            bool end = false;
+            if (owner >= 0 && rank == owner) {
+                w = tail ? -1 : first_over(lane < kWarps ? warp_w[lane] : 0.0, kWarps, before, x, base, last);
+                end = w < 0;
+                if (end) {
+                    (void)first_over(lane < kWarps ? warp_w[lane] : 0.0, kWarps, 0.0, INFINITY, base, last);
+                    w = last;
                 }
+            }
+            if (lane == 0) {
+                const int64_t d0 = w < 0 ? 0 : min(((int64_t)rank * kWarps + w) * per, chunks);
+                search.base = base;
+                search.x = x;
+                search.c0 = d0;
+                search.c1 = w < 0 ? 0 : min(d0 + per, chunks);
+                search.end = end;
+                owner_s = rank == (owner < 0 ? 0 : owner);
+            }
+        }
+        __syncthreads();
+        if (owner_s) {
+            const int64_t token = slice_find(row, search, vocab);  // -1: no weight anywhere
+            if (token >= -1) {
                 int32_t *to = tokens_out + s * (max_draft + 1);
                 for (int j = lane; j <= max_draft; j += 32)
-                    to[j] = j < a ? tokens[s * max_draft + j] : (j == a ? token : -1);
+                    to[j] = j < a ? tokens[s * max_draft + j] : (j == a ? (int)token : -1);
                 if (lane == 0) n_accepted[s] = a;
             }
         }
