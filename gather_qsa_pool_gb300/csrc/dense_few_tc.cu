@@ -1021,7 +1021,9 @@ bool dense_few_ok(const DenseArgs &a, int64_t max_q)
     if (a.d != kD || a.q_dtype != QSA_BF16 || (!e8 && a.kv_dtype != QSA_BF16) || a.pool_rows <= 0 ||
         a.pool_rows > 0x7fffffffLL || (e8 && (a.kv.ld_k % 16 || a.kv.ld_v % 16)))
         return false;
-    if (G > 32 || max_q * G > 32) return false;
+    if (G > 32 || max_q * G > (e8 ? 64 : 32)) return false;
+    // (e4m3: two row tiles read the cells twice and still beat the 128-row kernel, whose conversion bounds
+    // it: 64 sequences of up to 8,000 cells, 64 rows, 142 us here and 243 there; bf16, 32 rows, 103 and 124)
     if (max_q * G > 16) return true;
     // Up to 16 rows over short contexts are dense_decode.cu's: a part costs more here, a cell less.  By what
     // the host knows, the most cells a sequence may have, measured there and here (us; one token, 32 / 4

@@ -56,6 +56,13 @@ def test_few_rows(case, kv_dtype):
 
 
 @pytest.mark.parametrize("kv_dtype", [BF16, E4M3])
+@pytest.mark.parametrize("news,H_q", [([8, 5, 1, 0], 32), ([16, 3, 9, 2], 16), ([11, 1, 7, 5], 20)])
+def test_rows_of_two_tiles(news, H_q, kv_dtype):
+    """Up to 64 rows: e4m3 cells are read once for each 32 of them."""
+    run_paged(widen(Pool([700, 5, 260, 40], 4, 128, 64, kv_dtype, seed=27)), news, H_q, BF16, seed=28)
+
+
+@pytest.mark.parametrize("kv_dtype", [BF16, E4M3])
 @pytest.mark.parametrize("news", [[1, 1], [4, 2]])
 def test_few_rows_without_causal_mask(news, kv_dtype):
     run_paged(widen(Pool([333, 129], 2, 128, 32, kv_dtype, seed=3)), news, 16, BF16, seed=4, causal=False)
