@@ -40,8 +40,6 @@ constexpr uint32_t kTmemCols = 512;
 __host__ __device__ constexpr uint32_t col_s(int g) { return g ? 128u : 0u; }
 __host__ __device__ constexpr uint32_t col_o(int g) { return g ? 384u : 256u; }
 
-constexpr int kMaxStages = 5;
-
 // What differs between caches.  bf16: five stages, two warps for the tiles with a causal edge.
 // e4m3: four stages of bf16 filled by six warps from two raw 16 KB tiles.
 // Registers: 640 x 96 at launch = 512 x 104 + 128 x 64; 768 x 80 = 512 x 96 + 256 x 48.
@@ -52,22 +50,26 @@ struct Cfg {
     static constexpr int kThreads = 32 * (kAuxWarp + kAuxWarps);
 };
 constexpr int kAuxBar = 9;                // their named barriers: 9, 10
+constexpr int kSoftBar = 11;              // the softmax warps'
 
+template <bool E8>
 struct Bars {
-    uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t raw[kMaxStages];                        // bf16: copies of a stage with an edge
+    uint64_t full[Cfg<E8>::kStages], empty[Cfg<E8>::kStages];
+    uint64_t raw[E8 ? 1 : Cfg<E8>::kStages];         // bf16: copies of a stage with an edge
     uint64_t raw_full[2], raw_empty[2];              // e4m3: raw tiles
     uint64_t s_full[2], p_full[2], o_full[2], q_full[2], q_free[2], drain;
     uint32_t tmem, pad;
     int32_t odd[kSlots], bad[kSlots];  // number + 1 of the part that set it
-    uint8_t exps[2][2][kN];            // e4m3: exponents of the cells of K and V tiles, two turns
+    uint8_t exps[2][2][E8 ? kN : 1];   // e4m3: exponents of the cells of K and V tiles, two turns
     float row[2][kM];                  // exchanged by the two threads of a row
+    Parts part[2];                     // the softmax warps' part, and the next
+    int64_t per;                       // places of a CTA
 };
 
 template <bool E8>
 __host__ __device__ constexpr size_t tc_smem()
 {
-    return 1024 + 2 * kTileB + (size_t)Cfg<E8>::kStages * kTileB + (E8 ? 2 * kRawTile : 0) + sizeof(Bars);
+    return 1024 + 2 * kTileB + (size_t)Cfg<E8>::kStages * kTileB + (E8 ? 2 * kRawTile : 0) + sizeof(Bars<E8>);
 }
 static_assert(tc_smem<false>() <= 227 * 1024 && tc_smem<true>() <= 227 * 1024, "shared memory of one CTA");
 
@@ -85,7 +87,7 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);  // [group][dim half]
     unsigned char *ring = sQ + 2 * kTileB;
     unsigned char *raw_tiles = ring + (size_t)kStages * kTileB;  // e4m3: two
-    Bars &bars = *reinterpret_cast<Bars *>(raw_tiles + (E8 ? 2 * kRawTile : 0));
+    Bars<E8> &bars = *reinterpret_cast<Bars<E8> *>(raw_tiles + (E8 ? 2 * kRawTile : 0));
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform, as the compiler sees it
@@ -93,7 +95,7 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&bars.full[s], E8 ? kTeamWarps : kAuxWarps);
             mbar_init(&bars.empty[s], 1);
-            mbar_init(&bars.raw[s], 1);
+            if (!E8) mbar_init(&bars.raw[s], 1);
         }
         for (int g = 0; g < 2; ++g) {
             mbar_init(&bars.s_full[g], 1);
@@ -134,6 +136,10 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
                      "r"(kTmemCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid == 0) {
+        bars.part[0] = p;
+        bars.per = per;
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
@@ -416,7 +422,11 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
         const uint32_t colS = tmem + lrow + col_s(gi), colO = tmem + lrow + col_o(gi) + 64 * hf;
         float *const swap = &bars.row[gi][r];
         uint32_t cs = 0, co = 0;  // waits on s_full, o_full so far
+        // (the part is read where it lies: its fields would take the registers of logits)
+        int n = 0;
+        bool more;
         do {
+            const Parts &p = bars.part[n & 1];
             const int tok = gi * rt2 + r / G;  // of the item
             const bool group = gi == 0 || p.toks > rt2;
             const bool live = r < rt2 * G && tok < p.toks;
@@ -530,9 +540,9 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
             }
             // ---- the part's result: finished rows, or a record to be joined
             const bool starts = p.tile0 == 0, ends = p.tile1 == p.it.tiles;
-            const bool odd = *reinterpret_cast<volatile int32_t *>(&bars.odd[p.n % kSlots]) == p.n + 1;
+            const bool odd = *reinterpret_cast<volatile int32_t *>(&bars.odd[n % kSlots]) == n + 1;
             const bool bad = !ok || !p.fits ||
-                             *reinterpret_cast<volatile int32_t *>(&bars.bad[p.n % kSlots]) == p.n + 1;
+                             *reinterpret_cast<volatile int32_t *>(&bars.bad[n % kSlots]) == n + 1;
             if (group) {
                 if (bad) l = NAN;
                 const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
@@ -588,8 +598,13 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
             }
             if (starts && tid == 0 && !whole_items)
                 note_split(splits, by_item, p.it, ends,
-                           div_pos(p.it.start + ws.over + p.it.tiles - 1, per));
-        } while (p.next(kv, sv, ws));
+                           div_pos(p.it.start + ws.over + p.it.tiles - 1, bars.per));
+            Parts next = p;
+            more = next.next(kv, sv, ws);
+            if (tid == 0) bars.part[(n + 1) & 1] = next;
+            named_sync<32 * kSoftWarps>(kSoftBar);
+            ++n;
+        } while (more);
     }
 
     if (!ok) report_timeout(wc);
