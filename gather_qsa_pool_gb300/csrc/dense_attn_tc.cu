@@ -42,7 +42,8 @@ __host__ __device__ constexpr uint32_t col_o(int g) { return g ? 384u : 256u; }
 
 // What differs between caches.  bf16: five stages, two warps for the tiles with a causal edge.
 // e4m3: four stages of bf16 filled by six warps from two raw 16 KB tiles.
-// Registers: 640 x 96 at launch = 512 x 104 + 128 x 64; 768 x 80 = 512 x 96 + 256 x 48.
+// Registers: 640 x 96 at launch = 512 x 104 + 128 x 64; 768 x 80 = 512 x 88 + 256 x 64 (a chunk of
+// 1,024 tokens over 61,789 e4m3 cells 1,253 us, bound by the conversion; 1,355 with 96 and 48).
 template <bool E8>
 struct Cfg {
     static constexpr int kStages = E8 ? 4 : 5;
@@ -149,7 +150,7 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
     const int rt2 = ws.rt / 2;  // tokens of a group
     bool ok = true;
     if (warp >= kSoftWarps) {
-        if constexpr (E8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if constexpr (E8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == kMmaWarp) {
             // ---- MMA issue (all lanes walk, one issues)
@@ -410,7 +411,7 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
         }
         __syncwarp();
     } else {
-        if constexpr (E8) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+        if constexpr (E8) asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
         else asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
         // ---- softmax of group gi: row r by two threads, cells 64 hf .. 64 hf + 63 of each tile.
         // The two warps of a row stay in step (pair barriers): what one of them cannot wait for
