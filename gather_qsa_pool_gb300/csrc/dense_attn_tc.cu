@@ -242,10 +242,19 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
             uint32_t n = 0, nq[2] = {0, 0};
             uint32_t edge_last = 0, raw_phase = 0, used = 0;  // bits by stage
             do {
+                // (a tile's pages are looked up two tiles ahead: nothing waits for them)
+                PageAhead ahead[2];
+                auto look = [&](int t) {
+                    PageAhead a;
+                    a.load(kv, p, t < p.tile1 && lane < boxes, (int64_t)t * kN + lane * box_rows);
+                    return a;
+                };
+                ahead[0] = look(p.tile0);
+                ahead[1] = look(p.tile0 + 1);
                 for (int t = p.tile0; ok && t < p.tile1; ++t) {
-                    const int j = t * kN + lane * box_rows;
-                    int64_t row = -2;
-                    if (lane < boxes && j < p.n_see) row = cell_row(kv, p.it.s, p.t0, j);
+                    const int row = ahead[0].row(kv, p);
+                    ahead[0] = ahead[1];
+                    ahead[1] = look(t + 2);
                     const uint32_t go = __ballot_sync(0xffffffffu, row >= 0);
                     if (__any_sync(0xffffffffu, row == -1) && lane == 0)
                         *reinterpret_cast<volatile int32_t *>(&bars.bad[p.n % kSlots]) = p.n + 1;
@@ -266,7 +275,7 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
                             if (row >= 0)
                                 tma_box(smem_u32(raw_tiles) + (uint32_t)s * kRawTile +
                                             (uint32_t)(lane * box_rows) * 128,
-                                        map, p.it.g * kD, (int)row, &bars.raw_full[s]);
+                                        map, p.it.g * kD, row, &bars.raw_full[s]);
                         } else {
                             const int s = (int)(n % kStages);
                             if (n >= kStages &&
@@ -288,8 +297,8 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
                             if (row >= 0) {
                                 const uint32_t dst =
                                     smem_u32(ring) + (uint32_t)s * kTileB + (uint32_t)(lane * box_rows) * 128;
-                                tma_box(dst, map, p.it.g * kD, (int)row, bar);
-                                tma_box(dst + kHalf, map, p.it.g * kD + 64, (int)row, bar);
+                                tma_box(dst, map, p.it.g * kD, row, bar);
+                                tma_box(dst + kHalf, map, p.it.g * kD + 64, row, bar);
                             }
                         }
                         if (half == 0 && t == p.tile0) {

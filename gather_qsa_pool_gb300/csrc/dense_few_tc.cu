@@ -165,30 +165,6 @@ __device__ __forceinline__ float col_reduce(float (&v)[N])
     return v[0];
 }
 
-// A cell's page entry, loaded some tiles ahead and not looked at until then (packed rows: none), and
-// the cell's row: -1 when its page is not in the pool, -2 when there is no such cell.
-struct PageAhead {
-    int32_t page;
-    int32_t cell;  // below 0: none
-    __device__ __forceinline__ void load(const KvView &kv, const Parts &p, bool on, int64_t j)
-    {
-        on = on && j < p.n_see;
-        cell = on ? (int32_t)j : -1;
-        page = 0;
-        if (on && kv.table) {
-            const int64_t k = j >> kv.page_shift;
-            page = k < kv.ld_table ? kv.table[(int64_t)p.it.s * kv.ld_table + k] : -1;
-        }
-    }
-    __device__ __forceinline__ int row(const KvView &kv, const Parts &p) const
-    {
-        if (cell < 0) return -2;
-        if (!kv.table) return (int)p.t0 + cell;
-        if ((uint32_t)page >= (uint32_t)kv.n_pages) return -1;
-        return (page << kv.page_shift) | (cell & ((1 << kv.page_shift) - 1));
-    }
-};
-
 // Two fp16 numbers as their upper bytes, and what those leave.
 __device__ __forceinline__ uint32_t less_upper(uint32_t h)
 {

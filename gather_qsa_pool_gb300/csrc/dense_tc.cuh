@@ -156,6 +156,30 @@ struct Parts {
     __device__ __forceinline__ bool edge(int t) const { return t * kN + kN - 1 > pos0; }
 };
 
+// A cell's page entry, loaded some tiles ahead and not looked at until then (packed rows: none), and
+// the cell's row: -1 when its page is not in the pool, -2 when there is no such cell.
+struct PageAhead {
+    int32_t page;
+    int32_t cell;  // below 0: none
+    __device__ __forceinline__ void load(const KvView &kv, const Parts &p, bool on, int64_t j)
+    {
+        on = on && j < p.n_see;
+        cell = on ? (int32_t)j : -1;
+        page = 0;
+        if (on && kv.table) {
+            const int64_t k = j >> kv.page_shift;
+            page = k < kv.ld_table ? kv.table[(int64_t)p.it.s * kv.ld_table + k] : -1;
+        }
+    }
+    __device__ __forceinline__ int row(const KvView &kv, const Parts &p) const
+    {
+        if (cell < 0) return -2;
+        if (!kv.table) return (int)p.t0 + cell;
+        if ((uint32_t)page >= (uint32_t)kv.n_pages) return -1;
+        return (page << kv.page_shift) | (cell & ((1 << kv.page_shift) - 1));
+    }
+};
+
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
                                    const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
                                    const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
