@@ -84,10 +84,12 @@ __device__ __forceinline__ int seq_cells(const SeqView &sv, int s, int len)
     return sv.kv_len ? max(sv.kv_len[s], 0) : len;
 }
 
-// A paged sequence longer than its row of the table cannot be right: its outputs become NaN.
+// A paged sequence longer than its row of the table cannot be right: its outputs become NaN.  (Nor is one
+// looked at whose last tile's end would pass 31 bits.)
+constexpr int32_t kMostCells = 0x7fffff00;
 __device__ __forceinline__ bool cells_fit(const KvView &kv, int cells)
 {
-    return kv.table == nullptr || (int64_t)cells <= (kv.ld_table << kv.page_shift);
+    return cells <= kMostCells && (kv.table == nullptr || (int64_t)cells <= (kv.ld_table << kv.page_shift));
 }
 
 // Pool row of the cell at position p of sequence s; -1 when its page is not in the pool.
@@ -116,11 +118,14 @@ struct WorkShape {
                      // places without a tile before each item's first
     int32_t H_kv;
     int32_t causal;
+    int32_t most;    // the most cells a sequence may have: a longer one cannot be right, and nothing of it
+                     // is looked at
 };
 
 // Cells that the tokens of row tile t see together.
 __device__ __forceinline__ int item_cells(const WorkShape &w, int len, int cells, int t)
 {
+    if (cells > w.most) return 0;
     if (!w.causal) return cells;
     const int64_t last = (int64_t)(t + 1) * w.rt;
     const int64_t seen = (int64_t)cells - len + (last < len ? last : len);
@@ -131,7 +136,7 @@ __device__ __forceinline__ int item_tiles(const WorkShape &w, int len, int cells
 {
     if (w.kt == 0) return 1;
     const int n = item_cells(w, len, cells, t);
-    return n > 0 ? (n + w.kt - 1) / w.kt : 1;
+    return n > 0 ? (n - 1) / w.kt + 1 : 1;
 }
 
 // a / b, b > 0, with one 32-bit division where that is enough.
@@ -152,7 +157,7 @@ __device__ __forceinline__ int64_t floor_div(int64_t a, int64_t b)
 // (1, 2, 4 ... heads per KV head) and is a loop otherwise.
 __device__ __forceinline__ int64_t tiles_before(const WorkShape &w, int len, int cells, int t)
 {
-    if (!w.causal || w.kt == 0) return (int64_t)t * item_tiles(w, len, cells, 0);
+    if (!w.causal || w.kt == 0 || cells > w.most) return (int64_t)t * item_tiles(w, len, cells, 0);
     const int64_t base = (int64_t)cells - len;
     int64_t i0 = base < 0 ? div_pos(-base, w.rt) : 0;  // row tiles that see nothing
     if (i0 > t) i0 = t;
@@ -349,6 +354,13 @@ struct DenseArgs {
     int causal;
     int64_t pool_rows;  // rows of K and V
 };
+
+// Row tiles of rt tokens, cells in tiles of kt, `over` places an item.
+inline WorkShape work_shape(const DenseArgs &a, int rt, int kt, int over)
+{
+    const int64_t most = a.kv.table ? a.kv.ld_table << a.kv.page_shift : kMostCells;
+    return {rt, kt, over, a.kv.H_kv, a.causal, (int32_t)(most < kMostCells ? most : kMostCells)};
+}
 
 // Any shape: d a multiple of 8 up to 256, fp32 arithmetic on the CUDA cores.
 cudaError_t launch_dense_attn(const DenseArgs &a, cudaStream_t st);

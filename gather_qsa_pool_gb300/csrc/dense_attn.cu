@@ -195,12 +195,7 @@ template <typename TQ, typename TK>
 cudaError_t run(const DenseArgs &a, cudaStream_t st)
 {
     const int G = a.H_q / a.kv.H_kv;
-    WorkShape ws;
-    ws.rt = G >= kRows ? 1 : kRows / G;
-    ws.kt = 0;
-    ws.H_kv = a.kv.H_kv;
-    ws.causal = a.causal;
-    ws.over = 0;
+    const WorkShape ws = work_shape(a, G >= kRows ? 1 : kRows / G, 0, 0);
     const size_t smem = dense_smem(a.d);
     cudaError_t e = ensure_kernel_attrs<dense_attn_kernel<TQ, TK>>(smem);
     if (e != cudaSuccess) return e;

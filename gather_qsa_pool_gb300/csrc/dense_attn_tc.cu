@@ -648,6 +648,7 @@ constexpr int kMaxCtas = kTargetSMs;
 bool dense_tc_ok(const DenseArgs &a)
 {
     const int G = a.H_q / a.kv.H_kv;
+    if (a.kv.ld_k > kMaxStride || a.kv.ld_v > kMaxStride || a.ld_q > kMaxStride) return false;
     // (a TMA map's strides are multiples of 16 bytes; the softmax takes its maximum over unscaled
     // logits: a positive scale)
     const bool cells = a.kv_dtype == QSA_BF16 ||
@@ -673,12 +674,7 @@ static qsa_status run_tc(const DenseArgs &a, void *workspace, cudaStream_t st)
         !make_map(&mk, a.kv.K, a.pool_rows, width, a.kv.ld_k, box_rows, E8, !E8) ||
         !make_map(&mv, a.kv.V, a.pool_rows, width, a.kv.ld_v, box_rows, E8, !E8))
         return QSA_ERR_CUDA;
-    WorkShape ws;
-    ws.rt = 2 * (kM / G);
-    ws.kt = kN;
-    ws.H_kv = a.kv.H_kv;
-    ws.causal = a.causal;
-    ws.over = kOver;
+    const WorkShape ws = work_shape(a, 2 * (kM / G), kN, kOver);
     constexpr size_t smem = tc_smem<E8>();
     if (ensure_kernel_attrs<dense_tc_kernel<E8>>(smem) != cudaSuccess) return QSA_ERR_CUDA;
     int ctas = device_sm_count();

@@ -748,12 +748,7 @@ template <bool E8, typename TQ, int NT>
 cudaError_t run(const DenseArgs &a, void *workspace, cudaStream_t st)
 {
     const int G = a.H_q / a.kv.H_kv;
-    WorkShape ws;
-    ws.rt = 16 / G;
-    ws.kt = kWarps * Shape<E8>::kKeys;
-    ws.H_kv = a.kv.H_kv;
-    ws.causal = a.causal;
-    ws.over = 0;
+    const WorkShape ws = work_shape(a, 16 / G, kWarps * Shape<E8>::kKeys, 0);
     // the kernel takes a positive scale: a negative one turns the queries' signs, zero clears them
     const float scale = (a.scale == 0.0f ? 1.0f : fabsf(a.scale)) * kLog2e;
     const float q_sign = a.scale == 0.0f ? 0.0f : (a.scale < 0.0f ? -1.0f : 1.0f);

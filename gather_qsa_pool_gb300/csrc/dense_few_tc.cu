@@ -964,12 +964,7 @@ qsa_status run_few(const DenseArgs &a, void *workspace, cudaStream_t st)
     if (!make_map(&mk, a.kv.K, a.pool_rows, width, a.kv.ld_k, box_rows, E8, true) ||
         !make_map(&mv, a.kv.V, a.pool_rows, width, a.kv.ld_v, box_rows, E8, true))
         return QSA_ERR_CUDA;
-    WorkShape ws;
-    ws.rt = NR / G;
-    ws.kt = kN;
-    ws.H_kv = a.kv.H_kv;
-    ws.causal = a.causal;
-    ws.over = F::kOver;
+    const WorkShape ws = work_shape(a, NR / G, kN, F::kOver);
     // the kernel takes a positive scale: a negative one turns the queries' signs, zero clears them
     const float scale = (a.scale == 0.0f ? 1.0f : fabsf(a.scale)) * kLog2e;
     const float q_sign = a.scale == 0.0f ? 0.0f : (a.scale < 0.0f ? -1.0f : 1.0f);
@@ -993,7 +988,8 @@ bool dense_few_ok(const DenseArgs &a, int64_t max_q)
 {
     const int G = a.H_q / a.kv.H_kv;
     const bool e8 = a.kv_dtype == QSA_E4M3;
-    // (a TMA map's strides are multiples of 16 bytes)
+    // (a TMA map's strides are multiples of 16 bytes, and below 2^40)
+    if (a.kv.ld_k > kMaxStride || a.kv.ld_v > kMaxStride) return false;
     if (a.d != kD || a.q_dtype != QSA_BF16 || (!e8 && a.kv_dtype != QSA_BF16) || a.pool_rows <= 0 ||
         a.pool_rows > 0x7fffffffLL || (e8 && (a.kv.ld_k % 16 || a.kv.ld_v % 16)))
         return false;

@@ -20,6 +20,7 @@ constexpr uint32_t kRawTile = 128 * 128;  // 16 KB: 128 cells of codes
 constexpr int kTeamWarps = 3;             // warps that convert K tiles, and V tiles
 constexpr float kMove = 8.0f;            // move the reference past 2^8 growth
 constexpr int kSlots = 8;                // parts whose flags are kept
+constexpr int64_t kMaxStride = 1 << 28;  // elements between rows that a tensor map takes
 
 __device__ __forceinline__ void mbar_arrive_n(uint64_t *bar, uint32_t n)
 {

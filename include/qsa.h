@@ -744,8 +744,8 @@ qsa_status qsa_paged_read(const qsa_paged_cache *cache, const int32_t *table, in
  *   out[i][h][:] = sum_j softmax_j(scale * q[i][h] . K[j][g]) V[j][g][:]
  *   lse_out[i][h] = log(sum_j exp(scale * q[i][h] . K[j][g]))   (natural log; optional)
  * A token that sees no cell (p < 0) gives out = 0, lse = -inf.  Cells a token does not see do
- * not enter its result, whatever they hold.  A sequence longer than its table row gives out = NaN
- * and lse = NaN, and so does a token that sees a cell on a page outside the pool (the sequence's
+ * not enter its result, whatever they hold.  A sequence longer than its table row (or than 2^31 - 256
+ * cells) gives out = NaN and lse = NaN, and so does a token that sees a cell on a page outside the pool (the sequence's
  * other tokens may then be NaN too).
  *
  *   q        [n_tok][H_q][d] of type q_dtype (QSA_F32 or QSA_BF16), ld_q elements between tokens

@@ -63,6 +63,34 @@ def test_rows_of_two_tiles(news, H_q, kv_dtype):
 
 
 @pytest.mark.parametrize("kv_dtype", [BF16, E4M3])
+def test_more_tokens_than_the_host_said(kv_dtype):
+    """max_q chooses the kernel only: chunks and prompts by the kernel of few rows."""
+    run_paged(widen(Pool([400, 90, 61], 2, 128, 64, kv_dtype, seed=29)), [150, 90, 1], 16, BF16, seed=30, max_q=1)
+
+
+@pytest.mark.parametrize("kv_dtype", [BF16, E4M3])
+def test_few_rows_counts_beyond_the_buffers(kv_dtype):
+    """cu_q that runs past the buffers, or back, and lengths below zero, are clipped; nothing behind the
+    buffers is touched."""
+    pool = widen(Pool([300, 200, 100], 2, 128, 64, kv_dtype, seed=31))
+    q = torch.randn(12, 16, 128, device=DEV).to(BF16)
+    big = torch.full((30, 16, 128), -7.0, dtype=BF16, device=DEV)
+    lse = torch.full((30, 16), -7.0, device=DEV)
+    ws = torch.zeros(qsa.paged_attn_workspace_size(12, 3, 4, 16, 2, 128), dtype=torch.uint8, device=DEV)
+    for cu, lens in (([0, 4, 2, 90], [300, 200, 100]), ([-5, 4, 2 ** 31 - 1, 3], [300, 200, 100]),
+                     ([0, 4, 8, 12], [-1, 2 ** 31 - 1, 100]), ([0, 0, 0, 0], [300, 200, 100])):
+        qsa.paged_attn(pool.cache, pool.table, i32(cu), i32(lens), q, big[:12], 0.1, 4, lse=lse[:12], workspace=ws)
+        torch.cuda.synchronize()
+        assert (big[12:] == -7).all() and (lse[12:] == -7).all()
+    # a sequence of no cell gives zeros, one longer than its row of the table NaN
+    big.fill_(-7.0)
+    qsa.paged_attn(pool.cache, pool.table, i32([0, 4, 8, 12]), i32([-1, 2 ** 31 - 1, 100]), q, big[:12], 0.1, 4, lse=lse[:12],
+                   workspace=ws)
+    assert (big[:4] == 0).all() and torch.isneginf(lse[:4]).all()
+    assert torch.isnan(big[4:8].float()).all() and torch.isfinite(big[8:12].float()).all()
+
+
+@pytest.mark.parametrize("kv_dtype", [BF16, E4M3])
 @pytest.mark.parametrize("news", [[1, 1], [4, 2]])
 def test_few_rows_without_causal_mask(news, kv_dtype):
     run_paged(widen(Pool([333, 129], 2, 128, 32, kv_dtype, seed=3)), news, 16, BF16, seed=4, causal=False)
@@ -314,3 +342,58 @@ def test_few_rows_give_up_and_recover(news, kv_dtype):
     for _ in range(2):
         run()
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("kv_dtype", [BF16, E4M3])
+@pytest.mark.parametrize("news", [1, 4, 90])
+def test_short_limits_give_nan_or_the_result(news, kv_dtype):
+    """Limits that run out somewhere in the middle: every row is right or NaN, whoever gives up first, and
+    the next call is right."""
+    pool = widen(Pool([6000, 700, 100], 2, 128, 64, kv_dtype, seed=32))
+    n = 3 * news
+    q = torch.randn(n, 16, 128, device=DEV).to(BF16)
+    out, lse = torch.zeros_like(q), torch.zeros(n, 16, device=DEV)
+    ws = torch.zeros(qsa.paged_attn_workspace_size(n, 3, news, 16, 2, 128), dtype=torch.uint8, device=DEV)
+    cu = i32(starts([news] * 3))
+
+    def run():
+        qsa.paged_attn(pool.cache, pool.table, cu, pool.kv_len, q, out, 0.1, news, lse=lse, workspace=ws)
+        torch.cuda.synchronize()
+
+    run()
+    want = out.clone(), lse.clone()
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    try:
+        for limit in (1, 300, 1000, 2000, 4000, 8000, 30000):
+            qsa.set_wait_options(status, limit)
+            for _ in range(3):
+                status.zero_()
+                out.fill_(3.0)
+                run()
+                same = (out == want[0]).all(-1) & (lse == want[1])
+                lost = torch.isnan(out.float()).all(-1) & torch.isnan(lse)
+                assert (same | lost).all()
+                assert int(status.item()) == 4 or same.all()
+    finally:
+        qsa.set_wait_options(None, qsa.QSA_WAIT_DEFAULT_NS)
+    run()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("H_q,H,d,q_dtype", [(16, 2, 128, BF16), (16, 2, 128, F32), (6, 2, 72, BF16)])
+@pytest.mark.parametrize("news", [1, 60])
+def test_lengths_that_cannot_be(news, H_q, H, d, q_dtype):
+    """The largest length there is, a negative one and a right one, in every kernel: NaN, zeros, the result."""
+    pool = Pool([300, 200, 100], H, d, 64, BF16, seed=33)
+    n = 3 * news
+    q = torch.randn(n, H_q, d, device=DEV).to(q_dtype)
+    out, lse = torch.full_like(q, -7.0), torch.full((n, H_q), -7.0, device=DEV)
+    ws = torch.zeros(max(16, qsa.paged_attn_workspace_size(n, 3, news, H_q, H, d)), dtype=torch.uint8, device=DEV)
+    qsa.paged_attn(pool.cache, pool.table, i32(starts([news] * 3)), i32([2 ** 31 - 1, -2 ** 31, 100]), q, out, 0.1, news,
+                   lse=lse, workspace=ws)
+    torch.cuda.synchronize()
+    assert torch.isnan(out[:news].float()).all() and torch.isnan(lse[:news]).all()
+    assert (out[news:2 * news] == 0).all() and torch.isneginf(lse[news:2 * news]).all()
+    a = 2 * news
+    check_attention(out[a:].double().cpu().numpy(), lse[a:].double().cpu().numpy(), q[a:].double().cpu().numpy(), pool.k[2],
+                    pool.v[2], 100 - news, 0.1, True, q_dtype, BF16)
