@@ -83,7 +83,8 @@ struct Bars {
     uint32_t qmax[2][8];
     alignas(16) float nm[kGroups][32], mref[kGroups][32];  // -m, m of a group's rows
     float2 al[kGroups][32], fac[kGroups][32];  // factors 2^x as two, each in range
-    float red[kGroups][4][32], sum[kGroups][4][32];
+    alignas(16) float red[kGroups][4][32];
+    float sum[kGroups][4][32];
     float inv[32];
     int32_t see[32];                   // last cell of a row
     int64_t at[32];                    // place of a row's results, -1: none
@@ -142,10 +143,10 @@ __device__ __forceinline__ void tmem_ld_async(uint32_t taddr, float *v)
     else tmem_ld4_async(taddr, v);
 }
 
-// N values (16 or 32) of each lane reduced over the warp's lanes: lane i returns value i % N.  A step halves
+// N values (16 or 32) of each lane summed over the warp's lanes: lane i returns value i % N.  A step halves
 // the values that a lane holds.
-template <bool Max, int N>
-__device__ __forceinline__ float col_reduce(float (&v)[N])
+template <int N>
+__device__ __forceinline__ float col_sum(float (&v)[N])
 {
     const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -154,15 +155,18 @@ __device__ __forceinline__ float col_reduce(float (&v)[N])
 #pragma unroll
         for (int i = 0; i < h; ++i) {
             const float keep = up ? v[i + h] : v[i], send = up ? v[i] : v[i + h];
-            const float got = __shfl_xor_sync(0xffffffffu, send, h);
-            v[i] = Max ? fmaxf(keep, got) : keep + got;
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, h);
         }
     }
-    if constexpr (N == 16) {
-        const float got = __shfl_xor_sync(0xffffffffu, v[0], 16);
-        v[0] = Max ? fmaxf(v[0], got) : v[0] + got;
-    }
+    if constexpr (N == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
     return v[0];
+}
+// The largest over the warp's lanes, in every lane (a NaN counts for nothing).
+__device__ __forceinline__ float lane_max(float v)
+{
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 
 // Two fp16 numbers as their upper bytes, and what those leave.
@@ -586,17 +590,37 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
         const uint32_t colS = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)g * F::kStride;
         unsigned char *const prow = sP + (size_t)g * F::kPBytes + r * 128;
         uint32_t waits = 0;  // bit 0, 1: the phase of s_full, o_full
+        // e4m3: the exponents of this group's tile, and the page of its next one's cell.  They are on their
+        // way while the logits are (the copies' warp had them brought to L2); those of a part's first tile
+        // while the part before ends.
+        uint32_t ke1 = kExpBias, ve1 = kExpBias;
+        PageAhead ahead = {0, -1};
+        auto look = [&](const Parts &w, int k) {
+            const int at = w.tile0 + kGroups * k + g;
+            ahead.load(kv, w, at < w.tile1, (int64_t)at * kN + r);
+        };
+        auto fetch = [&](const Parts &w) {
+            const int row = ahead.row(kv, w);
+            ke1 = ve1 = kExpBias;
+            if (row >= 0) {
+                ke1 = kv.K_exp[(int64_t)row * kv.H_kv + w.it.g];
+                ve1 = kv.V_exp[(int64_t)row * kv.H_kv + w.it.g];
+            }
+        };
+        if constexpr (E8) look(p, 0);
         if (tid < NR * 8) {
             lay_queries<E8, NR, NR * 8, kBarFirst>(p, tid, true, q, ld_q, G, inv_g, q_sign, sQ, bars.qmax[0],
                                                    &bars.qs[0]);
             named_sync<NR * 8>(kBarFirst);
             if (tid == 0) mbar_arrive_n(&bars.q_full[0], kAuxWarps);
         }
+        if constexpr (E8) fetch(p);
         // the part is read where it lies: its fields would take the registers that the weights need
         int n = 0;
         do {
             const Parts &p = bars.part[n % kSlots];
             const int tiles = p.tile1 - p.tile0, mine = (tiles + kGroups - 1 - g) / kGroups;
+            bool told;
             float l[NR];
 #pragma unroll
             for (int c = 0; c < NR; ++c) l[c] = 0.0f;
@@ -606,26 +630,12 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
                 bars.mref[g][r] = -INFINITY;
                 bars.nm[g][r] = kUnset;
             }
-            named_sync<128>(kBarVote + g);
-            // e4m3: the page of this group's next cell
-            PageAhead ahead = {0, -1};
-            auto look = [&](int k) {
-                ahead.load(kv, p, k < mine, (int64_t)(p.tile0 + kGroups * k + g) * kN + r);
-            };
-            if constexpr (E8) look(0);
             const float *nm = bars.nm[g];
             for (int k = 0; ok && k < mine; ++k) {
                 const int t = p.tile0 + kGroups * k + g;
-                // e4m3: the exponents, on their way while the logits are (the copies' warp had them brought
-                // to L2)
-                uint32_t ke1 = kExpBias, ve1 = kExpBias;
                 if constexpr (E8) {
-                    const int row = ahead.row(kv, p);
-                    if (row >= 0) {
-                        ke1 = kv.K_exp[(int64_t)row * kv.H_kv + p.it.g];
-                        ve1 = kv.V_exp[(int64_t)row * kv.H_kv + p.it.g];
-                    }
-                    look(k + 1);
+                    if (k > 0) fetch(p);
+                    look(p, k + 1);
                 }
                 bool here = bar_wait_warp(&bars.s_full[g], waits & 1u, wc.limit_ns);
                 waits ^= 1u;
@@ -726,9 +736,11 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
                     if (k > 0) logits();
                     const int tid = thread_again(), lane = tid & 31, quarter = (tid >> 5) & 3;
                     const uint32_t colO = tmem + ((uint32_t)(quarter * 32) << 16) + kGroups * F::kStride;
-                    {
-                        const float cm = col_reduce<true>(v);
-                        if (lane < NR) bars.red[g][quarter][lane] = cm;
+#pragma unroll
+                    for (int c = 0; c < NR; c += 4) {
+                        const float4 m4 = make_float4(lane_max(v[c]), lane_max(v[c + 1]), lane_max(v[c + 2]),
+                                                      lane_max(v[c + 3]));
+                        if (lane == 0) *reinterpret_cast<float4 *>(&bars.red[g][quarter][c]) = m4;
                     }
                     named_sync<128>(kBarVote + g);
                     if (keeper) {
@@ -770,7 +782,6 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
                         }
                         tmem_wait_st();
                     }
-                    logits();
                     weights();
                 }
                 // ---- their sum, and their terms for the product
@@ -835,7 +846,7 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
                 for (int c = 0; c < NR; ++c) l[c] *= 1.0f / (1 << 30);
             }
             {
-                const float cm = col_reduce<false>(l);
+                const float cm = col_sum(l);
                 if (lane < NR) bars.sum[g][quarter][lane] = cm;
             }
             if (ok && mine > 0) {
@@ -843,7 +854,12 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
                 waits ^= 2u;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             }
-            if (named_or<32 * kSoftWarps>(kBarAll, !ok)) ok = false;
+            // the next part as the query warps found it (its own look-up is a chain of loads)
+            const int slot = (n + 1) % kSlots;
+            const bool here = bar_wait_warp(&bars.part_full[slot], (uint32_t)((n + 1) / kSlots) & 1u, wc.limit_ns);
+            told = !named_or<32 * kSoftWarps>(kBarAll, !ok || !here);
+            ok = ok && told;
+            if (E8 && told && bars.more[slot]) look(bars.part[slot], 0);
             const bool starts = p.tile0 == 0, ends = p.tile1 == p.it.tiles, whole = starts && ends;
             float *rec = partial + (2 * (int64_t)blockIdx.x + (starts ? 1 : 0)) * partial_floats(NR, kD);
             if (tid < NR) {
@@ -876,6 +892,7 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
                 }
             }
             named_sync<32 * kSoftWarps>(kBarAll);
+            if (E8 && told && bars.more[slot]) fetch(bars.part[slot]);
             // dim r of the rows c0 .. c0 + kRows - 1
             constexpr int kRows = NR / kGroups;
             const int c0 = (warp >> 2) * kRows;
@@ -923,12 +940,10 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
             if (starts && tid == 0)
                 note_split(splits, by_item, p.it, ends, div_pos(p.it.start + ws.over + p.it.tiles - 1, bars.per));
             }
-            // the next part as the query warps found it (its own look-up is a chain of loads).  Behind the
-            // barrier no group's output is read any more: its next weights let it be written.
+            // behind this barrier no group's output is read any more: its next weights let it be written
+            named_sync<32 * kSoftWarps>(kBarAll);
             const int slot = (n + 1) % kSlots;
-            const bool told = bar_wait_warp(&bars.part_full[slot], (uint32_t)((n + 1) / kSlots) & 1u, wc.limit_ns);
-            if (named_or<32 * kSoftWarps>(kBarAll, !told)) {
-                ok = false;
+            if (!told) {  // (some wait gave up: everyone finds the part by itself)
                 Parts next = p;
                 const bool more = next.next(kv, sv, ws);
                 if (tid == 0) bars.part[slot] = next;
