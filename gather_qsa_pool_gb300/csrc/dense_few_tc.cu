@@ -30,11 +30,11 @@
 // cell.  Per tile the tensor cores run O_g += V' P_g and S_g of the group's next tile, while the other
 // group computes.
 //
-// What bounds it: bf16, the bytes (64 sequences of up to 8,000 cells, 32 / 4 heads, one token: 101 us,
-// 5.4 TB/s; one of 255,181: 95 us).  e4m3, the weights' turn from logits to terms and back to the tensor
+// What bounds it: bf16, the bytes (64 sequences of up to 8,000 cells, 32 / 4 heads, one token: 99 us,
+// 5.4 TB/s; one of 255,181: 92 us).  e4m3, the weights' turn from logits to terms and back to the tensor
 // cores, about 1,500 cycles a tile with two groups in flight where the bytes take 1,000 (48 sequences of
-// up to 16,384 cells, 32 rows: 105 us; 16 rows: 90 us, 4.5 TB/s), and about 10,000 cycles at each end of a
-// part (references, sums and outputs joined, the next part's first loads).
+// up to 16,384 cells, 32 rows: 99 us; 16 rows: 86 us, 4.7 TB/s), and about 8,000 cycles at each end of a
+// part (references, sums and outputs joined, the first references).
 //
 // Every mbarrier wait is bounded: after one gives up, nothing new is issued, what was issued is waited
 // for, the rows not finished become NaN and the tensor memory is returned.
@@ -652,7 +652,7 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
                 }
                 // the logits in log2 units (e4m3: with the exponent of the cell's values)
                 float v[NR];
-                constexpr int kStep = 8;  // columns of a term loaded together
+                constexpr int kStep = 8;  // columns of a term loaded together (16: 104.5 us instead of 99.2, registers)
                 auto logits = [&]() {
                     const float2 k2 = make_float2(ks, ks), v2 = make_float2(vs, vs);
 #pragma unroll
@@ -1013,12 +1013,14 @@ bool dense_few_ok(const DenseArgs &a, int64_t max_q)
     // it: 64 sequences of up to 8,000 cells, 64 rows, 142 us here and 243 there; bf16, 32 rows, 103 and 124)
     if (max_q * G > 16) return true;
     // Up to 16 rows over short contexts are dense_decode.cu's: a part costs more here, a cell less.  By what
-    // the host knows, the most cells a sequence may have, measured there and here (us; one token, 32 / 4
-    // heads or 8 / 2): bf16, one sequence of 2,050 cells 11.9 and 14.2, of 8,000 18.9 and 17.3; e4m3, one
-    // of 8,000 15.9 and 18.7, of 30,000 25.4 and 22.7; 64 of up to 2,050 and 4 KV heads, bf16 48.4 and
-    // 44.9, e4m3 43.5 and 40.5, of up to 500 24.7 and 29.1.
+    // the host knows, the most cells a sequence may have; measured there and here (us, one token, replayed
+    // from a graph): bf16, one sequence of 4,000 cells and 2 KV heads 13.7 and 14.9, of 8,000 17.3 and 17.1,
+    // eight of up to 2,050 and 4 KV heads 18.0 and 15.9, 64 of up to 500 and 2 18.6 and 20.0, of up to
+    // 1,000 23.0 and 21.9; e4m3, one of 8,000 and 2 15.7 and 18.3, of 16,000 20.2 and 18.0, eight of up to
+    // 8,000 20.0 and 18.1, 64 of up to 500 and 4 24.5 and 27.0, of up to 1,000 and 2 23.1 and 22.4.
     const int64_t cells = a.kv.table ? a.kv.ld_table << a.kv.page_shift : a.sv.n_tok;
-    return cells >= (e8 ? 16384 : 4096) || (double)cells * (double)a.sv.n_seq * a.kv.H_kv >= (double)(1 << 18);
+    return cells >= (e8 ? 10240 : 6144) ||
+           (cells >= 1024 && (double)cells * (double)a.sv.n_seq * a.kv.H_kv >= (e8 ? 1e5 : 6e4));
 }
 
 size_t dense_few_workspace()
