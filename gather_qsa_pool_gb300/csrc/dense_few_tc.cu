@@ -92,6 +92,7 @@ struct Bars {
     int32_t more[kSlots];
     int64_t per;                       // places of a CTA
     Parts now[2];                      // the part that a query warp is at
+    Parts alone[2];                    // after a wait that gave up: the softmax warps' part, and the next
 };
 
 template <bool E8, int NR>
@@ -582,7 +583,8 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
                 if (aux == 0 && lane == 0) mbar_arrive(&bars.full[s]);
             }
             nv += (uint32_t)tiles;
-        } while (more);
+            // (one that gave up tells nothing more: it would overtake those who read)
+        } while (ok && more);
         __syncwarp();
     } else {
         // ---- weights: this thread's cell is number r of every tile of group g
@@ -617,8 +619,9 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
         if constexpr (E8) fetch(p);
         // the part is read where it lies: its fields would take the registers that the weights need
         int n = 0;
+        bool alone = false;  // some wait gave up: the parts are looked up here, into places of their own
         do {
-            const Parts &p = bars.part[n % kSlots];
+            const Parts &p = alone ? bars.alone[n & 1] : bars.part[n % kSlots];
             const int tiles = p.tile1 - p.tile0, mine = (tiles + kGroups - 1 - g) / kGroups;
             bool told;
             float l[NR];
@@ -856,7 +859,7 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
             }
             // the next part as the query warps found it (its own look-up is a chain of loads)
             const int slot = (n + 1) % kSlots;
-            const bool here = bar_wait_warp(&bars.part_full[slot], (uint32_t)((n + 1) / kSlots) & 1u, wc.limit_ns);
+            const bool here = !alone && bar_wait_warp(&bars.part_full[slot], (uint32_t)((n + 1) / kSlots) & 1u, wc.limit_ns);
             told = !named_or<32 * kSoftWarps>(kBarAll, !ok || !here);
             ok = ok && told;
             if (E8 && told && bars.more[slot]) look(bars.part[slot], 0);
@@ -943,11 +946,12 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
             // behind this barrier no group's output is read any more: its next weights let it be written
             named_sync<32 * kSoftWarps>(kBarAll);
             const int slot = (n + 1) % kSlots;
-            if (!told) {  // (some wait gave up: everyone finds the part by itself)
+            if (!told) {
                 Parts next = p;
                 const bool more = next.next(kv, sv, ws);
-                if (tid == 0) bars.part[slot] = next;
+                if (tid == 0) bars.alone[(n + 1) & 1] = next;
                 named_sync<32 * kSoftWarps>(kBarAll);
+                alone = true;
                 if (!more) break;
             } else if (!bars.more[slot]) {
                 break;

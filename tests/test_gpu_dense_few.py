@@ -345,16 +345,17 @@ def test_few_rows_give_up_and_recover(news, kv_dtype):
 
 
 @pytest.mark.parametrize("kv_dtype", [BF16, E4M3])
-@pytest.mark.parametrize("news", [1, 4, 90])
-def test_short_limits_give_nan_or_the_result(news, kv_dtype):
+@pytest.mark.parametrize("news,many", [(1, False), (4, False), (90, False), (1, True), (4, True)])
+def test_short_limits_give_nan_or_the_result(news, many, kv_dtype):
     """Limits that run out somewhere in the middle: every row is right or NaN, whoever gives up first, and
     the next call is right."""
-    pool = widen(Pool([6000, 700, 100], 2, 128, 64, kv_dtype, seed=32))
-    n = 3 * news
+    lens = [6000, 700, 100] + ([130, 300, 128] * 300 if many else [])  # many: a score of parts a CTA
+    pool = widen(Pool(lens, 2, 128, 64, kv_dtype, seed=32))
+    n = len(lens) * news
     q = torch.randn(n, 16, 128, device=DEV).to(BF16)
     out, lse = torch.zeros_like(q), torch.zeros(n, 16, device=DEV)
-    ws = torch.zeros(qsa.paged_attn_workspace_size(n, 3, news, 16, 2, 128), dtype=torch.uint8, device=DEV)
-    cu = i32(starts([news] * 3))
+    ws = torch.zeros(qsa.paged_attn_workspace_size(n, len(lens), news, 16, 2, 128), dtype=torch.uint8, device=DEV)
+    cu = i32(starts([news] * len(lens)))
 
     def run():
         qsa.paged_attn(pool.cache, pool.table, cu, pool.kv_len, q, out, 0.1, news, lse=lse, workspace=ws)
@@ -364,7 +365,7 @@ def test_short_limits_give_nan_or_the_result(news, kv_dtype):
     want = out.clone(), lse.clone()
     status = torch.zeros(1, dtype=torch.int32, device=DEV)
     try:
-        for limit in (1, 300, 1000, 2000, 4000, 8000, 30000):
+        for limit in (1, 300, 1000, 2000, 4000, 8000, 12000, 20000, 30000):
             qsa.set_wait_options(status, limit)
             for _ in range(3):
                 status.zero_()
