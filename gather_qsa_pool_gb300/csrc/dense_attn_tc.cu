@@ -34,7 +34,6 @@ namespace {
 constexpr int kM = 128;                  // rows of a group
 constexpr int kSoftWarps = 16, kMmaWarp = 16, kLoadWarp = 17, kAuxWarp = 18;
 constexpr int kOver = 4;                 // an item's fixed cost in tiles
-constexpr int kWholeTiles = 8;           // items of no more tiles are not cut where each has a CTA
 constexpr uint32_t kTmemCols = 512;
 
 __host__ __device__ constexpr uint32_t col_s(int g) { return g ? 128u : 0u; }
@@ -681,11 +680,17 @@ static qsa_status run_tc(const DenseArgs &a, void *workspace, cudaStream_t st)
     if (ctas > kMaxCtas) ctas = kMaxCtas;
     Split *splits = static_cast<Split *>(workspace);
     float *partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + kMaxCtas * sizeof(Split));
-    // few items of few tiles, as far as the host knows: a CTA each, and nothing to join (a prompt of
-    // 777 tokens, 8 / 2 heads: 21.6 us instead of 31.2)
+    // Items that each have a CTA and are not too long are not cut: a CTA each, and nothing to join.  Whole,
+    // a call takes about 13 us and 1.4 a tile of the longest item; cut, 32 and 2.4 a tile of a CTA's share,
+    // which is the items' tiles (of prompts half of the longest's, of chunks nearer to it) over the CTAs.
+    // Measured whole and cut: prompts of 777 tokens, 8 / 2 heads, 20.2 and 30.9, of 3,000 45.9 and 54.7, of
+    // 3,000 with 4 / 4 heads 47.5 and 40.1; chunks, 32 / 4 heads, of 400 tokens over 2,000 cells 34.8 and
+    // 44.2, of 64 over 3,000 46.6 and 32.3.
     const int64_t items = ((a.sv.n_tok + ws.rt - 1) / ws.rt + a.sv.n_seq) * a.kv.H_kv;
     const int64_t cells = a.kv.table ? a.kv.ld_table << a.kv.page_shift : a.sv.n_tok;
-    const bool whole = items <= ctas && cells <= kWholeTiles * kN;
+    const double tiles = (double)cells / kN, tokens = (double)a.sv.n_tok / ws.rt;
+    const double share = (a.kv.table ? 0.75 : 0.5) * (tokens > a.sv.n_seq ? tokens : a.sv.n_seq) * a.kv.H_kv / ctas;
+    const bool whole = items <= ctas && 13.0 + 1.4 * tiles < 32.0 + 2.4 * tiles * share;
     if (whole) ctas = (int)items;
     cudaError_t e = launch(dense_tc_kernel<E8>, dim3((unsigned)ctas), dim3(Cfg<E8>::kThreads), smem, st, 1, mq,
                            mk, mv, a.kv, a.sv, ws, box_rows, a.H_q, a.scale * kLog2e,

@@ -757,7 +757,7 @@ qsa_status qsa_paged_read(const qsa_paged_cache *cache, const int32_t *table, in
  *            the same time need one each
  * All sums, the softmax statistics and the output are held in fp32.  With d = 128 and a QSA_BF16
  * or QSA_E4M3 pool the products run on the tensor cores: QSA_BF16 queries with the softmax weights
- * rounded to 16 bits (bf16, or fp16 for a few tokens on a QSA_E4M3 pool), QSA_F32 queries (up to
+ * rounded to 8 significant bits (for a few tokens on a QSA_E4M3 pool 9 or 11), QSA_F32 queries (up to
  * 16 heads per KV head) with queries and weights as sums of three bf16 terms on a QSA_BF16 pool
  * (24 bits) and of two fp16 terms on a QSA_E4M3 pool (22 bits).  Other shapes, and QSA_BF16
  * chunks with scale <= 0, take fp32 arithmetic on the CUDA cores, which is right but slower.
