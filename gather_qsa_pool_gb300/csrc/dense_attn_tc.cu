@@ -680,17 +680,23 @@ static qsa_status run_tc(const DenseArgs &a, void *workspace, cudaStream_t st)
     if (ctas > kMaxCtas) ctas = kMaxCtas;
     Split *splits = static_cast<Split *>(workspace);
     float *partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + kMaxCtas * sizeof(Split));
-    // Items that each have a CTA and are not too long are not cut: a CTA each, and nothing to join.  Whole,
-    // a call takes about 13 us and 1.4 a tile of the longest item; cut, 32 and 2.4 a tile of a CTA's share,
-    // which is the items' tiles (of prompts half of the longest's, of chunks nearer to it) over the CTAs.
-    // Measured whole and cut: prompts of 777 tokens, 8 / 2 heads, 20.2 and 30.9, of 3,000 45.9 and 54.7, of
-    // 3,000 with 4 / 4 heads 47.5 and 40.1; chunks, 32 / 4 heads, of 400 tokens over 2,000 cells 34.8 and
-    // 44.2, of 64 over 3,000 46.6 and 32.3.
+    // Items that are not too long are not cut: a CTA an item (in turns, where there are more than run at
+    // once), and nothing to join.  Two models of both costs, in us, fitted to measurements: `tiles` of the
+    // longest item, `turns` items a CTA, `share` tiles a CTA (of prompts half of the longest's an item, of
+    // chunks nearer to it).  Lengths the host does not know: prompts count as half as long again as their
+    // mean.  Measured whole and cut: prompts of 777 tokens, 8 / 2 heads, 20.2 and 30.9, of 3,000 45.9 and
+    // 54.7, with 4 / 4 heads 47.5 and 40.1, three of 900, 32 / 4 heads, 51.6 and 64.5, one of 8,000, 8 / 2
+    // heads, 157 and 135; chunks, 32 / 4 heads, of 400 tokens over 2,000 cells 34.8 and 44.2, of 64 over
+    // 3,000 46.6 and 32.3, of 1,500 over 4,000 102 and 97.
     const int64_t items = ((a.sv.n_tok + ws.rt - 1) / ws.rt + a.sv.n_seq) * a.kv.H_kv;
-    const int64_t cells = a.kv.table ? a.kv.ld_table << a.kv.page_shift : a.sv.n_tok;
-    const double tiles = (double)cells / kN, tokens = (double)a.sv.n_tok / ws.rt;
-    const double share = (a.kv.table ? 0.75 : 0.5) * (tokens > a.sv.n_seq ? tokens : a.sv.n_seq) * a.kv.H_kv / ctas;
-    const bool whole = items <= ctas && 13.0 + 1.4 * tiles < 32.0 + 2.4 * tiles * share;
+    const double n_tok = (double)a.sv.n_tok, n_seq = (double)a.sv.n_seq;
+    const double cells = a.kv.table ? (double)(a.kv.ld_table << a.kv.page_shift)
+                                    : (n_seq > 1.0 ? fmin(n_tok, 1.5 * n_tok / n_seq) : n_tok);
+    const double tiles = cells / kN, turns = fmax(n_tok / ws.rt, n_seq) * a.kv.H_kv / ctas;
+    const double share = (a.kv.table ? 0.75 : 0.5) * tiles * turns;
+    const bool whole = items <= ctas ? 13.0 + 1.4 * tiles < 32.0 + 2.4 * share
+                                     : items <= 16 * (int64_t)ctas &&
+                                           13.0 + 1.2 * tiles + 1.4 * share + 7.0 * turns < 34.0 + 1.8 * share + 5.5 * turns;
     if (whole) ctas = (int)items;
     cudaError_t e = launch(dense_tc_kernel<E8>, dim3((unsigned)ctas), dim3(Cfg<E8>::kThreads), smem, st, 1, mq,
                            mk, mv, a.kv, a.sv, ws, box_rows, a.H_q, a.scale * kLog2e,
