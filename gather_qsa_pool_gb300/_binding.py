@@ -479,17 +479,28 @@ def _head_rows(name, t, H, d):
                      f"got {tuple(t.shape)} with strides {tuple(t.stride())} on {t.device}")
 
 
+def _pool_rows(name, t):
+    """[n_pages][page_size] rows as [n_pages * page_size] of the same memory: a copy would be a pool
+    of its own, which the caller's program neither fills nor reads."""
+    try:
+        return t.view(t.shape[0] * t.shape[1], *t.shape[2:])
+    except RuntimeError:
+        raise ValueError(f"{name}: rows at one stride through all pages are wanted (other pools cannot be "
+                         f"taken without a copy), got {tuple(t.shape)} with strides {tuple(t.stride())}") from None
+
+
 class PagedCache:
     """A qsa_paged_cache: a pool of pages in K and V, [n_pages * page_size][H_kv][d] (or with a
-    leading [n_pages][page_size]) of float32, bfloat16 or float8_e4m3fn; the last with its
-    exponent bytes K_exp, V_exp [n_pages * page_size][H_kv] uint8.  Holds the tensors."""
+    leading [n_pages][page_size] whose rows follow one another at one stride) of float32, bfloat16
+    or float8_e4m3fn; the last with its exponent bytes K_exp, V_exp [n_pages * page_size][H_kv]
+    uint8.  Holds the tensors, and never a copy of them."""
 
     def __init__(self, K, V, page_size, K_exp=None, V_exp=None):
         torch = _use_torch()
-        if K.dim() == 4:
-            K, V = K.flatten(0, 1), V.flatten(0, 1)
-            if K_exp is not None:
-                K_exp, V_exp = K_exp.flatten(0, 1), V_exp.flatten(0, 1)
+        if K.dim() == 4 and V.dim() == 4:
+            K, V = _pool_rows("K", K), _pool_rows("V", V)
+            if K_exp is not None and V_exp is not None:
+                K_exp, V_exp = _pool_rows("K_exp", K_exp), _pool_rows("V_exp", V_exp)
         _need(K.dim() == 3 and K.shape == V.shape and K.dtype == V.dtype and K.device == V.device,
               "K and V: two tensors of one type and shape [rows][H_kv][d]")
         types = {torch.float32: QSA_F32, torch.bfloat16: QSA_BF16, torch.float8_e4m3fn: QSA_E4M3}
