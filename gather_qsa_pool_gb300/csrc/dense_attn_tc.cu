@@ -505,6 +505,9 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
                             ok = false;
                             break;
                         }
+                        // the weights stored so far land before those that replace them: two stores
+                        // of a thread to one place are ordered by a wait alone
+                        tmem_wait_st();
                         const bool move = mt > m + kMove;  // also the first finite maximum
                         const float alpha = move ? ex2_approx(m - mt) : 1.0f;
                         if (move) {
