@@ -686,20 +686,41 @@ static qsa_status run_tc(const DenseArgs &a, void *workspace, cudaStream_t st)
     // Items that are not too long are not cut: a CTA an item (in turns, where there are more than run at
     // once), and nothing to join.  Two models of both costs, in us, fitted to measurements: `tiles` of the
     // longest item, `turns` items a CTA, `share` tiles a CTA (of prompts half of the longest's an item, of
-    // chunks nearer to it).  Lengths the host does not know: prompts count as half as long again as their
-    // mean.  Measured whole and cut: prompts of 777 tokens, 8 / 2 heads, 20.2 and 30.9, of 3,000 45.9 and
-    // 54.7, with 4 / 4 heads 47.5 and 40.1, three of 900, 32 / 4 heads, 51.6 and 64.5, one of 8,000, 8 / 2
-    // heads, 157 and 135; chunks, 32 / 4 heads, of 400 tokens over 2,000 cells 34.8 and 44.2, of 64 over
-    // 3,000 46.6 and 32.3, of 1,500 over 4,000 102 and 97.
+    // chunks nearer to it).  Measured whole and cut: prompts of 777 tokens, 8 / 2 heads, 20.2 and 30.9, of
+    // 3,000 45.9 and 54.7, with 4 / 4 heads 47.5 and 40.1, three of 900, 32 / 4 heads, 51.6 and 64.5, one of
+    // 8,000, 8 / 2 heads, 157 and 135; chunks, 32 / 4 heads, of 400 tokens over 2,000 cells 34.8 and 44.2, of
+    // 64 over 3,000 46.6 and 32.3, of 1,500 over 4,000 102 and 97.
+    // Of several sequences the host does not know the lengths, so both ends of what they may be are looked
+    // at: much alike (chunks as long as the table allows, prompts half as long again as their mean), and
+    // all but one short.  Whole must be faster in the first, and what it may lose in the second no more than
+    // what cutting loses in the first (8 us of it lie within the models' errors).  Measured whole and cut (with
+    // nothing in L2, which costs some 10 us), 32 / 4 heads, four chunks of 256 tokens over 60,000 cells each 712 and 730, over 60,000, 500, 500 and 500 704
+    // and 218; over 2,000 each 48 and 81, over 2,000 and three times 300 46 and 63; sixteen of 512 over 4,000
+    // each 400 and 407, over 4,000 and fifteen times 600 145 and 153; a prompt of 8,000 tokens beside fifteen
+    // of one, 8 / 2 heads, 168 and 144; one of 2,500 beside one of 700, 16 / 2 heads, 64 and 78.
     const int64_t items = ((a.sv.n_tok + ws.rt - 1) / ws.rt + a.sv.n_seq) * a.kv.H_kv;
     const double n_tok = (double)a.sv.n_tok, n_seq = (double)a.sv.n_seq;
-    const double cells = a.kv.table ? (double)(a.kv.ld_table << a.kv.page_shift)
-                                    : (n_seq > 1.0 ? fmin(n_tok, 1.5 * n_tok / n_seq) : n_tok);
-    const double tiles = cells / kN, turns = fmax(n_tok / ws.rt, n_seq) * a.kv.H_kv / ctas;
-    const double share = (a.kv.table ? 0.75 : 0.5) * tiles * turns;
-    const bool whole = items <= ctas ? 13.0 + 1.4 * tiles < 32.0 + 2.4 * share
-                                     : items <= 16 * (int64_t)ctas &&
-                                           13.0 + 1.2 * tiles + 1.4 * share + 7.0 * turns < 34.0 + 1.8 * share + 5.5 * turns;
+    const double turns = fmax(n_tok / ws.rt, n_seq) * a.kv.H_kv / ctas;
+    struct Cost {
+        double whole, cut;
+    };
+    const auto cost = [&](double tiles, double share) -> Cost {
+        if (items <= ctas) return {13.0 + 1.4 * tiles, 32.0 + 2.4 * share};
+        return {13.0 + 1.2 * tiles + 1.4 * share + 7.0 * turns, 34.0 + 1.8 * share + 5.5 * turns};
+    };
+    Cost alike, one_long;
+    if (a.kv.table) {
+        const double tiles = (double)(a.kv.ld_table << a.kv.page_shift) / kN;
+        alike = cost(tiles, 0.75 * tiles * turns);
+        one_long = a.sv.n_seq > 1 ? cost(tiles, 0.75 * tiles * turns / n_seq + turns) : alike;
+    } else {
+        const double tiles = (a.sv.n_seq > 1 ? fmin(n_tok, 1.5 * n_tok / n_seq) : n_tok) / kN;
+        const double most = fmax(n_tok - n_seq + 1.0, 1.0) / kN;
+        alike = cost(tiles, 0.5 * tiles * turns);
+        one_long = cost(most, 0.5 * most * turns);
+    }
+    const bool whole = items <= 16 * (int64_t)ctas && alike.whole < alike.cut &&
+                       (a.sv.n_seq == 1 || one_long.whole - one_long.cut < alike.cut - alike.whole + 8.0);
     if (whole) ctas = (int)items;
     cudaError_t e = launch(dense_tc_kernel<E8>, dim3((unsigned)ctas), dim3(Cfg<E8>::kThreads), smem, st, 1, mq,
                            mk, mv, a.kv, a.sv, ws, box_rows, a.H_q, a.scale * kLog2e,
