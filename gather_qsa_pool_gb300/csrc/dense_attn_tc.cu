@@ -692,12 +692,14 @@ static qsa_status run_tc(const DenseArgs &a, void *workspace, cudaStream_t st)
     // 64 over 3,000 46.6 and 32.3, of 1,500 over 4,000 102 and 97.
     // Of several sequences the host does not know the lengths, so both ends of what they may be are looked
     // at: much alike (chunks as long as the table allows, prompts half as long again as their mean), and
-    // all but one short.  Whole must be faster in the first, and what it may lose in the second no more than
-    // what cutting loses in the first (8 us of it lie within the models' errors).  Measured whole and cut (with
-    // nothing in L2, which costs some 10 us), 32 / 4 heads, four chunks of 256 tokens over 60,000 cells each 712 and 730, over 60,000, 500, 500 and 500 704
-    // and 218; over 2,000 each 48 and 81, over 2,000 and three times 300 46 and 63; sixteen of 512 over 4,000
-    // each 400 and 407, over 4,000 and fifteen times 600 145 and 153; a prompt of 8,000 tokens beside fifteen
-    // of one, 8 / 2 heads, 168 and 144; one of 2,500 beside one of 700, 16 / 2 heads, 64 and 78.
+    // all but one short.  Whole must be faster in the first, and what it may lose in the second no more
+    // than what cutting loses in the first (8 us of it lie within the models' errors).  Measured whole and
+    // cut (with nothing in L2, which costs some 10 us), 32 / 4 heads: four chunks of 256 tokens over 60,000
+    // cells each 712 and 730, over 60,000, 500, 500 and 500 704 and 218; over 8,000 each 117 and 145, over
+    // 8,000 and three times 500 115 and 81; over 2,000 each 48 and 81, over 2,000 and three times 300 46 and
+    // 63; sixteen of 512 over 4,000 each 400 and 407, over 4,000 and fifteen times 600 145 and 153; 8 / 2
+    // heads, a prompt of 8,000 tokens beside fifteen of one 168 and 144; 16 / 2, one of 2,500 beside one of
+    // 700 64 and 78.
     const int64_t items = ((a.sv.n_tok + ws.rt - 1) / ws.rt + a.sv.n_seq) * a.kv.H_kv;
     const double n_tok = (double)a.sv.n_tok, n_seq = (double)a.sv.n_seq;
     const double turns = fmax(n_tok / ws.rt, n_seq) * a.kv.H_kv / ctas;
