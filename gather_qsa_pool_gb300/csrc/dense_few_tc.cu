@@ -18,8 +18,10 @@
 // weight, is three e5m2 terms that lie beside each other as columns: e5m2 is the upper byte of fp16, so
 // the terms of an fp16 number are its upper byte, the upper byte of what that leaves, and of what that
 // leaves: 3 + 3 + 3 significant bits.  A bf16 query (8 bits) is exact in them down to 2^-31 of the
-// item's largest; weights are rounded to 9 bits, and end at 2^-26 of the largest.  The sum l adds
-// 2^(x - ve), from the weight where |ve| is at most 50.
+// item's largest.  Weights are rounded to 9 bits; what a weight's terms leave for the next is taken 8 times
+// as large (and their products that much smaller), so that small weights are not cut off where e5m2 ends
+// (2^-16) while the sum counts them: a weight is off by 2^-9 of itself or by 3 * 2^-23, where the largest
+// is at least 2^10.  The sum l adds 2^(x - ve), from the weight where |ve| is at most 50.
 //
 // Shape: one persistent CTA per SM, an equal share of the flattened list of (sequence, KV head, row
 // tile) items in tiles of 128 cells (dense.cuh).  Warps 0-7: two groups that take the weights of the
@@ -175,6 +177,13 @@ __device__ __forceinline__ uint32_t less_upper(uint32_t h)
 {
     const uint32_t u = h & 0xff00ff00u;
     const __half2 r = __hsub2(reinterpret_cast<const __half2 &>(h), reinterpret_cast<const __half2 &>(u));
+    return reinterpret_cast<const uint32_t &>(r);
+}
+// The same, what is left 8 times as large (exact; of numbers of at most 2^15 it stays below 2^15).
+__device__ __forceinline__ uint32_t less_upper_grown(uint32_t h)
+{
+    const uint32_t u = less_upper(h);
+    const __half2 r = __hmul2(reinterpret_cast<const __half2 &>(u), __floats2half2_rn(8.0f, 8.0f));
     return reinterpret_cast<const uint32_t &>(r);
 }
 
@@ -817,7 +826,7 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
                         }
                         if (i < 2) {
 #pragma unroll
-                            for (int c = 0; c < NR / 2; ++c) h[c] = less_upper(h[c]);
+                            for (int c = 0; c < NR / 2; ++c) h[c] = less_upper_grown(h[c]);
                         }
                     }
                     if (far) {
@@ -916,7 +925,7 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
                     for (int c = 0; c < kRows; ++c) {
                         const float2 f = bars.fac[i][c0 + c];
                         float y = x[c];
-                        if constexpr (E8) y += x[kRows + c] + x[2 * kRows + c];
+                        if constexpr (E8) y = fmaf(fmaf(x[2 * kRows + c], 0.125f, x[kRows + c]), 0.125f, y);
                         o[c] += y * f.x * f.y;
                     }
                 }
