@@ -10,7 +10,9 @@
 // lanes, one vote only.  On e4m3 cells v_j = c_j 2^e_j; the weight that multiplies the code is
 // 2^(s_j + e_j - mx) with a reference of its own, so that the fp16 weights keep their bits on
 // the cells that matter for o whatever the rows' exponents are; the sum l then adds 2^-e_j times it (and,
-// where exponents lie more than 2^50 from one, exponentials of the logits alone).
+// where exponents lie more than 2^50 from one, exponentials of the logits alone).  fp16 weights end at
+// 2^-25, so mx lies 13 below the maximum where it is set, and moves when a logit passes that by more than 2:
+// the largest weight is 2^13 to 2^15, and a weight that the product loses is 2^-38 of it or less.
 //
 // Shape: a CTA of four warps takes a share of the flattened list of (sequence, KV head, row
 // tile) items (dense.cuh), equal for every CTA, whatever the lengths: ragged batches stay
@@ -40,7 +42,11 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kD = 128;
 constexpr uint32_t kTile = 4096;                 // bytes of K (and of V) of a warp's stage
-constexpr float kMove = 8.0f;                    // move the reference past 2^8 growth
+// A reference lies kBelow under the maximum where it is set, and moves once a logit is kMove above it.
+template <bool E8>
+constexpr float kBelow = E8 ? 13.0f : 0.0f;
+template <bool E8>
+constexpr float kMove = E8 ? 15.0f : 8.0f;
 // Exponents of e4m3 rows within 2^+-50 of one: their sums are taken from the weights (2^(x - mx)
 // times 2^-e stays far from fp32's ends); beyond it they get exponentials of their own.
 constexpr float kFar = 50.0f;
@@ -484,7 +490,7 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
                     // (-inf before the first cell: any finite logit moves it)
-                    const float over = E8 ? mx[hf] + kMove : (mx[hf] + kMove) * inv_scale;
+                    const float over = E8 ? mx[hf] + kMove<E8> : (mx[hf] + kMove<E8>) * inv_scale;
 #pragma unroll
                     for (int n = 0; n < S::kGroups * 2; ++n)
                         move |= fmaxf(s[n][2 * hf], s[n][2 * hf + 1]) > over;
@@ -506,7 +512,7 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 const float v = s[n][2 * hf + e];
-                                b = fmaxf(b, E8 ? v : v * scale_log2);
+                                b = fmaxf(b, E8 ? v - kBelow<E8> : v * scale_log2);
                                 if constexpr (E8) {
                                     if (wide) a = fmaxf(a, v - ex[8 * n + 2 * c4 + e].y);
                                 }

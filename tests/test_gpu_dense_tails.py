@@ -5,15 +5,17 @@ others add, 2^-20 and less of the largest weight each.
 Tolerances, with A = sum_j softmax_j |v_j| and ds as in test_gpu_dense; a weight (times its cell's unit u_j)
 is off by
   9 bits (bf16 queries, few rows, long contexts)   2^-9 of itself, or 3 * 2^-23 where the largest is >= 2^10
+  fp16 (bf16 queries, short contexts)              2^-11 of itself, or 2^-25 where the largest is >= 2^13
+  two fp16 terms (fp32 queries)                    2^-22 of itself, or 2^-25 where the largest is >= 2^13
 so the output by A * (2 ds + (n + 64) * 2^-24 + rel) + small * max_j(softmax_j u_j) * sum_j |v_j| / u_j, with
-small = 3 * 2^-33; and a bf16 output by half its step, 2^-8 |out|."""
+small = 3 * 2^-33, 2^-38, 2^-38; and a bf16 output by half its step, 2^-8 |out|."""
 import numpy as np
 import pytest
 import torch
 
 import dense_reference as ref
 import gather_qsa_pool_gb300 as qsa
-from test_gpu_dense import BF16, DEV, E4M3, i32, small_weights
+from test_gpu_dense import BF16, DEV, E4M3, F32, i32, small_weights
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +68,14 @@ def _check(n, width, q_dtype, rel, small, unit):
 @pytest.mark.parametrize("n", [300, 12000])
 def test_few_rows_on_the_tensor_cores(n, unit):
     _check(n, 16384, BF16, 2.0 ** -9, 3 * 2.0 ** -33, unit)
+
+
+@pytest.mark.parametrize("unit", [127, 117])
+def test_short_contexts(unit):
+    _check(2000, 2048, BF16, 2.0 ** -11, 2.0 ** -38, unit)
+
+
+@pytest.mark.parametrize("unit", [127, 117])
+@pytest.mark.parametrize("n", [300, 12000])
+def test_fp32_queries(n, unit):
+    _check(n, 16384, F32, 2.0 ** -22, 2.0 ** -38, unit)
