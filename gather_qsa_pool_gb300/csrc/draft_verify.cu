@@ -44,7 +44,11 @@ __device__ __forceinline__ void add_pair(float &s, float &c, float x)
     s = t;
 }
 
-// Weight of one index: max(p - q, 0) as a pair (d, e); a NaN or negative value counts as 0.
+// A probability of the draft's: what is negative or NaN counts as 0.  (The target's needs no such step: with
+// q >= 0 a p that is negative or NaN passes no comparison below.)
+__device__ __forceinline__ float draft_prob(float q) { return fmaxf(q, 0.0f); }
+
+// Weight of one index: max(p - q, 0) as a pair (d, e), q a draft_prob.
 __device__ __forceinline__ void weight_of(float p, float q, float &d, float &e)
 {
     d = __fsub_rn(p, q);
@@ -66,7 +70,7 @@ struct Row {
     __device__ __forceinline__ void weight(float pv, float qv, int64_t i, float &d, float &e) const
     {
         if (q) {
-            weight_of(pv, qv, d, e);
+            weight_of(pv, draft_prob(qv), d, e);
         } else {
             d = pv > 0.0f && i != skip ? pv : 0.0f;
             e = 0.0f;
@@ -101,6 +105,7 @@ __device__ __forceinline__ double slice_sum(const Row &row, int64_t c0, int64_t 
     auto take = [&](float2 p, float2 q, int64_t i) {
         float2 d = p, e = make_float2(0.0f, 0.0f);
         if (row.q) {
+            q = make_float2(draft_prob(q.x), draft_prob(q.y));
             d = sub2(p, q);
             const float2 b = sub2(d, p);
             e = sub2(sub2(p, sub2(d, b)), add2(q, b));
@@ -289,7 +294,7 @@ draft_verify_kernel(const float *__restrict__ target, int64_t ld_t, const float 
             bool refuse = j < n;  // a token outside the vocabulary is refused
             if (j < max_draft && t >= 0 && t < vocab) {
                 const float p = target[(s * (max_draft + 1) + j) * ld_t + t];
-                const float q = draft ? draft[(s * max_draft + j) * ld_d + t] : 1.0f;
+                const float q = draft ? draft_prob(draft[(s * max_draft + j) * ld_d + t]) : 1.0f;
                 refuse = j < n && !((double)uj * (double)q < (double)p);
             }
             const uint32_t b = __ballot_sync(0xffffffffu, refuse);
