@@ -430,40 +430,51 @@ def _dp(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream(stream, device):
+def _gpu(name, t):
+    """Index of the GPU that a call works on, by its first tensor; the others have to be there too, as the
+    kernels get bare addresses."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: a CUDA tensor is wanted, got {tuple(t.shape)} on {t.device}")
+    return dev
+
+
+def _raw_stream(stream, dev):
     """The stream's handle: `stream`, or the current stream of the current device, on which the
     tensors must be."""
-    if stream is not None:
-        return stream.cuda_stream
     here = _torch._C._cuda_getDevice()
-    if device.index != here:
-        raise ValueError(f"tensors on {device}, but the current device is cuda:{here}")
-    return _raw_stream_of(here)
+    if dev != here:
+        raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{here}")
+    if stream is None:
+        return _raw_stream_of(here)
+    if stream.device_index != here:
+        raise ValueError(f"tensors on cuda:{here}, but a stream of cuda:{stream.device_index}")
+    return stream.cuda_stream
 
 
-def _bad_i32(name, t, shape):
-    raise ValueError(f"{name}: a packed int32 CUDA tensor of shape {shape} or more is wanted, "
+def _bad_i32(name, t, shape, dev):
+    raise ValueError(f"{name}: a packed int32 tensor of shape {shape} or more on cuda:{dev} is wanted, "
                      f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _i32_vector(name, t, n):
+def _i32_vector(name, t, n, dev):
     """int32, on the GPU, contiguous, n entries or more; its address."""
-    if t.dtype is not _torch.int32 or not t.is_cuda or t.dim() != 1 or t.shape[0] < n or \
+    if t.dtype is not _torch.int32 or t.get_device() != dev or t.dim() != 1 or t.shape[0] < n or \
             not t.is_contiguous():
-        _bad_i32(name, t, (n,))
+        _bad_i32(name, t, (n,), dev)
     return t.data_ptr()
 
 
-def _i32_table(t, n_seq):
-    if t.dtype is not _torch.int32 or not t.is_cuda or t.dim() != 2 or t.shape[0] < n_seq or \
+def _i32_table(t, n_seq, dev):
+    if t.dtype is not _torch.int32 or t.get_device() != dev or t.dim() != 2 or t.shape[0] < n_seq or \
             not t.is_contiguous():
-        _bad_i32("table", t, (n_seq, "pages"))
+        _bad_i32("table", t, (n_seq, "pages"), dev)
     return t.data_ptr()
 
 
-def _head_rows(name, t, H, d):
+def _head_rows(name, t, H, d, dev):
     """[n][H][d] (or [n][H*d]) rows whose heads are contiguous; the stride between rows."""
-    if t.is_cuda:
+    if t.get_device() == dev:
         shape, stride = t.shape, t.stride()
         if len(shape) == 3 and shape[1] == H and shape[2] == d:
             if shape[0] == 0:
@@ -475,7 +486,7 @@ def _head_rows(name, t, H, d):
                 return H * d
             if stride[1] == 1:
                 return stride[0] if shape[0] > 1 else H * d
-    raise ValueError(f"{name}: a CUDA tensor of shape [n][{H}][{d}] with contiguous rows is wanted, "
+    raise ValueError(f"{name}: a tensor of shape [n][{H}][{d}] with contiguous rows on cuda:{dev} is wanted, "
                      f"got {tuple(t.shape)} with strides {tuple(t.stride())} on {t.device}")
 
 
@@ -508,14 +519,16 @@ class PagedCache:
             raise TypeError(f"a paged cache is float32, bfloat16 or float8_e4m3fn, got {K.dtype}")
         rows, self.H_kv, self.d = K.shape
         _need(page_size > 0 and rows % page_size == 0, "K and V: a whole number of pages")
-        ld_k = _head_rows("K", K, self.H_kv, self.d)
-        ld_v = _head_rows("V", V, self.H_kv, self.d)
+        dev = _gpu("K", K)
+        ld_k = _head_rows("K", K, self.H_kv, self.d, dev)
+        ld_v = _head_rows("V", V, self.H_kv, self.d, dev)
         if K.dtype == torch.float8_e4m3fn:
             for e in (K_exp, V_exp):
                 _need(e is not None and e.dtype == torch.uint8 and e.is_contiguous()
                       and e.device == K.device and tuple(e.shape) == (rows, self.H_kv),
                       "K_exp and V_exp: contiguous uint8 [rows][H_kv] beside an 8-bit cache")
         self.K, self.V, self.K_exp, self.V_exp = K, V, K_exp, V_exp
+        self._dev = dev
         self.page_size, self.n_pages = page_size, rows // page_size
         self._struct = _PagedCacheStruct(_dp(K), _dp(V), _dp(K_exp), _dp(V_exp), types[K.dtype],
                                          self.H_kv, self.d, ld_k, ld_v, self.n_pages, page_size)
@@ -525,18 +538,18 @@ class PagedCache:
 def paged_write(cache, table, cu_q, kv_len, k, v, stream=None):
     """qsa_paged_write: rows k, v [n_tok][H_kv][d] (float32 or bfloat16) of the new tokens into
     the pages of their sequences (table [n_seq][>= pages], cu_q [n_seq + 1], kv_len [n_seq])."""
-    n_seq, n_tok = kv_len.shape[0], k.shape[0]
-    tb, cu, kl = (_i32_table(table, n_seq), _i32_vector("cu_q", cu_q, n_seq + 1),
-                  _i32_vector("kv_len", kv_len, 0))
-    ld_k = _head_rows("k", k, cache.H_kv, cache.d)
-    ld_v = _head_rows("v", v, cache.H_kv, cache.d)
+    n_seq, n_tok, dev = kv_len.shape[0], k.shape[0], cache._dev
+    tb, cu, kl = (_i32_table(table, n_seq, dev), _i32_vector("cu_q", cu_q, n_seq + 1, dev),
+                  _i32_vector("kv_len", kv_len, 0, dev))
+    ld_k = _head_rows("k", k, cache.H_kv, cache.d, dev)
+    ld_v = _head_rows("v", v, cache.H_kv, cache.d, dev)
     if v.shape[0] != n_tok or v.dtype is not k.dtype:
         raise ValueError("k and v: one type and length")
     if n_tok == 0:
         return  # an empty tensor has no address
     st = load().qsa_paged_write(
         cache._ref, tb, table.shape[1], n_seq, cu, kl, k.data_ptr(), v.data_ptr(), _dtype(k), n_tok,
-        ld_k, ld_v, _raw_stream(stream, k.device))
+        ld_k, ld_v, _raw_stream(stream, dev))
     if st:
         raise QSAError("qsa_paged_write", st)
 
@@ -545,36 +558,42 @@ def paged_read(cache, table, kv_len, n_cells, max_cells, K_out, V_out, pos=None,
                stream=None):
     """qsa_paged_read: the listed cells (pos [n_list][max_cells], or the first n_cells[i] of each
     sequence) as values, K_out / V_out [n_list][max_cells][H_kv][d] float32 or bfloat16."""
-    n_seq, n_list = kv_len.shape[0], n_cells.shape[0]
-    tb, kl, nc = (_i32_table(table, n_seq), _i32_vector("kv_len", kv_len, 0),
-                  _i32_vector("n_cells", n_cells, 0))
-    if pos is not None and (pos.dtype is not _torch.int32 or not pos.is_cuda or
+    n_seq, n_list, dev = kv_len.shape[0], n_cells.shape[0], cache._dev
+    tb, kl, nc = (_i32_table(table, n_seq, dev), _i32_vector("kv_len", kv_len, 0, dev),
+                  _i32_vector("n_cells", n_cells, 0, dev))
+    if pos is not None and (pos.dtype is not _torch.int32 or pos.get_device() != dev or
                             tuple(pos.shape) != (n_list, max_cells) or not pos.is_contiguous()):
-        _bad_i32("pos", pos, (n_list, max_cells))
+        _bad_i32("pos", pos, (n_list, max_cells), dev)
     if seq is not None:
-        _i32_vector("seq", seq, n_list)
+        _i32_vector("seq", seq, n_list, dev)
     elif n_list > n_seq:
         raise ValueError("n_cells: one list per sequence unless seq is given")
     size = n_list * max_cells * cache.H_kv * cache.d
     for t in (K_out, V_out):
-        if not t.is_cuda or not t.is_contiguous() or t.numel() < size or t.dtype is not K_out.dtype:
-            raise ValueError("K_out and V_out: packed [n_list][max_cells][H_kv][d] of one type")
+        if t.get_device() != dev or not t.is_contiguous() or t.numel() < size or t.dtype is not K_out.dtype:
+            raise ValueError(f"K_out and V_out: packed [n_list][max_cells][H_kv][d] of one type on cuda:{dev}")
     if size == 0:
         return
     st = load().qsa_paged_read(
         cache._ref, tb, table.shape[1], n_seq, kl, _dp(seq), _dp(pos), nc, n_list, max_cells,
-        K_out.data_ptr(), V_out.data_ptr(), _dtype(K_out), _raw_stream(stream, K_out.device))
+        K_out.data_ptr(), V_out.data_ptr(), _dtype(K_out), _raw_stream(stream, dev))
     if st:
         raise QSAError("qsa_paged_read", st)
 
 
-def _attn_outputs(q, out, lse, n_tok, H_q, d):
-    if out.dtype is not q.dtype or not out.is_cuda or not out.is_contiguous() or \
+def _attn_outputs(q, out, lse, workspace, n_tok, H_q, d, dev):
+    """Checks what a call writes; the workspace's address and bytes."""
+    if out.dtype is not q.dtype or out.get_device() != dev or not out.is_contiguous() or \
             out.numel() != n_tok * H_q * d:
-        raise ValueError("out: packed, of q's type and shape")
-    if lse is not None and (lse.dtype is not _torch.float32 or not lse.is_cuda or
+        raise ValueError(f"out: packed, of q's type and shape, on cuda:{dev}")
+    if lse is not None and (lse.dtype is not _torch.float32 or lse.get_device() != dev or
                             not lse.is_contiguous() or lse.numel() != n_tok * H_q):
-        raise ValueError("lse: packed float32 [n_tok][H_q]")
+        raise ValueError(f"lse: packed float32 [n_tok][H_q] on cuda:{dev}")
+    if workspace is None:
+        return None, 0
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: packed, on cuda:{dev}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def paged_attn_workspace_size(n_tok, n_seq, max_q, H_q, H_kv, d) -> int:
@@ -586,19 +605,18 @@ def paged_attn(cache, table, cu_q, kv_len, q, out, scale, max_q, causal=True, ls
     """qsa_paged_attn: q [n_tok][H_q][d] (float32 or bfloat16) of the new tokens over the cells
     of their sequences; out like q, lse [n_tok][H_q] float32.  workspace:
     paged_attn_workspace_size() bytes of device memory."""
-    n_seq, n_tok, d = kv_len.shape[0], q.shape[0], cache.d
+    n_seq, n_tok, d, dev = kv_len.shape[0], q.shape[0], cache.d, cache._dev
     H_q = q.shape[1] if q.dim() == 3 else q.shape[-1] // d
-    tb, cu, kl = (_i32_table(table, n_seq), _i32_vector("cu_q", cu_q, n_seq + 1),
-                  _i32_vector("kv_len", kv_len, 0))
-    ld_q = _head_rows("q", q, H_q, d)
-    _attn_outputs(q, out, lse, n_tok, H_q, d)
+    tb, cu, kl = (_i32_table(table, n_seq, dev), _i32_vector("cu_q", cu_q, n_seq + 1, dev),
+                  _i32_vector("kv_len", kv_len, 0, dev))
+    ld_q = _head_rows("q", q, H_q, d, dev)
+    ws, ws_bytes = _attn_outputs(q, out, lse, workspace, n_tok, H_q, d, dev)
     if n_tok == 0:
         return
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = load().qsa_paged_attn(
         cache._ref, tb, table.shape[1], n_seq, cu, kl, q.data_ptr(), _dtype(q), n_tok, max_q, ld_q,
-        H_q, scale, 1 if causal else 0, out.data_ptr(), _dp(lse), _dp(workspace), ws_bytes,
-        _raw_stream(stream, q.device))
+        H_q, scale, 1 if causal else 0, out.data_ptr(), _dp(lse), ws, ws_bytes,
+        _raw_stream(stream, dev))
     if st:
         raise QSAError("qsa_paged_attn", st)
 
@@ -617,39 +635,39 @@ def prompt_attn(q, k, v, cu_seq, out, scale, causal=True, lse=None, workspace=No
         raise ValueError("q, k, v: [n_tok][heads][d]")
     n_tok, H_q, d = q.shape
     H_kv = k.shape[1]
-    cu = _i32_vector("cu_seq", cu_seq, 1)
-    ld_q, ld_k, ld_v = (_head_rows("q", q, H_q, d), _head_rows("k", k, H_kv, d),
-                        _head_rows("v", v, H_kv, d))
+    dev = _gpu("q", q)
+    cu = _i32_vector("cu_seq", cu_seq, 1, dev)
+    ld_q, ld_k, ld_v = (_head_rows("q", q, H_q, d, dev), _head_rows("k", k, H_kv, d, dev),
+                        _head_rows("v", v, H_kv, d, dev))
     if k.shape[0] != n_tok or v.shape[0] != n_tok or k.dtype is not q.dtype or v.dtype is not q.dtype:
         raise ValueError("q, k, v: one type and length")
-    _attn_outputs(q, out, lse, n_tok, H_q, d)
+    ws, ws_bytes = _attn_outputs(q, out, lse, workspace, n_tok, H_q, d, dev)
     if n_tok == 0:
         return
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = load().qsa_prompt_attn(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype(q), n_tok, ld_q, ld_k, ld_v, cu,
         cu_seq.shape[0] - 1, H_q, H_kv, d, scale, 1 if causal else 0, out.data_ptr(), _dp(lse),
-        _dp(workspace), ws_bytes, _raw_stream(stream, q.device))
+        ws, ws_bytes, _raw_stream(stream, dev))
     if st:
         raise QSAError("qsa_prompt_attn", st)
 
 
-def _prob_rows(name, t, n_seq, n, vocab):
+def _prob_rows(name, t, n_seq, n, vocab, dev):
     """float32 [n_seq][n][vocab] with every row at one stride from the one before; the stride."""
-    if t.dtype is _torch.float32 and t.is_cuda and tuple(t.shape) == (n_seq, n, vocab):
+    if t.dtype is _torch.float32 and t.get_device() == dev and tuple(t.shape) == (n_seq, n, vocab):
         if n == 0 or n_seq == 0:
             return vocab
         s = t.stride()
         ld = s[1] if n > 1 else (s[0] if n_seq > 1 else vocab)
         if (s[2] == 1 or vocab == 1) and (n_seq == 1 or s[0] == n * ld):
             return ld
-    raise ValueError(f"{name}: float32 [{n_seq}][{n}][{vocab}] on the GPU with contiguous rows at one "
-                     f"stride is wanted, got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+    raise ValueError(f"{name}: float32 [{n_seq}][{n}][{vocab}] on cuda:{dev} with contiguous rows at one stride "
+                     f"is wanted, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
-def _packed(name, t, dtype, shape):
-    if t.dtype is not dtype or not t.is_cuda or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: packed {dtype} {shape} on the GPU")
+def _packed(name, t, dtype, shape, dev):
+    if t.dtype is not dtype or t.get_device() != dev or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: packed {dtype} {shape} on cuda:{dev}")
     return t.data_ptr()
 
 
@@ -664,17 +682,18 @@ def draft_verify(target, draft, tokens, u, tokens_out, n_accepted, n_draft=None,
     n_seq, n_rows, vocab = target.shape
     max_draft = n_rows - 1
     i32, f32 = _torch.int32, _torch.float32
-    ld_t = _prob_rows("target", target, n_seq, n_rows, vocab)
-    ld_d = 0 if draft is None else _prob_rows("draft", draft, n_seq, max_draft, vocab)
-    tk, to, na, uu = (_packed("tokens", tokens, i32, (n_seq, max_draft)),
-                      _packed("tokens_out", tokens_out, i32, (n_seq, n_rows)),
-                      _packed("n_accepted", n_accepted, i32, (n_seq,)),
-                      _packed("u", u, f32, (n_seq, n_rows)))
-    nd = None if n_draft is None else _i32_vector("n_draft", n_draft, n_seq)
+    dev = _gpu("target", target)
+    ld_t = _prob_rows("target", target, n_seq, n_rows, vocab, dev)
+    ld_d = 0 if draft is None else _prob_rows("draft", draft, n_seq, max_draft, vocab, dev)
+    tk, to, na, uu = (_packed("tokens", tokens, i32, (n_seq, max_draft), dev),
+                      _packed("tokens_out", tokens_out, i32, (n_seq, n_rows), dev),
+                      _packed("n_accepted", n_accepted, i32, (n_seq,), dev),
+                      _packed("u", u, f32, (n_seq, n_rows), dev))
+    nd = None if n_draft is None else _i32_vector("n_draft", n_draft, n_seq, dev)
     if n_seq == 0:
         return
     st = load().qsa_draft_verify(
         target.data_ptr(), ld_t, _dp(draft), ld_d, tk, nd, uu, n_seq, max_draft, vocab, to, na,
-        _raw_stream(stream, target.device))
+        _raw_stream(stream, dev))
     if st:
         raise QSAError("qsa_draft_verify", st)
