@@ -151,10 +151,38 @@ __device__ __forceinline__ int64_t floor_div(int64_t a, int64_t b)
     return a >= 0 ? div_pos(a, b) : -div_pos(-a + b - 1, b);
 }
 
-// Tiles of the row tiles before t (t <= the last row tile) of one KV head of a sequence.  A row
-// tile i < t sees c = cells - len + (i + 1) rt cells: one tile if that is none, else
-// floor((c - 1) / kt) + 1; the sum has a closed form when one of rt and kt divides the other
-// (1, 2, 4 ... heads per KV head) and is a loop otherwise.
+// Sum of floor((a i + b) / m) over 0 <= i < n (a, b >= 0, m > 0).  Whole multiples of m in a and b leave it
+// in closed form; the rest counts the lattice points under a line, which counted along the other axis is a
+// sum of the same kind with a and m exchanged: a few turns, as in Euclid's algorithm.
+__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b)
+{
+    int64_t sum = 0;
+    for (;;) {
+        if (a >= m) {
+            const int64_t q = div_pos(a, m);
+            sum += n * (n - 1) / 2 * q;
+            a -= q * m;
+        }
+        if (b >= m) {
+            const int64_t q = div_pos(b, m);
+            sum += n * q;
+            b -= q * m;
+        }
+        const int64_t y = a * n + b;
+        if (y < m) return sum;
+        n = div_pos(y, m);
+        b = y - n * m;
+        const int64_t t = a;
+        a = m;
+        m = t;
+    }
+}
+
+// Tiles of the row tiles before t (t <= the last row tile) of one KV head of a sequence.  A row tile
+// i < t sees c = cells - len + (i + 1) rt cells: one tile if that is none, else
+// floor((c - 1) / kt) + 1; the sum is shortest when one of rt and kt divides the other (1, 2, 4 ...
+// heads per KV head).  (Added up tile by tile for the others, a prompt of 65,536 tokens, 28 / 4 heads, took
+// 23.1 ms instead of 20.7.)
 __device__ __forceinline__ int64_t tiles_before(const WorkShape &w, int len, int cells, int t)
 {
     if (!w.causal || w.kt == 0 || cells > w.most) return (int64_t)t * item_tiles(w, len, cells, 0);
@@ -174,8 +202,7 @@ __device__ __forceinline__ int64_t tiles_before(const WorkShape &w, int len, int
             sum += (r * (q1 * (q1 - 1) / 2) + q1 * (n1 - q1 * r)) -
                    (r * (q0 * (q0 - 1) / 2) + q0 * (n0 - q0 * r));
     } else {
-        sum = 0;
-        for (int i = 0; i < t; ++i) sum += item_tiles(w, len, cells, i);
+        if (t > i0) sum += floor_sum(t - i0, w.kt, w.rt, B + i0 * w.rt);
     }
     return sum;
 }
