@@ -397,8 +397,9 @@ bool dense_decode_ok(const DenseArgs &a, int64_t max_q);
 size_t dense_decode_workspace();
 cudaError_t launch_dense_decode(const DenseArgs &a, void *workspace, cudaStream_t st);
 
-// The same with bf16 queries on the tcgen05 tensor cores, up to 32 rows (tokens x heads of a KV head);
-// short contexts of up to 16 rows it leaves to the above.
+// The same with bf16 queries on the tcgen05 tensor cores, up to 32 rows (tokens x heads of a KV head) over
+// bf16 cells and up to 64, as two row tiles, over e4m3 cells; short contexts of up to 16 rows it leaves to
+// the above.
 bool dense_few_ok(const DenseArgs &a, int64_t max_q);
 size_t dense_few_workspace();
 qsa_status launch_dense_few(const DenseArgs &a, int64_t max_q, void *workspace, cudaStream_t st);

@@ -149,8 +149,7 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
     const int rt2 = ws.rt / 2;  // tokens of a group
     bool ok = true;
     if (warp >= kSoftWarps) {
-        if constexpr (E8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == kMmaWarp) {
             // ---- MMA issue (all lanes walk, one issues)
             const uint32_t lead = elect_leader();

@@ -131,19 +131,12 @@ __device__ __forceinline__ void tmem_ld8_async(uint32_t taddr, float *v)
                  : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
                  : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_ld4_async(uint32_t taddr, float *v)
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
-                 : "r"(taddr));
-}
 template <int N>
 __device__ __forceinline__ void tmem_ld_async(uint32_t taddr, float *v)
 {
-    static_assert(N == 4 || N == 8 || N == 16, "columns of a load");
+    static_assert(N == 8 || N == 16, "columns of a load");
     if constexpr (N == 16) tmem_ld16_async(taddr, v);
-    else if constexpr (N == 8) tmem_ld8_async(taddr, v);
-    else tmem_ld4_async(taddr, v);
+    else tmem_ld8_async(taddr, v);
 }
 
 // N values (16 or 32) of each lane summed over the warp's lanes: lane i returns value i % N.  A step halves

@@ -33,11 +33,11 @@ __device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t saddr, uint32_t 
     return d;
 }
 
-// Instruction descriptor, kind::f16: fp32 accumulator, bf16 A and B (fp16 when f16), M 128, the
-// given N, B MN-major when b_mn.
-__host__ __device__ constexpr uint32_t idesc_m128(int n, bool b_mn, bool f16 = false)
+// Instruction descriptor, kind::f16: fp32 accumulator, bf16 A and B, M 128, the given N, B MN-major
+// when b_mn.
+__host__ __device__ constexpr uint32_t idesc_m128(int n, bool b_mn)
 {
-    return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (b_mn ? (1u << 16) : 0u) |
+    return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? (1u << 16) : 0u) |
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
