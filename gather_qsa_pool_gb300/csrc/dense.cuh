@@ -42,6 +42,33 @@ __device__ __forceinline__ void load8(const __nv_bfloat16 *p, float *x)
     }
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)),
+          "l"(reinterpret_cast<uint64_t &>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return d;
+}
+
 // The views below hold plain pointers (not __restrict__): a load through one is an ordinary load,
 // which the compiler does not move before a kernel's wait for its predecessor, so the kernels
 // read the views where they lie, in the parameters.
@@ -102,6 +129,19 @@ __device__ __forceinline__ int64_t cell_row(const KvView &kv, int s, int64_t fir
     const int32_t page = kv.table[(int64_t)s * kv.ld_table + j];
     if ((uint32_t)page >= (uint32_t)kv.n_pages) return -1;
     return ((int64_t)page << kv.page_shift) | (p & ((1 << kv.page_shift) - 1));
+}
+
+// An infinite or NaN value of V (element i of the pool, bf16 or codes) as the attention kernels add it to the
+// rows that see it, zero where it is finite.
+template <bool E8>
+__device__ __forceinline__ float odd_value_at(const KvView &kv, int64_t i)
+{
+    if constexpr (E8) {
+        return (static_cast<const uint8_t *>(kv.V)[i] & 0x7f) == 0x7f ? NAN : 0.0f;
+    } else {
+        const float f = __bfloat162float(static_cast<const __nv_bfloat16 *>(kv.V)[i]);
+        return isfinite(f) ? 0.0f : f;
+    }
 }
 
 // ------------------------------------------------------------------ the flattened work list

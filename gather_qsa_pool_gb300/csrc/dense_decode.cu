@@ -34,6 +34,7 @@
 
 #include "dense_join.cuh"
 #include "mma_frag.cuh"
+#include "umma.cuh"
 
 namespace qsa {
 namespace {
@@ -90,13 +91,6 @@ template <int N>
 __device__ __forceinline__ void cp_wait()
 {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 template <bool F16>
@@ -164,20 +158,6 @@ __device__ __forceinline__ uint32_t v_off(int r, int c)
 {
     const int x = E8 ? (((r >> 1) & 3) << 1) : (r & 7);
     return (uint32_t)r * Shape<E8>::kRowBytes + (uint32_t)((c ^ x) << 4);
-}
-
-// Value of a cell that may be infinite or NaN, as its row's sum sees it.
-template <bool E8>
-__device__ __forceinline__ float odd_value(const KvView &kv, int64_t row, int g, int e)
-{
-    if constexpr (E8) {
-        const uint8_t c = static_cast<const uint8_t *>(kv.V)[row * kv.ld_v + (int64_t)g * kD + e];
-        return (c & 0x7f) == 0x7f ? NAN : 0.0f;
-    } else {
-        const float v =
-            __bfloat162float(static_cast<const __nv_bfloat16 *>(kv.V)[row * kv.ld_v + (int64_t)g * kD + e]);
-        return isfinite(v) ? 0.0f : v;
-    }
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -519,14 +499,14 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
                             }
                         b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 1));
                         b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 2));
-                        const float ao = b == -INFINITY ? 1.0f : ex2(mx[hf] - b);
+                        const float ao = b == -INFINITY ? 1.0f : ex2_approx(mx[hf] - b);
                         mx[hf] = b;
                         float al = ao;
                         if constexpr (E8) {
                             if (wide) {
                                 a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
                                 a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-                                al = a == -INFINITY ? 1.0f : ex2(ms[hf] - a);
+                                al = a == -INFINITY ? 1.0f : ex2_approx(ms[hf] - a);
                                 ms[hf] = a;
                             }
                         }
@@ -559,7 +539,7 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 const float v = s[2 * kg + n][2 * hf + e];
-                                const float p = ex2(E8 ? v - ux : fmaf(v, scale_log2, -ux));
+                                const float p = ex2_approx(E8 ? v - ux : fmaf(v, scale_log2, -ux));
                                 w[n][hf][e] = p;
                                 if constexpr (E8) {
                                     const float g = e ? iv[n].y : iv[n].x;
@@ -578,8 +558,8 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
                                 for (int n = 0; n < 2; ++n)
 #pragma unroll
                                     for (int e = 0; e < 2; ++e)
-                                        l[hf] += ex2(s[2 * kg + n][2 * hf + e] -
-                                                         ex[8 * (2 * kg + n) + 2 * c4 + e].y - us);
+                                        l[hf] += ex2_approx(s[2 * kg + n][2 * hf + e] -
+                                                            ex[8 * (2 * kg + n) + 2 * c4 + e].y - us);
                             }
                         }
                     }
@@ -710,7 +690,8 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
                 for (int j = max(pos0 + 1, tile0 * ws.kt); j <= to && j < tile1 * ws.kt; ++j) {
                     const int64_t row = cell_row(kv, it.s, t0, j);
                     if (row >= 0)
-                        for (int k = 0; k < 4; ++k) v[k] += odd_value<E8>(kv, row, it.g, c + k);
+                        for (int k = 0; k < 4; ++k)
+                            v[k] += odd_value_at<E8>(kv, row * kv.ld_v + (int64_t)it.g * kD + c + k);
                 }
             }
             if (nan_out) sum = NAN;

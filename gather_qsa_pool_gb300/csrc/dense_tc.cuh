@@ -91,33 +91,6 @@ __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float *v)
           "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
         : "r"(taddr));
 }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    float2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(reinterpret_cast<uint64_t &>(d))
-        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)),
-          "l"(reinterpret_cast<uint64_t &>(c)));
-    return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b)
-{
-    float2 d;
-    asm("add.rn.f32x2 %0, %1, %2;"
-        : "=l"(reinterpret_cast<uint64_t &>(d))
-        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
-    return d;
-}
-
-__device__ __forceinline__ float2 mul2(float2 a, float2 b)
-{
-    float2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;"
-        : "=l"(reinterpret_cast<uint64_t &>(d))
-        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
-    return d;
-}
-
 // The CTA's share of the list, part by part; every role walks the same parts.
 struct Parts {
     WorkItem it;
@@ -319,18 +292,6 @@ template <int kLanes>
 __device__ __forceinline__ void named_sync(int id)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kLanes) : "memory");
-}
-
-// An infinite or NaN value of V as the epilogue adds it, zero where it is finite.
-template <bool E8>
-__device__ __forceinline__ float odd_value_at(const KvView &kv, int64_t i)
-{
-    if constexpr (E8) {
-        return (static_cast<const uint8_t *>(kv.V)[i] & 0x7f) == 0x7f ? NAN : 0.0f;
-    } else {
-        const float f = __bfloat162float(static_cast<const __nv_bfloat16 *>(kv.V)[i]);
-        return isfinite(f) ? 0.0f : f;
-    }
 }
 
 }  // namespace qsa

@@ -79,22 +79,9 @@ struct Row {
 };
 
 // The packed forms of the above: two indices at a time.
-__device__ __forceinline__ float2 add2(float2 a, float2 b)
-{
-    float2 d;
-    asm("add.rn.f32x2 %0, %1, %2;"
-        : "=l"(reinterpret_cast<uint64_t &>(d))
-        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
-    return d;
-}
 __device__ __forceinline__ float2 sub2(float2 a, float2 b)  // a + (-1) b: one rounding, as a - b
 {
-    float2 d, n = make_float2(-1.0f, -1.0f);
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(reinterpret_cast<uint64_t &>(d))
-        : "l"(reinterpret_cast<uint64_t &>(b)), "l"(reinterpret_cast<uint64_t &>(n)),
-          "l"(reinterpret_cast<uint64_t &>(a)));
-    return d;
+    return fma2(b, make_float2(-1.0f, -1.0f), a);
 }
 
 // Sum of the warp's chunks [c0, c1) of the row's weights; every lane gets it.

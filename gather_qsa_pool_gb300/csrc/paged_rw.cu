@@ -83,15 +83,6 @@ struct Src8<__nv_bfloat16> {
 };
 constexpr uint32_t kInfBits = 0x7f800000u;
 
-__device__ __forceinline__ float2 mul2(float2 a, float2 b)
-{
-    float2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;"
-        : "=l"(reinterpret_cast<uint64_t &>(d))
-        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
-    return d;
-}
-
 // Eight e4m3 codes of x * 2^-e (inv = 2^-e), packed little-endian; the conversion clamps finite
 // values to 448 and keeps NaN.  all: every value is finite; else infinities become NaN too.
 template <typename T>
