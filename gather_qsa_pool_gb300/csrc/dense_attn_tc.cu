@@ -663,6 +663,60 @@ size_t dense_tc_workspace()
     return kMaxCtas * sizeof(Split) + (size_t)2 * kMaxCtas * partial_floats(2 * kM, kD) * sizeof(float);
 }
 
+// Items that are not too long are not cut: a CTA an item (in turns, where there are more than run at once),
+// and nothing to join.  What either way costs, in us, fitted to measurements (with nothing in L2, less the
+// 8.5 us of an empty call; off by a tenth at most, a few by a quarter): `longest` tiles of the longest item,
+// `share` tiles a CTA, `turns` items a CTA.  Long work on bf16 cells runs at the power cap when calls follow one
+// another, and more SMs at work win less there: the chunk of 1,024 tokens below takes 745 whole and 777 cut
+// in a row of calls, after a pause 730 and 693.
+//
+// The host does not know the lengths.  A sequence alone is taken to be as long as it may be.  Of several, both
+// ends of what they may be are looked at: much alike (chunks as long as the table allows, prompts half as
+// long again as their mean), and all but one short.  Whole must be faster in the first, and lose no more in
+// the second than cutting loses in the first, nor more than three tenths.
+//
+// Measured whole and cut, bf16 cells, 32 / 4 heads: a chunk of 1,024 tokens over 61,789 cells 730 and 693, over
+// 8,000 115 and 137, of 400 over 2,000 46 and 59, of 64 over 3,000 59 and 48; on e4m3 cells the first 1,482
+// and 1,224, over 4,000 118 and 128.  Four chunks of 256 tokens over 60,000 cells each 712 and 730, over
+// 60,000, 500, 500 and 500 704 and 218; over 8,000 each 117 and 145, over 8,000 and three times 500 115 and 81;
+// over 2,000 each 48 and 81, over 2,000 and three times 300 46 and 63; sixteen of 512 over 4,000 each 400 and
+// 407, over 4,000 and fifteen times 600 145 and 153.  Prompts: 777 tokens, 8 / 2 heads, 30 and 45, of 8,000
+// 168 and 149, and beside fifteen of one token 168 and 144; three of 900, 32 / 4 heads, 62 and 77.
+template <bool E8>
+static bool whole_items(const DenseArgs &a, int rt, int64_t items, int ctas)
+{
+    if (items > 16 * (int64_t)ctas) return false;
+    const double n_tok = (double)a.sv.n_tok, n_seq = (double)a.sv.n_seq;
+    const double turns = fmax(n_tok / rt, n_seq) * a.kv.H_kv / ctas;
+    struct Cost {
+        double whole, cut;
+    };
+    const auto cost = [&](double longest, double share) -> Cost {
+        const double held = 1.6 * share + (items <= ctas ? 0.2 : 0.1) * fmax(0.0, share - 100.0);
+        if (items <= ctas)
+            return E8 ? Cost{12.0 + 3.0 * longest, 36.0 + 2.9 * share + 15.0 * turns}
+                      : Cost{14.0 + 1.46 * longest, 35.0 + held + 16.0 * turns};
+        return E8 ? Cost{15.0 + 1.6 * longest + 3.0 * share + 4.6 * turns, 37.0 + 2.75 * share + 10.0 * turns}
+                  : Cost{14.0 + 0.9 * longest + 1.5 * share + 8.0 * turns, 41.0 + held + 7.0 * turns};
+    };
+    Cost alike, one_long;
+    if (a.kv.table) {
+        const double cells = fmax((double)(a.kv.ld_table << a.kv.page_shift), 1.0), longest = cells / kN;
+        // (a row tile in the midst of the new tokens does not see those behind it)
+        const double share = longest * turns * (1.0 - 0.5 * fmin(1.0, n_tok / n_seq / cells));
+        alike = cost(longest, share);
+        one_long = cost(longest, share / n_seq + turns);
+    } else {
+        const double longest = (a.sv.n_seq > 1 ? fmin(n_tok, 1.5 * n_tok / n_seq) : n_tok) / kN;
+        const double most = fmax(n_tok - n_seq + 1.0, 1.0) / kN;
+        alike = cost(longest, 0.5 * longest * turns);
+        one_long = cost(most, 0.5 * most * turns);
+    }
+    return alike.whole < alike.cut &&
+           (a.sv.n_seq == 1 || (one_long.whole - one_long.cut < alike.cut - alike.whole &&
+                                one_long.whole < 1.3 * one_long.cut));
+}
+
 template <bool E8>
 static qsa_status run_tc(const DenseArgs &a, void *workspace, cudaStream_t st)
 {
@@ -682,46 +736,8 @@ static qsa_status run_tc(const DenseArgs &a, void *workspace, cudaStream_t st)
     if (ctas > kMaxCtas) ctas = kMaxCtas;
     Split *splits = static_cast<Split *>(workspace);
     float *partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + kMaxCtas * sizeof(Split));
-    // Items that are not too long are not cut: a CTA an item (in turns, where there are more than run at
-    // once), and nothing to join.  Two models of both costs, in us, fitted to measurements: `tiles` of the
-    // longest item, `turns` items a CTA, `share` tiles a CTA (of prompts half of the longest's an item, of
-    // chunks nearer to it).  Measured whole and cut: prompts of 777 tokens, 8 / 2 heads, 20.2 and 30.9, of
-    // 3,000 45.9 and 54.7, with 4 / 4 heads 47.5 and 40.1, three of 900, 32 / 4 heads, 51.6 and 64.5, one of
-    // 8,000, 8 / 2 heads, 157 and 135; chunks, 32 / 4 heads, of 400 tokens over 2,000 cells 34.8 and 44.2, of
-    // 64 over 3,000 46.6 and 32.3, of 1,500 over 4,000 102 and 97.
-    // Of several sequences the host does not know the lengths, so both ends of what they may be are looked
-    // at: much alike (chunks as long as the table allows, prompts half as long again as their mean), and
-    // all but one short.  Whole must be faster in the first, and what it may lose in the second no more
-    // than what cutting loses in the first (8 us of it lie within the models' errors).  Measured whole and
-    // cut (with nothing in L2, which costs some 10 us), 32 / 4 heads: four chunks of 256 tokens over 60,000
-    // cells each 712 and 730, over 60,000, 500, 500 and 500 704 and 218; over 8,000 each 117 and 145, over
-    // 8,000 and three times 500 115 and 81; over 2,000 each 48 and 81, over 2,000 and three times 300 46 and
-    // 63; sixteen of 512 over 4,000 each 400 and 407, over 4,000 and fifteen times 600 145 and 153; 8 / 2
-    // heads, a prompt of 8,000 tokens beside fifteen of one 168 and 144; 16 / 2, one of 2,500 beside one of
-    // 700 64 and 78.
     const int64_t items = ((a.sv.n_tok + ws.rt - 1) / ws.rt + a.sv.n_seq) * a.kv.H_kv;
-    const double n_tok = (double)a.sv.n_tok, n_seq = (double)a.sv.n_seq;
-    const double turns = fmax(n_tok / ws.rt, n_seq) * a.kv.H_kv / ctas;
-    struct Cost {
-        double whole, cut;
-    };
-    const auto cost = [&](double tiles, double share) -> Cost {
-        if (items <= ctas) return {13.0 + 1.4 * tiles, 32.0 + 2.4 * share};
-        return {13.0 + 1.2 * tiles + 1.4 * share + 7.0 * turns, 34.0 + 1.8 * share + 5.5 * turns};
-    };
-    Cost alike, one_long;
-    if (a.kv.table) {
-        const double tiles = (double)(a.kv.ld_table << a.kv.page_shift) / kN;
-        alike = cost(tiles, 0.75 * tiles * turns);
-        one_long = a.sv.n_seq > 1 ? cost(tiles, 0.75 * tiles * turns / n_seq + turns) : alike;
-    } else {
-        const double tiles = (a.sv.n_seq > 1 ? fmin(n_tok, 1.5 * n_tok / n_seq) : n_tok) / kN;
-        const double most = fmax(n_tok - n_seq + 1.0, 1.0) / kN;
-        alike = cost(tiles, 0.5 * tiles * turns);
-        one_long = cost(most, 0.5 * most * turns);
-    }
-    const bool whole = items <= 16 * (int64_t)ctas && alike.whole < alike.cut &&
-                       (a.sv.n_seq == 1 || one_long.whole - one_long.cut < alike.cut - alike.whole + 8.0);
+    const bool whole = whole_items<E8>(a, ws.rt, items, ctas);
     if (whole) ctas = (int)items;
     cudaError_t e = launch(dense_tc_kernel<E8>, dim3((unsigned)ctas), dim3(Cfg<E8>::kThreads), smem, st, 1, mq,
                            mk, mv, a.kv, a.sv, ws, box_rows, a.H_q, a.scale * kLog2e,

@@ -14,7 +14,7 @@ from test_gpu_dense_few import widen
 pytestmark = pytest.mark.gpu
 
 
-def chunk_cuts(lens, news, H_q, H, page=64, cells=0):
+def chunk_cuts(lens, news, H_q, H, page=64, cells=0, kv_dtype=BF16):
     """Whether paged_attn of `news` tokens over `lens` cells cuts its items; cells: the table's width."""
     counts = [-(-n // page) for n in lens]
     table = torch.full((len(lens), max(max(counts), cells // page)), -1, dtype=torch.int32, device=DEV)
@@ -22,8 +22,9 @@ def chunk_cuts(lens, news, H_q, H, page=64, cells=0):
     for s, c in enumerate(counts):
         table[s, :c] = torch.arange(at, at + c, device=DEV)
         at += c
-    K = torch.zeros(at * page, H, 128, dtype=BF16, device=DEV)
-    cache = qsa.PagedCache(K, K.clone(), page)
+    K = torch.zeros(at * page, H, 128, device=DEV).to(kv_dtype)
+    e = torch.full((at * page, H), 127, dtype=torch.uint8, device=DEV) if kv_dtype == E4M3 else None
+    cache = qsa.PagedCache(K, K.clone(), page, K_exp=e, V_exp=e)
     n = sum(news)
     q = torch.randn(n, H_q, 128, device=DEV).to(BF16)
     out = torch.full_like(q, -7.0)
@@ -56,6 +57,17 @@ def prompt_cuts(lens, H_q, H):
 ])
 def test_a_long_chunk_among_short_ones_is_cut(lens, news, cut):
     assert chunk_cuts(lens, news, 32, 4) == cut
+
+
+@pytest.mark.parametrize("lens,news,kv_dtype,cut", [
+    # 128 items, not 152: whole, they leave SMs idle, which on e4m3 cells costs more than joining; bf16
+    # products of that length run at the power cap, where fewer SMs are as fast
+    ([61789], [1024], BF16, False), ([61789], [1024], E4M3, True),
+    ([8000], [1024], BF16, False), ([8000], [1024], E4M3, True),
+    ([2000], [1024], BF16, False), ([2000], [1024], E4M3, False),
+])
+def test_a_chunk_of_nearly_as_many_items_as_ctas(lens, news, kv_dtype, cut):
+    assert chunk_cuts(lens, news, 32, 4, kv_dtype=kv_dtype) == cut
 
 
 @pytest.mark.parametrize("lens,H_q,H,cut", [
