@@ -16,9 +16,9 @@
 //
 // One thread-block cluster per sequence: every CTA decides a itself (a few gathers), sums its
 // slice of the row(s), and the warps of the CTA that holds the drawn point scan, a chunk each, the
-// slice of the one warp that holds it (64 sequences, vocabulary of 131,072: 22.9 us; 31.7 with one
+// slice of the one warp that holds it (64 sequences, vocabulary of 131,072: 23.0 us; 31.7 with one
 // warp scanning).  One launch, no workspace, no atomics: the same result every time.  Bound by one
-// pass over one or two rows (10 of the 22.9 us, at the copy bandwidth) and the chain around it:
+// pass over one or two rows (10 of the 23.0 us, at the copy bandwidth) and the chain around it:
 // token -> gather -> row, the cluster's barrier, the chunk.
 #include <cooperative_groups.h>
 

@@ -170,8 +170,9 @@ __device__ __forceinline__ int token_seq(const SeqView &sv, int64_t tok)
 // the tokens' K and V rows of all KV heads, eight values a lane, d / 8 lanes per head (a power of two
 // of them, up to 32), so a head's largest magnitude is a shuffle over its lanes (K's and V's of bf16
 // rows in one word); four loads are in flight.  Prompts (26,900 tokens, 4 heads of 128, bf16 to e4m3):
-// 20.1 us, 0.61 of the copy bandwidth, bound by the instructions of the encoding and by the last turn;
-// with few tokens by the launch and the look-up's dependent loads.
+// 19.8 us, 0.61 of the copy bandwidth; neither the memory nor issue slots (61%) nor a pipe (ALU 57%) is full:
+// a warp's loads and its long encoding alternate, with nothing loaded ahead and 38% of the warps resident.
+// With few tokens bound by the launch and the look-up's dependent loads.
 template <typename TS, typename TD>
 __global__ void __launch_bounds__(128, sizeof(TS) == 4 && sizeof(TD) == 1 ? 6 : 8)
 paged_write_kernel(const TS *__restrict__ k, const TS *__restrict__ v, int64_t ld_k, int64_t ld_v,

@@ -751,7 +751,10 @@ qsa_status qsa_paged_read(const qsa_paged_cache *cache, const int32_t *table, in
  *   q        [n_tok][H_q][d] of type q_dtype (QSA_F32 or QSA_BF16), ld_q elements between tokens
  *   out      [n_tok][H_q][d] packed, of type q_dtype;  lse_out [n_tok][H_q] fp32 or NULL
  *   max_q    the largest number of new tokens of one sequence, as far as the host knows: it
- *            chooses the kernel, and no result depends on it
+ *            chooses the kernel, and no result depends on it beyond rounding (the kernels hold the
+ *            softmax weights in different numbers of bits, see below).  So does the number of cells
+ *            that a row of the table has room for: it is taken as the longest that a sequence may
+ *            be, and a row much longer than that can cost time
  *   workspace  qsa_paged_attn_workspace_size() bytes, 256-byte aligned, for the parts of rows
  *            whose cells are shared out; its contents do not matter, and calls that may run at
  *            the same time need one each
@@ -759,8 +762,12 @@ qsa_status qsa_paged_read(const qsa_paged_cache *cache, const int32_t *table, in
  * or QSA_E4M3 pool the products run on the tensor cores: QSA_BF16 queries with the softmax weights
  * rounded to 8 significant bits (for a few tokens on a QSA_E4M3 pool 9 or 11), QSA_F32 queries (up to
  * 16 heads per KV head) with queries and weights as sums of three bf16 terms on a QSA_BF16 pool
- * (24 bits) and of two fp16 terms on a QSA_E4M3 pool (22 bits).  Other shapes, and QSA_BF16
- * chunks with scale <= 0, take fp32 arithmetic on the CUDA cores, which is right but slower.
+ * (24 bits) and of two fp16 terms on a QSA_E4M3 pool (22 bits).  With a few tokens, or QSA_F32 queries,
+ * on a QSA_E4M3 pool a weight times its cell's power of two is held to 3 * 2^-33 (9 bits) or 2^-38 (11
+ * and 22 bits) of the row's largest, and smaller ones may count as nothing; and queries are held to 2^-31
+ * of the largest magnitude among up to 32 rows (tokens x heads) of their sequence and KV head.  Other
+ * shapes, and QSA_BF16 chunks with scale <= 0, take fp32 arithmetic on the CUDA cores, which is right but
+ * slower (no tensor cores, contexts not shared out).
  * Errors: INVALID_ARG for null pointers, sizes < 0, H_q not a multiple of H_kv, ld_q < H_q*d, a
  * misaligned pointer (q and out 16 bytes, rows of q a multiple of 16 bytes), a workspace smaller
  * than required; UNSUPPORTED for n_seq, n_tok or their work beyond 2^31 - 1 rows.
