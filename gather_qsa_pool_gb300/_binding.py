@@ -17,7 +17,7 @@ LIB_PATH = os.path.join(HERE, "_build", "libqsa.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "qsa.h")
 
 QSA_OK, QSA_ERR_INVALID_ARG, QSA_ERR_UNSUPPORTED, QSA_ERR_CUDA, QSA_ERR_TIMEOUT = range(5)
-QSA_F32, QSA_BF16, QSA_E4M3 = 0, 1, 2
+QSA_F32, QSA_BF16, QSA_E4M3, QSA_E2M1 = 0, 1, 2, 3
 QSA_PREC_F32, QSA_PREC_BF16_TC = 0, 1
 QSA_WAIT_DEFAULT_NS = 2_000_000_000
 
@@ -76,6 +76,10 @@ _SIGNATURES = {
                                     _p, _i64, _i64, _p, _p, _p, _p]),
     "qsa_paged_write": (_int, [_p, _p, _i64, _i64, _p, _p, _p, _p, _int, _i64, _i64, _i64, _p]),
     "qsa_paged_read": (_int, [_p, _p, _i64, _i64, _p, _p, _p, _p, _i64, _i64, _p, _p, _int, _p]),
+    "qsa_paged_append": (_int, [_p, _p, _i64, _i64, _p, _p, _p, _p, _p, _int, _i64, _int, _i64, _i64,
+                                _i64, _p, _int, _d, _p, _p, _p]),
+    "qsa_paged_sparse_attn": (_int, [_p, _p, _i64, _i64, _p, _p, _p, _p, _i64, _p, _int, _i64, _i64,
+                                     _int, _f, _p, _p, _p]),
     "qsa_paged_attn": (_int, [_p, _p, _i64, _i64, _p, _p, _p, _int, _i64, _i64, _i64, _int, _f,
                               _int, _p, _p, _p, _sz, _p]),
     "qsa_paged_attn_workspace_size": (_sz, [_i64, _i64, _i64, _int, _int, _int]),
@@ -403,6 +407,12 @@ class _PagedCacheStruct(ctypes.Structure):
                 ("page_size", _int)]
 
 
+class _PagedCacheScales(_PagedCacheStruct):
+    """The whole struct: the scales of 4-bit caches come last."""
+
+    _fields_ = [("K_scale", _p), ("V_scale", _p)]
+
+
 # The calls below are made once per layer and step, many of them on tensors that take the GPU a few
 # microseconds: their checks are plain comparisons, and messages are made only when one fails.
 
@@ -504,9 +514,11 @@ class PagedCache:
     """A qsa_paged_cache: a pool of pages in K and V, [n_pages * page_size][H_kv][d] (or with a
     leading [n_pages][page_size] whose rows follow one another at one stride) of float32, bfloat16
     or float8_e4m3fn; the last with its exponent bytes K_exp, V_exp [n_pages * page_size][H_kv]
-    uint8.  Holds the tensors, and never a copy of them."""
+    uint8.  K and V of uint8, [..][H_kv][d / 2], are a 4-bit cache: two e2m1 codes a byte, with
+    exponent bytes as above and the scales K_scale, V_scale [n_pages][H_kv][page_size][d / 16] of
+    float8_e4m3fn.  Holds the tensors, and never a copy of them."""
 
-    def __init__(self, K, V, page_size, K_exp=None, V_exp=None):
+    def __init__(self, K, V, page_size, K_exp=None, V_exp=None, K_scale=None, V_scale=None):
         torch = _use_torch()
         if K.dim() == 4 and V.dim() == 4:
             K, V = _pool_rows("K", K), _pool_rows("V", V)
@@ -514,24 +526,39 @@ class PagedCache:
                 K_exp, V_exp = _pool_rows("K_exp", K_exp), _pool_rows("V_exp", V_exp)
         _need(K.dim() == 3 and K.shape == V.shape and K.dtype == V.dtype and K.device == V.device,
               "K and V: two tensors of one type and shape [rows][H_kv][d]")
-        types = {torch.float32: QSA_F32, torch.bfloat16: QSA_BF16, torch.float8_e4m3fn: QSA_E4M3}
+        types = {torch.float32: QSA_F32, torch.bfloat16: QSA_BF16, torch.float8_e4m3fn: QSA_E4M3,
+                 torch.uint8: QSA_E2M1}
         if K.dtype not in types:
-            raise TypeError(f"a paged cache is float32, bfloat16 or float8_e4m3fn, got {K.dtype}")
-        rows, self.H_kv, self.d = K.shape
+            raise TypeError(f"a paged cache is float32, bfloat16, float8_e4m3fn or uint8 (4-bit codes), got {K.dtype}")
+        rows, self.H_kv, width = K.shape
         _need(page_size > 0 and rows % page_size == 0, "K and V: a whole number of pages")
         dev = _gpu("K", K)
-        ld_k = _head_rows("K", K, self.H_kv, self.d, dev)
-        ld_v = _head_rows("V", V, self.H_kv, self.d, dev)
-        if K.dtype == torch.float8_e4m3fn:
+        ld_k = _head_rows("K", K, self.H_kv, width, dev)
+        ld_v = _head_rows("V", V, self.H_kv, width, dev)
+        four = K.dtype == torch.uint8
+        self.d = 2 * width if four else width
+        if four:  # two values a byte
+            ld_k, ld_v = 2 * ld_k, 2 * ld_v
+        if four or K.dtype == torch.float8_e4m3fn:
             for e in (K_exp, V_exp):
                 _need(e is not None and e.dtype == torch.uint8 and e.is_contiguous()
                       and e.device == K.device and tuple(e.shape) == (rows, self.H_kv),
-                      "K_exp and V_exp: contiguous uint8 [rows][H_kv] beside an 8-bit cache")
-        self.K, self.V, self.K_exp, self.V_exp = K, V, K_exp, V_exp
-        self._dev = dev
+                      "K_exp and V_exp: contiguous uint8 [rows][H_kv] beside an 8-bit or 4-bit cache")
         self.page_size, self.n_pages = page_size, rows // page_size
-        self._struct = _PagedCacheStruct(_dp(K), _dp(V), _dp(K_exp), _dp(V_exp), types[K.dtype],
-                                         self.H_kv, self.d, ld_k, ld_v, self.n_pages, page_size)
+        if four:
+            _need(self.d % 16 == 0, "K and V: 16 values share a scale")
+            for e in (K_scale, V_scale):
+                _need(e is not None and e.dtype == torch.float8_e4m3fn and e.is_contiguous()
+                      and e.device == K.device and e.data_ptr() % 16 == 0
+                      and tuple(e.shape) == (self.n_pages, self.H_kv, page_size, self.d // 16),
+                      "K_scale and V_scale: contiguous float8_e4m3fn [n_pages][H_kv][page_size][d / 16], "
+                      "16-byte aligned, beside a 4-bit cache")
+        self.K, self.V, self.K_exp, self.V_exp = K, V, K_exp, V_exp
+        self.K_scale, self.V_scale = K_scale, V_scale
+        self._dev = dev
+        self._struct = _PagedCacheScales(_dp(K), _dp(V), _dp(K_exp), _dp(V_exp), types[K.dtype],
+                                         self.H_kv, self.d, ld_k, ld_v, self.n_pages, page_size,
+                                         _dp(K_scale), _dp(V_scale))
         self._ref = ctypes.addressof(self._struct)
 
 
@@ -552,6 +579,44 @@ def paged_write(cache, table, cu_q, kv_len, k, v, stream=None):
         ld_k, ld_v, _raw_stream(stream, dev))
     if st:
         raise QSAError("qsa_paged_write", st)
+
+
+def paged_append(cache, table, cu_q, kv_len, k, v, rope_base, rot=None, q=None, q_out=None, k_out=None,
+                 pos=None, stream=None):
+    """qsa_paged_append: paged_write of rows k, v [n_tok][H_kv][d] (float32 or bfloat16) with the first
+    `rot` values (None: all) of k's heads, and of q's [n_tok][H_q][d], rotated by the tokens' places in
+    their sequences (or by pos [n_tok] int32).  The rotated queries go to q_out, packed (None: into q,
+    which then has to be packed); the rotated keys, where k_out is given, there too.  Returns q_out."""
+    n_seq, n_tok, dev, H, d = kv_len.shape[0], k.shape[0], cache._dev, cache.H_kv, cache.d
+    tb, cu, kl = (_i32_table(table, n_seq, dev), _i32_vector("cu_q", cu_q, n_seq + 1, dev),
+                  _i32_vector("kv_len", kv_len, 0, dev))
+    ld_k, ld_v = _head_rows("k", k, H, d, dev), _head_rows("v", v, H, d, dev)
+    if v.shape[0] != n_tok or v.dtype is not k.dtype:
+        raise ValueError("k and v: one type and length")
+    H_q = ld_q = 0
+    if q is not None:
+        H_q = q.shape[1] if q.dim() == 3 else q.shape[-1] // d
+        ld_q = _head_rows("q", q, H_q, d, dev)
+        if q_out is None:
+            q_out = q
+        if q.shape[0] != n_tok or q.dtype is not k.dtype:
+            raise ValueError("q: k's type and length")
+        _packed_rows("q_out", q_out, k.dtype, n_tok * H_q * d, dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if k_out is not None:
+        _packed_rows("k_out", k_out, k.dtype, n_tok * H * d, dev)
+    if pos is not None:
+        _i32_vector("pos", pos, n_tok, dev)
+    if n_tok == 0:
+        return q_out
+    st = load().qsa_paged_append(
+        cache._ref, tb, table.shape[1], n_seq, cu, kl, _dp(q), k.data_ptr(), v.data_ptr(), _dtype(k), n_tok, H_q,
+        ld_q, ld_k, ld_v, _dp(pos), d if rot is None else rot, rope_base, _dp(q_out), _dp(k_out),
+        _raw_stream(stream, dev))
+    if st:
+        raise QSAError("qsa_paged_append", st)
+    return q_out
 
 
 def paged_read(cache, table, kv_len, n_cells, max_cells, K_out, V_out, pos=None, seq=None,
@@ -579,6 +644,12 @@ def paged_read(cache, table, kv_len, n_cells, max_cells, K_out, V_out, pos=None,
         K_out.data_ptr(), V_out.data_ptr(), _dtype(K_out), _raw_stream(stream, dev))
     if st:
         raise QSAError("qsa_paged_read", st)
+
+
+def _packed_rows(name, t, dtype, n, dev):
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{name}: packed, {n} values of {dtype} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on "
+                         f"{t.device}")
 
 
 def _attn_outputs(q, out, lse, workspace, n_tok, H_q, d, dev):
@@ -619,6 +690,28 @@ def paged_attn(cache, table, cu_q, kv_len, q, out, scale, max_q, causal=True, ls
         _raw_stream(stream, dev))
     if st:
         raise QSAError("qsa_paged_attn", st)
+
+
+def paged_sparse_attn(cache, table, cu_q, kv_len, blocks, counts, q, out, scale, lse=None, stream=None):
+    """qsa_paged_sparse_attn: q [n_tok][H_q][d] (float32 or bfloat16) of the new tokens, each over the
+    cells of its selected blocks (blocks [n_tok][k_blk], counts [n_tok], as topk_blocks writes them) and
+    its open block; out like q, lse [n_tok][H_q] float32."""
+    n_seq, n_tok, d, dev = kv_len.shape[0], q.shape[0], cache.d, cache._dev
+    H_q = q.shape[1] if q.dim() == 3 else q.shape[-1] // d
+    tb, cu, kl, nc = (_i32_table(table, n_seq, dev), _i32_vector("cu_q", cu_q, n_seq + 1, dev),
+                      _i32_vector("kv_len", kv_len, 0, dev), _i32_vector("counts", counts, n_tok, dev))
+    if blocks.dtype is not _torch.int32 or blocks.get_device() != dev or blocks.dim() != 2 or \
+            blocks.shape[0] < n_tok or not blocks.is_contiguous():
+        _bad_i32("blocks", blocks, (n_tok, "k_blk"), dev)
+    ld_q = _head_rows("q", q, H_q, d, dev)
+    _attn_outputs(q, out, lse, None, n_tok, H_q, d, dev)
+    if n_tok == 0:
+        return
+    st = load().qsa_paged_sparse_attn(
+        cache._ref, tb, table.shape[1], n_seq, cu, kl, _dp(blocks), nc, blocks.shape[1], q.data_ptr(), _dtype(q),
+        n_tok, ld_q, H_q, scale, out.data_ptr(), _dp(lse), _raw_stream(stream, dev))
+    if st:
+        raise QSAError("qsa_paged_sparse_attn", st)
 
 
 def prompt_attn_workspace_size(n_tok, n_seq, H_q, H_kv, d) -> int:

@@ -78,7 +78,8 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b)
 // table == NULL: packed sequences, the cell is row cu[s] + p.
 struct KvView {
     const void *K, *V;
-    const uint8_t *K_exp, *V_exp;  // [rows][H_kv], QSA_E4M3 only
+    const uint8_t *K_exp, *V_exp;  // [rows][H_kv], QSA_E4M3 and QSA_E2M1 only
+    const uint8_t *K_scale, *V_scale;  // [pages][H_kv][page][d / 16], QSA_E2M1 only
     int64_t ld_k, ld_v;            // elements between rows
     const int32_t *table;
     int64_t ld_table;
@@ -142,6 +143,49 @@ __device__ __forceinline__ float odd_value_at(const KvView &kv, int64_t i)
         const float f = __bfloat162float(static_cast<const __nv_bfloat16 *>(kv.V)[i]);
         return isfinite(f) ? 0.0f : f;
     }
+}
+
+// ------------------------------------------------------------------ listed blocks
+// Blocks of four cells selected for each token (blocks NULL: every cell is seen, no lists).
+struct ListView {
+    const int32_t *blocks, *counts;
+    int64_t k_blk;  // entries of a token's list
+};
+
+// A token's sequence, the position it has there, and the sequence's cells.  False: of no sequence.  All 32 lanes of
+// a warp call it.
+__device__ __forceinline__ bool token_place(const SeqView &sv, int64_t tok, int &s, int &p, int &cells)
+{
+    const int lane = threadIdx.x & 31;
+    for (s = 0;; s += 32) {
+        const bool behind = s + lane < sv.n_seq && (int64_t)sv.cu[s + lane + 1] <= tok;
+        const int n = __popc(__ballot_sync(0xffffffffu, behind));
+        if (n < 32) {
+            s += n;
+            break;
+        }
+    }
+    p = -1;
+    cells = 0;
+    if (s >= sv.n_seq) return false;
+    int64_t t0;
+    int len;
+    seq_tokens(sv, s, t0, len);
+    if (tok < t0 || tok >= t0 + len) return false;
+    cells = seq_cells(sv, s, len);
+    p = cells - len + (int)(tok - t0);
+    return true;
+}
+
+// Cell number i of the list of a token at position p: of its n listed blocks, then of its open block.  -1: none.
+__device__ __forceinline__ int list_cell(const int32_t *list, int n, int p, int i)
+{
+    if ((i >> 2) < n) {
+        const int b = list[i >> 2];
+        return b >= 0 && b <= ((p - 3) >> 2) ? 4 * b + (i & 3) : -1;
+    }
+    const int j = ((p + 1) & ~3) + (i & 3);
+    return (i >> 2) == n && j <= p ? j : -1;
 }
 
 // ------------------------------------------------------------------ the flattened work list
@@ -420,6 +464,7 @@ struct DenseArgs {
     float scale;
     int causal;
     int64_t pool_rows;  // rows of K and V
+    ListView list = {};  // blocks selected for each token: dense_attn.cu only
 };
 
 // Row tiles of rt tokens, cells in tiles of kt, `over` places an item.

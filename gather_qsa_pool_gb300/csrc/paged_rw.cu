@@ -1,5 +1,6 @@
 // paged_rw.cu -- the paged key/value cache: rows of new tokens written into their pages
-// (quantised to e4m3 on the way when the pool holds 8-bit codes) and listed cells read back.
+// (quantised to e4m3 on the way when the pool holds 8-bit codes) and listed cells read back.  4-bit
+// rows (e2m1.cuh) are read here and written by paged_append.cu.
 //
 // Mathematics of the 8-bit form: a row is the d values of one token and KV head.  With
 // top = max |x| over the row's finite values, e is the least integer with top <= 448 * 2^e
@@ -11,7 +12,9 @@
 // floating point themselves.  value = code * 2^e is exact in bf16 and fp32.
 #include <cuda_fp8.h>
 
-#include "dense.cuh"
+#include <type_traits>
+
+#include "e2m1.cuh"
 #include "paged.cuh"
 
 namespace qsa {
@@ -311,6 +314,22 @@ struct Raw {
     }
 };
 
+// 4-bit rows: sixteen codes a lane, which share a scale.
+struct E2m1Codes {
+    uint8_t pair;
+};
+template <>
+struct Raw<E2m1Codes, 16> {
+    uint2 c;
+    uint8_t scale;
+    __device__ __forceinline__ void clear()
+    {
+        c = make_uint2(0u, 0u);
+        scale = 0;
+    }
+    __device__ __forceinline__ void load(const E2m1Codes *p) { c = *reinterpret_cast<const uint2 *>(p); }
+};
+
 template <typename TS, typename TD, int kVec>
 __global__ void __launch_bounds__(128, 8)
 paged_read_kernel(KvView kv, int H, int d, int d_log2, int group, const int32_t *__restrict__ seq,
@@ -360,9 +379,14 @@ paged_read_kernel(KvView kv, int H, int d, int d_log2, int group, const int32_t 
                 if (s0 + u < steps && e < hd) {
                     to[u] = (is_v ? V_out : K_out) + (i * max_cells + j0 + cell) * hd + e;
                     if (row >= 0) {
-                        raw[u].load((is_v ? V + row * kv.ld_v : K + row * kv.ld_k) + e);
+                        constexpr bool kFour = std::is_same_v<TS, E2m1Codes>;
+                        const int64_t at = (int64_t)row * (is_v ? kv.ld_v : kv.ld_k) + e;
+                        raw[u].load((is_v ? V : K) + (kFour ? at >> 1 : at));
                         if constexpr (sizeof(TS) == 1) {
                             const int h = d_log2 >= 0 ? e >> d_log2 : e / d;
+                            if constexpr (kFour)
+                                raw[u].scale = (is_v ? kv.V_scale : kv.K_scale)[scale_row(kv, row, h) * (d / kGroup) +
+                                                                                (e - h * d) / kGroup];
                             mul[u] = two_to(min(max((int)(is_v ? kv.V_exp : kv.K_exp)[(int64_t)row * H + h] -
                                                         kExpBias, kExpMin), kExpMax));
                         }
@@ -376,11 +400,18 @@ paged_read_kernel(KvView kv, int H, int d, int d_log2, int group, const int32_t 
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 if (!to[u]) continue;
+                if constexpr (std::is_same_v<TS, E2m1Codes>) {
+                    float x[16];
+                    decode16(raw[u].c, raw[u].scale, mul[u], x);
+                    store8(to[u], x);
+                    store8(to[u] + 8, x + 8);
+                } else {
 #pragma unroll
-                for (int k = 0; k < kVec / 8; ++k) {
-                    float x[8];
-                    raw[u].eight(k, mul[u], x);
-                    store8(to[u] + 8 * k, x);
+                    for (int k = 0; k < kVec / 8; ++k) {
+                        float x[8];
+                        raw[u].eight(k, mul[u], x);
+                        store8(to[u] + 8 * k, x);
+                    }
                 }
             }
         }
@@ -473,6 +504,11 @@ cudaError_t launch_paged_read(const KvView &kv, qsa_dtype cache_dtype, int d, co
 {
     const bool f32 = out_dtype == QSA_F32;
     switch (cache_dtype) {
+        case QSA_E2M1:
+            return f32 ? read_vec<E2m1Codes, float, 16>(kv, d, seq, kv_len, n_seq, pos, n_cells, n_list, max_cells,
+                                                        K_out, V_out, st)
+                       : read_vec<E2m1Codes, __nv_bfloat16, 16>(kv, d, seq, kv_len, n_seq, pos, n_cells, n_list,
+                                                                max_cells, K_out, V_out, st);
         case QSA_E4M3:
             return f32 ? read_to<uint8_t, float>(kv, d, seq, kv_len, n_seq, pos, n_cells, n_list,
                                                  max_cells, K_out, V_out, st)

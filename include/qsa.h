@@ -52,9 +52,10 @@ typedef enum {
                                 see qsa_set_wait_options) */
 } qsa_status;
 
-/* QSA_E4M3 (8-bit floating point with one exponent byte per row) is a type of paged caches
- * only, see qsa_paged_cache. */
-typedef enum { QSA_F32 = 0, QSA_BF16 = 1, QSA_E4M3 = 2 } qsa_dtype;
+/* QSA_E4M3 (8-bit floating point with one exponent byte per row) and QSA_E2M1 (4-bit floating
+ * point with a scale for 16 values and one exponent byte per row) are types of paged caches only,
+ * see qsa_paged_cache. */
+typedef enum { QSA_F32 = 0, QSA_BF16 = 1, QSA_E4M3 = 2, QSA_E2M1 = 3 } qsa_dtype;
 
 typedef enum {
     QSA_PREC_F32 = 0,    /* fp32 operands, fp32 accumulation (CUDA cores) */
@@ -69,7 +70,8 @@ const char *qsa_status_str(qsa_status s);
  * several queries per decode step, the host-fed decode step; minor 1: decode plans;
  * minor 2: qsa_mask_sparse_attn; minor 3: qsa_sparse_attn_union; minor 4:
  * qsa_set_wait_options; minor 5: the paged cache (qsa_paged_write, _read, _attn),
- * qsa_prompt_attn and qsa_draft_verify. */
+ * qsa_prompt_attn and qsa_draft_verify; minor 6: QSA_E2M1 caches, qsa_paged_append and
+ * qsa_paged_sparse_attn. */
 int qsa_version(void);
 
 /*
@@ -669,11 +671,17 @@ qsa_status qsa_mask_sparse_eligible(int has_mask, float max_bias, float softcap,
  *
  *   dtype      QSA_F32, QSA_BF16, or QSA_E4M3: e4m3 codes (one byte each; 4 significant bits)
  *              with one exponent byte b per row and KV head in K_exp / V_exp [rows][H_kv]; the
- *              value is code * 2^(b - 127), b in [27, 227]
+ *              value is code * 2^(b - 127), b in [27, 227]; or QSA_E2M1: e2m1 codes (4 bits: 0, 0.5,
+ *              1, 1.5, 2, 3, 4, 6 and their negatives; two a byte, the even value in the low half)
+ *              with an e4m3 scale for each 16 values in K_scale / V_scale
+ *              [n_pages][H_kv][page_size][d / 16] and an exponent byte as above; the value is
+ *              code * scale * 2^(b - 127)
  *   page_size  tokens per page, a power of two from 8 to 4096
  *   n_pages    pages in the pool, n_pages * page_size < 2^31
  * Requirements (INVALID_ARG otherwise): K, V non-null and 16-byte aligned, ld_k, ld_v >= H_kv*d
- * with rows a multiple of 16 bytes (8 for QSA_E4M3), d a multiple of 8; UNSUPPORTED for d > 256.
+ * with rows a multiple of 16 bytes (8 for codes), d a multiple of 8 (16 for QSA_E2M1, whose
+ * scales are 16-byte aligned); UNSUPPORTED for d > 256.  Strides count values: a row of QSA_E2M1
+ * takes ld / 2 bytes.
  *
  * Sequences.  table [n_seq][ld_table] int32 gives each sequence's pages in order (entries past
  * its length are not read); kv_len [n_seq] int32 its cells, the new tokens among them; cu_q
@@ -685,12 +693,13 @@ qsa_status qsa_mask_sparse_eligible(int has_mask, float max_bias, float softcap,
  */
 typedef struct {
     void *K, *V;
-    uint8_t *K_exp, *V_exp; /* QSA_E4M3 only, else NULL */
+    uint8_t *K_exp, *V_exp; /* QSA_E4M3 and QSA_E2M1 only, else NULL */
     qsa_dtype dtype;
     int H_kv, d;
     int64_t ld_k, ld_v; /* elements between rows */
     int64_t n_pages;
     int page_size;
+    uint8_t *K_scale, *V_scale; /* QSA_E2M1 only; not looked at for other types */
 } qsa_paged_cache;
 
 /*
@@ -702,6 +711,10 @@ typedef struct {
  * clamped to [-100, 100], and the codes nearest to x * 2^-e (ties to even; clamped to 448 when
  * e = 100; infinities and NaN become NaN).  A power of two scales exactly, so each value is
  * rounded once, to 4 significant bits (3 below 2^-6 * 2^e and fewer from there).
+ * A QSA_E2M1 row gets the least exponent e with max|x| <= 6 * 448 * 2^e over its finite values,
+ * clamped to [-100, 100]; each 16 values get the e4m3 scale s nearest to max|x| * 2^-e / 6 (at most
+ * 448), and the codes nearest to x * 2^-e / s, ties to the even code, clamped to 6 (all zero where s
+ * is); 16 values with an infinity or NaN among them get a NaN scale, and are NaN.
  * A token whose position is negative or whose page is not in the pool is skipped.  Two tokens
  * of one call never share a cell unless the table names a page twice; then the cell holds
  * either one's row, or a mixture.
@@ -780,6 +793,71 @@ qsa_status qsa_paged_attn(const qsa_paged_cache *cache, const int32_t *table, in
 
 size_t qsa_paged_attn_workspace_size(int64_t n_tok, int64_t n_seq, int64_t max_q, int H_q, int H_kv,
                                      int d);
+
+/*
+ * qsa_paged_append -- qsa_paged_write with the position rotation on the way: one pass over the new
+ * tokens' queries, keys and values as the projections left them.
+ *
+ * The first `rot` values of each head of q and k are rotated by the token's position p: values i and
+ * i + rot / 2 (i < rot / 2), (a, b) -> (a cos t - b sin t, b cos t + a sin t), t = p * base^(-2i / rot)
+ * (the pairing and frequencies of qsa_pool_update); the others stay.  p is the token's place in its
+ * sequence (kv_len - n + i for token i of n), or pos[token] where pos is not NULL.  Angles are right
+ * to 2^-23 of a radian (beyond position 2^28, to p * 2^-51); the arithmetic is fp32.  The rotated
+ * keys, and the values, are stored as qsa_paged_write stores them (fp32 results, rounded once).
+ *
+ *   q       [n_tok][H_q][d] of type src_dtype, ld_q elements between tokens, or NULL (no queries)
+ *   q_out   [n_tok][H_q][d] packed, of type src_dtype: the rotated queries (with packed q, q itself may
+ *           be it); may not overlap k or v
+ *   k, v    as for qsa_paged_write
+ *   k_out   [n_tok][H_kv][d] packed, of type src_dtype: the rotated keys (for qsa_prompt_attn on the
+ *           same tokens), or NULL; with packed k, k itself may be it
+ *   pos     [n_tok] int32 device, or NULL
+ *   rot     0 (no rotation) to d, a multiple of 16;  base >= 1
+ * A token that is skipped by qsa_paged_write (its cell is not there) still has q_out and k_out
+ * written; tokens from cu_q[n_seq] on have not.
+ * Errors: those of qsa_paged_write; INVALID_ARG for rot < 0, > d or not a multiple of 16, a base that
+ * is not finite or below 1, q without q_out, H_q < 1 with q, ld_q < H_q*d, a misaligned pointer (q,
+ * q_out, k_out 16 bytes, pos 4); UNSUPPORTED for H_q * d above 2^24.
+ */
+qsa_status qsa_paged_append(const qsa_paged_cache *cache, const int32_t *table, int64_t ld_table,
+                            int64_t n_seq, const int32_t *cu_q, const int32_t *kv_len,
+                            const void *q, const void *k, const void *v, qsa_dtype src_dtype,
+                            int64_t n_tok, int H_q, int64_t ld_q, int64_t ld_k, int64_t ld_v,
+                            const int32_t *pos, int rot, double base, void *q_out, void *k_out,
+                            qsa_stream_t stream);
+
+/*
+ * qsa_paged_sparse_attn -- attention of new tokens over the blocks that their scores selected, read
+ * in place from a paged cache: the last step of the sparse path for a batch of sequences (one token,
+ * a few drafts, or a prefill chunk each).
+ *
+ * Token i of sequence s at position p attends over the cells of its listed blocks (blocks[i][0 ..
+ * min(counts[i], k_blk)), as qsa_topk_blocks writes them; block b is cells 4b .. 4b + 3) and its open
+ * block's, 4 * floor((p + 1) / 4) .. p:
+ *   out[i][h][:] = sum_j softmax_j(scale * q[i][h] . K[j][g]) V[j][g][:]
+ *   lse_out[i][h] = log(sum_j exp(scale * q[i][h] . K[j][g]))   (natural log; optional)
+ * A listed block that is negative or not complete at p (4b + 3 > p) has no cells; one that is listed
+ * twice counts twice.  A token that sees no cell gives out = 0, lse = -inf.  A sequence longer than
+ * its table row gives out = NaN and lse = NaN, and so does a token that sees a cell on a page outside
+ * the pool.  Tokens from cu_q[n_seq] on are left as they were.
+ *
+ *   blocks   [n_tok][k_blk] int32, counts [n_tok] int32 (device; a negative count is none)
+ *   q        [n_tok][H_q][d] of type q_dtype (QSA_F32 or QSA_BF16), ld_q elements between tokens
+ *   out      [n_tok][H_q][d] packed, of type q_dtype;  lse_out [n_tok][H_q] fp32 or NULL
+ * No workspace: a token's parts are joined inside a thread-block cluster.  Sums, softmax statistics and
+ * outputs are held in fp32.  With d = 128, up to 32 heads per KV head and a QSA_BF16, QSA_E4M3 or
+ * QSA_E2M1 pool the products run on the tensor cores with the terms that qsa_paged_attn documents for
+ * a few tokens (QSA_BF16 queries: weights of 8 bits on a QSA_BF16 pool, 11 on the others; QSA_F32
+ * queries: three bf16 terms, two fp16 terms).  Other shapes take fp32 arithmetic on the CUDA cores.
+ * Errors: those of qsa_paged_attn; INVALID_ARG for k_blk < 0, null counts, or null blocks with
+ * k_blk > 0; UNSUPPORTED for k_blk above 2^28 or n_tok * H_kv * 8 beyond 2^31 - 1.
+ */
+qsa_status qsa_paged_sparse_attn(const qsa_paged_cache *cache, const int32_t *table, int64_t ld_table,
+                                 int64_t n_seq, const int32_t *cu_q, const int32_t *kv_len,
+                                 const int32_t *blocks, const int32_t *counts, int64_t k_blk,
+                                 const void *q, qsa_dtype q_dtype, int64_t n_tok, int64_t ld_q,
+                                 int H_q, float scale, void *out, float *lse_out,
+                                 qsa_stream_t stream);
 
 /*
  * qsa_prompt_attn -- attention of whole prompts, packed one after another: every token over the
