@@ -1,5 +1,6 @@
 // capi_dense.cu -- the extern "C" entry points of the paged cache, the dense attention and the
 // draft verification: argument validation on the host, then one launcher call per operation.
+#include <algorithm>
 #include <cmath>
 
 #include "dense.cuh"
@@ -90,6 +91,11 @@ qsa_status run_attn(const DenseArgs &a, int64_t max_q, void *workspace, size_t w
             return QSA_ERR_INVALID_ARG;
         return launch_dense_few(a, max_q, workspace, st);
     }
+    if (few_four_ok(a, max_q)) {
+        if (!workspace || !aligned(workspace, 256) || workspace_bytes < few_four_workspace())
+            return QSA_ERR_INVALID_ARG;
+        return from_cuda(launch_few_four(a, max_q, workspace, st));
+    }
     if (dense_decode_ok(a, max_q)) {
         if (!workspace || !aligned(workspace, 256) || workspace_bytes < dense_decode_workspace())
             return QSA_ERR_INVALID_ARG;
@@ -107,8 +113,7 @@ qsa_status run_attn(const DenseArgs &a, int64_t max_q, void *workspace, size_t w
 size_t attn_workspace(int64_t n_tok, int64_t n_seq, int H_q, int H_kv, int d)
 {
     if (n_tok <= 0 || n_seq <= 0 || H_q < 1 || H_kv < 1 || d < 1) return 0;
-    const size_t x = dense_decode_workspace(), y = dense_tc_workspace(), z = dense_few_workspace();
-    return x > y ? (x > z ? x : z) : (y > z ? y : z);
+    return std::max({dense_decode_workspace(), dense_tc_workspace(), dense_few_workspace(), few_four_workspace()});
 }
 
 }  // namespace

@@ -489,6 +489,12 @@ bool dense_few_ok(const DenseArgs &a, int64_t max_q);
 size_t dense_few_workspace();
 qsa_status launch_dense_few(const DenseArgs &a, int64_t max_q, void *workspace, cudaStream_t st);
 
+// A few new tokens per sequence over a 4-bit cache, d 128: up to 64 rows (tokens x heads of a KV head) of bf16
+// queries, any number of fp32 queries.
+bool few_four_ok(const DenseArgs &a, int64_t max_q);
+size_t few_four_workspace();
+cudaError_t launch_few_four(const DenseArgs &a, int64_t max_q, void *workspace, cudaStream_t st);
+
 // Many query rows on the tensor cores: bf16 queries, d 128.
 bool dense_tc_ok(const DenseArgs &a);
 size_t dense_tc_workspace();
