@@ -15,8 +15,10 @@
 // take 0.5 of these instructions a cycle and SM; the conversion of a 4-bit fragment's two registers, two
 // conversions and two multiplications, runs beside it.)  Weights pass from the accumulators of S' to the B fragments
 // of the second product by a transposing move of 8 x 8 registers halves.
-// A CTA of four warps; each warp runs a ring of stages of its own (cp.async) over its own 16 (bf16) or 32 (codes)
-// cells of every tile, and meets the others only at the end of a part.
+// A CTA of four warps; each warp runs a ring of stages of its own (cp.async) over 16 (bf16) or 32 (codes) cells of
+// every tile and meets the others only at the end of a part.  The warps take one, two or four KV heads of the same
+// cells (`hpc` heads of a CTA), so that the heads of a row are read together: L2 fetches more than a head's 64
+// bytes of 4-bit codes, and with the heads in different CTAs 306 MB of cells took 510 MB of reads.
 //   rows of codes and values lie swizzled in shared memory, and the cells of a fragment are numbered, such that
 //   both the reads along a cell (keys) and across four cells (values) touch every bank once.
 #pragma once
@@ -55,26 +57,32 @@ constexpr float kFar = 50.0f;
 // Stages of a warp's ring and CTAs per SM.
 template <int C, int NB, int NT>
 struct Plan {
-    static constexpr int kCtas = NB == 4 ? 2 : (NB * NT == 1 && C == QSA_E2M1 ? 4 : 3);
-    static constexpr int kStages = C == QSA_E2M1 ? (kCtas == 4 ? 2 : 3) : 2;
+    static constexpr int kCtas = NB == 4 || NB * NT == 4 ? 2 : 3;
+    static constexpr int kStages = C == QSA_E2M1 ? 3 : 2;
 };
 
+// Of one head.
 template <int NB, int NT>
 __host__ __device__ constexpr size_t q_bytes() { return (size_t)NT * NB * 4 * 32 * 16; }
 template <int NB>
 __host__ __device__ constexpr size_t fin_bytes() { return (size_t)8 * NB * (kPitch + 2) * 4; }
 template <int C, int NB, int NT, bool LIST>
-__host__ __device__ constexpr size_t few_cells_smem()
+__host__ __device__ constexpr size_t few_cells_smem(int hpc)
 {
     constexpr int S = kWarps * Plan<C, NB, NT>::kStages;
-    return (size_t)S * Cell<C>::kStage + q_bytes<NB, NT>() + (Cell<C>::kF16 ? (size_t)S * 32 * 16 : 0) +
-           (LIST ? fin_bytes<NB>() : 0);
+    return (size_t)S * Cell<C>::kStage + (Cell<C>::kF16 ? (size_t)S * 32 * 16 : 0) +
+           hpc * (q_bytes<NB, NT>() + (LIST ? fin_bytes<NB>() : 0));
 }
 
 // `bytes` (0, 8, 16) of 16 from global memory, zeros behind.
+// (a head's 4-bit row is 64 bytes: L2 fetches no more, as the other heads' bytes would go again unused)
+template <int C>
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes)
 {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    if constexpr (C == QSA_E2M1)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    else
+        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -146,6 +154,8 @@ __device__ __forceinline__ int frag_cell(int f)
 {
     return C == QSA_E2M1 ? (f & 4) | ((0x2130 >> (4 * (f & 3))) & 3) : f;
 }
+constexpr float kUnset = -3.0e38f;  // a reference before the first cell: any finite logit moves it
+
 // The first of the dims (and the step to the second) that rows g8 and g8 + 8 of the fragment of dims number t hold.
 template <int C>
 __device__ __forceinline__ int frag_dim(int t, int g8, int half)
@@ -153,41 +163,138 @@ __device__ __forceinline__ int frag_dim(int t, int g8, int half)
     return C == QSA_BF16 ? 16 * t + 8 * half + g8 : 16 * g8 + 2 * t + half;
 }
 
+// ------------------------------------------------------------------ shares of the work
+// As dense.cuh's flattened list, made short: every row tile of a sequence counts the tiles of its whole context (the
+// earlier ones of a few tokens see hardly less; turns behind what they see read nothing), so that a share is found
+// with shifts and a few 32-bit divisions.  (The exact list took 11,000 to 24,000 cycles at 64 sequences, most of
+// them fetching code that runs once.)
+struct Item {
+    int32_t s, g, t;     // sequence, group of heads, row tile
+    int32_t tiles;
+    int32_t len, cells;  // of the sequence
+    int32_t nt;          // its row tiles
+    int64_t t0;          // its first token
+    int64_t start;       // the item's first place in the list
+    int64_t index;       // its number
+};
+
+// A sequence's tokens, cells, tiles of an item and row tiles.
+__device__ __forceinline__ void look_at(const SeqView &sv, const WorkShape &w, int kt_log2, Item &it)
+{
+    seq_tokens(sv, it.s, it.t0, it.len);
+    it.cells = seq_cells(sv, it.s, it.len);
+    it.nt = it.len <= w.rt ? (it.len > 0) : (int)((uint32_t)(it.len + w.rt - 1) / (uint32_t)w.rt);
+    it.tiles = it.cells > 0 && it.cells <= w.most ? ((it.cells - 1) >> kt_log2) + 1 : 1;
+}
+
+// The share of CTA `cta` of `ctas`: places [x0, x1) and the item at x0; false when there is none.  One warp calls it.
+__device__ __forceinline__ bool share_of(const SeqView &sv, const WorkShape &w, int kt_log2, int cta, int ctas, int64_t &per,
+                                         int64_t &x0, int64_t &x1, Item &it)
+{
+    const int lane = threadIdx.x & 31;
+    int64_t total = 0;
+#pragma unroll 1
+    for (int s = lane; s < sv.n_seq; s += 32) {
+        Item i;
+        i.s = s;
+        look_at(sv, w, kt_log2, i);
+        total += (int64_t)i.tiles * ((int64_t)i.nt * w.H_kv);
+    }
+    total = warp_sum_i64(total);
+    per = div_pos(total + ctas - 1, ctas);
+    x0 = cta * per;
+    x1 = x0 + per < total ? x0 + per : total;
+    if (x0 >= x1) return false;
+    int64_t base = 0, before = 0;  // places and items of the sequences so far
+#pragma unroll 1
+    for (int s0 = 0;; s0 += 32) {
+        it.s = s0 + lane;
+        it.nt = it.tiles = 0;
+        if (it.s < sv.n_seq) look_at(sv, w, kt_log2, it);
+        const int64_t items = (int64_t)it.nt * w.H_kv, mine = items * it.tiles;
+        int64_t upto = mine, items_upto = items;
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, upto, o), u = __shfl_up_sync(0xffffffffu, items_upto, o);
+            if (lane >= o) {
+                upto += v;
+                items_upto += u;
+            }
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, x0 < base + upto);
+        if (hit) {
+            // the first lane whose sum passes x0 has it
+            const int j = __ffs(hit) - 1;
+            const int64_t first = base + upto - mine, n = div_pos(lane == j ? x0 - first : 0, max(it.tiles, 1));
+            it.g = (int)div_pos(n, max(it.nt, 1));
+            it.t = (int)(n - (int64_t)it.g * it.nt);
+            it.start = first + n * it.tiles;
+            it.index = before + items_upto - items + n;
+            uint32_t *const words = reinterpret_cast<uint32_t *>(&it);
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(Item) / 4; ++i) words[i] = __shfl_sync(0xffffffffu, words[i], j);
+            return true;
+        }
+        base += __shfl_sync(0xffffffffu, upto, 31);
+        before += __shfl_sync(0xffffffffu, items_upto, 31);
+    }
+}
+
+// The item after `it`; false past the end.  Any thread, by itself.
+__device__ __forceinline__ bool item_after(const SeqView &sv, const WorkShape &w, int kt_log2, Item &it)
+{
+    it.start += it.tiles;
+    ++it.index;
+    if (++it.t < it.nt) return true;
+    it.t = 0;
+    if (++it.g < w.H_kv) return true;
+    it.g = 0;
+    do {
+        if (++it.s >= sv.n_seq) return false;
+        look_at(sv, w, kt_log2, it);
+    } while (it.nt == 0);
+    return true;
+}
+
 // ------------------------------------------------------------------ the kernel
-// NB: blocks of eight rows.  NT: 16-bit terms of a query and a weight.  LIST: a cluster takes one token and KV head,
-// its CTAs equal shares of the token's listed cells; else shares of the flattened list (dense.cuh).
+// NB: blocks of eight rows.  NT: 16-bit terms of a query and a weight.  LIST: a cluster takes one token and hpc KV
+// heads, its CTAs equal shares of the token's listed cells; else shares of the flattened list (dense.cuh), in which
+// hpc heads are one.  Warp w: head w mod hpc, cells w / hpc of a tile's 4 / hpc parts.
 template <int C, typename TQ, int NB, int NT, bool LIST>
 __global__ void __launch_bounds__(kThreads, (Plan<C, NB, NT>::kCtas))
 few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const ListView lv, const TQ *__restrict__ q,
                  int64_t ld_q, int H_q, float scale_log2, float q_sign, TQ *__restrict__ out, float *__restrict__ lse,
-                 float *__restrict__ partial, Split *__restrict__ splits, int by_item)
+                 float *__restrict__ partial, Split *__restrict__ splits, int by_item, int hpc_log2, int kt_log2)
 {
     using S = Cell<C>;
     constexpr int kRows = 8 * NB, kStages = Plan<C, NB, NT>::kStages, kKeys = S::kKeys, kGroups = S::kGroups;
     constexpr bool F16 = S::kF16;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int bad_s, odd_s;
-    __shared__ float red_m[kWarps][kRows], red_l[kWarps][kRows], top_s[kWarps];
+    __shared__ float red_m[kWarps][kRows], red_l[kWarps][kRows];
+    __shared__ uint32_t top_s[kWarps];
     __shared__ uint32_t there_s[kWarps][kStages];  // LIST: cells of a stage that are there
+    __shared__ Item item_s;
+    __shared__ int64_t share_s[3];  // a share's places: of each CTA, the first, behind the last
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g8 = lane >> 2, c4 = lane & 3;
     unsigned char *const ring = smem + (size_t)warp * kStages * S::kStage;
-    uint4 *const qf = reinterpret_cast<uint4 *>(smem + (size_t)kWarps * kStages * S::kStage);
-    unsigned char *after_q = reinterpret_cast<unsigned char *>(qf) + q_bytes<NB, NT>();
+    const int hpc = 1 << hpc_log2, head = warp & (hpc - 1), part = warp >> hpc_log2;
     // per cell of a stage (codes): factor of the logit, exponent e of the value, 2^-e
-    float4 *const exps = reinterpret_cast<float4 *>(after_q) + warp * kStages * 32;
-    float *const fin = reinterpret_cast<float *>(after_q + (F16 ? (size_t)kWarps * kStages * 32 * 16 : 0));
+    float4 *const exps = reinterpret_cast<float4 *>(smem + (size_t)kWarps * kStages * S::kStage) + warp * kStages * 32;
+    uint4 *const q_all = reinterpret_cast<uint4 *>(smem + (size_t)kWarps * kStages * (S::kStage + (F16 ? 512 : 0)));  // by head
+    const uint4 *const qf = q_all + head * (int)(q_bytes<NB, NT>() / 16);
+    float *const fin = reinterpret_cast<float *>(q_all + hpc * (int)(q_bytes<NB, NT>() / 16));  // LIST, rows head by head
 
     pdl_wait();
     const TQ *qp = q;
     QSA_AFTER_WAIT(qp);
     pdl_trigger();
 
-    const float inv_scale = 1.0f / scale_log2;
     const int G = H_q / kv.H_kv;
-    int64_t per = 0, x = 0, x1 = 0;
-    WorkItem it = {};
+    int64_t x = 0, x1 = 0;
+    Item it;
     uint32_t rank = 0, ranks = 1;
     int n_list = 0, pos = 0, cells = 0;
     const int32_t *list = nullptr;
@@ -196,15 +303,29 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
         asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
         asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ranks));
         const unsigned item = blockIdx.x / ranks;
-        tok = item / (unsigned)kv.H_kv;
-        it.g = (int)(item % (unsigned)kv.H_kv);
+        tok = item / (unsigned)ws.H_kv;
+        it.g = (int)(item % (unsigned)ws.H_kv);
         if (!token_place(sv, tok, it.s, pos, cells)) return;  // (all CTAs of the cluster)
         n_list = (int)min((int64_t)max(lv.counts[tok], 0), lv.k_blk);
         list = lv.blocks + tok * lv.k_blk;
-        it.tiles = n_list / (ws.kt / 4) + 1;  // of 4 n_list + 4 cells
+        it.tiles = (n_list >> (kt_log2 - 2)) + 1;  // of 4 n_list + 4 cells
     } else {
         if (!by_item && tid == 0) splits[blockIdx.x].s = -1;
-        if (!work_share(sv, ws, blockIdx.x, gridDim.x, per, x, x1, it)) return;
+        if (warp == 0) {
+            int64_t per;
+            if (!share_of(sv, ws, kt_log2, blockIdx.x, gridDim.x, per, x, x1, it)) it.s = -1;
+            if (lane == 0) {
+                item_s = it;
+                share_s[0] = per;
+                share_s[1] = x;
+                share_s[2] = x1;
+            }
+        }
+        __syncthreads();
+        it = item_s;
+        if (it.s < 0) return;
+        x = share_s[1];
+        x1 = share_s[2];
     }
     for (;;) {
         int tile0, tile1, len = 1, rows = G, tok0 = 0, n_see, pos0 = 0;
@@ -217,8 +338,9 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
             item_end = it.start + it.tiles;
             tile0 = (int)(x - it.start);
             tile1 = (int)((item_end < x1 ? item_end : x1) - it.start);
-            seq_tokens(sv, it.s, t0, len);
-            cells = seq_cells(sv, it.s, len);
+            t0 = it.t0;
+            len = it.len;
+            cells = it.cells;
             tok0 = it.t * ws.rt;
             rows = min(ws.rt, len - tok0) * G;
             // the first token's position: cells behind it are not seen by every row
@@ -227,6 +349,7 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
         const bool starts = tile0 == 0, ends = tile1 == it.tiles;
         const bool fits = cells_fit(kv, cells);
         n_see = !fits ? 0 : (LIST ? 4 * n_list + 4 : item_cells(ws, len, cells, it.t));
+        const int kv_head = (it.g << hpc_log2) + head;
 
         __syncthreads();  // the previous part's shared memory is free
         if (tid == 0) bad_s = odd_s = 0;
@@ -234,7 +357,7 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
         // p_next, entry_next: this lane's cell of the next tile to issue, and its page; blk_next: the list entry of
         // its cell of the tile after that
         const int my_key = lane < kKeys ? lane : 0;
-        bool bad = false, odd = false;
+        bool bad = false, odd = false, far = false;
         int32_t p_next = -1, entry_next = -1, blk_next = -1;
         auto look_page = [&](int p) {
             p_next = p;
@@ -244,12 +367,12 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
             }
         };
         auto look_list = [&](int tile) {
-            const int i = tile * ws.kt + warp * kKeys + my_key;
+            const int i = (tile << kt_log2) + part * kKeys + my_key;
             blk_next = tile < tile1 && (i >> 2) < n_list ? list[i >> 2] : -1;
         };
         // the cell of tile `tile`, whose entry is in blk_next; then the entry of the tile after it
         auto look_up = [&](int tile) {
-            const int i = tile * ws.kt + warp * kKeys + my_key;
+            const int i = (tile << kt_log2) + part * kKeys + my_key;
             if constexpr (LIST) {
                 int p = -1;
                 if (tile < tile1 && n_see > 0) {
@@ -271,34 +394,39 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
             return (entry_next << kv.page_shift) | (p_next & ((1 << kv.page_shift) - 1));
         };
         int pend_k[kStages - 1], pend_v[kStages - 1];  // exponents on their way
+        const uint8_t *const Ke = F16 ? kv.K_exp + kv_head : nullptr, *const Ve = F16 ? kv.V_exp + kv_head : nullptr;
         auto load_exps = [&](int32_t row, int i) {
-            pend_k[i] = row >= 0 ? kv.K_exp[(int64_t)row * kv.H_kv + it.g] : kExpBias;
-            pend_v[i] = row >= 0 ? kv.V_exp[(int64_t)row * kv.H_kv + it.g] : kExpBias;
+            const uint64_t at = (uint64_t)(uint32_t)row * (uint32_t)kv.H_kv;
+            pend_k[i] = row >= 0 ? Ke[at] : kExpBias;
+            pend_v[i] = row >= 0 ? Ve[at] : kExpBias;
         };
         constexpr int kChunks = S::kRowBytes / 16, kAt = 32 / kChunks;
         const int cc = lane & (kChunks - 1), r0 = lane / kChunks;
-        const unsigned char *const Kl = static_cast<const unsigned char *>(kv.K) + (int64_t)it.g * S::kRowBytes + cc * 16;
-        const unsigned char *const Vl = static_cast<const unsigned char *>(kv.V) + (int64_t)it.g * S::kRowBytes + cc * 16;
-        const int ldk_b = (int)(C == QSA_E2M1 ? kv.ld_k / 2 : kv.ld_k * (C == QSA_BF16 ? 2 : 1));
-        const int ldv_b = (int)(C == QSA_E2M1 ? kv.ld_v / 2 : kv.ld_v * (C == QSA_BF16 ? 2 : 1));
+        const unsigned char *const Kl = static_cast<const unsigned char *>(kv.K) + (int64_t)kv_head * S::kRowBytes + cc * 16;
+        const unsigned char *const Vl = static_cast<const unsigned char *>(kv.V) + (int64_t)kv_head * S::kRowBytes + cc * 16;
+        const uint32_t ldk_b = (uint32_t)(C == QSA_E2M1 ? kv.ld_k / 2 : kv.ld_k * (C == QSA_BF16 ? 2 : 1));
+        const uint32_t ldv_b = (uint32_t)(C == QSA_E2M1 ? kv.ld_v / 2 : kv.ld_v * (C == QSA_BF16 ? 2 : 1));
+        // (rows kAt apart, a multiple of eight but for bf16's two, lie on the same places of the swizzle)
+        const uint32_t ring_u = smem_u32(ring), to_k = cell_off<C>(r0, cc);
+        // scales of two cells (neighbours in a page): K's by the lower lanes, V's by the upper
+        const int pair = lane & 15;
+        const uint32_t to_s = 2 * S::kTile + (lane < 16 ? 0 : S::kScales) + pair * 16;
+        const uint8_t *const Sl = C == QSA_E2M1 ? (lane < 16 ? kv.K_scale : kv.V_scale) + ((int64_t)kv_head << (kv.page_shift + 3)) : nullptr;
         auto issue = [&](int stage, int32_t row) {
-            const uint32_t st = smem_u32(ring + stage * S::kStage);
+            const uint32_t st = ring_u + stage * S::kStage;
 #pragma unroll
             for (int i = 0; i < kKeys / kAt; ++i) {
-                const int r = r0 + kAt * i;
-                const int32_t rr = __shfl_sync(0xffffffffu, row, r);
+                const int32_t rr = __shfl_sync(0xffffffffu, row, r0 + kAt * i);
                 const int on = rr >= 0 ? 16 : 0;
-                const int64_t at = rr >= 0 ? rr : 0;
-                cp16(st + cell_off<C>(r, cc), Kl + at * ldk_b, on);
-                cp16(st + S::kTile + cell_off<C>(r, cc), Vl + at * ldv_b, on);
+                const uint32_t at = max(rr, 0), to = st + (kAt % 8 == 0 ? to_k + kAt * i * S::kRowBytes : cell_off<C>(r0 + kAt * i, cc));
+                cp16<C>(to, Kl + (uint64_t)at * ldk_b, on);
+                cp16<C>(to + S::kTile, Vl + (uint64_t)at * ldv_b, on);
             }
             if constexpr (C == QSA_E2M1) {
-                // scales of two cells (neighbours in a page): K's by the lower lanes, V's by the upper
-                const int pair = lane & 15;
                 const int32_t ra = __shfl_sync(0xffffffffu, row, 2 * pair), rb = __shfl_sync(0xffffffffu, row, 2 * pair + 1);
-                const uint8_t *const from = lane < 16 ? kv.K_scale : kv.V_scale;
-                cp16(st + 2 * S::kTile + (lane < 16 ? 0 : S::kScales) + pair * 16,
-                     from + scale_row(kv, ra >= 0 ? ra : 0, it.g) * 8, ra >= 0 ? (rb >= 0 ? 16 : 8) : 0);
+                const uint32_t at = max(ra, 0), off = at & ((1u << kv.page_shift) - 1);
+                // scale_row's place: rows of a page head by head
+                cp16<C>(st + to_s, Sl + (uint64_t)(at - off) * (8u * (uint32_t)kv.H_kv) + 8u * off, ra >= 0 ? (rb >= 0 ? 16 : 8) : 0);
             }
         };
         if constexpr (LIST) look_list(tile0);
@@ -321,56 +449,71 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
         // kE values of each 4 kE
         float q_back = 1.0f;  // what undoes the queries' scaling
         {
-            constexpr int E = S::kE, kBlocks = kD / (4 * E);
-            float xa[32];
-            const int r = 8 * warp + g8;
-            const bool mine = warp < NB;
-            if (mine) {
-                const TQ *src = qp + (t0 + tok0 + (LIST ? 0 : r / G)) * ld_q + (int64_t)(it.g * G + (LIST ? r : r % G)) * kD + c4 * E;
+            constexpr int E = S::kE;
+            // unit u: block u mod NB of head u / NB; warp w takes units w, w + 4, ...: up to NB of them
+            constexpr int kWords = sizeof(TQ) == 2 ? 16 : 32;
+            const int units = hpc * NB;
+            uint32_t raw[NB][kWords];
+            uint32_t top = 0;  // the largest finite magnitude, by its bits
 #pragma unroll
-                for (int b = 0; b < kBlocks; ++b)
+            for (int i = 0; i < NB; ++i) {
+                const int u = warp + kWarps * i, r = 8 * (u % NB) + g8, h = ((it.g << hpc_log2) + u / NB) * G;
+                const int tk = LIST || r < G ? 0 : (int)((uint32_t)r / (uint32_t)G);
+                const uint4 *const src = reinterpret_cast<const uint4 *>(
+                    qp + (t0 + tok0 + tk) * ld_q + (int64_t)(h + r - tk * G) * kD + c4 * E);
+                constexpr int kStep = 4 * E * (int)sizeof(TQ) / 16, kOf = E * (int)sizeof(TQ) / 16;  // of 16 bytes
 #pragma unroll
-                    for (int e = 0; e < E; e += 8) {
-                        if (r < rows) {
-                            load8(src + b * 4 * E + e, xa + b * E + e);
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) xa[b * E + e + k] = 0.0f;
-                        }
-                    }
+                for (int k = 0; k < kWords / 4; ++k) {
+                    uint4 y = make_uint4(0u, 0u, 0u, 0u);
+                    if (u < units && r < rows) y = src[(k / kOf) * kStep + k % kOf];
+                    raw[i][4 * k] = y.x;
+                    raw[i][4 * k + 1] = y.y;
+                    raw[i][4 * k + 2] = y.z;
+                    raw[i][4 * k + 3] = y.w;
+                }
             }
             float mul = q_sign;
             if constexpr (F16) {
                 // fp16 holds the queries once the rows' largest magnitude is below 2^8: one power of two for all
-                float top = 0.0f;
-                if (mine) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (isfinite(xa[e])) top = fmaxf(top, fabsf(xa[e]));
-                    top = warp_max(top);
-                }
+                for (int i = 0; i < NB; ++i)
+#pragma unroll
+                    for (int k = 0; k < kWords; ++k) {
+                        const uint32_t a = (sizeof(TQ) == 2 ? raw[i][k] << 16 : raw[i][k]) & 0x7fffffffu;
+                        const uint32_t b = sizeof(TQ) == 2 ? raw[i][k] & 0x7fff0000u : 0u;
+                        top = max(top, max(a < 0x7f800000u ? a : 0u, b < 0x7f800000u ? b : 0u));
+                    }
+                top = __reduce_max_sync(0xffffffffu, top);
                 if (lane == 0) top_s[warp] = top;
                 __syncthreads();
-                top = fmaxf(fmaxf(top_s[0], top_s[1]), fmaxf(top_s[2], top_s[3]));
-                const int ex = (int)(__float_as_uint(top) >> 23) - 127;
-                const int sh = top > 0.0f ? min(max(7 - ex, -120), 100) : 0;
+                top = max(max(top_s[0], top_s[1]), max(top_s[2], top_s[3]));
+                const int sh = top > 0u ? min(max(134 - (int)(top >> 23), -120), 100) : 0;
                 q_back = two_to(-sh);
                 mul = q_sign * two_to(sh);
             }
-            if (mine) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) xa[e] *= mul;
+            for (int i = 0; i < NB; ++i) {
+                const int u = warp + kWarps * i;
+                if (u >= units) break;
+                uint4 *const to = q_all + (u / NB) * (int)(q_bytes<NB, NT>() / 16);
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int k = 0; k < 4; ++k) {  // two steps of 16 dims
+                    float xa[8];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {  // two steps of 16 dims
-                        uint4 f;
-                        f.x = pack16<F16>(xa[8 * k], xa[8 * k + 1]);
-                        f.y = pack16<F16>(xa[8 * k + 2], xa[8 * k + 3]);
-                        f.z = pack16<F16>(xa[8 * k + 4], xa[8 * k + 5]);
-                        f.w = pack16<F16>(xa[8 * k + 6], xa[8 * k + 7]);
-                        qf[((n * NB + warp) * 4 + k) * 32 + lane] = f;
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t w = sizeof(TQ) == 2 ? raw[i][(4 * k + e / 2) % kWords] : raw[i][(8 * k + e) % kWords];
+                        xa[e] = __uint_as_float(sizeof(TQ) == 4 ? w : (e & 1 ? w & 0xffff0000u : w << 16)) * mul;
                     }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        uint4 f;
+                        f.x = pack16<F16>(xa[0], xa[1]);
+                        f.y = pack16<F16>(xa[2], xa[3]);
+                        f.z = pack16<F16>(xa[4], xa[5]);
+                        f.w = pack16<F16>(xa[6], xa[7]);
+                        to[((n * NB + u % NB) * 4 + k) * 32 + lane] = f;
+                    }
+                }
             }
         }
         __syncthreads();
@@ -378,6 +521,7 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
         auto keep_exps = [&](int stage, int i) {
             const int ek = min(max(pend_k[i] - kExpBias, kExpMin), kExpMax);
             const int ev = min(max(pend_v[i] - kExpBias, kExpMin), kExpMax);
+            far |= abs(ev) > (int)kFar;
             exps[stage * 32 + lane] = make_float4(two_to(ek) * key_scale, (float)ev, two_to(-ev), 0.0f);
         };
         if constexpr (F16) {
@@ -408,10 +552,13 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
         for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                ms[n][e] = mx[n][e] = -INFINITY;
+                ms[n][e] = mx[n][e] = kUnset;
                 l[n][e] = 0.0f;
             }
         bool wide = false;
+        // where this thread's parts of a fragment lie: key rows f0 (+ 8, + 16 kg), values of cells va, vb (likewise)
+        const int f0 = frag_cell<C>(g8), va = frag_cell<C>(2 * c4), vb = frag_cell<C>(2 * c4 + 1);
+        const uint32_t at_k = cell_off<C>(f0, c4);
 
         int slot = 0;
         for (int tile = tile0; tile < tile1; ++tile) {
@@ -419,7 +566,7 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
             __syncwarp();
             unsigned char *const sk = ring + slot * S::kStage, *const sv_ = sk + S::kTile;
             const float4 *const ex = exps + slot * 32;
-            const int j0 = tile * ws.kt + warp * kKeys;
+            const int j0 = (tile << kt_log2) + part * kKeys;
             const uint32_t there = LIST ? there_s[warp][slot] : 0u;
             // ---- issue the tile kStages - 1 ahead into the stage read in the last turn
             {
@@ -463,19 +610,16 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
                     for (int n = 0; n < NB; ++n)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) s[kg][n][e] = 0.0f;
-                const int f0 = frag_cell<C>(g8);
                 if constexpr (C == QSA_E2M1) {
                     uint4 kr[kGroups][2];
-                    uint32_t sc[kGroups][2][2];  // scales of the lane's two groups of a cell, twice each
+                    __half2 sc[kGroups][2];  // scales of the lane's two groups of a cell
 #pragma unroll
                     for (int kg = 0; kg < kGroups; ++kg)
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf) {
-                            const int r = 16 * kg + 8 * hf + f0;
-                            kr[kg][hf] = *reinterpret_cast<const uint4 *>(sk + cell_off<C>(r, c4));
-                            const uint32_t h = half_of_scales(*reinterpret_cast<const uint16_t *>(sk + 2 * S::kTile + r * 8 + 2 * c4));
-                            sc[kg][hf][0] = __byte_perm(h, h, 0x1010);
-                            sc[kg][hf][1] = __byte_perm(h, h, 0x3232);
+                            kr[kg][hf] = *reinterpret_cast<const uint4 *>(sk + at_k + (16 * kg + 8 * hf) * S::kRowBytes);
+                            const uint32_t h = half_of_scales(*reinterpret_cast<const uint16_t *>(sk + 2 * S::kTile + f0 * 8 + 2 * c4 + (16 * kg + 8 * hf) * 8));
+                            sc[kg][hf] = reinterpret_cast<const __half2 &>(h);
                         }
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {  // eight dims of each lane: two steps
@@ -486,7 +630,8 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
                             for (int hf = 0; hf < 2; ++hf) {
                                 const uint4 &u = kr[kg][hf];
                                 const uint32_t w = k == 0 ? u.x : (k == 1 ? u.y : (k == 2 ? u.z : u.w));
-                                const uint32_t by = sc[kg][hf][k >> 1];
+                                const __half2 two = k < 2 ? __low2half2(sc[kg][hf]) : __high2half2(sc[kg][hf]);
+                                const uint32_t by = reinterpret_cast<const uint32_t &>(two);
                                 a[kg][0][hf] = half2_mul(half_of_codes<0>(w), by);
                                 a[kg][0][2 + hf] = half2_mul(half_of_codes<1>(w), by);
                                 a[kg][1][hf] = half2_mul(half_of_codes<2>(w), by);
@@ -513,7 +658,7 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
                         for (int kg = 0; kg < kGroups; ++kg)
 #pragma unroll
                             for (int hf = 0; hf < 2; ++hf)
-                                kr[kg][hf] = *reinterpret_cast<const uint4 *>(sk + cell_off<C>(16 * kg + 8 * hf + f0, 4 * b + c4));
+                                kr[kg][hf] = *reinterpret_cast<const uint4 *>(sk + cell_off<C>(f0, 4 * b + c4) + (16 * kg + 8 * hf) * S::kRowBytes);
 #pragma unroll
                         for (int j = 0; j < kWords; ++j) {
                             uint32_t a[kGroups][2][4];
@@ -550,25 +695,27 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
                         }
                     }
                 }
-                // ---- masked, and the references moved where they have to: of bf16 cells the raw logit is compared,
-                // of codes x = logit + e in log2 units takes its place
-                bool far = false;
+                // ---- log2 units (codes: with the exponent of the cell's values, x = logit + e), masked; d: above the
+                // reference, which moves where it has to
                 float inv_e[kGroups][2];  // 2^-e of this thread's cells
-                if constexpr (F16) {
 #pragma unroll
-                    for (int kg = 0; kg < kGroups; ++kg)
+                for (int kg = 0; kg < kGroups; ++kg)
 #pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            const float4 f = ex[16 * kg + 8 * hf + f0];
-                            inv_e[kg][hf] = f.z;
-                            far |= fabsf(f.y) > kFar;
-#pragma unroll
-                            for (int n = 0; n < NB; ++n) {
-                                s[kg][n][2 * hf] = fmaf(s[kg][n][2 * hf], f.x, f.y);
-                                s[kg][n][2 * hf + 1] = fmaf(s[kg][n][2 * hf + 1], f.x, f.y);
-                            }
+                    for (int hf = 0; hf < 2; ++hf) {
+                        float2 f = make_float2(scale_log2, 0.0f);
+                        if constexpr (F16) {
+                            const float4 e4 = ex[16 * kg + 8 * hf + f0];
+                            inv_e[kg][hf] = e4.z;
+                            f = make_float2(e4.x, e4.y);
                         }
-                }
+#pragma unroll
+                        for (int n = 0; n < NB; ++n) {
+                            float2 y = make_float2(s[kg][n][2 * hf], s[kg][n][2 * hf + 1]);
+                            y = F16 ? fma2(y, make_float2(f.x, f.x), make_float2(f.y, f.y)) : mul2(y, make_float2(f.x, f.x));
+                            s[kg][n][2 * hf] = y.x;
+                            s[kg][n][2 * hf + 1] = y.y;
+                        }
+                    }
                 if (edge) {
 #pragma unroll
                     for (int kg = 0; kg < kGroups; ++kg)
@@ -582,16 +729,26 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
                                     if (LIST ? !((there >> c) & 1u) : j0 + c > last[n][e]) s[kg][n][2 * hf + e] = -INFINITY;
                         }
                 }
+                float d[kGroups][NB][4];
                 bool move = false;
+                auto above = [&]() {
 #pragma unroll
-                for (int n = 0; n < NB; ++n)
+                    for (int n = 0; n < NB; ++n) {
+                        const float2 m2 = make_float2(-mx[n][0], -mx[n][1]);
+                        float top = -INFINITY;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        // (-inf before the first cell: any finite logit moves it)
-                        const float over = F16 ? mx[n][e] + S::kMove : (mx[n][e] + S::kMove) * inv_scale;
+                        for (int kg = 0; kg < kGroups; ++kg)
 #pragma unroll
-                        for (int kg = 0; kg < kGroups; ++kg) move |= fmaxf(s[kg][n][e], s[kg][n][2 + e]) > over;
+                            for (int hf = 0; hf < 2; ++hf) {
+                                const float2 y = add2(make_float2(s[kg][n][2 * hf], s[kg][n][2 * hf + 1]), m2);
+                                d[kg][n][2 * hf] = y.x;
+                                d[kg][n][2 * hf + 1] = y.y;
+                                top = fmaxf(top, fmaxf(y.x, y.y));
+                            }
+                        move |= top > S::kMove;
                     }
+                };
+                above();
                 if constexpr (F16) {
                     if (!wide && __any_sync(0xffffffffu, far)) {
                         wide = true;  // so far l is in units of mx
@@ -613,21 +770,21 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
 #pragma unroll
                                 for (int hf = 0; hf < 2; ++hf) {
                                     const float v = s[kg][n][2 * hf + e];
-                                    b = fmaxf(b, F16 ? v - S::kBelow : v * scale_log2);
+                                    b = fmaxf(b, v - S::kBelow);
                                     if constexpr (F16) {
                                         if (wide) a = fmaxf(a, v - ex[16 * kg + 8 * hf + f0].y);
                                     }
                                 }
 #pragma unroll
                             for (int k = 4; k < 32; k <<= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, k));
-                            const float ao = b == -INFINITY ? 1.0f : ex2_approx(mx[n][e] - b);
+                            const float ao = ex2_approx(mx[n][e] - b);
                             mx[n][e] = b;
                             float al = ao;
                             if constexpr (F16) {
                                 if (wide) {
 #pragma unroll
                                     for (int k = 4; k < 32; k <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, k));
-                                    al = a == -INFINITY ? 1.0f : ex2_approx(ms[n][e] - a);
+                                    al = ex2_approx(ms[n][e] - a);
                                     ms[n][e] = a;
                                 }
                             }
@@ -638,6 +795,7 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
                                 o[t][n][2 + e] *= ao;
                             }
                         }
+                    above();
                 }
                 // ---- weights and their product with the values, 16 cells at a time
 #pragma unroll
@@ -646,38 +804,47 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
 #pragma unroll
                     for (int n = 0; n < NB; ++n) {
                         float w[2][2];  // [cell half][row]
+                        float2 l2 = make_float2(l[n][0], l[n][1]);
 #pragma unroll
-                        for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const float ux = mx[n][e] == -INFINITY ? 0.0f : mx[n][e];
-                                const float v = s[kg][n][2 * hf + e];
-                                const float y = ex2_approx(F16 ? v - ux : fmaf(v, scale_log2, -ux));
-                                w[hf][e] = y;
-                                if constexpr (F16) {
-                                    if (!wide) l[n][e] = fmaf(y, inv_e[kg][hf], l[n][e]);
-                                    else l[n][e] += ex2_approx(v - ex[16 * kg + 8 * hf + f0].y - (ms[n][e] == -INFINITY ? 0.0f : ms[n][e]));
-                                } else {
-                                    l[n][e] += y;
-                                }
+                        for (int hf = 0; hf < 2; ++hf) {
+                            w[hf][0] = ex2_approx(d[kg][n][2 * hf]);
+                            w[hf][1] = ex2_approx(d[kg][n][2 * hf + 1]);
+                            const float2 w2 = make_float2(w[hf][0], w[hf][1]);
+                            if constexpr (F16) {
+                                if (!wide) l2 = fma2(w2, make_float2(inv_e[kg][hf], inv_e[kg][hf]), l2);
+                            } else {
+                                l2 = add2(l2, w2);
                             }
+                        }
+                        l[n][0] = l2.x;
+                        l[n][1] = l2.y;
 #pragma unroll
                         for (int t = 0; t < NT; ++t)
 #pragma unroll
                             for (int hf = 0; hf < 2; ++hf) p[n][t][hf] = transposed(pack16<F16>(w[hf][0], w[hf][1]));
                     }
+                    if constexpr (F16) {
+                        if (wide) {
+#pragma unroll
+                            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    l[n][i & 1] += ex2_approx(s[kg][n][i] - ex[16 * kg + 8 * (i >> 1) + f0].y - ms[n][i & 1]);
+                        }
+                    }
                     if constexpr (C == QSA_E2M1) {
                         // cells 2 c4, 2 c4 + 1 of the fragment (and + 8): eight bytes of their rows, the codes of two
                         // cells interleaved so that a byte holds a pair
-                        const int ra = 16 * kg + frag_cell<C>(2 * c4), rb = 16 * kg + frag_cell<C>(2 * c4 + 1);
+                        const uint32_t at_a = cell_off<C>(va, g8 >> 1) + (g8 & 1) * 8, at_b = cell_off<C>(vb, g8 >> 1) + (g8 & 1) * 8;
                         uint2 v[2][2];
                         uint32_t by[2];
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf) {
-                            v[hf][0] = *reinterpret_cast<const uint2 *>(sv_ + cell_off<C>(ra + 8 * hf, g8 >> 1) + (g8 & 1) * 8);
-                            v[hf][1] = *reinterpret_cast<const uint2 *>(sv_ + cell_off<C>(rb + 8 * hf, g8 >> 1) + (g8 & 1) * 8);
-                            const unsigned char *const sc = sk + 2 * S::kTile + S::kScales;
-                            by[hf] = half_of_scales((uint32_t)sc[(ra + 8 * hf) * 8 + g8] | (uint32_t)sc[(rb + 8 * hf) * 8 + g8] << 8);
+                            const int r = 16 * kg + 8 * hf;
+                            v[hf][0] = *reinterpret_cast<const uint2 *>(sv_ + at_a + r * S::kRowBytes);
+                            v[hf][1] = *reinterpret_cast<const uint2 *>(sv_ + at_b + r * S::kRowBytes);
+                            const unsigned char *const sc = sk + 2 * S::kTile + S::kScales + r * 8 + g8;
+                            by[hf] = half_of_scales(__byte_perm((uint32_t)sc[va * 8], (uint32_t)sc[vb * 8], 0x5540));
                         }
 #pragma unroll
                         for (int hw = 0; hw < 2; ++hw) {
@@ -707,7 +874,7 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
                         for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
                             for (int e = 0; e < 2; ++e)
-                                v[hf][e] = *reinterpret_cast<const uint4 *>(sv_ + cell_off<C>(16 * kg + 8 * hf + 2 * c4 + e, g8));
+                                v[hf][e] = *reinterpret_cast<const uint4 *>(sv_ + cell_off<C>(2 * c4 + e, g8) + (16 * kg + 8 * hf) * S::kRowBytes);
 #pragma unroll
                         for (int w = 0; w < 4; ++w) {
                             uint32_t pr[2][2];  // [half][dims 0, 1 / 2, 3]: codes of two cells side by side
@@ -760,7 +927,9 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
         for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+                if (mx[n][e] == kUnset) mx[n][e] = -INFINITY;
                 if (!F16 || !wide) ms[n][e] = mx[n][e];
+                if (ms[n][e] == kUnset) ms[n][e] = -INFINITY;
                 float sum = l[n][e];
 #pragma unroll
                 for (int k = 4; k < 32; k <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
@@ -770,9 +939,21 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
                 }
             }
         __syncthreads();  // every warp is done with its ring
+        if constexpr (!LIST) {
+            if (starts && tid == 0) {
+                // (as dense_join.cuh's note_split)
+                const bool uncut = ends;
+                if (!uncut || by_item) {
+                    const int64_t last_cta = div_pos(item_end - 1, share_s[0]);
+                    splits[by_item ? it.index : (int64_t)blockIdx.x] = {uncut ? -1 : it.s, it.g, it.t, (int32_t)blockIdx.x,
+                                                                        (int32_t)(last_cta - blockIdx.x) + 1, {0, 0, 0}};
+                }
+            }
+        }
         const bool whole = starts && ends;
         const bool nan_out = bad_s != 0 || !fits;
-        float *const rec = LIST ? nullptr : partial + (2 * (int64_t)blockIdx.x + (starts ? 1 : 0)) * partial_floats(kRows, kD);
+        const int rec_rows = kRows << hpc_log2, heads = G << hpc_log2;  // of a record: rows token by token
+        float *const rec = LIST ? nullptr : partial + (2 * (int64_t)blockIdx.x + (starts ? 1 : 0)) * partial_floats(rec_rows, kD);
         constexpr int kTurn = NB > 2 ? 2 : NB;  // blocks that are joined at a time
         float *const ob = reinterpret_cast<float *>(smem);  // [warp][row][kPitch]
         static_assert((size_t)kWarps * 8 * kTurn * kPitch * 4 <= (size_t)kWarps * kStages * S::kStage, "the warps' sums fit over the ring");
@@ -784,9 +965,10 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int r = 8 * n + 2 * c4 + e;
-                    const float m = fmaxf(fmaxf(red_m[0][r], red_m[1][r]), fmaxf(red_m[2][r], red_m[3][r]));
+                    float m = -INFINITY;
+                    for (int w = head; w < kWarps; w += hpc) m = fmaxf(m, red_m[w][r]);
                     const float u = m == -INFINITY ? 0.0f : m;
-                    const float f = mx[n][e] == -INFINITY ? 0.0f : exp2f(mx[n][e] - u);
+                    const float f = mx[n][e] == -INFINITY ? 0.0f : ex2_approx(mx[n][e] - u);
                     float *const dst = ob + (size_t)(warp * 8 * kTurn + r - 8 * n0) * kPitch;
 #pragma unroll
                     for (int t = 0; t < 8; ++t)
@@ -794,32 +976,30 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
                         for (int hf = 0; hf < 2; ++hf) dst[frag_dim<C>(t, g8, hf)] = o[t][n][2 * hf + e] * f;
                 }
             __syncthreads();
-            for (int i = tid; i < 8 * kTurn * (kD / 4); i += kThreads) {
-                const int rl = i / (kD / 4), r = 8 * n0 + rl, c = (i % (kD / 4)) * 4;
-                if (r >= rows) break;
+            for (int i = tid; i < (8 * kTurn * (kD / 4)) << hpc_log2; i += kThreads) {
+                const int rl = (i / (kD / 4)) % (8 * kTurn), h = i / (kD / 4 * 8 * kTurn), r = 8 * n0 + rl, c = (i % (kD / 4)) * 4;
+                if (r >= rows) continue;
                 float m = -INFINITY, sum = 0.0f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) m = fmaxf(m, red_m[w][r]);
+                for (int w = h; w < kWarps; w += hpc) m = fmaxf(m, red_m[w][r]);
                 const float u = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w)
-                    sum += red_m[w][r] == -INFINITY ? red_l[w][r] : red_l[w][r] * exp2f(red_m[w][r] - u);
                 float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
+                for (int w = h; w < kWarps; w += hpc) {
+                    sum += red_m[w][r] == -INFINITY ? red_l[w][r] : red_l[w][r] * ex2_approx(red_m[w][r] - u);
                     const float4 y = *reinterpret_cast<const float4 *>(&ob[(size_t)(w * 8 * kTurn + rl) * kPitch + c]);
                     v[0] += y.x; v[1] += y.y; v[2] += y.z; v[3] += y.w;
                 }
                 if (!LIST && odd_s) {
                     const int to = min(n_see - 1, ws.causal ? pos0 + r / G : cells - 1);
-                    for (int j = max(pos0 + 1, tile0 * ws.kt); j <= to && j < tile1 * ws.kt; ++j) {
+                    for (int j = max(pos0 + 1, tile0 << kt_log2); j <= to && j < tile1 << kt_log2; ++j) {
                         const int64_t row = cell_row(kv, it.s, t0, j);
-                        if (C == QSA_E2M1 && row >= 0 && scale_is_nan(kv.V_scale[scale_row(kv, row, it.g) * 8 + (c >> 4)]))
+                        if (C == QSA_E2M1 && row >= 0 &&
+                            scale_is_nan(kv.V_scale[scale_row(kv, row, (it.g << hpc_log2) + h) * 8 + (c >> 4)]))
                             v[0] = v[1] = v[2] = v[3] = NAN;
                     }
                 }
                 if (nan_out) sum = NAN;
-                const int64_t at = (t0 + tok0 + (LIST ? 0 : r / G)) * H_q + it.g * G + (LIST ? r : r % G);
+                const int q_head = h * G + (LIST ? r : r % G);  // of the record's
+                const int64_t at = (t0 + tok0 + (LIST ? 0 : r / G)) * H_q + it.g * heads + q_head;
                 if (LIST ? ranks == 1 : whole) {
                     const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
                     TQ *const dst = out + at * kD + c;
@@ -829,16 +1009,17 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
                         *reinterpret_cast<float4 *>(dst) = make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
                     if (c == 0 && lse) lse[at] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
                 } else if constexpr (LIST) {
-                    *reinterpret_cast<float4 *>(fin + r * kPitch + c) = make_float4(v[0], v[1], v[2], v[3]);
+                    *reinterpret_cast<float4 *>(fin + q_head * kPitch + c) = make_float4(v[0], v[1], v[2], v[3]);
                     if (c == 0) {
-                        fin[kRows * kPitch + r] = m;
-                        fin[kRows * kPitch + kRows + r] = sum;
+                        fin[rec_rows * kPitch + q_head] = m;
+                        fin[rec_rows * kPitch + rec_rows + q_head] = sum;
                     }
                 } else {
-                    *reinterpret_cast<float4 *>(rec + 2 * kRows + (int64_t)r * kD + c) = make_float4(v[0], v[1], v[2], v[3]);
+                    const int rr = (r / G) * heads + q_head;
+                    *reinterpret_cast<float4 *>(rec + 2 * rec_rows + (int64_t)rr * kD + c) = make_float4(v[0], v[1], v[2], v[3]);
                     if (c == 0) {
-                        rec[r] = m;
-                        rec[kRows + r] = sum;
+                        rec[rr] = m;
+                        rec[rec_rows + rr] = sum;
                     }
                 }
             }
@@ -858,13 +1039,13 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
                     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(a) : "memory");
                     return f;
                 };
-                for (int i = (int)rank * kThreads + tid; i < rows * (kD / 4); i += (int)ranks * kThreads) {
+                for (int i = (int)rank * kThreads + tid; i < heads * (kD / 4); i += (int)ranks * kThreads) {
                     const int r = i / (kD / 4), c = (i % (kD / 4)) * 4;
                     float m = -INFINITY, sum = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    for (uint32_t k = 0; k < ranks; ++k) m = fmaxf(m, load1(there(k, kRows * kPitch + r)));
+                    for (uint32_t k = 0; k < ranks; ++k) m = fmaxf(m, load1(there(k, rec_rows * kPitch + r)));
                     const float u = m == -INFINITY ? 0.0f : m;
                     for (uint32_t k = 0; k < ranks; ++k) {
-                        const float km = load1(there(k, kRows * kPitch + r)), kl = load1(there(k, kRows * kPitch + kRows + r));
+                        const float km = load1(there(k, rec_rows * kPitch + r)), kl = load1(there(k, rec_rows * kPitch + rec_rows + r));
                         const float f = km == -INFINITY ? 1.0f : exp2f(km - u);  // an unset side is zero or NaN
                         float4 y;
                         asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -874,7 +1055,7 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
                         sum += kl * f;
                         v[0] += y.x * f; v[1] += y.y * f; v[2] += y.z * f; v[3] += y.w * f;
                     }
-                    const int64_t at = tok * H_q + it.g * G + r;
+                    const int64_t at = tok * H_q + it.g * heads + r;
                     const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
                     TQ *const dst = out + at * kD + c;
                     if constexpr (sizeof(TQ) == 2)
@@ -888,10 +1069,8 @@ few_cells_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const Li
             }
             return;
         }
-        if (starts && tid == 0) note_split(splits, by_item, it, ends, div_pos(item_end - 1, per));
         x = it.start + tile1;
-        if (x >= x1) break;
-        if (!work_next(sv, ws, it)) break;
+        if (x >= x1 || !item_after(sv, ws, kt_log2, it)) break;
     }
 }
 

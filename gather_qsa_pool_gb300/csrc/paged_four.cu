@@ -5,29 +5,35 @@
 namespace qsa {
 namespace {
 
-constexpr int kMaxCtas = 4 * kTargetSMs;
+constexpr int kMaxCtas = 3 * kTargetSMs;
+
+// KV heads of a CTA, as a power of two.
+int heads_log2(int H_kv) { return H_kv % 4 == 0 ? 2 : (H_kv % 2 == 0 ? 1 : 0); }
 
 template <typename TQ, int NB, int NT>
 cudaError_t run(const DenseArgs &a, void *workspace, cudaStream_t st)
 {
     using P = few::Plan<QSA_E2M1, NB, NT>;
-    const int G = a.H_q / a.kv.H_kv;
-    const WorkShape ws = work_shape(a, 8 * NB / G, few::kWarps * few::Cell<QSA_E2M1>::kKeys, 0);
+    const int G = a.H_q / a.kv.H_kv, hl = heads_log2(a.kv.H_kv), hpc = 1 << hl;
+    DenseArgs b = a;  // as the work list and the join see it: hpc KV heads are one
+    b.kv.H_kv >>= hl;
+    static_assert(few::kWarps * few::Cell<QSA_E2M1>::kKeys == 1 << 7, "a tile of one head");
+    const WorkShape ws = work_shape(b, 8 * NB / G, (1 << 7) >> hl, 0);
     // the kernel takes a positive scale: a negative one turns the queries' signs, zero clears them
     const float scale = (a.scale == 0.0f ? 1.0f : fabsf(a.scale)) * kLog2e;
     const float q_sign = a.scale == 0.0f ? 0.0f : (a.scale < 0.0f ? -1.0f : 1.0f);
-    constexpr size_t smem = few::few_cells_smem<QSA_E2M1, NB, NT, false>();
     constexpr auto kernel = few::few_cells_kernel<QSA_E2M1, TQ, NB, NT, false>;
-    cudaError_t e = ensure_kernel_attrs<few::few_cells_kernel<QSA_E2M1, TQ, NB, NT, false>>(smem);
+    cudaError_t e = ensure_kernel_attrs<few::few_cells_kernel<QSA_E2M1, TQ, NB, NT, false>>(
+        few::few_cells_smem<QSA_E2M1, NB, NT, false>(few::kWarps));
     if (e != cudaSuccess) return e;
     const int sms = device_sm_count(), ctas = P::kCtas * (sms < kTargetSMs ? sms : kTargetSMs);
     Split *splits = static_cast<Split *>(workspace);
     float *partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + kMaxCtas * sizeof(Split));
-    e = launch(kernel, dim3((unsigned)ctas), dim3(few::kThreads), smem, st, 1, a.kv, a.sv, ws, a.list,
-               static_cast<const TQ *>(a.q), a.ld_q, a.H_q, scale, q_sign, static_cast<TQ *>(a.out), a.lse, partial, splits,
-               (int)join_by_item(a, ws.rt, ctas));
+    e = launch(kernel, dim3((unsigned)ctas), dim3(few::kThreads), few::few_cells_smem<QSA_E2M1, NB, NT, false>(hpc), st, 1, a.kv,
+               a.sv, ws, a.list, static_cast<const TQ *>(a.q), a.ld_q, a.H_q, scale, q_sign, static_cast<TQ *>(a.out),
+               a.lse, partial, splits, (int)join_by_item(b, ws.rt, ctas), hl, 7 - hl);
     if (e != cudaSuccess) return e;
-    return launch_dense_join<TQ>(splits, partial, ctas, 8 * NB, ws.rt, a, st);
+    return launch_dense_join<TQ>(splits, partial, ctas, 8 * NB * hpc, ws.rt, b, st);
 }
 
 }  // namespace
@@ -43,8 +49,8 @@ bool few_four_ok(const DenseArgs &a, int64_t max_q)
 
 size_t few_four_workspace()
 {
-    // NB 4: two CTAs per SM, 2: three, 1: four
-    return kMaxCtas * sizeof(Split) + (size_t)2 * (kMaxCtas / 2) * partial_floats(32, few::kD) * sizeof(float);
+    // 128 rows at two CTAs per SM; of fewer rows three are no more
+    return kMaxCtas * sizeof(Split) + (size_t)4 * kTargetSMs * partial_floats(128, few::kD) * sizeof(float);
 }
 
 cudaError_t launch_few_four(const DenseArgs &a, int64_t max_q, void *workspace, cudaStream_t st)

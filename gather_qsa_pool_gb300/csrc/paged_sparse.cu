@@ -10,23 +10,29 @@ template <int C, typename TQ, int NB, int NT>
 cudaError_t run(const SparseArgs &a, cudaStream_t st)
 {
     using P = few::Plan<C, NB, NT>;
-    const int kt = few::kWarps * few::Cell<C>::kKeys;
-    WorkShape ws = {1, kt, 0, a.kv.H_kv, 1, 0};
     const float scale = (a.scale == 0.0f ? 1.0f : fabsf(a.scale)) * kLog2e;
     const float q_sign = a.scale == 0.0f ? 0.0f : (a.scale < 0.0f ? -1.0f : 1.0f);
-    constexpr size_t smem = few::few_cells_smem<C, NB, NT, true>();
     constexpr auto kernel = few::few_cells_kernel<C, TQ, NB, NT, true>;
-    cudaError_t e = ensure_kernel_attrs<few::few_cells_kernel<C, TQ, NB, NT, true>>(smem);
+    // (a head's queries and results take shared memory: four heads' as far as three CTAs fit an SM)
+    constexpr int kMost = C == QSA_BF16 || NB * NT > 4 ? 0 : (NB * NT > 2 ? 1 : 2);
+    cudaError_t e = ensure_kernel_attrs<few::few_cells_kernel<C, TQ, NB, NT, true>>(few::few_cells_smem<C, NB, NT, true>(1 << kMost));
     if (e != cudaSuccess) return e;
-    // CTAs of a token and KV head: as many as fill the GPU, a tile each at most, up to the portable cluster's eight
-    const int64_t items = a.sv.n_tok * a.kv.H_kv, tiles = a.k_blk / (kt / 4) + 1;
-    int64_t parts = (int64_t)P::kCtas * device_sm_count() / items;
+    // CTAs of a token and its heads: as many as fill the GPU, a tile each at most, up to the portable cluster's
+    // eight; the heads of a row go to one CTA where that leaves enough CTAs
+    const int64_t most = (int64_t)P::kCtas * device_sm_count();
+    int hl = kMost;
+    while (hl > 0 && a.kv.H_kv % (1 << hl)) --hl;
+    while (hl > 0 && (a.sv.n_tok * a.kv.H_kv >> hl) * 8 < most) --hl;
+    const int kt = (few::kWarps >> hl) * few::Cell<C>::kKeys;
+    const WorkShape ws = {1, kt, 0, a.kv.H_kv >> hl, 1, 0};
+    const int64_t items = a.sv.n_tok * ws.H_kv, tiles = a.k_blk / (kt / 4) + 1;
+    int64_t parts = most / items;
     if (parts > tiles) parts = tiles;
     if (parts > 8) parts = 8;
     if (parts < 1) parts = 1;
-    return launch(kernel, dim3((unsigned)(items * parts)), dim3(few::kThreads), smem, st, (int)parts, a.kv, a.sv, ws,
-                  ListView{a.blocks, a.counts, a.k_blk}, static_cast<const TQ *>(a.q), a.ld_q, a.H_q, scale, q_sign,
-                  static_cast<TQ *>(a.out), a.lse, (float *)nullptr, (Split *)nullptr, 0);
+    return launch(kernel, dim3((unsigned)(items * parts)), dim3(few::kThreads), few::few_cells_smem<C, NB, NT, true>(1 << hl), st,
+                  (int)parts, a.kv, a.sv, ws, ListView{a.blocks, a.counts, a.k_blk}, static_cast<const TQ *>(a.q), a.ld_q,
+                  a.H_q, scale, q_sign, static_cast<TQ *>(a.out), a.lse, (float *)nullptr, (Split *)nullptr, 0, hl, (C == QSA_BF16 ? 6 : 7) - hl);
 }
 
 template <int C>
