@@ -43,8 +43,9 @@ __device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b)
 // Two e4m3 scales (the low 16 bits) as two fp16 values.
 __device__ __forceinline__ uint32_t half_of_scales(uint32_t s)
 {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)s, __NV_E4M3);
-    return (uint32_t)h.x | (uint32_t)h.y << 16;
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(s));
+    return r;
 }
 
 __device__ __forceinline__ float scale_value(uint8_t s)
