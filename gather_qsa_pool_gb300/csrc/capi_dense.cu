@@ -94,7 +94,7 @@ qsa_status run_attn(const DenseArgs &a, int64_t max_q, void *workspace, size_t w
     if (few_four_ok(a, max_q)) {
         if (!workspace || !aligned(workspace, 256) || workspace_bytes < few_four_workspace())
             return QSA_ERR_INVALID_ARG;
-        return launch_few_four(a, max_q, workspace, st);
+        return from_cuda(launch_few_four(a, max_q, workspace, st));
     }
     if (dense_decode_ok(a, max_q)) {
         if (!workspace || !aligned(workspace, 256) || workspace_bytes < dense_decode_workspace())

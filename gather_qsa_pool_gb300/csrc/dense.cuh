@@ -493,7 +493,7 @@ qsa_status launch_dense_few(const DenseArgs &a, int64_t max_q, void *workspace, 
 // queries, any number of fp32 queries.
 bool few_four_ok(const DenseArgs &a, int64_t max_q);
 size_t few_four_workspace();
-qsa_status launch_few_four(const DenseArgs &a, int64_t max_q, void *workspace, cudaStream_t st);
+cudaError_t launch_few_four(const DenseArgs &a, int64_t max_q, void *workspace, cudaStream_t st);
 
 // Many query rows on the tensor cores: bf16 queries, d 128.
 bool dense_tc_ok(const DenseArgs &a);

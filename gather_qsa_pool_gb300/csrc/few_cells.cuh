@@ -123,20 +123,17 @@ __device__ __forceinline__ uint32_t half_of_e4m3(uint32_t codes)
     return r;
 }
 
-// Offset of 16-byte chunk c of row r of a tile.  PAIR: 4-bit rows of two heads beside one another (chunks 0-3 and 4-7
-// of a 128-byte row), as TMA's 128-byte swizzle lays them.
-template <int C, bool PAIR = false>
+// Offset of 16-byte chunk c of row r of a tile.
+template <int C>
 __device__ __forceinline__ uint32_t cell_off(int r, int c)
 {
-    const int x = PAIR ? r & 7 : (C == QSA_E2M1 ? (r >> 1) & 3 : (C == QSA_E4M3 ? (r & 6) ^ ((r & 1) << 2) : ((r & 1) << 2) | ((r >> 1) & 3)));
-    return (uint32_t)r * (PAIR ? 128 : Cell<C>::kRowBytes) + (uint32_t)((c ^ x) << 4);
+    const int x = C == QSA_E2M1 ? (r >> 1) & 3 : (C == QSA_E4M3 ? (r & 6) ^ ((r & 1) << 2) : ((r & 1) << 2) | ((r >> 1) & 3));
+    return (uint32_t)r * Cell<C>::kRowBytes + (uint32_t)((c ^ x) << 4);
 }
-// The cell that is row f (of eight) of a fragment.  4-bit rows, two to a line of banks: 0, 3, 1, 2, 4, 7, 5, 6; pairs of
-// heads: 0, 5, 2, 7, 4, 1, 6, 3.
-template <int C, bool PAIR = false>
+// The cell that is row f (of eight) of a fragment: 4-bit rows, two to a line of banks, are taken as 0, 3, 1, 2, ...
+template <int C>
 __device__ __forceinline__ int frag_cell(int f)
 {
-    if constexpr (PAIR) return f ^ ((f & 1) << 2);
     return C == QSA_E2M1 ? (f & 4) | ((0x2130 >> (4 * (f & 3))) & 3) : f;
 }
 constexpr float kUnset = -3.0e38f;  // a reference before the first cell: any finite logit moves it
@@ -231,7 +228,7 @@ __device__ __forceinline__ float stage_queries(int tid, const TQ *from, int64_t 
 // ------------------------------------------------------------------ a warp's rows over its cells
 // NB: blocks of eight rows.  NT: 16-bit terms of a query and a weight.  Rows 8 n + 2 c4 + e (e = 0, 1) are lane
 // (g8, c4)'s, with the dims frag_dim(t, g8, 0 and 1) of each.
-template <int C, int NB, int NT, bool PAIR = false>
+template <int C, int NB, int NT>
 struct Rows {
     using S = Cell<C>;
     static constexpr bool F16 = S::kF16;
@@ -259,18 +256,18 @@ struct Rows {
         wide = false;
     }
 
-    // The cells of one stage: sk, sv: their keys and values (PAIR: chunks c0 .. c0 + 3 of the rows), ks, vs: scales (4 bits
-    // only); ex: per cell 2^ke, the exponent e of the value, 2^-e (codes only); far: some e is beyond kFar; qf: the
-    // queries' fragments; edge: hide(c, n, e) says whether row (n, e) does not see cell c.
+    // The cells of one stage: sk: K, V (codes' scales behind them); ex: per cell 2^ke, the exponent e of the value,
+    // 2^-e (codes only); far: some e is beyond kFar; qf: the queries' fragments; edge: hide(c, n, e) says whether row
+    // (n, e) does not see cell c.
     template <typename Hide>
-    __device__ __forceinline__ void tile(const unsigned char *sk, const unsigned char *sv, const unsigned char *ks, const unsigned char *vs, int c0,
-                                         const float4 *ex, const uint4 *qf, float key_scale, bool far, bool edge, Hide hide)
+    __device__ __forceinline__ void tile(const unsigned char *sk, const float4 *ex, const uint4 *qf, float key_scale, bool far, bool edge,
+                                         Hide hide)
     {
-        constexpr int kPitchB = PAIR ? 128 : S::kRowBytes;
+        const unsigned char *const sv = sk + S::kTile, *const ks = sv + S::kTile, *const vs = ks + S::kScales;
         const int lane = threadIdx.x & 31, g8 = lane >> 2, c4 = lane & 3;
         // where this thread's parts of a fragment lie: key rows f0 (+ 8, + 16 kg), values of cells va, vb (likewise)
-        const int f0 = frag_cell<C, PAIR>(g8), va = frag_cell<C, PAIR>(2 * c4), vb = frag_cell<C, PAIR>(2 * c4 + 1);
-        const uint32_t at_k = cell_off<C, PAIR>(f0, c0 + c4);
+        const int f0 = frag_cell<C>(g8), va = frag_cell<C>(2 * c4), vb = frag_cell<C>(2 * c4 + 1);
+        const uint32_t at_k = cell_off<C>(f0, c4);
         // ---- logits: fragments of 16 cells x 8 rows
         float s[kGroups][NB][4];
 #pragma unroll
@@ -286,7 +283,7 @@ struct Rows {
             for (int kg = 0; kg < kGroups; ++kg)
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-                    kr[kg][hf] = *reinterpret_cast<const uint4 *>(sk + at_k + (16 * kg + 8 * hf) * kPitchB);
+                    kr[kg][hf] = *reinterpret_cast<const uint4 *>(sk + at_k + (16 * kg + 8 * hf) * S::kRowBytes);
                     const uint32_t h = half_of_scales(*reinterpret_cast<const uint16_t *>(ks + f0 * 8 + 2 * c4 + (16 * kg + 8 * hf) * 8));
                     sc[kg][hf] = reinterpret_cast<const __half2 &>(h);
                 }
@@ -506,14 +503,14 @@ struct Rows {
             if constexpr (C == QSA_E2M1) {
                 // cells 2 c4, 2 c4 + 1 of the fragment (and + 8): eight bytes of their rows, the codes of two
                 // cells interleaved so that a byte holds a pair
-                const uint32_t at_a = cell_off<C, PAIR>(va, c0 + (g8 >> 1)) + (g8 & 1) * 8, at_b = cell_off<C, PAIR>(vb, c0 + (g8 >> 1)) + (g8 & 1) * 8;
+                const uint32_t at_a = cell_off<C>(va, g8 >> 1) + (g8 & 1) * 8, at_b = cell_off<C>(vb, g8 >> 1) + (g8 & 1) * 8;
                 uint2 v[2][2];
                 uint32_t by[2];
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
                     const int r = 16 * kg + 8 * hf;
-                    v[hf][0] = *reinterpret_cast<const uint2 *>(sv + at_a + r * kPitchB);
-                    v[hf][1] = *reinterpret_cast<const uint2 *>(sv + at_b + r * kPitchB);
+                    v[hf][0] = *reinterpret_cast<const uint2 *>(sv + at_a + r * S::kRowBytes);
+                    v[hf][1] = *reinterpret_cast<const uint2 *>(sv + at_b + r * S::kRowBytes);
                     const unsigned char *const sc = vs + r * 8 + g8;
                     by[hf] = half_of_scales(__byte_perm((uint32_t)sc[va * 8], (uint32_t)sc[vb * 8], 0x5540));
                 }

@@ -107,18 +107,23 @@ paged_sparse_kernel(const KvView kv, const SeqView sv, const ListView lv, const 
         }
         return (entry_next << kv.page_shift) | (p_next & ((1 << kv.page_shift) - 1));
     };
-    int pend_k[kStages - 1], pend_v[kStages - 1];  // exponents on their way
+    int pend_k[kStages - 1], pend_v[kStages - 1];  // exponents of the next tiles, on their way
     const uint8_t *const Ke = F16 ? kv.K_exp + kv_head : nullptr, *const Ve = F16 ? kv.V_exp + kv_head : nullptr;
     auto load_exps = [&](int32_t row, int i) {
         const uint64_t at = (uint64_t)(uint32_t)row * (uint32_t)kv.H_kv;
         pend_k[i] = row >= 0 ? Ke[at] : kExpBias;
         pend_v[i] = row >= 0 ? Ve[at] : kExpBias;
     };
-    auto keep_exps = [&](int stage, int i) {
-        const int ek = min(max(pend_k[i] - kExpBias, kExpMin), kExpMax);
-        const int ev = min(max(pend_v[i] - kExpBias, kExpMin), kExpMax);
+    auto keep_exps = [&](int stage) {  // the next tile's
+        const int ek = min(max(pend_k[0] - kExpBias, kExpMin), kExpMax);
+        const int ev = min(max(pend_v[0] - kExpBias, kExpMin), kExpMax);
         far = far || __any_sync(0xffffffffu, abs(ev) > (int)kFar);
         exps[stage * 32 + lane] = make_float4(two_to(ek), (float)ev, two_to(-ev), 0.0f);
+#pragma unroll
+        for (int i = 0; i + 1 < kStages - 1; ++i) {
+            pend_k[i] = pend_k[i + 1];
+            pend_v[i] = pend_v[i + 1];
+        }
     };
     constexpr int kChunks = S::kRowBytes / 16, kAt = 32 / kChunks;
     const int cc = lane & (kChunks - 1), r0 = lane / kChunks;
@@ -170,37 +175,28 @@ paged_sparse_kernel(const KvView kv, const SeqView sv, const ListView lv, const 
                                                               q_sign, q_all, top_s, [] { __syncthreads(); });
     __syncthreads();
     const float key_scale = scale_log2 * q_back;
-    if constexpr (F16) {
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i)
-            if (tile0 + i < tile1) keep_exps(i, i);
-    }
     Rows<C, NB, NT> w;
     w.clear();
     int slot = 0;
     for (int tile = tile0; tile < tile1; ++tile) {
         cp_wait<kStages - 2>();
+        if constexpr (F16) keep_exps(slot);
         __syncwarp();
         const uint32_t there = there_s[warp][slot];
         const int nslot = slot == 0 ? kStages - 1 : slot - 1;
-        const bool far_now = far;
         // ---- issue the tile kStages - 1 ahead into the stage read in the last turn
         note_there(nslot);
         const int32_t row = row_next();
         look_up(tile + kStages);
         if (tile + kStages - 1 < tile1) {
             issue(nslot, row);
-            if constexpr (F16) load_exps(row, 0);
+            if constexpr (F16) load_exps(row, kStages - 2);
         }
         cp_commit();
         constexpr uint32_t kAll = 0xffffffffu << (32 - kKeys);
-        const unsigned char *const sk = ring + slot * S::kStage;
         if (there << (32 - kKeys))
-            w.tile(sk, sk + S::kTile, sk + 2 * S::kTile, sk + 2 * S::kTile + S::kScales, 0, exps + slot * 32, qf, key_scale, far_now, there << (32 - kKeys) != kAll,
+            w.tile(ring + slot * S::kStage, exps + slot * 32, qf, key_scale, far, there << (32 - kKeys) != kAll,
                    [&](int c, int, int) { return !((there >> c) & 1u); });
-        if constexpr (F16) {
-            if (tile + kStages - 1 < tile1) keep_exps(nslot, 0);
-        }
         __syncwarp();
         slot = slot == kStages - 1 ? 0 : slot + 1;
     }
