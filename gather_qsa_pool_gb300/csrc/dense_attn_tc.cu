@@ -73,7 +73,8 @@ __host__ __device__ constexpr size_t tc_smem()
 }
 static_assert(tc_smem<false>() <= 227 * 1024 && tc_smem<true>() <= 227 * 1024, "shared memory of one CTA");
 
-template <bool E8>
+// E8: cells of codes; E4: of 4-bit codes.
+template <bool E8, bool E4 = false>
 __global__ void __launch_bounds__(Cfg<E8>::kThreads, 1)
 dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                 const __grid_constant__ CUtensorMap mapV, const KvView kv, const SeqView sv,
@@ -267,13 +268,22 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
                             }
                             if (lane == 0)
                                 mbar_arrive_expect_tx(&bars.raw_full[s],
-                                                      (uint32_t)__popc(go) * (uint32_t)box_rows * 128u);
+                                                      (uint32_t)__popc(go) * (uint32_t)box_rows * (E4 ? 72u : 128u));
                             ++n;
                             __syncwarp();
-                            if (row >= 0)
+                            if (E4 && row >= 0) {
+                                // codes, and behind the tile's the scales
+                                unsigned char *const to = raw_tiles + (size_t)s * kRawTile;
+                                tma_box(smem_u32(to) + (uint32_t)(lane * box_rows) * 64, map, p.it.g * (kD / 2), row,
+                                        &bars.raw_full[s]);
+                                bulk_g2s(to + kN * 64 + lane * box_rows * 8,
+                                         (half ? kv.V_scale : kv.K_scale) + scale_row(kv, row, p.it.g) * 8,
+                                         (uint32_t)box_rows * 8u, &bars.raw_full[s]);
+                            } else if (row >= 0) {
                                 tma_box(smem_u32(raw_tiles) + (uint32_t)s * kRawTile +
                                             (uint32_t)(lane * box_rows) * 128,
                                         map, p.it.g * kD, row, &bars.raw_full[s]);
+                            }
                         } else {
                             const int s = (int)(n % kStages);
                             if (n >= kStages &&
@@ -365,8 +375,16 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
                     const uint32_t n = 2 * turn + (uint32_t)team;  // raw tile `team`, stage n
                     const int st = (int)(n % kStages);
                     uint8_t *const exps = bars.exps[team][turn & 1u];
-                    exps[at] = (uint8_t)ex[0];
-                    if (at + 32 * kTeamWarps < kN) exps[at + 32 * kTeamWarps] = (uint8_t)ex[1];
+                    unsigned char *const raw = raw_tiles + (size_t)team * kRawTile;
+                    // (4 bits: as factors, behind the scales)
+                    float *const factors = reinterpret_cast<float *>(raw + kN * 72) + (turn & 1u) * kN;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int c = at + 32 * kTeamWarps * i;
+                        if (c >= kN) continue;
+                        if constexpr (E4) factors[c] = two_to(min(max((int)ex[i] - kExpBias, kExpMin), kExpMax));
+                        else exps[c] = (uint8_t)ex[i];
+                    }
                     bool here = bar_wait_warp(&bars.raw_full[team], turn & 1u, wc.limit_ns);
                     if (here && n >= kStages)
                         here = bar_wait_warp(&bars.empty[st], ((n / kStages) - 1) & 1u, wc.limit_ns);
@@ -379,8 +397,8 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
                     load_exps(t + 1);
                     const bool edge = team && p.edge(t);
                     const int e0 = edge ? max(0, p.pos0 + 1 - t * kN) : kN, e1 = p.n_see - t * kN;
-                    const bool odd = convert_tile<32 * kTeamWarps>(raw_tiles + (size_t)team * kRawTile,
-                                                                   ring + (size_t)st * kTileB, exps, at, e0, e1);
+                    const bool odd = E4 ? convert_tile4<32 * kTeamWarps>(raw, ring + (size_t)st * kTileB, factors, at, e0, e1)
+                                        : convert_tile<32 * kTeamWarps>(raw, ring + (size_t)st * kTileB, exps, at, e0, e1);
                     if (odd) *reinterpret_cast<volatile int32_t *>(&bars.odd[p.n % kSlots]) = p.n + 1;
                     // written by this warp (generic proxy), read by the tensor cores (async proxy)
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -578,8 +596,15 @@ dense_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
                             const int64_t row = cell_row(kv, p.it.s, p.t0, j);
                             if (row < 0) continue;
                             const int64_t v0 = row * kv.ld_v + (int64_t)p.it.g * kD + 64 * hf + c;
+                            if constexpr (E4) {
+                                const uint8_t *const sc = kv.V_scale + scale_row(kv, row, p.it.g) * 8 + 4 * hf + c / 16;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] += odd_value_at<E8>(kv, v0 + e);
+                                for (int e = 0; e < 32; ++e)
+                                    if (scale_is_nan(sc[e / 16])) o[e] = NAN;
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] += odd_value_at<E8>(kv, v0 + e);
+                            }
                         }
                     }
                     if (whole) {
@@ -653,7 +678,8 @@ bool dense_tc_ok(const DenseArgs &a)
     // (a TMA map's strides are multiples of 16 bytes; the softmax takes its maximum over unscaled
     // logits: a positive scale)
     const bool cells = a.kv_dtype == QSA_BF16 ||
-                       (a.kv_dtype == QSA_E4M3 && a.kv.ld_k % 16 == 0 && a.kv.ld_v % 16 == 0);
+                       (a.kv_dtype == QSA_E4M3 && a.kv.ld_k % 16 == 0 && a.kv.ld_v % 16 == 0) ||
+                       (a.kv_dtype == QSA_E2M1 && a.kv.ld_k % 32 == 0 && a.kv.ld_v % 32 == 0);
     return a.d == kD && a.q_dtype == QSA_BF16 && cells && G <= kM && a.scale > 0.0f && a.pool_rows > 0 &&
            a.pool_rows <= 0x7fffffffLL;
 }
@@ -717,7 +743,20 @@ static bool whole_items(const DenseArgs &a, int rt, int64_t items, int ctas)
                                 one_long.whole < 1.3 * one_long.cut));
 }
 
-template <bool E8>
+// 4-bit rows in boxes of one head's 64 bytes x box_rows rows, row after row.
+static bool make_map4(CUtensorMap *m, const void *base, int64_t rows, int H_kv, int64_t ld, int box_rows)
+{
+    const EncodeTiledFn fn = encode_tiled();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)H_kv * (kD / 2), (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld / 2};
+    const cuuint32_t box[2] = {kD / 2, (cuuint32_t)box_rows}, estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool E8, bool E4 = false>
 static qsa_status run_tc(const DenseArgs &a, void *workspace, cudaStream_t st)
 {
     const int G = a.H_q / a.kv.H_kv;
@@ -725,13 +764,15 @@ static qsa_status run_tc(const DenseArgs &a, void *workspace, cudaStream_t st)
     const int box_rows = a.kv.table && page < kN ? page : kN;
     CUtensorMap mq, mk, mv;
     const int64_t width = (int64_t)a.kv.H_kv * kD;
-    if (!make_query_map(&mq, a.q, a.sv.n_tok, a.H_q, a.ld_q, G) ||
-        !make_map(&mk, a.kv.K, a.pool_rows, width, a.kv.ld_k, box_rows, E8, !E8) ||
-        !make_map(&mv, a.kv.V, a.pool_rows, width, a.kv.ld_v, box_rows, E8, !E8))
+    if (!make_query_map(&mq, a.q, a.sv.n_tok, a.H_q, a.ld_q, G)) return QSA_ERR_CUDA;
+    if (E4 ? !make_map4(&mk, a.kv.K, a.pool_rows, a.kv.H_kv, a.kv.ld_k, box_rows) ||
+                 !make_map4(&mv, a.kv.V, a.pool_rows, a.kv.H_kv, a.kv.ld_v, box_rows)
+           : !make_map(&mk, a.kv.K, a.pool_rows, width, a.kv.ld_k, box_rows, E8, !E8) ||
+                 !make_map(&mv, a.kv.V, a.pool_rows, width, a.kv.ld_v, box_rows, E8, !E8))
         return QSA_ERR_CUDA;
     const WorkShape ws = work_shape(a, 2 * (kM / G), kN, kOver);
     constexpr size_t smem = tc_smem<E8>();
-    if (ensure_kernel_attrs<dense_tc_kernel<E8>>(smem) != cudaSuccess) return QSA_ERR_CUDA;
+    if (ensure_kernel_attrs<dense_tc_kernel<E8, E4>>(smem) != cudaSuccess) return QSA_ERR_CUDA;
     int ctas = device_sm_count();
     if (ctas > kMaxCtas) ctas = kMaxCtas;
     Split *splits = static_cast<Split *>(workspace);
@@ -739,7 +780,7 @@ static qsa_status run_tc(const DenseArgs &a, void *workspace, cudaStream_t st)
     const int64_t items = ((a.sv.n_tok + ws.rt - 1) / ws.rt + a.sv.n_seq) * a.kv.H_kv;
     const bool whole = whole_items<E8>(a, ws.rt, items, ctas);
     if (whole) ctas = (int)items;
-    cudaError_t e = launch(dense_tc_kernel<E8>, dim3((unsigned)ctas), dim3(Cfg<E8>::kThreads), smem, st, 1, mq,
+    cudaError_t e = launch(dense_tc_kernel<E8, E4>, dim3((unsigned)ctas), dim3(Cfg<E8>::kThreads), smem, st, 1, mq,
                            mk, mv, a.kv, a.sv, ws, box_rows, a.H_q, a.scale * kLog2e,
                            static_cast<__nv_bfloat16 *>(a.out), a.lse, partial, splits,
                            (int)join_by_item(a, ws.rt, ctas), (int)whole, current_wait_ctl());
@@ -750,6 +791,7 @@ static qsa_status run_tc(const DenseArgs &a, void *workspace, cudaStream_t st)
 
 qsa_status launch_dense_tc(const DenseArgs &a, void *workspace, cudaStream_t st)
 {
+    if (a.kv_dtype == QSA_E2M1) return run_tc<true, true>(a, workspace, st);
     return a.kv_dtype == QSA_E4M3 ? run_tc<true>(a, workspace, st) : run_tc<false>(a, workspace, st);
 }
 

@@ -7,6 +7,7 @@
 #include <cuda_fp8.h>
 
 #include "dense.cuh"
+#include "e2m1.cuh"
 #include "mma_frag.cuh"
 #include "umma.cuh"
 
@@ -269,6 +270,43 @@ __device__ __forceinline__ bool convert_tile(const unsigned char *src, unsigned 
         const uint4 hi = make_uint4(o[4], o[5], o[6], o[7]);
         *reinterpret_cast<uint4 *>(w + r * 128 + ((first ^ (r & 7)) << 4)) = c >> 2 ? hi : lo;
         *reinterpret_cast<uint4 *>(w + r * 128 + ((second ^ (r & 7)) << 4)) = c >> 2 ? lo : hi;
+    }
+    return odd;
+}
+
+// The same of 4-bit codes with their scales behind them (128 cells x 64 bytes, then x 8): a lane's 16 codes share a
+// scale; value = code * (scale * 2^e), exact (factors: 2^e of each cell).
+template <int kLanes>
+__device__ __forceinline__ bool convert_tile4(const unsigned char *src, unsigned char *dst, const float *factors, int at, int e0, int e1)
+{
+    bool odd = false;
+    const int c = at & 7;
+    unsigned char *const w = dst + (c >> 2) * kHalf;
+    const int first = 2 * (c & 3) + (c >> 2), second = first ^ 1;
+    // (unrolled once, a chunk of 1,024 tokens over 61,789 cells takes 1,429 us instead of 1,344)
+#pragma unroll 2
+    for (int r = at >> 3; r < kN; r += kLanes / 8) {
+        uint2 v = *reinterpret_cast<const uint2 *>(src + r * 64 + c * 8);
+        uint8_t sc = src[kN * 64 + r * 8 + c];
+        if (r >= e0) {
+            odd |= scale_is_nan(sc) && r < e1;
+            if (r >= e1 || scale_is_nan(sc)) {
+                v = make_uint2(0u, 0u);
+                sc = 0;
+            }
+        }
+        const float f = scale_value(sc) * factors[r];
+        const float2 f2 = make_float2(f, f);
+        uint32_t o[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t u = (k < 4) == (c < 4) ? v.x : v.y;  // the lanes of the upper dim half begin with the second chunk
+            const uint32_t h = (k & 3) == 0 ? half_of_codes<0>(u) : ((k & 3) == 1 ? half_of_codes<1>(u) : ((k & 3) == 2 ? half_of_codes<2>(u) : half_of_codes<3>(u)));
+            const float2 x = mul2(__half22float2(reinterpret_cast<const __half2 &>(h)), f2);
+            o[k] = pack_bf16(x.x, x.y);
+        }
+        *reinterpret_cast<uint4 *>(w + r * 128 + ((first ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4 *>(w + r * 128 + ((second ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
     }
     return odd;
 }
