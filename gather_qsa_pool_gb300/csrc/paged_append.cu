@@ -6,8 +6,13 @@
 // token's position p:  (a, b) -> (a cos - b sin, b cos + a sin).  The angle is formed as a fraction of a turn in 64
 // bits: with f_i = 2^64 base^(-2 i / rot) / (2 pi), rounded, p * f_i modulo 2^64 is the angle's fraction of a turn
 // with an error of p / 2 units of 2^-64, and the whole turns drop out exactly, whatever p is.  In 64-bit
-// floating point the same product and its reduction would be bound by this GPU's few fp64 units.  The fraction,
-// as a signed number of [-1/2, 1/2) turns in 24 bits, is off by at most 2^-26: 9.4e-8 of the angle's cosine and sine.
+// floating point the same product and its reduction would be bound by this GPU's few fp64 units.  The nearest quarter
+// turn is taken off, and cosine and sine of the rest (at most pi / 4) are sums of two fp32 numbers, from their power
+// series: the first terms in both, the rest, below 2^-6, in one; together right to 2^-29.
+// Keys are rotated with both numbers, and the sum of the products carried in two as well: what is then cut down to
+// few bits, a code or a bf16 number, is the exact value's but for 2^-28 of it, where an fp32 result would fall to the
+// other side of a border fifty times as often.  (The fp32 number on the way is rounded to odd: its last bit says
+// whether anything was left, so the second rounding goes by the exact value.)  Queries take the first numbers alone.
 // The quantised forms are paged_rw.cu's (8 bits) and e2m1.cuh's (4 bits).
 //
 // Shape.  A warp takes some heads of a token, eight values a lane and d / 8 lanes a head (a power of two of them);
@@ -156,12 +161,59 @@ struct AppendArgs {
     int32_t per_warp;    // units of a warp
 };
 
+// Cosine and sine of a fraction of a turn (in 2^-64), each as the sum of two numbers: c.x + c.y, s.x + s.y.
+__device__ __forceinline__ void turn_of(uint64_t frac, float2 &c, float2 &s)
+{
+    const uint32_t quarter = (uint32_t)((frac + (1ull << 61)) >> 62);
+    const int64_t rest = (int64_t)(frac - ((uint64_t)quarter << 62));  // of [-2^61, 2^61)
+    const float rh = (float)rest, rl = (float)(rest - (int64_t)rh);
+    constexpr double kStep = 6.283185307179586 / 18446744073709551616.0;  // radians
+    constexpr float ph = (float)kStep, pl = (float)(kStep - (double)ph);
+    const float xh = __fmul_rn(rh, ph), xl = fmaf(rh, ph, -xh) + fmaf(rh, pl, rl * ph);  // |x| <= pi / 4
+    const float th = __fmul_rn(xh, xh), tl = fmaf(xh, xh, -th) + 2.0f * xh * xl;          // x^2
+    // cos x = 1 - x^2 / 2 + x^4 (1 / 24 - ...)
+    const float uh = fmaf(th, -0.5f, 1.0f);
+    const float t2 = fmaf(th, th, 2.0f * th * tl);
+    float u = t2 * fmaf(th, fmaf(th, fmaf(th, -1.0f / 3628800.0f, 1.0f / 40320.0f), -1.0f / 720.0f), 1.0f / 24.0f);
+    u += fmaf(th, -0.5f, 1.0f - uh) - 0.5f * tl;
+    float2 co = make_float2(uh + u, 0.0f);
+    co.y = u - (co.x - uh);
+    // sin x = x (1 - x^2 / 6 + x^4 (1 / 120 - ...))
+    constexpr float k6h = (float)(1.0 / 6.0), k6l = (float)(1.0 / 6.0 - (double)k6h);
+    const float mh = __fmul_rn(th, k6h), ml = fmaf(th, k6h, -mh) + fmaf(th, k6l, tl * k6h), vh = __fsub_rn(1.0f, mh);
+    const float v = ((1.0f - vh) - mh) - ml +
+                    t2 * fmaf(th, fmaf(th, fmaf(th, -1.0f / 39916800.0f, 1.0f / 362880.0f), -1.0f / 5040.0f), 1.0f / 120.0f);
+    const float sh = __fmul_rn(xh, vh), sl = fmaf(xh, vh, -sh) + fmaf(xh, v, xl * vh);
+    float2 si = make_float2(sh + sl, 0.0f);
+    si.y = sl - (si.x - sh);
+    const bool swap = quarter & 1;
+    c = swap ? si : co;
+    s = swap ? co : si;
+    if (quarter == 1 || quarter == 2) c = make_float2(-c.x, -c.y);
+    if (quarter >= 2) s = make_float2(-s.x, -s.y);
+}
+
+// a (c.x + c.y) + b (s.x + s.y), rounded to fp32 (even), and to odd in `odd`.
+__device__ __forceinline__ float turned(float a, float b, float2 c, float2 s, float &odd)
+{
+    // (no product is fused into a sum unasked: what each rounding leaves is counted)
+    const float p = __fmul_rn(a, c.x), q = __fmul_rn(b, s.x), h = __fadd_rn(p, q), z = __fsub_rn(h, p);
+    const float e = (p - (h - z)) + (q - z);  // p + q = h + e
+    const float l = e + (fmaf(a, c.x, -p) + fmaf(b, s.x, -q)) + fmaf(a, c.y, b * s.y);
+    const float y = h + l, rest = l - (y - h);
+    odd = y;
+    if (!isfinite(y)) return odd = h;  // (an infinity times a rest is none)
+    const uint32_t bits = __float_as_uint(y);
+    if (rest != 0.0f && !(bits & 1u)) odd = __uint_as_float((rest > 0.0f) == (y > 0.0f) ? bits + 1u : bits - 1u);
+    return y;
+}
+
 // A unit: the heads of a step (32 lanes) of q, or of both k and v.
 template <typename TS, int DT>
 __global__ void __launch_bounds__(32 * kWarps, 6)
 paged_append_kernel(const AppendArgs a, const __grid_constant__ Turns turns, const SeqView sv, const KvView kv)
 {
-    __shared__ float2 cs_s[kWarps][128];
+    __shared__ float4 cs_s[kWarps][128];  // cosine, sine, and what they leave
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -192,20 +244,20 @@ paged_append_kernel(const AppendArgs a, const __grid_constant__ Turns turns, con
     const int hr = a.rot >> 4;  // lanes of half the rotated values
     const bool turn = c < 2 * hr;
     const int other = c < hr ? lane + hr : (turn ? lane - hr : lane);
+    const int first = turn ? 8 * (c < hr ? c : c - hr) : 0;  // of its angles
+    float4 *const cs = cs_s[warp];
     float co[8], si[8];
     if (hr > 0) {
         const int64_t p = a.pos ? (int64_t)a.pos[tok] : place;
-        float2 *const cs = cs_s[warp];
         for (int i = lane; i < 8 * hr; i += 32) {
-            const float x = (float)(int64_t)((uint64_t)p * turns.f[i]) * 1.0842021724855044e-19f;  // 2^-63: half turns
-            float2 t;
-            sincospif(x, &t.y, &t.x);
-            cs[i] = t;
+            float2 c2, s2;
+            turn_of((uint64_t)p * turns.f[i], c2, s2);
+            cs[i] = make_float4(c2.x, s2.x, c2.y, s2.y);
         }
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float2 t = cs[turn ? 8 * (c < hr ? c : c - hr) + i : 0];
+            const float4 t = cs[first + i];
             co[i] = t.x;
             si[i] = c < hr ? -t.y : t.y;
         }
@@ -254,15 +306,32 @@ paged_append_kernel(const AppendArgs a, const __grid_constant__ Turns turns, con
             for (int i = 0; i < (int)sizeof(x[0].w) / 4; ++i) x[0].w[i] = x[1].w[i] = 0u;
         }
         float y[8], z[8];
-        if (hr > 0) {
-            rotated(x[0], y);
-        } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = x[0].at(i);
+        for (int i = 0; i < 8; ++i) {
+            y[i] = x[0].at(i);
+            z[i] = x[1].at(i);
         }
+        if (hr > 0) {
+            Eight<TS> pw;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = x[1].at(i);
-        if (k_out && mine) store8(k_out + (tok * H + h) * d + 8 * c, y);
+            for (int i = 0; i < (int)sizeof(x[0].w) / 4; ++i) pw.w[i] = __shfl_sync(0xffffffffu, x[0].w[i], other);
+            float even[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float4 t = cs[first + i];
+                even[i] = y[i];
+                if (turn)
+                    even[i] = turned(y[i], pw.at(i), make_float2(t.x, t.z), c < hr ? make_float2(-t.y, -t.w) : make_float2(t.y, t.w), y[i]);
+            }
+            // (fp32 results are the nearest; what is rounded again goes on from the odd ones)
+            if (k_out && mine) store8(k_out + (tok * H + h) * d + 8 * c, sizeof(TS) == 4 ? even : y);
+            if constexpr (DT == QSA_F32) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = even[i];
+            }
+        } else if (k_out && mine) {
+            store8(k_out + (tok * H + h) * d + 8 * c, y);
+        }
         store_cell<DT>(kv, false, row, h, c, lanes, d, mine && row >= 0, y);
         store_cell<DT>(kv, true, row, h, c, lanes, d, mine && row >= 0, z);
     }

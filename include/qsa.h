@@ -802,8 +802,9 @@ size_t qsa_paged_attn_workspace_size(int64_t n_tok, int64_t n_seq, int64_t max_q
  * i + rot / 2 (i < rot / 2), (a, b) -> (a cos t - b sin t, b cos t + a sin t), t = p * base^(-2i / rot)
  * (the pairing and frequencies of qsa_pool_update); the others stay.  p is the token's place in its
  * sequence (kv_len - n + i for token i of n), or pos[token] where pos is not NULL.  Angles are right
- * to 2^-23 of a radian (beyond position 2^28, to p * 2^-51); the arithmetic is fp32.  The rotated
- * keys, and the values, are stored as qsa_paged_write stores them (fp32 results, rounded once).
+ * to p * 2^-51 radians.  Queries are rotated in fp32 and rounded once more to their type; keys are
+ * rotated to 2^-28 of the pair's magnitudes, and what qsa_paged_write makes of a value is made of that
+ * (rounded once, whatever the cache's type).  Values are stored as qsa_paged_write stores them.
  *
  *   q       [n_tok][H_q][d] of type src_dtype, ld_q elements between tokens, or NULL (no queries)
  *   q_out   [n_tok][H_q][d] packed, of type src_dtype: the rotated queries (with packed q, q itself may
