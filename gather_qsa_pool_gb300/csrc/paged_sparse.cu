@@ -17,8 +17,8 @@ constexpr int kThreads = 32 * kWarps;
 // Stages of a warp's ring and CTAs per SM.
 template <int C, int NB, int NT>
 struct Plan {
-    static constexpr int kCtas = NB == 4 || NB * NT == 4 ? 2 : 3;
-    static constexpr int kStages = C == QSA_E2M1 ? 3 : 2;
+    static constexpr int kCtas = NB == 4 || NB * NT == 4 ? 2 : C == QSA_E2M1 && NB * NT == 1 ? 4 : 3;
+    static constexpr int kStages = C == QSA_E2M1 && NB * NT > 1 ? 3 : 2;
 };
 
 template <int NB>
