@@ -605,7 +605,10 @@ bool few_four_ok(const DenseArgs &a, int64_t max_q)
     const int G = a.H_q / a.kv.H_kv;
     if (a.kv_dtype != QSA_E2M1 || a.d != few::kD || !a.kv.table || a.kv.ld_k % 32 || a.kv.ld_v % 32) return false;
     if (a.kv.ld_k > (1 << 28) || a.kv.ld_v > (1 << 28)) return false;  // strides in 32 bits
-    // fp32 queries come here however many tokens they are; bf16 queries of more rows are the tcgen05 kernel's
+    // fp32 queries come here however many tokens they are; bf16 queries of more than 64 rows (tokens x heads of a KV
+    // head) are the tcgen05 kernel's.  Here / there, us, groups of 8: 48 sequences of up to 16,384 cells with 4 tokens
+    // 158 / 281, 8 tokens 260 / 286, 12 tokens 361 / 287; one of 61,789 with 4 tokens 50 / 68, 8 tokens 68 / 68, 16 tokens
+    // 104 / 70; one of 4,000 32 / 37, 36 / 36, 48 / 38.  Groups of 4 cross at the same rows.
     return G <= (a.q_dtype == QSA_F32 ? 16 : 32) && (a.q_dtype == QSA_F32 || max_q * G <= 64);
 }
 
