@@ -1,5 +1,6 @@
 // dense.cuh -- shared pieces of the paged key/value cache and of the dense attention over it
-// (paged_rw.cu, dense_attn.cu, dense_decode.cu, dense_few_tc.cu, dense_attn_tc.cu): the device view of a cache,
+// (paged_rw.cu, paged_append.cu, paged_four.cu, paged_sparse.cu, dense_attn.cu, dense_decode.cu, dense_few_tc.cu,
+// dense_attn_tc.cu): the device view of a cache,
 // the row of a cell, the packed sequences and the flattened list of work.
 #pragma once
 
@@ -9,7 +10,7 @@
 
 namespace qsa {
 
-// Exponents of a QSA_E4M3 row: value = code * 2^(byte - 127), byte in [27, 227].
+// Exponents of a QSA_E4M3 or QSA_E2M1 row: value = code * 2^(byte - 127), byte in [27, 227].
 constexpr int kExpBias = 127;
 constexpr int kExpMin = -100, kExpMax = 100;
 

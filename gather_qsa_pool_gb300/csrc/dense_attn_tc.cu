@@ -13,8 +13,8 @@
 // warps, the chain logits -> maximum -> exponentials -> weights left the tensor cores idle for
 // half the time).  Warp 16 issues the MMAs; warp 17 stages queries, K and V tiles by TMA (one box
 // per page, 128-byte swizzle), K and V into a ring of 32 KB stages; warps 18 and 19 see to the
-// tiles where some row does not see some cell (e4m3 cells: six warps that also turn codes into
-// bf16).
+// tiles where some row does not see some cell (e4m3 and e2m1 cells: six warps that also turn codes
+// into bf16).
 //   tensor memory (512 columns): S of group A, S of group B (128 fp32 columns each; a row's
 //   weights P overwrite its own S as bf16, each thread's 64 over its own logits), O of A and of B
 //   (128 each).

@@ -771,16 +771,17 @@ qsa_status qsa_paged_read(const qsa_paged_cache *cache, const int32_t *table, in
  *   workspace  qsa_paged_attn_workspace_size() bytes, 256-byte aligned, for the parts of rows
  *            whose cells are shared out; its contents do not matter, and calls that may run at
  *            the same time need one each
- * All sums, the softmax statistics and the output are held in fp32.  With d = 128 and a QSA_BF16
- * or QSA_E4M3 pool the products run on the tensor cores: QSA_BF16 queries with the softmax weights
- * rounded to 8 significant bits (for a few tokens on a QSA_E4M3 pool 9 or 11), QSA_F32 queries (up to
- * 16 heads per KV head) with queries and weights as sums of three bf16 terms on a QSA_BF16 pool
- * (24 bits) and of two fp16 terms on a QSA_E4M3 pool (22 bits).  With a few tokens, or QSA_F32 queries,
- * on a QSA_E4M3 pool a weight times its cell's power of two is held to 3 * 2^-33 (9 bits) or 2^-38 (11
- * and 22 bits) of the row's largest, and smaller ones may count as nothing; and queries are held to 2^-31
- * of the largest magnitude among up to 32 rows (tokens x heads) of their sequence and KV head.  Other
- * shapes, and QSA_BF16 chunks with scale <= 0, take fp32 arithmetic on the CUDA cores, which is right but
- * slower (no tensor cores, contexts not shared out).
+ * All sums, the softmax statistics and the output are held in fp32.  With d = 128 and a QSA_BF16,
+ * QSA_E4M3 or QSA_E2M1 pool (of 4 bits: rows of codes 16 bytes or a multiple apart) the products run on the
+ * tensor cores: QSA_BF16 queries with the softmax weights rounded to 8 significant bits (for a few tokens
+ * on a QSA_E4M3 pool 9 or 11, on a QSA_E2M1 pool 11), QSA_F32 queries (up to 16 heads per KV head) with
+ * queries and weights as sums of three bf16 terms on a QSA_BF16 pool (24 bits) and of two fp16 terms on the
+ * others (22 bits).  With a few tokens, or QSA_F32 queries, on a QSA_E4M3 or QSA_E2M1 pool a weight times
+ * its cell's power of two is held to 3 * 2^-33 (9 bits) or 2^-38 (11 and 22 bits) of the row's largest, and
+ * smaller ones may count as nothing; and queries are held to 2^-31 of the largest magnitude among up to 32
+ * rows (tokens x heads) of their sequence and KV head (QSA_E2M1, and qsa_paged_sparse_attn: of up to 4
+ * neighbouring KV heads).  Other shapes, and QSA_BF16 chunks with scale <= 0, take fp32 arithmetic on the
+ * CUDA cores, which is right but slower (no tensor cores, contexts not shared out).
  * Errors: INVALID_ARG for null pointers, sizes < 0, H_q not a multiple of H_kv, ld_q < H_q*d, a
  * misaligned pointer (q and out 16 bytes, rows of q a multiple of 16 bytes), a workspace smaller
  * than required; UNSUPPORTED for n_seq, n_tok or their work beyond 2^31 - 1 rows.
