@@ -703,7 +703,7 @@ size_t dense_tc_workspace()
 //
 // Measured whole and cut, bf16 cells, 32 / 4 heads: a chunk of 1,024 tokens over 61,789 cells 730 and 693, over
 // 8,000 115 and 137, of 400 over 2,000 46 and 59, of 64 over 3,000 59 and 48; on e4m3 cells the first 1,482
-// and 1,224, over 4,000 118 and 128.  Four chunks of 256 tokens over 60,000 cells each 712 and 730, over
+// and 1,224, over 4,000 118 and 128 (4-bit cells take as long as these and go by their costs).  Four chunks of 256 tokens over 60,000 cells each 712 and 730, over
 // 60,000, 500, 500 and 500 704 and 218; over 8,000 each 117 and 145, over 8,000 and three times 500 115 and 81;
 // over 2,000 each 48 and 81, over 2,000 and three times 300 46 and 63; sixteen of 512 over 4,000 each 400 and
 // 407, over 4,000 and fifteen times 600 145 and 153.  Prompts: 777 tokens, 8 / 2 heads, 30 and 45, of 8,000

@@ -260,3 +260,34 @@ def test_captured_graph_follows_lengths(q_dtype, news):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("q_dtype", [BF16, F32])
+@pytest.mark.parametrize("news,max_q", [([40, 3], 1), ([40, 3], 8), ([1, 2], 500), ([200, 1], 3)])
+def test_what_the_host_knows_of_lengths(news, max_q, q_dtype):
+    """max_q chooses the kernel; the result is right where it is too small or too large."""
+    run_attn(Pool4([300, 90], 2, 128, 32, seed=15), news, 16, q_dtype, seed=16, max_q=max_q)
+
+
+@pytest.mark.parametrize("q_dtype", [BF16, F32])
+@pytest.mark.parametrize("news", [1, 3, 60])
+def test_queries_that_are_no_numbers(news, q_dtype):
+    """A NaN or an infinity among a row's queries: that row is NaN, the others of its tile are as without it, and so is
+    what is left of its head's other tokens."""
+    pool = Pool4([150, 150], 2, 128, 16, seed=17)
+    n = 2 * news
+    q = torch.randn(n, 8, 128, device=DEV).to(q_dtype)
+    out, clean = torch.zeros_like(q), torch.zeros_like(q)
+    ws = torch.zeros(qsa.paged_attn_workspace_size(n, 2, news, 8, 2, 128), dtype=torch.uint8, device=DEV)
+    cu = i32([0, news, n])
+    qsa.paged_attn(pool.cache, pool.table, cu, pool.kv_len, q, clean, 0.09, news, workspace=ws)
+    bad = q.clone()
+    bad[0, 1, 5], bad[n - 1, 6, 127], bad[n - 1, 0, 3] = float("nan"), float("inf"), float("-inf")
+    qsa.paged_attn(pool.cache, pool.table, cu, pool.kv_len, bad, out, 0.09, news, workspace=ws)
+    odd = torch.zeros(n, 8, dtype=torch.bool, device=DEV)
+    odd[0, 1] = odd[n - 1, 6] = odd[n - 1, 0] = True
+    assert torch.isnan(out[odd]).all()
+    assert torch.isfinite(out[~odd]).all()
+    # (the power of two that scales a tile's queries goes by their largest finite magnitude, which may have changed: no
+    # bits of the others do but what lies 2^-24 below, so the outputs differ by a rounding, one step of bf16, at most)
+    torch.testing.assert_close(out[~odd].float(), clean[~odd].float(), rtol=2.0 ** -7, atol=2.0 ** -9)
