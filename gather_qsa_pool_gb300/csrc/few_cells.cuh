@@ -361,8 +361,8 @@ struct Rows {
                 }
             }
         }
-        // ---- log2 units (codes: with the exponent of the cell's values, x = logit + e), masked; d: above the
-        // reference, which moves where it has to
+        // ---- log2 units (codes: with the exponent of the cell's values, x = logit + e), masked; the reference moves
+        // where one is too far above it
         float inv_e[kGroups][2];  // 2^-e of this thread's cells
 #pragma unroll
         for (int kg = 0; kg < kGroups; ++kg)
@@ -395,26 +395,18 @@ struct Rows {
                             if (hide(c, n, e)) s[kg][n][2 * hf + e] = -INFINITY;
                 }
         }
-        float d[kGroups][NB][4];
         bool move = false;
-        auto above = [&]() {
 #pragma unroll
-            for (int n = 0; n < NB; ++n) {
-                const float2 m2 = make_float2(-mx[n][0], -mx[n][1]);
-                float top = -INFINITY;
+        for (int n = 0; n < NB; ++n) {
+            float top[2];
 #pragma unroll
-                for (int kg = 0; kg < kGroups; ++kg)
+            for (int e = 0; e < 2; ++e) {
+                top[e] = fmaxf(s[0][n][e], s[0][n][2 + e]);
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        const float2 y = add2(make_float2(s[kg][n][2 * hf], s[kg][n][2 * hf + 1]), m2);
-                        d[kg][n][2 * hf] = y.x;
-                        d[kg][n][2 * hf + 1] = y.y;
-                        top = fmaxf(top, fmaxf(y.x, y.y));
-                    }
-                move |= top > S::kMove;
+                for (int kg = 1; kg < kGroups; ++kg) top[e] = fmaxf(top[e], fmaxf(s[kg][n][e], s[kg][n][2 + e]));
             }
-        };
-        above();
+            move |= fmaxf(top[0] - mx[n][0], top[1] - mx[n][1]) > S::kMove;
+        }
         if constexpr (F16) {
             if (!wide && far) {
                 wide = true;  // so far l is in units of mx
@@ -461,7 +453,6 @@ struct Rows {
                         o[t][n][2 + e] *= ao;
                     }
                 }
-            above();
         }
         if constexpr (F16) {
             if (wide) {
@@ -482,10 +473,12 @@ struct Rows {
             for (int n = 0; n < NB; ++n) {
                 float w[2][2];  // [cell half][row]
                 float2 l2 = make_float2(l[n][0], l[n][1]);
+                const float2 m2 = make_float2(-mx[n][0], -mx[n][1]);
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-                    w[hf][0] = ex2_approx(d[kg][n][2 * hf]);
-                    w[hf][1] = ex2_approx(d[kg][n][2 * hf + 1]);
+                    const float2 d = add2(make_float2(s[kg][n][2 * hf], s[kg][n][2 * hf + 1]), m2);
+                    w[hf][0] = ex2_approx(d.x);
+                    w[hf][1] = ex2_approx(d.y);
                     const float2 w2 = make_float2(w[hf][0], w[hf][1]);
                     if constexpr (F16) {
                         if (!wide) l2 = fma2(w2, make_float2(inv_e[kg][hf], inv_e[kg][hf]), l2);
