@@ -163,6 +163,9 @@ qsa_status qsa_paged_append(const qsa_paged_cache *cache, const int32_t *table, 
     if (q && (H_q < 1 || !q_out || !aligned(q_out, 16) || !rows_ok(q, ld_q, (int64_t)H_q * cache->d, src_dtype)))
         return QSA_ERR_INVALID_ARG;
     if (q && (int64_t)H_q * cache->d > (1 << 24)) return QSA_ERR_UNSUPPORTED;
+    // in place only where a token's row lies where its output goes
+    if ((q && q == q_out && n_tok > 1 && ld_q != (int64_t)H_q * cache->d) || (k == k_out && n_tok > 1 && ld_k != width))
+        return QSA_ERR_INVALID_ARG;
     if (n_tok == 0) return QSA_OK;
     const SeqView sv = {cu_q, kv_len, (int32_t)n_seq, n_tok};
     return from_cuda(launch_paged_append(q, k, v, src_dtype, ld_q, ld_k, ld_v, q ? H_q : 0, cache->d, rot, base, pos,

@@ -818,8 +818,8 @@ size_t qsa_paged_attn_workspace_size(int64_t n_tok, int64_t n_seq, int64_t max_q
  * A token that is skipped by qsa_paged_write (its cell is not there) still has q_out and k_out
  * written; tokens from cu_q[n_seq] on have not.
  * Errors: those of qsa_paged_write; INVALID_ARG for rot < 0, > d or not a multiple of 16, a base that
- * is not finite or below 1, q without q_out, H_q < 1 with q, ld_q < H_q*d, a misaligned pointer (q,
- * q_out, k_out 16 bytes, pos 4); UNSUPPORTED for H_q * d above 2^24.
+ * is not finite or below 1, q without q_out, q_out = q or k_out = k with rows that are not packed,
+ * H_q < 1 with q, ld_q < H_q*d, a misaligned pointer (q, q_out, k_out 16 bytes, pos 4); UNSUPPORTED for H_q * d above 2^24.
  */
 qsa_status qsa_paged_append(const qsa_paged_cache *cache, const int32_t *table, int64_t ld_table,
                             int64_t n_seq, const int32_t *cu_q, const int32_t *kv_len,

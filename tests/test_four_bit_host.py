@@ -81,6 +81,9 @@ def test_append_refuses(lib):
         assert call(base=b) == INVALID
     assert call(H_q=0) == INVALID and call(ld_q=4080) == INVALID and call(ld_q=4100) == INVALID
     assert call(ld_k=504) == INVALID and call(ld_v=516) == INVALID
+    far = FAKE + (1 << 20)
+    assert call(n_tok=2, q=far, q_out=far, ld_q=8192) == INVALID  # in place, but not packed
+    assert call(n_tok=2, k=far, k_out=far, ld_k=1024) == INVALID
     assert call(H_q=1 << 18, ld_q=1 << 26) == UNSUPPORTED and call(n_seq=1 << 31) == UNSUPPORTED
     assert call(n_tok=0) == 0 and call(n_tok=0, q=None, q_out=None, H_q=0, ld_q=0) == 0
 
