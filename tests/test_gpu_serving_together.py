@@ -288,6 +288,54 @@ def test_cells_beyond_32_bits(dtype, rows):
                 assert torch.equal(a, b)
 
 
+# ------------------------------------------------------------------ batches of nothing
+
+@pytest.mark.parametrize("q_dtype", [BF16, F32])
+@pytest.mark.parametrize("dtype", [E2M1, E4M3, BF16])
+@pytest.mark.parametrize("max_q", [1, 200])
+def test_padding_alone(dtype, q_dtype, max_q):
+    """No sequence has a new token: nothing is written."""
+    pool = any_pool([70, 0], 2, 128, 16, dtype, seed=61)
+    cu, n = i32([0, 0, 0]), 5
+    held = [t.clone() for t in (pool.K.view(torch.uint8) if dtype != BF16 else pool.K, pool.V.view(torch.uint8) if dtype != BF16 else pool.V)]
+    q, k, v = (torch.randn(n, h, 128, device=DEV).to(q_dtype) for h in (8, 2, 2))
+    outs = [torch.full_like(q, -7.0) for _ in range(3)]
+    qsa.paged_append(pool.cache, pool.table, cu, pool.kv_len, k, v, 10000.0, q=q, q_out=outs[0])
+    qsa.paged_attn(pool.cache, pool.table, cu, pool.kv_len, q, outs[1], 0.09, max_q, workspace=workspace(n, 2, max_q, 8, 2))
+    qsa.paged_sparse_attn(pool.cache, pool.table, cu, pool.kv_len, torch.zeros(n, 3, dtype=torch.int32, device=DEV),
+                          torch.full((n,), 3, dtype=torch.int32, device=DEV), q, outs[2], 0.09)
+    torch.cuda.synchronize()
+    assert all((o == -7).all() for o in outs)
+    now = (pool.K.view(torch.uint8), pool.V.view(torch.uint8)) if dtype != BF16 else (pool.K, pool.V)
+    assert all(torch.equal(a.nan_to_num() if a.is_floating_point() else a, b.nan_to_num() if b.is_floating_point() else b) for a, b in zip(held, now))
+
+
+@pytest.mark.parametrize("q_dtype", [BF16, F32])
+@pytest.mark.parametrize("news", [[2, 7], [1, 70]])
+def test_tokens_before_the_first_cell(news, q_dtype):
+    """More new tokens than cells: those at negative positions see nothing, give zero and -inf; the others as ever."""
+    lens = [0, 5]
+    pool = Pool4(lens, 2, 128, 16, seed=62)
+    n, cu = sum(news), starts(news)
+    q = torch.randn(n, 16, 128, device=DEV).to(q_dtype)
+    blocks, counts = np.zeros((n, 4), np.int32), np.full(n, 1, np.int32)
+    for listed in (False, True):
+        out, lse = torch.full_like(q, -7.0), torch.full((n, 16), -7.0, device=DEV)
+        if listed:
+            qsa.paged_sparse_attn(pool.cache, pool.table, i32(cu), pool.kv_len, i32(blocks), i32(counts), q, out, 0.09, lse=lse)
+        else:
+            qsa.paged_attn(pool.cache, pool.table, i32(cu), pool.kv_len, q, out, 0.09, max(news), lse=lse, workspace=workspace(n, 2, max(news), 16, 2))
+        torch.cuda.synchronize()
+        o, l, qn = (x.double().cpu().numpy() for x in (out, lse, q))
+        for s, m in enumerate(news):
+            for i in range(m):
+                t, p = cu[s] + i, lens[s] - m + i
+                if p < 0:
+                    assert (o[t] == 0).all() and np.isneginf(l[t]).all()
+                else:
+                    check_attention(o[t:t + 1], l[t:t + 1], qn[t:t + 1], pool.k[s][:p + 1], pool.v[s][:p + 1], p, 0.09, True, q_dtype, E4M3, pool.units[s][:p + 1])
+
+
 # ------------------------------------------------------------------ waits that run out
 
 def test_chunk_gives_up_and_recovers():
