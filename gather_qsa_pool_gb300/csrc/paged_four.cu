@@ -477,22 +477,26 @@ paged_four_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const T
     }
 }
 
-// The join of items in many parts (few items, listed by number): a CTA for each row.  The weights of the parts first,
-// all at once, then their outputs, independent of one another (one pass with a running maximum, 456 parts of one
-// sequence: 33 us behind the attention's 37).
-constexpr int kJoinWarps = 16;
+// The join of items in many parts (few items, listed by number): a CTA for 32 values of a row.  A thread takes the
+// reference and sum of one part, and eight lanes a part's values, eight parts in turn; all that is read at once, before
+// the weights are known, so that what remains is a chain of four loads.  (One pass with a running maximum, a CTA a row, 456
+// parts of one sequence: 33 us behind the attention's 37; weights first, then values by turns of eight: 15.)
+constexpr int kJoinWarps = 16, kJoinSlices = 4;
+constexpr int kJoinTurns = 8;  // parts of eight lanes
+static_assert(3 * kTargetSMs <= 32 * kJoinWarps && 4 * kJoinWarps * kJoinTurns >= 3 * kTargetSMs, "every part has its thread");
 template <typename TQ>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 join_many_kernel(const Split *__restrict__ splits, const float *__restrict__ partial, int rec_rows, const SeqView sv, int rt, int groups,
                  int heads, TQ *__restrict__ out, float *__restrict__ lse)
 {
-    __shared__ float weight[3 * kTargetSMs], red[2][kJoinWarps];
-    __shared__ float4 red_o[kJoinWarps][32];
+    __shared__ float weight[32 * kJoinWarps], red[2][kJoinWarps];
+    __shared__ float4 red_o[kJoinWarps][8];
     pdl_wait();
     QSA_AFTER_WAIT(splits);
     QSA_AFTER_WAIT(partial);
     pdl_trigger();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Split sp = splits[blockIdx.x];
     // fewer items than the host could tell have no entry
     int64_t items = 0;
     for (int s = lane; s < sv.n_seq; s += 32) {
@@ -502,7 +506,6 @@ join_many_kernel(const Split *__restrict__ splits, const float *__restrict__ par
         items += (len + rt - 1) / rt;
     }
     if ((int64_t)blockIdx.x >= warp_sum_i64(items) * groups) return;
-    const Split sp = splits[blockIdx.x];
     if (sp.s < 0) return;
     int64_t t0;
     int len;
@@ -511,54 +514,62 @@ join_many_kernel(const Split *__restrict__ splits, const float *__restrict__ par
     if (r >= rt * heads || tok >= len) return;
     const int64_t rec = partial_floats(rec_rows, kD);
     auto part_of = [&](int k) { return partial + (2 * (int64_t)(sp.cta + k) + (k == 0 ? 1 : 0)) * rec; };
-    const int n = min(sp.parts, 3 * kTargetSMs);
-    float m = -INFINITY, l = 0.0f;
-    for (int k = tid; k < n; k += 32 * kJoinWarps) m = fmaxf(m, part_of(k)[r]);
-    m = warp_max(m);
+    const int n = min(sp.parts, 3 * kTargetSMs), first = tid >> 3, dim = 32 * blockIdx.z + 4 * (lane & 7);
+    float4 y[kJoinTurns];
+#pragma unroll
+    for (int i = 0; i < kJoinTurns; ++i) {
+        const int k = first + 4 * kJoinWarps * i;
+        y[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (k < n) y[i] = *reinterpret_cast<const float4 *>(part_of(k) + 2 * rec_rows + (int64_t)r * kD + dim);
+    }
+    const float pm = tid < n ? part_of(tid)[r] : -INFINITY, pl = tid < n ? part_of(tid)[rec_rows + r] : 0.0f;
+    float m = warp_max(pm);
     if (lane == 0) red[0][warp] = m;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, red[0][w]);
-    const float u = m == -INFINITY ? 0.0f : m;
-    for (int k = tid; k < n; k += 32 * kJoinWarps) {
-        const float *const p = part_of(k);
-        const float pm = p[r], f = pm == -INFINITY ? 1.0f : exp2f(pm - u);  // an unset side is zero or NaN
-        weight[k] = f;
-        l += p[rec_rows + r] * f;
-    }
+    const float f = pm == -INFINITY ? 1.0f : exp2f(pm - (m == -INFINITY ? 0.0f : m));  // an unset side is zero or NaN
+    weight[tid] = f;
+    float l = pl * f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane == 0) red[1][warp] = l;
     __syncthreads();
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-    for (int k = warp; k < n; k += kJoinWarps) {
-        const float4 y = *reinterpret_cast<const float4 *>(part_of(k) + 2 * rec_rows + (int64_t)r * kD + 4 * lane);
-        const float f = weight[k];
-        o.x = fmaf(y.x, f, o.x);
-        o.y = fmaf(y.y, f, o.y);
-        o.z = fmaf(y.z, f, o.z);
-        o.w = fmaf(y.w, f, o.w);
+#pragma unroll
+    for (int i = 0; i < kJoinTurns; ++i) {
+        const float w = weight[first + 4 * kJoinWarps * i];
+        o.x = fmaf(y[i].x, w, o.x);
+        o.y = fmaf(y[i].y, w, o.y);
+        o.z = fmaf(y[i].z, w, o.z);
+        o.w = fmaf(y[i].w, w, o.w);
     }
-    red_o[warp][lane] = o;
+#pragma unroll
+    for (int k = 8; k < 32; k <<= 1) {
+        o.x += __shfl_xor_sync(0xffffffffu, o.x, k);
+        o.y += __shfl_xor_sync(0xffffffffu, o.y, k);
+        o.z += __shfl_xor_sync(0xffffffffu, o.z, k);
+        o.w += __shfl_xor_sync(0xffffffffu, o.w, k);
+    }
+    if (lane < 8) red_o[warp][lane] = o;
     __syncthreads();
-    if (warp > 0) return;
+    if (tid >= 8) return;
     l = 0.0f;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) l += red[1][w];
 #pragma unroll
     for (int w = 1; w < kJoinWarps; ++w) {
-        const float4 y = red_o[w][lane];
-        o.x += y.x; o.y += y.y; o.z += y.z; o.w += y.w;
+        const float4 z = red_o[w][lane];
+        o.x += z.x; o.y += z.y; o.z += z.z; o.w += z.w;
     }
     const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // a NaN sum stays NaN
     const int64_t at = (t0 + tok) * groups * heads + sp.g * heads + r % heads;
-    TQ *const dst = out + at * kD + 4 * lane;
+    TQ *const dst = out + at * kD + dim;
     if constexpr (sizeof(TQ) == 2)
         *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
     else
         *reinterpret_cast<float4 *>(dst) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-    if (lane == 0 && lse) lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+    if (dim == 0 && lse) lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 }  // namespace few
@@ -593,7 +604,7 @@ cudaError_t run(const DenseArgs &a, void *workspace, cudaStream_t st)
     // (items in a dozen parts or more each: few sequences)
     const int64_t items = ((a.sv.n_tok + ws.rt - 1) / ws.rt + a.sv.n_seq) * b.kv.H_kv;
     if (items * 12 <= ctas)
-        return launch(few::join_many_kernel<TQ>, dim3((unsigned)items, (unsigned)(8 * NB * hpc)), dim3(32 * few::kJoinWarps), 0, st, 1, splits,
+        return launch(few::join_many_kernel<TQ>, dim3((unsigned)items, (unsigned)(8 * NB * hpc), few::kJoinSlices), dim3(32 * few::kJoinWarps), 0, st, 1, splits,
                       partial, 8 * NB * hpc, a.sv, ws.rt, b.kv.H_kv, G << hl, static_cast<TQ *>(a.out), a.lse);
     return launch_dense_join<TQ>(splits, partial, ctas, 8 * NB * hpc, ws.rt, b, st);
 }
