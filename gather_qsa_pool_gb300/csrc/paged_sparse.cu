@@ -322,16 +322,16 @@ cudaError_t run(const SparseArgs &a, cudaStream_t st)
     constexpr int kMost = C == QSA_BF16 || NB * NT > 4 ? 0 : (NB * NT > 2 ? 1 : 2);
     cudaError_t e = ensure_kernel_attrs<few::paged_sparse_kernel<C, TQ, NB, NT>>(few::sparse_smem<C, NB, NT>(1 << kMost));
     if (e != cudaSuccess) return e;
-    // CTAs of a token and its heads.  One each where these are as many as SMs (64 tokens, 4 KV heads: clusters of six over
-    // two heads a CTA took 52 us, one CTA a head 31); else as many as fill the GPU but for what clusters of their size
-    // leave of it, a tile each at most, up to the portable cluster's eight.  With many tokens the heads of a row go
-    // to one CTA.
-    const int64_t sms = device_sm_count(), most = P::kCtas * sms;
+    // CTAs of a token and its heads: as many as fill the GPU but for what clusters of their size leave of it, a tile
+    // each at most, up to the portable cluster's eight.  (One each where tokens x heads are no fewer than SMs, instead:
+    // 2,052 cells, 4 KV heads, 38 tokens bf16 54 us and not 44, 64 tokens e2m1 40 and not 36; otherwise alike.)  With many
+    // tokens the heads of a row go to one CTA.
+    const int64_t most = P::kCtas * device_sm_count();
     int hl = kMost;
     while (hl > 0 && (a.kv.H_kv % (1 << hl) || (a.sv.n_tok * a.kv.H_kv >> hl) < 2 * most)) --hl;
     const int kt_log2 = (C == QSA_BF16 ? 6 : 7) - hl;
     const int64_t items = a.sv.n_tok * (a.kv.H_kv >> hl), tiles = (a.k_blk >> (kt_log2 - 2)) + 1;
-    int64_t parts = items >= sms ? 1 : most * 7 / 8 / items;
+    int64_t parts = most * 7 / 8 / items;
     if (parts > tiles) parts = tiles;
     if (parts > 8) parts = 8;
     if (parts < 1) parts = 1;
