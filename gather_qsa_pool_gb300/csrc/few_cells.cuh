@@ -148,11 +148,12 @@ __device__ __forceinline__ int frag_dim(int t, int g8, int half)
 // ------------------------------------------------------------------ queries
 // The queries' fragments of hpc heads to shared memory by W warps (tid: a thread's number among them; all call it),
 // k permuted as the key rows are read: lane (g8, c4) holds row g8 of a block, and kE values of each 4 kE.  Row r of a
-// head: token r / G, query head r mod G.  from: the first token's values of the first head.  top_s: a word a warp.
-// Returns what undoes the queries' scaling.  The caller's barrier follows.
-template <int C, typename TQ, int NB, int NT, int W, typename Sync>
-__device__ __forceinline__ float stage_queries(int tid, const TQ *from, int64_t ld_q, int G, int rows, int hpc, float q_sign, uint4 *q_all,
-                                               uint32_t *top_s, Sync sync)
+// head: token r / G, query head r mod G.  from: the first token's values of the first head.  fp16 holds a row's queries
+// times a power of two of its own (one for the tile would let a large query of one token or head take the bits of
+// another's); undo: what brings the row's logits back, 8 NB rows a head.  The caller's barrier follows.
+template <int C, typename TQ, int NB, int NT, int W>
+__device__ __forceinline__ void stage_queries(int tid, const TQ *from, int64_t ld_q, int G, int rows, int hpc, float q_sign, uint4 *q_all,
+                                              float *undo)
 {
     constexpr bool F16 = Cell<C>::kF16;
     constexpr int E = Cell<C>::kE, kWords = sizeof(TQ) == 2 ? 16 : 32;
@@ -161,7 +162,6 @@ __device__ __forceinline__ float stage_queries(int tid, const TQ *from, int64_t 
     constexpr int kMost = NB * 4 <= W ? 1 : NB * 4 / W;  // of a warp, with up to four heads
     const int units = hpc * NB;
     uint32_t raw[kMost][kWords];
-    uint32_t top = 0;  // the largest finite magnitude, by its bits
 #pragma unroll
     for (int i = 0; i < kMost; ++i) {
         const int u = warp + W * i, r = 8 * (u % NB) + g8;
@@ -178,30 +178,26 @@ __device__ __forceinline__ float stage_queries(int tid, const TQ *from, int64_t 
             raw[i][4 * k + 3] = y.w;
         }
     }
-    float mul = q_sign, back = 1.0f;
-    if constexpr (F16) {
-        // fp16 holds the queries once the rows' largest magnitude is below 2^8: one power of two for all
 #pragma unroll
-        for (int i = 0; i < kMost; ++i)
+    for (int i = 0; i < kMost; ++i) {
+        const int u = warp + W * i;
+        if (u >= units) break;
+        float mul = q_sign;
+        if constexpr (F16) {
+            // the row's largest finite magnitude, by its bits, becomes at least 2^7 and less than 2^8
+            uint32_t top = 0;
 #pragma unroll
             for (int k = 0; k < kWords; ++k) {
                 const uint32_t a = (sizeof(TQ) == 2 ? raw[i][k] << 16 : raw[i][k]) & 0x7fffffffu;
                 const uint32_t b = sizeof(TQ) == 2 ? raw[i][k] & 0x7fff0000u : 0u;
                 top = max(top, max(a < 0x7f800000u ? a : 0u, b < 0x7f800000u ? b : 0u));
             }
-        top = __reduce_max_sync(0xffffffffu, top);
-        if (lane == 0) top_s[warp] = top;
-        sync();
-#pragma unroll
-        for (int w = 0; w < W; ++w) top = max(top, top_s[w]);
-        const int sh = top > 0u ? min(max(134 - (int)(top >> 23), -120), 100) : 0;
-        back = two_to(-sh);
-        mul = q_sign * two_to(sh);
-    }
-#pragma unroll
-    for (int i = 0; i < kMost; ++i) {
-        const int u = warp + W * i;
-        if (u >= units) break;
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int sh = top > 0u ? min(max(134 - (int)(top >> 23), -120), 100) : 0;
+            mul = q_sign * two_to(sh);
+            if (c4 == 0) undo[8 * u + g8] = two_to(-sh);
+        }
         uint4 *const to = q_all + (u / NB) * (int)(q_bytes<NB, NT>() / 16);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {  // two steps of 16 dims
@@ -222,7 +218,6 @@ __device__ __forceinline__ float stage_queries(int tid, const TQ *from, int64_t 
             }
         }
     }
-    return back;
 }
 
 // ------------------------------------------------------------------ a warp's rows over its cells
@@ -257,11 +252,11 @@ struct Rows {
     }
 
     // The cells of one stage: sk: K, V (codes' scales behind them); ex: per cell 2^ke, the exponent e of the value,
-    // 2^-e (codes only); far: some e is beyond kFar; qf: the queries' fragments; edge: hide(c, n, e) says whether row
-    // (n, e) does not see cell c.
+    // 2^-e (codes only); far: some e is beyond kFar; qf: the queries' fragments, undo: what undoes their rows' scaling
+    // (codes only); edge: hide(c, n, e) says whether row (n, e) does not see cell c.
     template <typename Hide>
-    __device__ __forceinline__ void tile(const unsigned char *sk, const float4 *ex, const uint4 *qf, float key_scale, bool far, bool edge,
-                                         Hide hide)
+    __device__ __forceinline__ void tile(const unsigned char *sk, const float4 *ex, const uint4 *qf, const float *undo, float key_scale,
+                                         bool far, bool edge, Hide hide)
     {
         const unsigned char *const sv = sk + S::kTile, *const ks = sv + S::kTile, *const vs = ks + S::kScales;
         const int lane = threadIdx.x & 31, g8 = lane >> 2, c4 = lane & 3;
@@ -376,8 +371,9 @@ struct Rows {
                 }
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
-                    float2 y = make_float2(s[kg][n][2 * hf], s[kg][n][2 * hf + 1]);
-                    y = F16 ? fma2(y, make_float2(f.x, f.x), make_float2(f.y, f.y)) : mul2(y, make_float2(f.x, f.x));
+                    float2 y = make_float2(s[kg][n][2 * hf], s[kg][n][2 * hf + 1]), by = make_float2(f.x, f.x);
+                    if constexpr (F16) by = mul2(by, *reinterpret_cast<const float2 *>(undo + 8 * n + 2 * c4));
+                    y = F16 ? fma2(y, by, make_float2(f.y, f.y)) : mul2(y, by);
                     s[kg][n][2 * hf] = y.x;
                     s[kg][n][2 * hf + 1] = y.y;
                 }

@@ -156,7 +156,7 @@ paged_four_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const T
     __shared__ Walk walk_s, walks_s[kWarps];  // the first part; each warp's own
     __shared__ int64_t per_s;
     __shared__ int none_s, bad_s, odd_s[kWarps];  // number + 1 of the part that set it; odd_s: by head
-    __shared__ uint32_t top_s[kWarps];
+    __shared__ __align__(16) float undo_s[kWarps][kRows];  // by head
     __shared__ float red_m[kWarps][kRows], red_l[kWarps][kRows];
 
     const int tid = threadIdx.x, lane = tid & 31, g8 = lane >> 2, c4 = lane & 3;
@@ -293,10 +293,9 @@ paged_four_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const T
             look_up(tile0 + i + 1);
             cp_commit();
         }
-        const float q_back = stage_queries<QSA_E2M1, TQ, NB, NT, kWarps>(
-            tid, qp + (p.it.t0 + tok0) * ld_q + (int64_t)p.it.g * heads * kD, ld_q, G, rows, hpc, q_sign, q_all, top_s, [] { __syncthreads(); });
+        stage_queries<QSA_E2M1, TQ, NB, NT, kWarps>(tid, qp + (p.it.t0 + tok0) * ld_q + (int64_t)p.it.g * heads * kD, ld_q, G, rows, hpc,
+                                                    q_sign, q_all, undo_s[0]);
         __syncthreads();
-        const float key_scale = scale_log2 * q_back;
         int last[NB][2];  // the last cell each row sees
 #pragma unroll
         for (int i = 0; i < NB; ++i)
@@ -335,7 +334,7 @@ paged_four_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const T
                     }
                     __syncwarp();
                 }
-                w.tile(sk, exps + slot * 32, qf, key_scale, far, edge, [&](int c, int i, int e) { return j0 + c > last[i][e]; });
+                w.tile(sk, exps + slot * 32, qf, undo_s[head], scale_log2, far, edge, [&](int c, int i, int e) { return j0 + c > last[i][e]; });
             }
             __syncwarp();
             slot = slot == kStages - 1 ? 0 : slot + 1;

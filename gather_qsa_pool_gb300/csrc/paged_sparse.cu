@@ -41,7 +41,8 @@ paged_sparse_kernel(const KvView kv, const SeqView sv, const ListView lv, const 
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int bad_s;
     __shared__ float red_m[kWarps][kRows], red_l[kWarps][kRows];
-    __shared__ uint32_t top_s[kWarps], there_s[kWarps][kStages];  // there_s: cells of a stage that are there
+    __shared__ __align__(16) float undo_s[kWarps][kRows];  // by head
+    __shared__ uint32_t there_s[kWarps][kStages];          // cells of a stage that are there
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g8 = lane >> 2, c4 = lane & 3;
@@ -171,10 +172,9 @@ paged_sparse_kernel(const KvView kv, const SeqView sv, const ListView lv, const 
         }
         cp_commit();
     }
-    const float q_back = stage_queries<C, TQ, NB, NT, kWarps>(tid, qp + tok * ld_q + (int64_t)(group << hpc_log2) * G * kD, ld_q, G, G, hpc,
-                                                              q_sign, q_all, top_s, [] { __syncthreads(); });
+    stage_queries<C, TQ, NB, NT, kWarps>(tid, qp + tok * ld_q + (int64_t)(group << hpc_log2) * G * kD, ld_q, G, G, hpc, q_sign, q_all,
+                                         undo_s[0]);
     __syncthreads();
-    const float key_scale = scale_log2 * q_back;
     Rows<C, NB, NT> w;
     w.clear();
     int slot = 0;
@@ -195,7 +195,7 @@ paged_sparse_kernel(const KvView kv, const SeqView sv, const ListView lv, const 
         cp_commit();
         constexpr uint32_t kAll = 0xffffffffu << (32 - kKeys);
         if (there << (32 - kKeys))
-            w.tile(ring + slot * S::kStage, exps + slot * 32, qf, key_scale, far, there << (32 - kKeys) != kAll,
+            w.tile(ring + slot * S::kStage, exps + slot * 32, qf, undo_s[head], scale_log2, far, there << (32 - kKeys) != kAll,
                    [&](int c, int, int) { return !((there >> c) & 1u); });
         __syncwarp();
         slot = slot == kStages - 1 ? 0 : slot + 1;
