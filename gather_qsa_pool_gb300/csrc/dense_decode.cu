@@ -174,7 +174,7 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
     constexpr int kRows = 16, kStages = Plan<NT>::kStages;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int bad_s, odd_s;
-    __shared__ float red_m[kWarps][kRows], red_l[kWarps][kRows], top_s;
+    __shared__ float red_m[kWarps][kRows], red_l[kWarps][kRows], undo_s[kRows];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g8 = lane >> 2, c4 = lane & 3;
@@ -272,8 +272,7 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
         }
         // ---- the query's fragments: lane's rows g8 and g8 + 8 of each fragment, k permuted as
         // the key rows are read (thread c4 holds 16 contiguous bytes of each block)
-        float q_back = 1.0f;  // what undoes the queries' scaling
-        {
+        if (warp == 0) {
             constexpr int E = E8 ? 16 : 8;       // dims of a thread in a block
             constexpr int kBlocks = kD / (4 * E);
             auto load_row = [&](int hf, float *xa) {
@@ -292,58 +291,46 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
                         }
                     }
             };
-            float mul = q_sign;
-            if constexpr (E8) {
-                // fp16 holds the queries once the tile's largest magnitude is below 2^8: one power
-                // of two for all rows, as a row 2^20 times smaller than another keeps 2^-13 of its
-                // own largest value and has logits that much smaller
-                if (warp == 0) {
+            float xa[2][kBlocks * E];
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                load_row(hf, xa[hf]);
+                float mul = q_sign;
+                if constexpr (E8) {
+                    // fp16 holds a row's queries once its largest magnitude is below 2^8: a power of two of the
+                    // row's own (one for the tile would let a large query of one token or head take another's bits)
                     float top = 0.0f;
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        float xa[kBlocks * E];
-                        load_row(hf, xa);
-#pragma unroll
-                        for (int e = 0; e < kBlocks * E; ++e)
-                            if (isfinite(xa[e])) top = fmaxf(top, fabsf(xa[e]));
-                    }
-                    top = warp_max(top);
-                    if (lane == 0) top_s = top;
-                }
-                __syncthreads();
-                const float top = top_s;
-                const int ex = (int)(__float_as_uint(top) >> 23) - 127;
-                const int sh = top > 0.0f ? min(max(7 - ex, -120), 100) : 0;
-                q_back = two_to(-sh);
-                mul = q_sign * two_to(sh);
-            }
-            if (warp == 0) {
-                float xa[2][kBlocks * E];
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    load_row(hf, xa[hf]);
-#pragma unroll
-                    for (int e = 0; e < kBlocks * E; ++e) xa[hf][e] *= mul;
+                    for (int e = 0; e < kBlocks * E; ++e)
+                        if (isfinite(xa[hf][e])) top = fmaxf(top, fabsf(xa[hf][e]));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const int ex = (int)(__float_as_uint(top) >> 23) - 127;
+                    const int sh = top > 0.0f ? min(max(7 - ex, -120), 100) : 0;
+                    if (c4 == 0) undo_s[g8 + 8 * hf] = two_to(-sh);
+                    mul = q_sign * two_to(sh);
                 }
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        uint4 f;
-                        f.x = pack16<E8>(xa[0][4 * k], xa[0][4 * k + 1]);
-                        f.y = pack16<E8>(xa[1][4 * k], xa[1][4 * k + 1]);
-                        f.z = pack16<E8>(xa[0][4 * k + 2], xa[0][4 * k + 3]);
-                        f.w = pack16<E8>(xa[1][4 * k + 2], xa[1][4 * k + 3]);
-                        qf[(n * 8 + k) * 32 + lane] = f;
-                    }
+                for (int e = 0; e < kBlocks * E; ++e) xa[hf][e] *= mul;
             }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    uint4 f;
+                    f.x = pack16<E8>(xa[0][4 * k], xa[0][4 * k + 1]);
+                    f.y = pack16<E8>(xa[1][4 * k], xa[1][4 * k + 1]);
+                    f.z = pack16<E8>(xa[0][4 * k + 2], xa[0][4 * k + 3]);
+                    f.w = pack16<E8>(xa[1][4 * k + 2], xa[1][4 * k + 3]);
+                    qf[(n * 8 + k) * 32 + lane] = f;
+                }
         }
         __syncthreads();
-        const float key_scale = scale_log2 * q_back;
+        const float undo[2] = {E8 ? undo_s[g8] : 1.0f, E8 ? undo_s[g8 + 8] : 1.0f};  // the rows' scaling
         auto keep_exps = [&](int stage, int i) {
             const int ek = min(max(pend_k[i] - kExpBias, kExpMin), kExpMax);
             const int ev = min(max(pend_v[i] - kExpBias, kExpMin), kExpMax);
-            exps[stage * 32 + lane] = make_float4(two_to(ek) * key_scale, (float)ev, two_to(-ev), 0.0f);
+            exps[stage * 32 + lane] = make_float4(two_to(ek) * scale_log2, (float)ev, two_to(-ev), 0.0f);
         };
         if constexpr (E8) {
 #pragma unroll
@@ -454,8 +441,8 @@ dense_decode_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const
                         far |= fabsf(f0.y) > kFar || fabsf(f1.y) > kFar;
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf) {
-                            s[n][2 * hf] = fmaf(s[n][2 * hf], f0.x, f0.y);
-                            s[n][2 * hf + 1] = fmaf(s[n][2 * hf + 1], f1.x, f1.y);
+                            s[n][2 * hf] = fmaf(s[n][2 * hf], f0.x * undo[hf], f0.y);
+                            s[n][2 * hf + 1] = fmaf(s[n][2 * hf + 1], f1.x * undo[hf], f1.y);
                         }
                     }
                 }
