@@ -81,8 +81,7 @@ struct Bars {
     uint64_t s_full[kGroups], p_full[kGroups], o_full[kGroups], q_full[2], q_free[2], drain;
     uint32_t tmem, pad;
     int32_t odd[kSlots], bad[kSlots];  // number + 1 of the part that set it
-    float qs[kSlots];                  // what the part's queries were divided by
-    uint32_t qmax[2][8];
+    alignas(16) float qs[kSlots][32];  // what the part's rows of queries were divided by
     alignas(16) float nm[kGroups][32], mref[kGroups][32];  // -m, m of a group's rows
     float2 al[kGroups][32], fac[kGroups][32];  // factors 2^x as two, each in range
     alignas(16) float red[kGroups][4][32];
@@ -207,12 +206,12 @@ __device__ __forceinline__ bool scrub_codes(unsigned char *tile, int r0, int r1,
 }
 
 // A part's queries in the form that the products take, by kLanes threads (`at`: this one's number;
-// barrier kBar is theirs): rows behind the part's last become zero.  qmax: a place per warp.  here: false
+// barrier kBar is theirs): rows behind the part's last become zero.  e4m3: a row is scaled by a power of two of its
+// own (one for the part would let a large query of one token or head take another's bits), undone by qs.  here: false
 // when this thread's warp has given up; false for all is returned then.
 template <bool E8, int NR, int kLanes, int kBar>
 __device__ __forceinline__ bool lay_queries(const Parts &w, int at, bool here, const __nv_bfloat16 *q, int64_t ld_q,
-                                            int G, uint32_t inv_g, float q_sign, unsigned char *dst, uint32_t *qmax,
-                                            float *qs)
+                                            int G, uint32_t inv_g, float q_sign, unsigned char *dst, float *qs)
 {
     constexpr int kUnits = NR * 8 / kLanes;  // 16 dims each
     const int rows = w.toks * G;
@@ -229,35 +228,28 @@ __device__ __forceinline__ bool lay_queries(const Parts &w, int at, bool here, c
             raw[i][1] = src[1];
         }
     }
-    float mul = q_sign;
-    if constexpr (E8) {
-        // the largest finite magnitude, by its bits
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < kUnits; ++i)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint32_t u = (&raw[i][k >> 2].x)[k & 3];
-                const uint32_t a = u & 0x7fffu, b = (u >> 16) & 0x7fffu;
-                top = max(top, a < 0x7f80u ? a : 0u);
-                top = max(top, b < 0x7f80u ? b : 0u);
-            }
-        top = __reduce_max_sync(0xffffffffu, top);
-        if ((at & 31) == 0) reinterpret_cast<volatile uint32_t *>(qmax)[at >> 5] = top;
-    }
     if (named_or<kLanes>(kBar, !here)) return false;
-    if constexpr (E8) {
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < kLanes / 32; ++i) top = max(top, reinterpret_cast<volatile uint32_t *>(qmax)[i]);
-        // the largest becomes at least 2^14 and less than 2^15
-        const int a = max(-100, (int)(top >> 7) - 141);
-        mul *= two_to(-a);
-        if (at == 0) *reinterpret_cast<volatile float *>(qs) = two_to(a);
-    }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
         const int r = (at + kLanes * i) >> 3, u = at & 7;
+        float mul = q_sign;
+        if constexpr (E8) {
+            // the row's largest finite magnitude, by its bits
+            uint32_t top = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t x = (&raw[i][k >> 2].x)[k & 3];
+                const uint32_t a = x & 0x7fffu, b = (x >> 16) & 0x7fffu;
+                top = max(top, a < 0x7f80u ? a : 0u);
+                top = max(top, b < 0x7f80u ? b : 0u);
+            }
+#pragma unroll
+            for (int k = 1; k < 8; k <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, k));
+            // it becomes at least 2^14 and less than 2^15
+            const int a = max(-100, (int)(top >> 7) - 141);
+            mul *= two_to(-a);
+            if (u == 0) *reinterpret_cast<volatile float *>(&qs[r]) = two_to(a);
+        }
         uint32_t h[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -552,8 +544,7 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
                 if (ok && ahead.n >= 2)
                     ok = bar_wait_warp(&bars.q_free[buf], (uint32_t)((ahead.n >> 1) - 1) & 1u, wc.limit_ns);
                 if (lay_queries<E8, NR, 32 * kAuxWarps, kBarAux>(ahead, aux * 32 + lane, ok, q, ld_q, G, inv_g, q_sign,
-                                                                 sQ + (size_t)buf * F::kQBytes, bars.qmax[buf],
-                                                                 &bars.qs[ahead.n % kSlots])) {
+                                                                 sQ + (size_t)buf * F::kQBytes, bars.qs[ahead.n % kSlots])) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars.q_full[buf]);
                 } else {
@@ -613,8 +604,7 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
         };
         if constexpr (E8) look(p, 0);
         if (tid < NR * 8) {
-            lay_queries<E8, NR, NR * 8, kBarFirst>(p, tid, true, q, ld_q, G, inv_g, q_sign, sQ, bars.qmax[0],
-                                                   &bars.qs[0]);
+            lay_queries<E8, NR, NR * 8, kBarFirst>(p, tid, true, q, ld_q, G, inv_g, q_sign, sQ, bars.qs[0]);
             named_sync<NR * 8>(kBarFirst);
             if (tid == 0) mbar_arrive_n(&bars.q_full[0], kAuxWarps);
         }
@@ -638,6 +628,7 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
             const float *nm = bars.nm[g];
             for (int k = 0; ok && k < mine; ++k) {
                 const int t = p.tile0 + kGroups * k + g;
+                const float *qs = bars.qs[n % kSlots];
                 if constexpr (E8) {
                     if (k > 0) fetch(p);
                     look(p, k + 1);
@@ -650,7 +641,7 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
                 if constexpr (E8) {
                     const int ke = min(max((int)ke1 - kExpBias, kExpMin), kExpMax);
                     const int ve = min(max((int)ve1 - kExpBias, kExpMin), kExpMax);
-                    ks = two_to(ke) * (scale_log2 * *reinterpret_cast<volatile float *>(&bars.qs[n % kSlots]));
+                    ks = two_to(ke) * scale_log2;
                     vs = (float)ve;
                     vi = two_to(-ve);
                     far = __any_sync(0xffffffffu, abs(ve) > kFar);
@@ -672,7 +663,7 @@ dense_few_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
                             float2 y = make_float2(x[c], x[c + 1]);
                             if constexpr (E8) {
                                 y = add2(y, add2(make_float2(x[kStep + c], x[kStep + c + 1]), make_float2(x[2 * kStep + c], x[2 * kStep + c + 1])));
-                                y = fma2(y, k2, v2);
+                                y = fma2(y, mul2(k2, *reinterpret_cast<const float2 *>(qs + at + c)), v2);
                             } else {
                                 y = mul2(y, k2);
                             }

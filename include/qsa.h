@@ -779,9 +779,8 @@ qsa_status qsa_paged_read(const qsa_paged_cache *cache, const int32_t *table, in
  * others (22 bits).  With a few tokens, or QSA_F32 queries, on a QSA_E4M3 or QSA_E2M1 pool a weight times
  * its cell's power of two is held to 3 * 2^-33 (9 bits) or 2^-38 (11 and 22 bits) of the row's largest, and
  * smaller ones may count as nothing; and queries are held to 2^-31 of the largest magnitude of their row (token
- * and head) on a QSA_E2M1 pool and in qsa_paged_sparse_attn, on a QSA_E4M3 pool here of that among up to 32 rows
- * of their sequence and KV head.  Other shapes, and QSA_BF16 chunks with scale <= 0, take fp32 arithmetic on the
- * CUDA cores, which is right but slower (no tensor cores, contexts not shared out).
+ * and head).  Other shapes, and QSA_BF16 chunks with scale <= 0, take fp32 arithmetic on the CUDA cores, which is
+ * right but slower (no tensor cores, contexts not shared out).
  * Errors: INVALID_ARG for null pointers, sizes < 0, H_q not a multiple of H_kv, ld_q < H_q*d, a
  * misaligned pointer (q and out 16 bytes, rows of q a multiple of 16 bytes), a workspace smaller
  * than required; UNSUPPORTED for n_seq, n_tok or their work beyond 2^31 - 1 rows.

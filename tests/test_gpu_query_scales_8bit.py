@@ -6,13 +6,13 @@ import pytest
 import torch
 
 from four_bit_pool import any_pool
-from test_gpu_dense import DEV, E4M3, F32
+from test_gpu_dense import BF16, DEV, E4M3, F32
 from test_gpu_query_scales import OUTLIERS, attn, check
 
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("q_dtype", [F32])
+@pytest.mark.parametrize("q_dtype", [BF16, F32])
 @pytest.mark.parametrize("lens", [[150, 333], [5000, 9001]])
 @pytest.mark.parametrize("news", [1, 2, 4])
 @pytest.mark.parametrize("H_q,H", OUTLIERS)
@@ -31,7 +31,7 @@ def test_a_large_query_is_its_rows_own(H_q, H, news, lens, q_dtype):
         check(pool, fresh, q, got, l, 0.09)
 
 
-@pytest.mark.parametrize("q_dtype", [F32])
+@pytest.mark.parametrize("q_dtype", [BF16, F32])
 @pytest.mark.parametrize("power", [-100, -60, -20, 20, 60, 100])
 @pytest.mark.parametrize("news,lens", [(1, [260, 37]), (4, [260, 37]), (1, [9001, 5000])])
 def test_magnitudes_of_all_queries(news, lens, power, q_dtype):
