@@ -150,10 +150,10 @@ __device__ __forceinline__ int frag_dim(int t, int g8, int half)
 // k permuted as the key rows are read: lane (g8, c4) holds row g8 of a block, and kE values of each 4 kE.  Row r of a
 // head: token r / G, query head r mod G.  from: the first token's values of the first head.  fp16 holds a row's queries
 // times a power of two of its own (one for the tile would let a large query of one token or head take the bits of
-// another's); undo: what brings the row's logits back, 8 NB rows a head.  The caller's barrier follows.
+// another's); undo: scale over that, what makes the row's products logits, 8 NB rows a head.  The caller's barrier follows.
 template <int C, typename TQ, int NB, int NT, int W>
-__device__ __forceinline__ void stage_queries(int tid, const TQ *from, int64_t ld_q, int G, int rows, int hpc, float q_sign, uint4 *q_all,
-                                              float *undo)
+__device__ __forceinline__ void stage_queries(int tid, const TQ *from, int64_t ld_q, int G, int rows, int hpc, float q_sign, float scale,
+                                              uint4 *q_all, float *undo)
 {
     constexpr bool F16 = Cell<C>::kF16;
     constexpr int E = Cell<C>::kE, kWords = sizeof(TQ) == 2 ? 16 : 32;
@@ -196,7 +196,7 @@ __device__ __forceinline__ void stage_queries(int tid, const TQ *from, int64_t l
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const int sh = top > 0u ? min(max(134 - (int)(top >> 23), -120), 100) : 0;
             mul = q_sign * two_to(sh);
-            if (c4 == 0) undo[8 * u + g8] = two_to(-sh);
+            if (c4 == 0) undo[8 * u + g8] = scale * two_to(-sh);
         }
         uint4 *const to = q_all + (u / NB) * (int)(q_bytes<NB, NT>() / 16);
 #pragma unroll
@@ -252,8 +252,8 @@ struct Rows {
     }
 
     // The cells of one stage: sk: K, V (codes' scales behind them); ex: per cell 2^ke, the exponent e of the value,
-    // 2^-e (codes only); far: some e is beyond kFar; qf: the queries' fragments, undo: what undoes their rows' scaling
-    // (codes only); edge: hide(c, n, e) says whether row (n, e) does not see cell c.
+    // 2^-e (codes only); far: some e is beyond kFar; qf: the queries' fragments, undo: what makes their products
+    // logits (codes; bf16: key_scale); edge: hide(c, n, e) says whether row (n, e) does not see cell c.
     template <typename Hide>
     __device__ __forceinline__ void tile(const unsigned char *sk, const float4 *ex, const uint4 *qf, const float *undo, float key_scale,
                                          bool far, bool edge, Hide hide)
@@ -360,24 +360,32 @@ struct Rows {
         // where one is too far above it
         float inv_e[kGroups][2];  // 2^-e of this thread's cells
 #pragma unroll
-        for (int kg = 0; kg < kGroups; ++kg)
+        for (int n = 0; n < NB; ++n) {
+            const float2 by = F16 ? *reinterpret_cast<const float2 *>(undo + 8 * n + 2 * c4) : make_float2(key_scale, key_scale);
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                float2 f = make_float2(key_scale, 0.0f);
-                if constexpr (F16) {
-                    const float4 e4 = ex[16 * kg + 8 * hf + f0];
-                    inv_e[kg][hf] = e4.z;
-                    f = make_float2(e4.x * key_scale, e4.y);
-                }
+            for (int kg = 0; kg < kGroups; ++kg)
 #pragma unroll
-                for (int n = 0; n < NB; ++n) {
-                    float2 y = make_float2(s[kg][n][2 * hf], s[kg][n][2 * hf + 1]), by = make_float2(f.x, f.x);
-                    if constexpr (F16) by = mul2(by, *reinterpret_cast<const float2 *>(undo + 8 * n + 2 * c4));
-                    y = F16 ? fma2(y, by, make_float2(f.y, f.y)) : mul2(y, by);
+                for (int hf = 0; hf < 2; ++hf) {
+                    const float2 y = mul2(make_float2(s[kg][n][2 * hf], s[kg][n][2 * hf + 1]), by);
                     s[kg][n][2 * hf] = y.x;
                     s[kg][n][2 * hf + 1] = y.y;
                 }
-            }
+        }
+        if constexpr (F16) {
+#pragma unroll
+            for (int kg = 0; kg < kGroups; ++kg)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const float4 e4 = ex[16 * kg + 8 * hf + f0];
+                    inv_e[kg][hf] = e4.z;
+#pragma unroll
+                    for (int n = 0; n < NB; ++n) {
+                        const float2 y = fma2(make_float2(s[kg][n][2 * hf], s[kg][n][2 * hf + 1]), make_float2(e4.x, e4.x), make_float2(e4.y, e4.y));
+                        s[kg][n][2 * hf] = y.x;
+                        s[kg][n][2 * hf + 1] = y.y;
+                    }
+                }
+        }
         if (edge) {
 #pragma unroll
             for (int kg = 0; kg < kGroups; ++kg)

@@ -294,7 +294,7 @@ paged_four_kernel(const KvView kv, const SeqView sv, const WorkShape ws, const T
             cp_commit();
         }
         stage_queries<QSA_E2M1, TQ, NB, NT, kWarps>(tid, qp + (p.it.t0 + tok0) * ld_q + (int64_t)p.it.g * heads * kD, ld_q, G, rows, hpc,
-                                                    q_sign, q_all, undo_s[0]);
+                                                    q_sign, scale_log2, q_all, undo_s[0]);
         __syncthreads();
         int last[NB][2];  // the last cell each row sees
 #pragma unroll

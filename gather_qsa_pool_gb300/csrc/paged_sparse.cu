@@ -172,8 +172,8 @@ paged_sparse_kernel(const KvView kv, const SeqView sv, const ListView lv, const 
         }
         cp_commit();
     }
-    stage_queries<C, TQ, NB, NT, kWarps>(tid, qp + tok * ld_q + (int64_t)(group << hpc_log2) * G * kD, ld_q, G, G, hpc, q_sign, q_all,
-                                         undo_s[0]);
+    stage_queries<C, TQ, NB, NT, kWarps>(tid, qp + tok * ld_q + (int64_t)(group << hpc_log2) * G * kD, ld_q, G, G, hpc, q_sign,
+                                         scale_log2, q_all, undo_s[0]);
     __syncthreads();
     Rows<C, NB, NT> w;
     w.clear();
