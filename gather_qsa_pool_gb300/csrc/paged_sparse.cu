@@ -3,8 +3,8 @@
 // joined through distributed shared memory (one launch, no workspace).
 //
 // Mathematics and a warp's products: few_cells.cuh.  Each warp runs a ring of stages of its own (cp.async) over its
-// cells of every tile: warp w takes head w mod hpc and part w / hpc of a tile's 4 / hpc parts.  A tile's list entries
-// are looked up two turns ahead of its copies and their pages one turn ahead.
+// cells of every tile: warp w takes head w mod hpc and part w / hpc of a tile's 4 / hpc parts (hpc is 1, 2 or 4).
+// A tile's list entries are looked up two turns ahead of its copies and their pages one turn ahead.
 #include "few_cells.cuh"
 #include "paged.cuh"
 
@@ -28,6 +28,22 @@ __host__ __device__ constexpr size_t sparse_smem(int hpc)
 {
     constexpr int S = kWarps * Plan<C, NB, NT>::kStages;
     return (size_t)S * Cell<C>::kStage + (Cell<C>::kF16 ? (size_t)S * 32 * 16 : 0) + hpc * (q_bytes<NB, NT>() + fin_bytes<NB>());
+}
+
+// CTAs of an SM as far as shared memory lets them (a CTA takes 1 KB besides, and what the kernel declares).
+template <int C, int NB, int NT>
+constexpr int ctas_that_fit(int hpc)
+{
+    const int n = (int)(228 * 1024 / (sparse_smem<C, NB, NT>(hpc) + 1024 + 128 + 3 * kWarps * 8 * NB * 4));
+    return n < Plan<C, NB, NT>::kCtas ? n : Plan<C, NB, NT>::kCtas;
+}
+// KV heads of rows of codes that may share a CTA, as a power of two: as many CTAs fit an SM as with one.
+template <int C, int NB, int NT>
+constexpr int most_heads()
+{
+    const int one = ctas_that_fit<C, NB, NT>(1);
+    if (!Cell<C>::kF16 || ctas_that_fit<C, NB, NT>(2) < one) return 0;
+    return ctas_that_fit<C, NB, NT>(4) < one ? 1 : 2;
 }
 
 template <int C, typename TQ, int NB, int NT>
@@ -318,14 +334,22 @@ cudaError_t run(const SparseArgs &a, cudaStream_t st)
     const float scale = (a.scale == 0.0f ? 1.0f : fabsf(a.scale)) * kLog2e;
     const float q_sign = a.scale == 0.0f ? 0.0f : (a.scale < 0.0f ? -1.0f : 1.0f);
     constexpr auto kernel = few::paged_sparse_kernel<C, TQ, NB, NT>;
-    // (a head's queries and results take shared memory: four heads' as far as three CTAs fit an SM)
-    constexpr int kMost = C == QSA_BF16 || NB * NT > 4 ? 0 : (NB * NT > 2 ? 1 : 2);
+    constexpr int kMost = few::most_heads<C, NB, NT>();
     cudaError_t e = ensure_kernel_attrs<few::paged_sparse_kernel<C, TQ, NB, NT>>(few::sparse_smem<C, NB, NT>(1 << kMost));
     if (e != cudaSuccess) return e;
-    // CTAs of a token and its heads: as many as fill the GPU but for what clusters of their size leave of it, a tile
-    // each at most, up to the portable cluster's eight.  (One each where tokens x heads are no fewer than SMs, instead:
-    // 2,052 cells, 4 KV heads, 38 tokens bf16 54 us and not 44, 64 tokens e2m1 40 and not 36; otherwise alike.)  With many
-    // tokens the heads of a row go to one CTA.
+    // Two or four heads of a row go to one CTA, so that a row is read in larger pieces, where as many CTAs fit an SM as
+    // with one and the GPU is filled twice. One head / several, us of a graph replayed cold, 2,052 cells, 4 KV heads in
+    // groups of 8, 4-bit cells: chunks of 608 tokens 169 / 164, 1,024 276 / 274, 2,048 534 / 510, a token of 1,216
+    // sequences (1,028 cells) 212 / 195; below that they lose as often as they win (512 tokens 151 / 146, 256 81 / 87; a
+    // token of 256 sequences 61 / 56, of 456 89 / 100). 1,024 tokens in groups of 32, 4-bit cells 761 / 706, of 16, 8-bit
+    // cells 466 / 413; fp32 queries in groups of 8, 8-bit cells 362 / 335 (four heads; two 341). Where fewer CTAs fit they
+    // are kept apart: 1,024 tokens in groups of 8, 8-bit cells 253 / 287, of 32 740 / 1,022; of 16, 4-bit cells 392 / 438,
+    // fp32 queries in groups of 8 341 / 388 (but a token of 1,216 sequences 319 / 286 and 276 / 257, with four).
+    // CTAs of a token and its heads: as many as fill the GPU but for what clusters of their size leave of it, a tile each
+    // at most, up to the portable cluster's eight.  (All of it instead of seven eighths, us: 38 tokens, 4-bit cells 37 and
+    // not 30, bf16 51 and not 46, 14 tokens 8-bit 30 and not 21; 48 tokens 36 and not 37; otherwise alike.  Five eighths:
+    // 64 tokens 4-bit 43 and not 40, 48 tokens 40 and not 34.  One each where tokens x heads are no fewer than SMs: 38
+    // tokens bf16 54 and not 44.)
     const int64_t most = P::kCtas * device_sm_count();
     int hl = kMost;
     while (hl > 0 && (a.kv.H_kv % (1 << hl) || (a.sv.n_tok * a.kv.H_kv >> hl) < 2 * most)) --hl;
