@@ -4,15 +4,18 @@
 //
 // Mathematics.  Values i and i + rot / 2 of a head, i < rot / 2, turn by the angle p * base^(-2 i / rot) of the
 // token's position p:  (a, b) -> (a cos - b sin, b cos + a sin).  The angle is formed as a fraction of a turn in 64
-// bits: with f_i = 2^64 base^(-2 i / rot) / (2 pi), rounded, p * f_i modulo 2^64 is the angle's fraction of a turn
-// with an error of p / 2 units of 2^-64, and the whole turns drop out exactly, whatever p is.  In 64-bit
-// floating point the same product and its reduction would be bound by this GPU's few fp64 units.  The nearest quarter
+// bits: with f_i = 2^64 base^(-2 i / rot) / (2 pi), a double's 53 bits of it, p * f_i modulo 2^64 is the angle's fraction
+// of a turn, and the whole turns drop out exactly, whatever p is.  What f_i lacks (up to 650 units of 2^-64 over bases of
+// 1 to 10^12, 274 with base 10,000 and 128 values) makes the angle right to p * 2^-52 radians.  In 64-bit floating
+// point the same product and its reduction would be bound by this GPU's few fp64 units.  The nearest quarter
 // turn is taken off, and cosine and sine of the rest (at most pi / 4) are sums of two fp32 numbers, from their power
-// series: the first terms in both, the rest, below 2^-6, in one; together right to 2^-29.
+// series: the first terms in both, the rest, below 2^-6, in one; together right to 2^-29 for that angle.
 // Keys are rotated with both numbers, and the sum of the products carried in two as well: what is then cut down to
-// few bits, a code or a bf16 number, is the exact value's but for 2^-28 of it, where an fp32 result would fall to the
-// other side of a border fifty times as often.  (The fp32 number on the way is rounded to odd: its last bit says
-// whether anything was left, so the second rounding goes by the exact value.)  Queries take the first numbers alone.
+// few bits, a code or a bf16 number, is the exact value's but for 2^-28 of it (and p * 2^-52, which passes that from
+// positions of 2^24 on).  Of the 13.7 million key codes of 26,792 bf16 tokens none differs from the exact value's;
+// with the rotation in fp32 19 e4m3 and 3 e2m1 codes fell to the other side of a border.  (The fp32 number on the way
+// is rounded to odd: its last bit says whether anything was left, so the second rounding goes by the exact value.)
+// Queries take the first numbers alone.
 // The quantised forms are paged_rw.cu's (8 bits) and e2m1.cuh's (4 bits).
 //
 // Shape.  A warp takes some heads of a token, eight values a lane and d / 8 lanes a head (a power of two of them).  A
@@ -442,7 +445,7 @@ paged_append_kernel(const AppendArgs a, const __grid_constant__ Turns turns, con
     }
 }
 
-// f_i to about 2^-52 of itself: the exponent i * (2 / rot) log2(base) in two parts, the first exact.
+// f_i to about 2^-51 of itself: the exponent i * (2 / rot) log2(base) in two parts, the first exact.
 void fill_turns(Turns &t, double base, int rot)
 {
     if (rot == 0) return;
