@@ -24,10 +24,11 @@ struct Four {
     static constexpr int kStages = NB * NT == 2 ? 2 : 3;
 };
 
-// As dense.cuh's flattened list, made short: every row tile of a sequence counts the tiles of its whole context (the
-// earlier ones of a few tokens see hardly less; turns behind what they see read nothing), so that a share is found
-// with shifts and a few 32-bit divisions.  (The exact list took 11,000 to 24,000 cycles at 64 sequences, most of
-// them fetching code that runs once.)
+// As dense.cuh's flattened list, made short: every row tile of a sequence counts the tiles of its whole context (turns
+// behind what a row tile sees read nothing), so that a share is found with shifts and a few 32-bit divisions.  (The exact
+// list took 11,000 to 24,000 cycles at 64 sequences, most of them fetching code that runs once.)  The row tiles of a few
+// tokens see hardly less.  Those of fp32 prompts, which come here too, do: shares are uneven then, and 8,192 tokens over
+// themselves (32 / 4 heads) take 5.5 ms where even ones would take 3.6 at the pace of 1,024 tokens over 8,192 cells (0.84).
 struct Item {
     int32_t s, g, t;     // sequence, group of heads, row tile
     int32_t tiles;

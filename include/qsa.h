@@ -675,7 +675,9 @@ qsa_status qsa_mask_sparse_eligible(int has_mask, float max_bias, float softcap,
  *              1, 1.5, 2, 3, 4, 6 and their negatives; two a byte, the even value in the low half)
  *              with an e4m3 scale for each 16 values in K_scale / V_scale
  *              [n_pages][H_kv][page_size][d / 16] and an exponent byte as above; the value is
- *              code * scale * 2^(b - 127)
+ *              code * scale * 2^(b - 127).  Attention reads less of a smaller type and converts more:
+ *              one token a sequence is fastest on QSA_E2M1, a few tokens a sequence on QSA_E4M3,
+ *              chunks and prompts on QSA_BF16 (0.6 of the others' time)
  *   page_size  tokens per page, a power of two from 8 to 4096
  *   n_pages    pages in the pool, n_pages * page_size < 2^31
  * Requirements (INVALID_ARG otherwise): K, V non-null and 16-byte aligned, ld_k, ld_v >= H_kv*d
@@ -780,7 +782,9 @@ qsa_status qsa_paged_read(const qsa_paged_cache *cache, const int32_t *table, in
  * its cell's power of two is held to 3 * 2^-33 (9 bits) or 2^-38 (11 and 22 bits) of the row's largest, and
  * smaller ones may count as nothing; and queries are held to 2^-31 of the largest magnitude of their row (token
  * and head).  Other shapes, and QSA_BF16 chunks with scale <= 0, take fp32 arithmetic on the CUDA cores, which is
- * right but slower (no tensor cores, contexts not shared out).
+ * right but slower (no tensor cores, contexts not shared out).  On the tensor cores a row of a chunk whose logits pass
+ * 2^30 in magnitude may be NaN or zeros, and QSA_F32 queries on a QSA_BF16 pool may make NaN of a row that sees an
+ * infinite key or value.
  * Errors: INVALID_ARG for null pointers, sizes < 0, H_q not a multiple of H_kv, ld_q < H_q*d, a
  * misaligned pointer (q and out 16 bytes, rows of q a multiple of 16 bytes), a workspace smaller
  * than required; UNSUPPORTED for n_seq, n_tok or their work beyond 2^31 - 1 rows.
@@ -814,6 +818,7 @@ size_t qsa_paged_attn_workspace_size(int64_t n_tok, int64_t n_seq, int64_t max_q
  *           same tokens), or NULL; with packed k, k itself may be it
  *   pos     [n_tok] int32 device, or NULL
  *   rot     0 (no rotation) to d, a multiple of 16;  base >= 1
+ * Outputs overlap no input but as said, nor one another, nor the pool.
  * A token that is skipped by qsa_paged_write (its cell is not there) still has q_out and k_out
  * written; tokens from cu_q[n_seq] on have not.
  * Errors: those of qsa_paged_write; INVALID_ARG for rot < 0, > d or not a multiple of 16, a base that
