@@ -18,10 +18,11 @@
 // weight, is three e5m2 terms that lie beside each other as columns: e5m2 is the upper byte of fp16, so
 // the terms of an fp16 number are its upper byte, the upper byte of what that leaves, and of what that
 // leaves: 3 + 3 + 3 significant bits.  A bf16 query (8 bits) is exact in them down to 2^-31 of the
-// item's largest.  Weights are rounded to 9 bits; what a weight's terms leave for the next is taken 8 times
-// as large (and their products that much smaller), so that small weights are not cut off where e5m2 ends
-// (2^-16) while the sum counts them: a weight is off by 2^-9 of itself or by 3 * 2^-23, where the largest
-// is at least 2^10.  The sum l adds 2^(x - ve), from the weight where |ve| is at most 50.
+// row's largest (a row is scaled for itself).  Weights are rounded to 9 bits; what a weight's terms
+// leave for the next is taken 8 times as large (and their products that much smaller), so that small
+// weights are not cut off where e5m2 ends (2^-16) while the sum counts them: a weight is off by 2^-9
+// of itself or by 3 * 2^-23, where the largest is at least 2^10.  The sum l adds 2^(x - ve), from the
+// weight where |ve| is at most 50.
 //
 // Shape: one persistent CTA per SM, an equal share of the flattened list of (sequence, KV head, row
 // tile) items in tiles of 128 cells (dense.cuh).  Warps 0-7: two groups that take the weights of the
@@ -35,7 +36,7 @@
 // What bounds it: bf16, the bytes (64 sequences of up to 8,000 cells, 32 / 4 heads, one token: 99 us,
 // 5.4 TB/s; one of 255,181: 92 us).  e4m3, the weights' turn from logits to terms and back to the tensor
 // cores, about 1,500 cycles a tile with two groups in flight where the bytes take 1,000 (48 sequences of
-// up to 16,384 cells, 32 rows: 99 us; 16 rows: 86 us, 4.7 TB/s), and about 8,000 cycles at each end of a
+// up to 16,384 cells, 32 rows: 101 us; 16 rows: 86 us, 4.7 TB/s), and about 8,000 cycles at each end of a
 // part (references, sums and outputs joined, the first references).
 //
 // Every mbarrier wait is bounded: after one gives up, nothing new is issued, what was issued is waited
