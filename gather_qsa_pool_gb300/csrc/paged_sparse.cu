@@ -368,6 +368,9 @@ template <int C>
 cudaError_t run_cells(const SparseArgs &a, cudaStream_t st)
 {
     const int G = a.H_q / a.kv.H_kv;
+    // Terms: of fp32 queries as many as hold 22 or 24 bits; of bf16 queries, which one holds, one, so that a weight has 8
+    // bits on bf16 cells (11 on codes): outputs are 0.0022 off in the 2-norm, 0.0017 with two (what the bf16 output's own
+    // rounding is), but 1,024 tokens take 300 us and not 358, one token 17.5 and not 18.6 (a graph replayed cold).
     constexpr int NT = C == QSA_BF16 ? 3 : 2;
     if (a.q_dtype == QSA_F32) {
         if (G <= 8) return run<C, float, 1, NT>(a, st);
