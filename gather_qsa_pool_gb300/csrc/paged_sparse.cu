@@ -339,12 +339,12 @@ cudaError_t run(const SparseArgs &a, cudaStream_t st)
     if (e != cudaSuccess) return e;
     // Two or four heads of a row go to one CTA, so that a row is read in larger pieces, where as many CTAs fit an SM as
     // with one and the GPU is filled twice. One head / several, us of a graph replayed cold, 2,052 cells, 4 KV heads in
-    // groups of 8, 4-bit cells: chunks of 608 tokens 169 / 164, 1,024 276 / 274, 2,048 534 / 510, a token of 1,216
-    // sequences (1,028 cells) 212 / 195; below that they lose as often as they win (512 tokens 151 / 146, 256 81 / 87; a
-    // token of 256 sequences 61 / 56, of 456 89 / 100). 1,024 tokens in groups of 32, 4-bit cells 761 / 706, of 16, 8-bit
-    // cells 466 / 413; fp32 queries in groups of 8, 8-bit cells 362 / 335 (four heads; two 341). Where fewer CTAs fit they
-    // are kept apart: 1,024 tokens in groups of 8, 8-bit cells 253 / 287, of 32 740 / 1,022; of 16, 4-bit cells 392 / 438,
-    // fp32 queries in groups of 8 341 / 388 (but a token of 1,216 sequences 319 / 286 and 276 / 257, with four).
+    // groups of 8, 4-bit cells: chunks of 608 tokens 167 / 161, 1,024 272 / 269, 2,048 526 / 503, a token of 1,216
+    // sequences (1,028 cells) 210 / 192; below that they lose as often as they win (512 tokens 148 / 143, 256 81 / 87; a
+    // token of 256 sequences 63 / 56, of 456 89 / 99). 1,024 tokens in groups of 32, 4-bit cells 700 / 646, of 16, 8-bit
+    // cells 450 / 401; fp32 queries in groups of 8, 8-bit cells 362 / 335 (four heads; two 339). Where fewer CTAs fit they
+    // are kept apart: 1,024 tokens in groups of 8, 8-bit cells 253 / 286, of 32 708 / 968; of 16, 4-bit cells 390 / 435,
+    // fp32 queries in groups of 8 340 / 386 (but a token of 1,216 sequences 318 / 286 and 275 / 258, with four).
     // CTAs of a token and its heads: as many as fill the GPU but for what clusters of their size leave of it, a tile each
     // at most, up to the portable cluster's eight.  (All of it instead of seven eighths, us: 38 tokens, 4-bit cells 37 and
     // not 30, bf16 51 and not 46, 14 tokens 8-bit 30 and not 21; 48 tokens 36 and not 37; otherwise alike.  Five eighths:
